@@ -59,6 +59,8 @@ extern "C" {
 #define MLA_STATUS_PLAN_MISMATCH 0x4 /* decode arguments differ from the plan's */
 #define MLA_STATUS_TIMEOUT 0x8      /* a bounded wait inside a kernel ran out */
 #define MLA_STATUS_BAD_LENGTH 0x10  /* context_lens[b] < 0 or beyond the block table */
+#define MLA_STATUS_NO_PAGES 0x20    /* mla_extend_tables: the free pages did not suffice */
+#define MLA_STATUS_BAD_POSITION 0x40 /* mla_rope_write: position beyond the angle table: row skipped */
 
 #define MLA_DTYPE_BF16 0
 #define MLA_DTYPE_FP8_E4M3 1
@@ -205,6 +207,135 @@ int mla_decode_q(const mla_kv_pool* pool, int layer, const void* q,
  * fp32 accumulation. */
 int mla_uv_project(const void* attn_out, const void* w_uv, void* y, int batch,
                    int num_heads, void* workspace, void* stream);
+
+/* ---------------------------------------------------------------- prefill step
+ * Three calls make a step that takes a chunk of new tokens per request (prompt
+ * chunks, mixed with single tokens): mla_extend_tables finds the tokens'
+ * places, mla_rope_write rotates and stores their latent rows and rotates
+ * their queries, mla_prefill attends. context_lens has its meaning of above
+ * throughout: the tokens cached before the step, so that the new ones sit at
+ * positions context_lens[b] .. and are attended once written. */
+
+/* Page tables of a step from request lengths, on the device. Request b holds
+ * context_lens[b] = L tokens, whose pages are the first ceil(L / page_size)
+ * entries of its block table row, and gets new_lens[b] = n >= 0 more. The pages
+ * that these need are taken off the top of the stack of free pages, in the
+ * order of requests and blocks: the first one is free_pages[count - 1].
+ *   context_lens, new_lens: device, [batch] int32.
+ *   free_pages:   device, [free_capacity] int32, the stack; the first
+ *                 *free_count entries are free pages. Not written.
+ *   free_count:   device int32. Not written unless state points at it.
+ *   block_table:  device, [batch][max_blocks] int32; the entries of new blocks
+ *                 are written, all others left as they were.
+ *   slot_mapping: device, [max_tokens] int64: the slot of each new token, request
+ *                 after request, as mla_kv_write and mla_rope_write take it.
+ *   positions:    device, [max_tokens] int32: its position; or NULL.
+ *                 Entries behind the last token are -1 in both (pad rows).
+ *   q_indptr:     device, [batch + 1] int32: where each request's tokens start.
+ *   page_indptr, page_ids: device, [batch + 1] and [max_page_ids] int32: the
+ *                 tables as CSR lists, of ceil((L + n) / page_size) pages each;
+ *                 or both NULL. Entries behind the last page are left as they were.
+ *   state:        device, [2] int32, written last: the free pages left, and the
+ *                 first request that was refused for want of pages (batch if
+ *                 none). state may be free_count's own address: the count is
+ *                 then updated in place.
+ * A request whose pages do not all remain (MLA_STATUS_NO_PAGES) takes none: its
+ * new tokens have slot and position -1, its CSR list only the pages it held.
+ * Requests after it that need pages are refused too, those that need none are
+ * served. A request with a negative length or more tokens than max_blocks
+ * blocks hold (MLA_STATUS_BAD_LENGTH) is refused alike; a negative n counts as
+ * no tokens. A page id outside [0, num_pages) (MLA_STATUS_BAD_PAGE) is stored
+ * as -1 and gives slot and position -1. Tokens beyond max_tokens and ids
+ * beyond max_page_ids are not written (MLA_STATUS_BAD_LENGTH).
+ *   workspace:    whose status word records this (a decode or prefill
+ *                 workspace), or NULL.
+ * page_size is 16, 32, 64 or 128 and max_blocks * page_size below 2^31. */
+int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int batch, int page_size, int num_pages,
+                      const int32_t* free_pages, const int32_t* free_count, int free_capacity, int32_t* block_table,
+                      int max_blocks, int64_t* slot_mapping, int32_t* positions, int max_tokens, int32_t* q_indptr,
+                      int32_t* page_indptr, int32_t* page_ids, int max_page_ids, int32_t* state, void* workspace,
+                      void* stream);
+
+/* Rotary positions of n new tokens, the latent rows' norm and their write.
+ * Pair j (of 32) of a row's last 64 dims is dims (2j, 2j + 1) if interleaved
+ * is nonzero, else (j, j + 32). It turns by the angle that cos_sin holds for
+ * position p = positions[pair_axis[j]][token]:
+ *   (x, y) -> (x cos - y sin, x sin + y cos),
+ *   cos = cos_sin[p][j], sin = cos_sin[p][32 + j].
+ * Rows (rows != NULL): c_kv (the first 512 dims) becomes
+ * c_kv / sqrt(mean(c_kv^2) + norm_eps) * norm_weight if norm_weight is given,
+ * the rope part turns, and the row is stored at its slot as mla_kv_write does,
+ * rounded once from fp32. Queries (q_rope != NULL): the 64 rope dims of every
+ * head turn and are rounded to bf16.
+ *   rows:         device, [n][576] bf16, 16-byte aligned.
+ *   slot_mapping: device, [n] int64; required with rows. A row with a negative
+ *                 slot is a pad row: neither its latent nor its queries are
+ *                 touched. A slot beyond the layer sets MLA_STATUS_BAD_SLOT and
+ *                 its latent row is skipped.
+ *   positions:    device, [num_axes][n] int32, 1 to 4 axes (text has one; time,
+ *                 height and width are three). A negative one marks a pad row;
+ *                 one >= max_position sets MLA_STATUS_BAD_POSITION and the row
+ *                 and its queries are skipped.
+ *   pair_axis:    host, [32]: each pair's axis; NULL is axis 0 for all.
+ *   cos_sin:      device, [max_position][64] fp32, 16-byte aligned.
+ *   norm_weight:  device, [512] bf16, 16-byte aligned, or NULL.
+ *   q_rope, q_out: device; the rope dims of head h of token t start
+ *                 (t * num_heads + h) * pitch elements further. Pitches are
+ *                 multiples of 8 and at least 64, pointers 16-byte aligned.
+ *                 q_out may be q_rope (in place) or rows that share no element
+ *                 with it; other overlaps are refused with MLA_ERR_ARG.
+ *   pool, layer:  used with rows only. workspace: for the status word, or NULL. */
+int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const int64_t* slot_mapping, int n,
+                   const int32_t* positions, int num_axes, const uint8_t* pair_axis, const float* cos_sin,
+                   int max_position, int interleaved, const void* norm_weight, float norm_eps, const void* q_rope,
+                   int64_t q_pitch, void* q_out, int64_t q_out_pitch, int num_heads, void* workspace, void* stream);
+
+/* Attention of a ragged chunk of new tokens over the paged cache, in the
+ * 192/128 multi-head form (the unabsorbed form of mla_decode_q followed by
+ * mla_uv_project, with a number of new tokens of its own for each request).
+ * Request b has n_b = q_indptr[b + 1] - q_indptr[b] new tokens (0 is fine) at
+ * positions L_b .. L_b + n_b - 1, written beforehand; for its token i, head h:
+ *   k_t = (c_kv[t] w_uk[h]^T, k_rope[t]), v_t = c_kv[t] w_uv[h],
+ *   s_t = softmax_scale * q[q_indptr[b] + i, h, :] . k_t
+ *         over t in [0 or max(0, L_b + i + 1 - window), L_b + i],
+ *   out = sum_t softmax(s)_t v_t,  lse = log(sum_t exp(s_t)).
+ * Keys and values of all heads are made once (512 bytes per head and attended
+ * position, in the workspace) and then attended at 640 flops a pair where the
+ * absorbed form costs 2,176. Making them costs as much as 410 queries'
+ * attention, so from about 170 new tokens a request this call does less work,
+ * and mla_decode / mla_decode_q serve shorter chunks and single tokens better.
+ *   q:        device, [q_rows][num_heads][192] bf16 (nope 128 || rope 64).
+ *   q_indptr: device, [batch + 1] int32, non-decreasing, within [0, q_rows].
+ *             Rows of out outside [q_indptr[0], q_indptr[batch]) stay as they were.
+ *   page_indptr / page_ids / max_blocks: the pages, as for mla_decode.
+ *   max_kv_tokens: at least the sum over requests of attended positions,
+ *             L_b + n_b - (0 or max(0, L_b + 1 - window)) where n_b > 0.
+ *   w_uk:     device, [num_heads][128][512] bf16; w_uv: [num_heads][512][128].
+ *   out:      device, [q_rows][num_heads][128] bf16, 32-byte aligned;
+ *   lse:      device, [q_rows][num_heads] fp32 or NULL. q, w_uk, w_uv 16-byte.
+ *   workspace: mla_prefill_workspace_size(batch, q_rows, max_kv_tokens,
+ *             num_heads, heads_per_pass) bytes, 256-byte aligned, its first 256
+ *             zeroed once before the first use. Of its own: not a decode
+ *             workspace, and not shared by calls that overlap on the GPU.
+ * num_heads is 1 to 1024. Arithmetic: fp32 accumulation, keys, values and
+ * softmax weights rounded to bf16 for the tensor core. fp8 pools: the codes
+ * are widened exactly and kv_scale multiplies the scores and the output.
+ * On the device: a bad page id sets MLA_STATUS_BAD_PAGE and its rows read as
+ * zero; a request with a bad length (negative, beyond its page list, or beyond
+ * max_kv_tokens in the sum) sets MLA_STATUS_BAD_LENGTH and its rows of out and
+ * lse are NaN; row pointers outside q set it and nothing is written. A cached
+ * row with an infinity or NaN in c_kv gives NaN to the rows that attend it
+ * and to no others. */
+int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t* q_indptr, const int32_t* page_indptr,
+                const int32_t* page_ids, int max_blocks, const int32_t* context_lens, int batch, int q_rows,
+                int64_t max_kv_tokens, int num_heads, const void* w_uk, const void* w_uv, float softmax_scale,
+                int window, void* workspace, size_t workspace_bytes, void* out, float* lse, void* stream);
+
+/* Bytes of workspace for mla_prefill with room for the keys and values of
+ * heads_per_pass heads (0: of all heads, or of as many as 8 GiB hold). A
+ * workspace of another size is used for as many heads a pass as fit; below
+ * one head's mla_prefill returns MLA_ERR_WORKSPACE. 0 on bad arguments. */
+size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, int num_heads, int heads_per_pass);
 
 /* Reads the status word of `workspace` into *code (MLA_STATUS_* bits) and, if
  * `clear` is nonzero, resets it. Synchronises `stream`: diagnostics only. */

@@ -13,6 +13,8 @@ Calls (same names as the C ABI in include/mla_decode.h):
   workspace_size_q / plan_q / decode_q: several query positions per request
   (q [batch, q_len, heads, 576]; causal within the step)
   uv_project(attn_out, w_uv, y, workspace=None)
+  extend_tables / rope_write / prefill: a step of ragged chunks of new tokens
+  (page tables from lengths, rotary latent write, 192/128 attention)
   get_error(workspace, clear=False)
 """
 from __future__ import annotations
@@ -34,16 +36,22 @@ STATUS_BAD_SLOT = 0x2
 STATUS_PLAN_MISMATCH = 0x4
 STATUS_TIMEOUT = 0x8
 STATUS_BAD_LENGTH = 0x10
+STATUS_NO_PAGES = 0x20
+STATUS_BAD_POSITION = 0x40
 DTYPE_BF16 = 0
 DTYPE_FP8_E4M3 = 1
 LATENT_DIM = 576
 KV_LORA_RANK = 512
 V_HEAD_DIM = 128
+NOPE_DIM = 128
+ROPE_DIM = 64
+QK_HEAD_DIM = 192
 
 EXPORTED = ["mla_kv_write", "mla_decode_workspace_size", "mla_decode_num_clusters",
             "mla_decode_plan", "mla_decode", "mla_uv_project", "mla_get_error",
             "mla_decode_noalloc", "mla_decode_workspace_size_q", "mla_decode_plan_q",
-            "mla_decode_q", "mla_selftest_bounded_wait"]
+            "mla_decode_q", "mla_selftest_bounded_wait", "mla_extend_tables", "mla_rope_write",
+            "mla_prefill", "mla_prefill_workspace_size"]
 NOALLOC_SCRATCH_BYTES = 48 << 20
 
 
@@ -96,6 +104,17 @@ def load_library(path: str = LIB_PATH):
     lib.mla_decode_q.argtypes = [ctypes.POINTER(_Pool), I, P, P, P, I, P, I, I, I, ctypes.c_float, I,
                                  P, P, P, P]
     lib.mla_decode_q.restype = I
+    L = ctypes.c_int64
+    lib.mla_extend_tables.argtypes = [P, P, I, I, I, P, P, I, P, I, P, P, I, P, P, P, I, P, P, P]
+    lib.mla_extend_tables.restype = I
+    lib.mla_rope_write.argtypes = [ctypes.POINTER(_Pool), I, P, P, I, P, I, ctypes.c_char_p, P, I, I, P,
+                                   ctypes.c_float, P, L, P, L, I, P, P]
+    lib.mla_rope_write.restype = I
+    lib.mla_prefill.argtypes = [ctypes.POINTER(_Pool), I, P, P, P, P, I, P, I, I, L, I, P, P, ctypes.c_float, I,
+                                P, Z, P, P, P]
+    lib.mla_prefill.restype = I
+    lib.mla_prefill_workspace_size.argtypes = [I, I, L, I, I]
+    lib.mla_prefill_workspace_size.restype = Z
     _lib = lib
     return lib
 
@@ -332,4 +351,191 @@ def decode_q(pool: KVPool, layer: int, q: torch.Tensor, context_lens: torch.Tens
                           window, _dev(workspace, "workspace"), _dev(out, "out", torch.bfloat16),
                           None if lse is None else _dev(lse, "lse", torch.float32), _stream(stream))
     _check(rc, "mla_decode_q")
+    return out
+
+
+# ----------------------------------------------------------------- prefill step
+
+def _here(t: torch.Tensor, name: str, dtype, device: int) -> int:
+    """_dev for tensors that have to live on the current device."""
+    p = _dev(t, name, dtype)
+    if t.get_device() != device:
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), device))
+    return p
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype, device: int):
+    return None if t is None else _here(t, name, dtype, device)
+
+
+def extend_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                  free_count: torch.Tensor, block_table: torch.Tensor, page_size: int, num_pages: int,
+                  slot_mapping: torch.Tensor, q_indptr: torch.Tensor, state: torch.Tensor,
+                  positions: Optional[torch.Tensor] = None, page_indptr: Optional[torch.Tensor] = None,
+                  page_ids: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Give new_lens[b] new tokens of each request their places: pages off the
+    top of the stack free_pages[:free_count] into block_table, slots and
+    positions of the tokens (-1 behind the last), their row pointers q_indptr,
+    and the tables as CSR lists. state becomes (free pages left, first request
+    refused for want of pages); it may share free_count's memory."""
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    if context_lens.dim() != 1 or new_lens.shape != context_lens.shape:
+        raise ValueError("context_lens and new_lens must be [batch]")
+    B = context_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [batch, max_blocks]")
+    if slot_mapping.dim() != 1 or (positions is not None and positions.shape != slot_mapping.shape):
+        raise ValueError("slot_mapping and positions must be [max_tokens]")
+    if q_indptr.shape != (B + 1,) or (page_indptr is not None and page_indptr.shape != (B + 1,)):
+        raise ValueError("q_indptr and page_indptr must be [batch + 1]")
+    if (page_indptr is None) != (page_ids is None):
+        raise ValueError("give page_indptr and page_ids together")
+    if free_count.numel() < 1 or state.numel() < 2:
+        raise ValueError("free_count needs one element and state two")
+    rc = load_library().mla_extend_tables(
+        _here(context_lens, "context_lens", i32, dev), _here(new_lens, "new_lens", i32, dev), B, page_size, num_pages,
+        _here(free_pages, "free_pages", i32, dev), _here(free_count, "free_count", i32, dev), free_pages.numel(),
+        _here(block_table, "block_table", i32, dev), block_table.shape[1],
+        _here(slot_mapping, "slot_mapping", torch.int64, dev), _opt(positions, "positions", i32, dev),
+        slot_mapping.shape[0], _here(q_indptr, "q_indptr", i32, dev), _opt(page_indptr, "page_indptr", i32, dev),
+        _opt(page_ids, "page_ids", i32, dev), 0 if page_ids is None else page_ids.numel(),
+        _here(state, "state", i32, dev), _opt(workspace, "workspace", None, dev), _stream(stream))
+    _check(rc, "mla_extend_tables")
+
+
+def _head_rows(t: torch.Tensor, name: str, device: int):
+    """Pointer and pitch of the [tokens, heads, 64] rope dims of queries, a view
+    whose (token, head) rows lie at one pitch."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device:
+        raise ValueError("%s must be a CUDA tensor on the current device" % name)
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != ROPE_DIM:
+        raise ValueError("%s must be bfloat16 [tokens, heads, 64]" % name)
+    n, h, _ = t.shape
+    s0, s1, s2 = t.stride()
+    pitch = s1 if h > 1 else s0 if n > 1 else ROPE_DIM
+    if s2 != 1 or (h > 1 and n > 1 and s0 != h * s1):
+        raise ValueError("%s: the (token, head) rows must lie at one pitch" % name)
+    return t.data_ptr(), pitch
+
+
+def rope_write(pool: Optional[KVPool], layer: int, rows: Optional[torch.Tensor], slot_mapping: Optional[torch.Tensor],
+               positions: torch.Tensor, cos_sin: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
+               norm_eps: float = 1e-6, q_rope: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+               pair_axis=None, interleaved: bool = True, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """Rotate the rope dims of new latent rows and of their queries, normalise
+    c_kv (norm_weight given) and store the rows at their slots. positions is
+    [tokens] or [axes, tokens]; pair_axis gives each of the 32 pairs its axis.
+    q_rope and q_out are views [tokens, heads, 64] of the queries' rope dims;
+    q_out None rotates in place. rows None (with pool and slot_mapping as may
+    be) rotates queries only."""
+    dev = torch.cuda.current_device()
+    if positions.dim() not in (1, 2):
+        raise ValueError("positions must be [tokens] or [axes, tokens]")
+    axes, n = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
+    if rows is None and q_rope is None:
+        raise ValueError("give rows, q_rope or both")
+    if rows is not None and (pool is None or slot_mapping is None or rows.shape != (n, LATENT_DIM)):
+        raise ValueError("rows [tokens, 576] go with pool and slot_mapping")
+    if slot_mapping is not None and slot_mapping.shape != (n,):
+        raise ValueError("slot_mapping must be [tokens]")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != ROPE_DIM:
+        raise ValueError("cos_sin must be [positions, 64]")
+    if norm_weight is not None and norm_weight.shape != (KV_LORA_RANK,):
+        raise ValueError("norm_weight must be [512]")
+    axis_of = None
+    if pair_axis is not None:
+        if len(pair_axis) != ROPE_DIM // 2 or min(pair_axis) < 0 or max(pair_axis) >= axes:
+            raise ValueError("pair_axis must name an axis for each of the 32 pairs")
+        axis_of = bytes(pair_axis)
+    qp = op = None
+    q_pitch = o_pitch = heads = 0
+    if q_rope is not None:
+        q_out = q_rope if q_out is None else q_out
+        if q_rope.shape[0] != n or q_out.shape != q_rope.shape:
+            raise ValueError("q_rope and q_out must be [tokens, heads, 64]")
+        qp, q_pitch = _head_rows(q_rope, "q_rope", dev)
+        op, o_pitch = _head_rows(q_out, "q_out", dev)
+        heads = q_rope.shape[1]
+        if heads == 0:
+            qp = op = None
+    elif q_out is not None:
+        raise ValueError("q_out goes with q_rope")
+    c = None
+    if rows is not None:
+        c = pool._c()
+        if pool.data.get_device() != dev:
+            raise ValueError("pool is not on the current device")
+        c = ctypes.byref(c)
+    elif qp is None:
+        return
+    rc = load_library().mla_rope_write(
+        c, layer, _opt(rows, "rows", torch.bfloat16, dev), _opt(slot_mapping, "slot_mapping", torch.int64, dev), n,
+        _here(positions, "positions", torch.int32, dev), axes, axis_of, _here(cos_sin, "cos_sin", torch.float32, dev),
+        cos_sin.shape[0], 1 if interleaved else 0, _opt(norm_weight, "norm_weight", torch.bfloat16, dev),
+        float(norm_eps), qp, q_pitch, op, o_pitch, heads, _opt(workspace, "workspace", None, dev), _stream(stream))
+    _check(rc, "mla_rope_write")
+
+
+def prefill_workspace_size(batch: int, q_rows: int, max_kv_tokens: int, num_heads: int, heads_per_pass: int = 0) -> int:
+    n = load_library().mla_prefill_workspace_size(batch, q_rows, max_kv_tokens, num_heads, heads_per_pass)
+    if n == 0:
+        raise MlaError("mla_prefill_workspace_size: unsupported arguments")
+    return n
+
+
+def alloc_prefill_workspace(batch: int, q_rows: int, max_kv_tokens: int, num_heads: int, heads_per_pass: int = 0,
+                            device=None) -> torch.Tensor:
+    """A workspace for prefill() with its status word cleared. heads_per_pass
+    bounds its size: the keys and values of so many heads are kept at once."""
+    ws = torch.empty(prefill_workspace_size(batch, q_rows, max_kv_tokens, num_heads, heads_per_pass),
+                     dtype=torch.uint8, device=device or torch.device("cuda"))
+    ws[:256].zero_()
+    return ws
+
+
+def prefill(pool: KVPool, layer: int, q: torch.Tensor, q_indptr: torch.Tensor, context_lens: torch.Tensor,
+            softmax_scale: float, w_uk: torch.Tensor, w_uv: torch.Tensor, workspace: torch.Tensor, out: torch.Tensor,
+            max_kv_tokens: int, block_table: Optional[torch.Tensor] = None,
+            page_indptr: Optional[torch.Tensor] = None, page_ids: Optional[torch.Tensor] = None, window: int = 0,
+            lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """q [rows, heads, 192] of ragged chunks (request b: rows q_indptr[b] to
+    q_indptr[b + 1], at positions from context_lens[b]) -> out [rows, heads,
+    128], lse [rows, heads]: causal attention over the paged cache, the new
+    tokens' latent rows written beforehand."""
+    dev = torch.cuda.current_device()
+    i32, bf16 = torch.int32, torch.bfloat16
+    if q.dim() != 3 or q.shape[2] != QK_HEAD_DIM:
+        raise ValueError("q must be [rows, heads, 192]")
+    T, H, _ = q.shape
+    if out.shape != (T, H, V_HEAD_DIM) or (lse is not None and lse.shape != (T, H)):
+        raise ValueError("out must be [rows, heads, 128], lse [rows, heads]")
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be [batch]")
+    B = context_lens.shape[0]
+    if q_indptr.shape != (B + 1,):
+        raise ValueError("q_indptr must be [batch + 1]")
+    if w_uk.shape != (H, NOPE_DIM, KV_LORA_RANK) or w_uv.shape != (H, KV_LORA_RANK, V_HEAD_DIM):
+        raise ValueError("w_uk [heads, 128, 512] and w_uv [heads, 512, 128] expected")
+    if block_table is not None:
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError("block_table must be [batch, max_blocks]")
+        indptr_p, ids_p, max_blocks = None, _here(block_table, "block_table", i32, dev), block_table.shape[1]
+    else:
+        if page_indptr is None or page_ids is None or page_indptr.shape != (B + 1,):
+            raise ValueError("give block_table, or page_indptr [batch+1] and page_ids")
+        indptr_p, ids_p, max_blocks = _here(page_indptr, "page_indptr", i32, dev), \
+            _here(page_ids, "page_ids", i32, dev), 0
+    if pool.data.get_device() != dev:
+        raise ValueError("pool is not on the current device")
+    c = pool._c()
+    rc = load_library().mla_prefill(
+        ctypes.byref(c), layer, _here(q, "q", bf16, dev), _here(q_indptr, "q_indptr", i32, dev), indptr_p, ids_p,
+        max_blocks, _here(context_lens, "context_lens", i32, dev), B, T, max_kv_tokens, H,
+        _here(w_uk, "w_uk", bf16, dev), _here(w_uv, "w_uv", bf16, dev), float(softmax_scale), window,
+        _here(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
+        _here(out, "out", bf16, dev), _opt(lse, "lse", torch.float32, dev), _stream(stream))
+    _check(rc, "mla_prefill")
     return out

@@ -3,10 +3,10 @@
 // stream synchronisation (except mla_get_error).
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <string.h>
 
 #include "../../include/mla_decode.h"
+#include "host_util.h"
 #include "mla_internal.h"
 
 // Scratch of mla_decode_noalloc: schedule, status and split partials.
@@ -14,37 +14,12 @@ static __device__ __align__(256) unsigned char g_noalloc_scratch[MLA_NOALLOC_SCR
 
 namespace {
 
+using mla::aligned;
+using mla::encode_fn;
+using mla::make_map_2d;
+using mla::valid_pool;
 using mla::WsHeader;
 using mla::WsLayout;
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
-// 2-D row-major map: rows x cols elements, row pitch `pitch_bytes`, box
-// {box_cols, box_rows}, zero fill out of bounds.
-bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t rows, uint64_t cols,
-                 uint64_t pitch_bytes, uint32_t box_cols, uint32_t box_rows,
-                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {pitch_bytes};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // 3-D view of a bf16 pool for one copy of a rank's four 64-dim chunks: dims
 // {64 dims, rows, 8 chunks}, strides {row pitch, 128 bytes}, box {64, 64, 4}
@@ -59,17 +34,6 @@ bool make_chunk_map(CUtensorMap* m, const void* base, uint64_t rows) {
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool valid_pool(const mla_kv_pool* pool) {
-  if (!pool || !pool->data || pool->num_layers <= 0 || pool->num_pages <= 0) return false;
-  if (pool->page_size != 16 && pool->page_size != 32 && pool->page_size != 64 && pool->page_size != 128)
-    return false;
-  if (pool->dtype != MLA_DTYPE_BF16 && pool->dtype != MLA_DTYPE_FP8_E4M3) return false;
-  if (pool->dtype == MLA_DTYPE_FP8_E4M3 && !(pool->kv_scale > 0.f)) return false;
-  return aligned(pool->data, 16);
 }
 
 int max_clusters() { return mla::decode_max_active_clusters(); }
