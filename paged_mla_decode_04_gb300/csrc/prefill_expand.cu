@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) hd->next_item = 0;  // for the attention that follows
   const int row_blocks = (hd->kv_rows + 127) / 128;
   const int64_t tiles = static_cast<int64_t>(row_blocks) * heads;
   auto fail = [&] {

@@ -106,11 +106,32 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
     rows_before += round_rows;
     tiles_before += round_tiles;
   }
+  // Tiles by falling cost (key steps, in 256 classes of the most expensive
+  // one's): blocks draw them in this order, so that what is drawn last is
+  // short. The order within a class varies from call to call and changes nothing
+  // but who computes a tile.
+  __shared__ int most, bins[256];
+  const int nt = static_cast<int>(min(tiles_before, a.lay.max_tiles));
+  int* order = reinterpret_cast<int*>(a.ws + a.lay.order);
+  if (threadIdx.x < 256) bins[threadIdx.x] = 0;
+  if (threadIdx.x == 0) most = 1;
+  __syncthreads();  // (also: tiles are written)
+  auto cost = [&](int i) { return pf_steps(tiles[i].kv_begin, tiles[i].kv_end); };
+  for (int i = threadIdx.x; i < nt; i += kPlanThreads) atomicMax(&most, cost(i));
+  __syncthreads();
+  auto bin = [&](int i) { return 255 - static_cast<int>(static_cast<int64_t>(cost(i)) * 255 / most); };
+  for (int i = threadIdx.x; i < nt; i += kPlanThreads) atomicAdd(&bins[bin(i)], 1);
+  __syncthreads();
+  int64_t first = threadIdx.x < 256 ? bins[threadIdx.x] : 0, ignored;
+  first = block_exclusive(first, sh, &ignored);
+  if (threadIdx.x < 256) bins[threadIdx.x] = static_cast<int>(first);
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt; i += kPlanThreads) order[atomicAdd(&bins[bin(i)], 1)] = i;
   if (threadIdx.x == 0) {
     const int64_t used = min(rows_before, a.lay.kv_capacity);
     reqs[a.batch] = {static_cast<int>(used), 0, 0, 0};
     hd->kv_rows = static_cast<int>(used);
-    hd->num_tiles = static_cast<int>(min(tiles_before, a.lay.max_tiles));
+    hd->num_tiles = nt;
     if (tiles_before > a.lay.max_tiles) atomicOr(&hd->status, MLA_STATUS_BAD_LENGTH);
   }
 }

@@ -91,11 +91,17 @@ struct PfHeader {
   int status;  // sticky MLA_STATUS_* bits
   int kv_rows;     // rows of the row buffer in use
   int num_tiles;
-  int pad[61];
+  int next_item;   // items of the current pass handed out beyond the first of each block
+  int pad[60];
 };
 
+// Key steps of a tile whose rows attend relative positions [begin, end).
+__host__ __device__ inline int pf_steps(int begin, int end) {
+  return end > begin ? (end - begin + kPfKvTile - 1) / kPfKvTile : 0;
+}
+
 struct PfLayout {
-  size_t requests, tiles, rows, keys, values, total;
+  size_t requests, tiles, order, rows, keys, values, total;
   int64_t kv_capacity;  // rows of the row buffer
   int64_t max_tiles;
   int heads;            // heads whose keys and values fit
@@ -112,6 +118,8 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int heads) 
   off = align_up(off + sizeof(PfRequest) * (static_cast<size_t>(batch) + 1), 256);
   L.tiles = off;
   off = align_up(off + sizeof(PfTile) * static_cast<size_t>(L.max_tiles), 256);
+  L.order = off;
+  off = align_up(off + sizeof(int) * static_cast<size_t>(L.max_tiles), 256);
   L.rows = off;
   off = align_up(off + static_cast<size_t>(L.kv_capacity) * kDimRow * 2, 1024);
   L.keys = off;
