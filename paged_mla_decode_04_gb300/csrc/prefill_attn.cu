@@ -3,23 +3,34 @@
 //   S_t = scale (q_nope . K[h][t] + q_rope . k_rope[t]) over the positions t
 //   that r may see (causal, windowed),  out = sum_t softmax(S)_t V[h][t].
 //
-// Per key: 2 * 192 + 2 * 128 flops a row, so it is bound by the tensor core.
-// A persistent block per SM draws items, (256 query rows, head), from a counter,
-// the expensive ones of a group of heads first. The two blocks of 128 rows run as two streams over the same 128-key steps: while the softmax
-// warps of one stream turn S into P, the tensor core works for the other.
-//   TMEM (512 columns): S0 [0, 128) S1 [128, 256) O0 [256, 384) O1 [384, 512);
-//   a stream's P (bf16 pairs, 64 columns) overwrites its S.
-//   Shared memory: Q (2 x 48 KB) and a ring of eight 16 KB slots: a step's
-//   keys take three (64 of the 192 dims each, K-major), its values two (64
-//   keys each, MN-major).
-// The issuing thread runs QK0(j), PV1(j-1), QK1(j), PV0(j): each stream's softmax
-// has the other stream's two products to hide under. All products are issued
-// by one thread and complete in order, so S(j) being complete implies that
-// P V (j-1) of that stream is: softmax warps may rescale O without asking.
+// Per key: 2 * 192 + 2 * 128 flops a row, so it is bound by the tensor core, and
+// next to it by shared memory: a 128-row product with both operands there
+// reads 128 bytes a cycle, all that an SM has, and copies and barriers then wait.
+// Hence pairs of SMs: a cluster of two blocks multiplies M = 256 rows by tiles of
+// which each block holds and reads one half (64 of a step's 128 keys; 64 of the 128
+// value dims), and the copies of keys and values halve as well.
+//
+// A persistent cluster per SM pair draws items, (up to 512 query rows, head), from a
+// counter, the expensive ones of a group of heads first. An item runs as two
+// streams: while the softmax warps of one turn S into P, the tensor core works for
+// the other. With more than 256 rows the streams are row blocks: rows [0, 256)
+// and [256, 512), both over every 128-key step. With fewer they share the rows and
+// take the even and the odd steps; their two results are merged at the end.
+//   TMEM of a block (512 columns): S0 [0, 128) S1 [128, 256) O0 [256, 384)
+//   O1 [384, 512), 128 rows each; a stream's P (bf16 pairs, 64 columns)
+//   overwrites its S.
+//   Shared memory of a block: its 128 rows of each stream's Q (2 x 48 KB) and three
+//   stages of a step: keys [64][192] (K-major, 24 KB), values [128][64]
+//   (MN-major, 16 KB).
+// The issuing thread (of the even block) runs QK of a unit (stream, step), then PV
+// of the unit before: each stream's softmax has the other stream's two products
+// to hide under. All products are issued by one thread and complete in order, so S
+// of a stream being complete implies that its previous P V is: softmax warps may
+// rescale O without asking.
 // Softmax: two threads of a warp share a row (64 keys of a step each; eight warps
-// a stream keep the chain from S to P short), base 2, the reference maximum moves only when
-// the running one exceeds it by 2^8 (the final division makes it exact); P is
-// rounded to bf16 for the product, its sum is kept in fp32.
+// a stream keep the chain from S to P short), base 2, the reference maximum moves
+// only when the running one exceeds it by 2^8 (the final division makes it exact);
+// P is rounded to bf16 for the product, its sum is kept in fp32.
 // Positions beyond a row's range are masked by selection, never by adding, so
 // NaN in them stays out; the last step multiplies only up to the last 16 keys
 // with a valid one, beyond which the buffer may hold another request's rows.
@@ -33,12 +44,15 @@
 namespace mla {
 namespace {
 
-constexpr int kSlots = 8;
-constexpr int kSlotBytes = 128 * 128;       // 128 rows of 64 bf16, or two 64-row halves
-constexpr int kQBytes = 3 * kSlotBytes;     // one stream's 128 rows of 192
+constexpr int kStages = 3;
+constexpr int kQChunk = 128 * 128;          // [128 rows][64 dims]
+constexpr int kQBytes = 3 * kQChunk;        // one stream's rows of this block
+constexpr int kKChunk = 64 * 128;           // [64 keys][64 dims]
+constexpr int kKBytes = 3 * kKChunk;
+constexpr int kVBytes = 128 * 128;          // [128 keys][64 value dims]
+constexpr int kStageBytes = kKBytes + kVBytes;
 constexpr int kOffRing = 2 * kQBytes;
-constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-constexpr int kSmemBytes = kOffBar + 512 + 1024;
+constexpr int kOffBar = kOffRing + kStages * kStageBytes;
 constexpr int kSoftmaxWarps = 16;           // eight a stream
 constexpr int kProducerWarp = 16, kIssueWarp = 17;
 constexpr int kThreads = 640;               // (the last two warps idle)
@@ -46,48 +60,69 @@ constexpr int kThreads = 640;               // (the last two warps idle)
 constexpr int kRegsSoftmax = 104, kRegsOther = 64;
 static_assert(4 * kRegsSoftmax + kRegsOther == 5 * 96, "register split");
 constexpr int kSched = 2;                   // items announced ahead
-// Items that a group of heads should have for each block: within a group the
+// Items that a group of heads should have for each cluster: within a group the
 // costly tiles of all its heads come first, groups follow each other so that
 // their keys and values stay in L2.
 constexpr int kGroupItems = 3;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-static_assert(kSmemBytes <= 232448, "shared memory");
 
 enum {
-  kBarFull = 0,                    // [slots] copy landed
-  kBarEmpty = kBarFull + kSlots,   // [slots] products that read it are complete
-  kBarQFull = kBarEmpty + kSlots,  // [streams]
-  kBarQEmpty = kBarQFull + 2,
-  kBarS = kBarQEmpty + 2,          // S complete
-  kBarP = kBarS + 2,               // P stored, O rescaled
-  kBarO = kBarP + 2,               // the tile's last P V complete
-  kBarItem = kBarO + 2,            // [kSched] item announced
-  kBarItemFree = kBarItem + kSched,  // [kSched] read by every role
+  // In the even block: a step's copies of both blocks landed.
+  kBarKFull = 0,                     // [stages]
+  kBarVFull = kBarKFull + kStages,   // [stages]
+  kBarQFull = kBarVFull + kStages,   // [streams]
+  kBarP = kBarQFull + 2,             // [streams] P stored and O rescaled, both blocks
+  kBarItemFree = kBarP + 2,          // [kSched] read by every role of both blocks
   kBarDrain = kBarItemFree + kSched,
+  // In both blocks: products complete, items announced.
+  kBarKFree = kBarDrain + 1,         // [stages]
+  kBarVFree = kBarKFree + kStages,   // [stages]
+  kBarQFree = kBarVFree + kStages,   // [streams]
+  kBarS = kBarQFree + 2,             // [streams] S complete
+  kBarO = kBarS + 2,                 // [streams] the item's last P V complete
+  kBarItem = kBarO + 2,              // [kSched]
+  // Within a block: stream 1's statistics of a shared row are there / read.
+  kBarStats = kBarItem + kSched,
+  kBarStatsFree,
   kNumBars
 };
-constexpr int kOffItems = 8 * kNumBars + 8;  // after TMEM address and abort flag
 
-// What the roles need of an item: a tile, its head within the pass and the steps of
-// each stream (0: no rows).
-struct Item {
+// What the roles need of an item. Sent to both blocks as three 16-byte words.
+struct alignas(16) Item {
   PfTile t;
-  int head;  // -1: no further items
-  int n0, n1, n;
-  int end0;  // end of stream 0's last row
+  int head;    // head within the pass; -1: no further items
+  int n0, n1;  // steps of each stream (0: none)
+  int shared;  // the streams share the rows and alternate over the steps
 };
-static_assert(kOffItems + kSched * sizeof(Item) <= 512, "barrier area");
+static_assert(sizeof(Item) == 48, "three 16-byte words");
+
+constexpr int kOffItems = (8 * kNumBars + 8 + 15) / 16 * 16;  // after TMEM address and abort flag
+constexpr int kOffStats = kOffItems + kSched * 48;            // float2 [128]: stream 1's maximum and sum
+constexpr int kSmemBytes = kOffBar + kOffStats + 1024 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
 
 __device__ __forceinline__ Item item_of(const PfTile& t, int head) {
   Item w;
   w.t = t;
   w.head = head;
-  w.end0 = t.first_end + min(t.rows, 128) - 1;
-  w.n0 = t.refused ? 0 : pf_steps(t.kv_begin, w.end0);
-  w.n1 = t.refused || t.rows <= 128 ? 0 : pf_steps(t.kv_begin, t.kv_end);
-  w.n = max(w.n0, w.n1);
+  w.shared = t.rows <= 256;
+  if (t.refused) {
+    w.n0 = w.n1 = w.shared = 0;
+  } else if (w.shared) {
+    const int n = pf_steps(t.kv_begin, t.kv_end);
+    w.n0 = (n + 1) / 2;
+    w.n1 = n / 2;
+  } else {
+    w.n0 = pf_steps(t.kv_begin, t.first_end + 255);
+    w.n1 = pf_steps(t.kv_begin, t.kv_end);
+  }
   return w;
+}
+
+// End of the positions that a stream's rows attend.
+__device__ __forceinline__ int end_of(const Item& w, int x) {
+  return x == 0 && !w.shared ? w.t.first_end + min(w.t.rows, 256) - 1 : w.t.kv_end;
 }
 
 // Tile rank and head of item `it`: groups of heads one after the other, within
@@ -95,11 +130,7 @@ __device__ __forceinline__ Item item_of(const PfTile& t, int head) {
 __device__ __forceinline__ void split_item(int64_t it, int num_tiles, int heads, int groups, int* rank, int* head) {
   int g = static_cast<int>(it * groups / (static_cast<int64_t>(num_tiles) * heads));
   int h0 = heads * g / groups, h1 = heads * (g + 1) / groups;
-  if (it < static_cast<int64_t>(h0) * num_tiles) {
-    --g;
-    h1 = h0;
-    h0 = heads * g / groups;
-  } else if (it >= static_cast<int64_t>(h1) * num_tiles) {
+  if (it >= static_cast<int64_t>(h1) * num_tiles) {
     ++g;
     h0 = h1;
     h1 = heads * (g + 1) / groups;
@@ -109,7 +140,7 @@ __device__ __forceinline__ void split_item(int64_t it, int num_tiles, int heads,
   *head = h0 + static_cast<int>(in % (h1 - h0));
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_attn_kernel(const __grid_constant__ PrefillMaps m, const __grid_constant__ PrefillArgs a, int head0, int heads) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -118,247 +149,293 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * kNumBars + 4);
+  Item* board = reinterpret_cast<Item*>(smem + kOffBar + kOffItems);
   PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
-  const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + a.lay.tiles);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cta = cluster_rank();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), (i >= kBarP && i < kBarP + 2) ? kSoftmaxWarps / 2
-                        : (i >= kBarItemFree && i < kBarItemFree + kSched) ? kSoftmaxWarps + 1 : 1);
+    for (int i = 0; i < kNumBars; ++i) {
+      int count = 1;
+      if (i >= kBarP && i < kBarP + 2) count = kSoftmaxWarps;                            // eight of each block
+      if (i >= kBarItemFree && i < kBarItemFree + kSched) count = 2 * (kSoftmaxWarps + 1);  // + issuer, + odd producer
+      if (i == kBarStats || i == kBarStatsFree) count = kSoftmaxWarps / 2;
+      mbar_init(bar(i), count);
+    }
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
   if (warp == kIssueWarp) {
-    tmem_alloc(smem_addr(tmem_slot), 512);
-    tmem_relinquish();
+    tmem_alloc2(smem_addr(tmem_slot), 512);
+    tmem_relinquish2();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // barriers of both blocks are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const uint32_t lead0 = mapa(bar0, 0);  // the even block's barriers
+  auto lead = [&](int i) -> uint32_t { return lead0 + 8u * i; };
   pdl_wait();
-  const int num_tiles = hd->num_tiles;
-  const int64_t items = static_cast<int64_t>(num_tiles) * heads;
-  Item* board = reinterpret_cast<Item*>(smem + kOffBar + kOffItems);
-  // The i-th item of this block, as every role but the producer reads it.
-  auto read_item = [&](uint32_t i, Item& w) -> bool {
-    if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarItem + i % kSched), (i / kSched) & 1u, abort_flag))) return false;
-    w = board[i % kSched];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(kBarItemFree + i % kSched));
-    return true;
-  };
   auto fail = [&] {
     *abort_flag = 1;
     atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
   };
+  // A wait of a whole warp: one lane polls (a poll by 32 lanes takes them in turn).
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+    int done = 1;
+    if (lane == 0) done = mbar_spin(b, parity, abort_flag);
+    done = __shfl_sync(0xffffffffu, done, 0);
+    __syncwarp();
+    return done != 0;
+  };
+
+  // The announced item comes from the even block: once its barrier is seen
+  // complete (polls have the block's scope), acquire at the cluster's.
+  auto acquire_item = [&](uint32_t i) { mbar_test_wait_cluster(bar(kBarItem + i % kSched), (i / kSched) & 1u); };
 
   if (warp >= kProducerWarp) setmaxnreg_dec<kRegsOther>();
   if (warp == kProducerWarp) {
     if (lane == 0) {
-      uint32_t k = 0;             // ring slots issued
+      const int num_tiles = hd->num_tiles;
+      const int64_t items = static_cast<int64_t>(num_tiles) * heads;
+      const int clusters = gridDim.x / 2;
+      const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + a.lay.tiles);
+      const int* order = reinterpret_cast<const int*>(a.ws + a.lay.order);
+      const int group_heads = static_cast<int>(
+          min(static_cast<int64_t>(heads), (static_cast<int64_t>(kGroupItems) * clusters + num_tiles - 1) / max(num_tiles, 1)));
+      const int groups = max(1, heads / max(group_heads, 1));
+      uint32_t k_steps = 0, v_steps = 0;  // steps whose copies are issued
       uint32_t q_use[2] = {0, 0};
       bool ok = true;
-      auto slot = [&](uint32_t bytes) -> uint32_t {  // waits for the next slot; its number, or kSlots on failure
-        const uint32_t s = k % kSlots;
-        if (!mbar_wait(bar(kBarEmpty + s), ((k / kSlots) & 1u) ^ 1u, abort_flag)) {
-          ok = false;
-          return kSlots;
-        }
-        mbar_arrive_expect_tx(bar(kBarFull + s), bytes);
-        ++k;
-        return s;
-      };
-      const int* order = reinterpret_cast<const int*>(a.ws + a.lay.order);
-      const int64_t group_items = static_cast<int64_t>(kGroupItems) * gridDim.x;
-      const int group_heads = static_cast<int>(min(static_cast<int64_t>(heads), (group_items + num_tiles - 1) / max(num_tiles, 1)));
-      const int groups = max(1, heads / max(group_heads, 1));
       auto load_item = [&](int64_t it) {
         int rank, head;
         if (it >= items) return item_of(PfTile{0, 0, 0, 0, 0, 0, 1, 0}, -1);
         split_item(it, num_tiles, heads, groups, &rank, &head);
         return item_of(tiles[order[rank]], head);
       };
-      Item w = load_item(blockIdx.x);
+      // The even block announces an item to both.
+      auto announce = [&](uint32_t i, const Item& w) {
+        if (!(ok = mbar_spin(bar(kBarItemFree + i % kSched), ((i / kSched) & 1u) ^ 1u, abort_flag))) return;
+        const int* v = reinterpret_cast<const int*>(&w);
+#pragma unroll
+        for (uint32_t r = 0; r < 2; ++r) {
+          const uint32_t rb = mapa(bar(kBarItem + i % kSched), r), dst = mapa(smem_addr(&board[i % kSched]), r);
+          mbar_arrive_expect_tx_cluster(rb, sizeof(Item));
+#pragma unroll
+          for (int c = 0; c < 3; ++c) st_async_v4(dst + 16 * c, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3], rb);
+        }
+      };
+      Item w, w_next;
+      if (cta == 0) {
+        w_next = load_item(blockIdx.x >> 1);
+        announce(0, w_next);
+      }
       for (uint32_t i = 0; ok; ++i) {
-        // Announce the item, draw the next one (its number comes while this
-        // item's copies are issued).
-        if (!(ok = mbar_wait(bar(kBarItemFree + i % kSched), ((i / kSched) & 1u) ^ 1u, abort_flag))) break;
-        board[i % kSched] = w;
-        mbar_arrive(bar(kBarItem + i % kSched));
+        int64_t next = 0;
+        if (cta == 0) {
+          w = w_next;
+        } else {
+          if (!(ok = mbar_spin(bar(kBarItem + i % kSched), (i / kSched) & 1u, abort_flag))) break;
+          acquire_item(i);
+          w = board[i % kSched];
+          mbar_arrive_cluster(lead(kBarItemFree + i % kSched));
+        }
         if (w.head < 0) break;
-        const int64_t next = static_cast<int64_t>(gridDim.x) + atomicAdd(&hd->next_item, 1);
-        const int hl = w.head;
-        for (int j = 0; j < w.n && ok; ++j) {
+        // The next item is drawn now, looked up and announced once this one's
+        // first copies are under way.
+        if (cta == 0) next = (gridDim.x >> 1) + static_cast<int64_t>(atomicAdd(&hd->next_item, 1));
+        bool drawn = cta != 0;
+        const int n = w.shared ? w.n0 + w.n1 : max(w.n0, w.n1);
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t s = k_steps % kStages, par = (k_steps / kStages) & 1u;
+          const uint32_t dst = sbase + kOffRing + s * kStageBytes;
           const int row = w.t.base + w.t.kv_begin + j * kPfKvTile;
-          for (int c = 0; c < 3; ++c) {
-            const uint32_t s = slot(kSlotBytes);
-            if (!ok) break;
-            const uint32_t dst = sbase + kOffRing + s * kSlotBytes;
-            if (c < 2) tma_load_3d(dst, &m.keys, bar(kBarFull + s), 64 * c, row, hl);
-            else tma_load_2d(dst, &m.rows, bar(kBarFull + s), kDimCkv, row);
-          }
+          if (!(ok = mbar_spin(bar(kBarKFree + s), par ^ 1u, abort_flag))) break;
+          ++k_steps;
+          if (cta == 0) mbar_arrive_expect_tx(bar(kBarKFull + s), 2 * kKBytes);
+          tma2_load_3d(dst, &m.keys, lead(kBarKFull + s), 0, row + 64 * cta, w.head);
+          tma2_load_3d(dst + kKChunk, &m.keys, lead(kBarKFull + s), 64, row + 64 * cta, w.head);
+          tma2_load_2d(dst + 2 * kKChunk, &m.ropes, lead(kBarKFull + s), kDimCkv, row + 64 * cta);
           if (j == 0) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (!ok || (x ? w.n1 : w.n0) == 0) continue;
-              if (!(ok = mbar_wait(bar(kBarQEmpty + x), (q_use[x] & 1u) ^ 1u, abort_flag))) continue;
+              if (!ok || (x == 1 && (w.shared || w.n1 == 0))) continue;
+              if (!(ok = mbar_spin(bar(kBarQFree + x), (q_use[x] & 1u) ^ 1u, abort_flag))) continue;
               ++q_use[x];
-              mbar_arrive_expect_tx(bar(kBarQFull + x), kQBytes);
+              if (cta == 0) mbar_arrive_expect_tx(bar(kBarQFull + x), 2 * kQBytes);
               for (int c = 0; c < 3; ++c)
-                tma_load_3d(sbase + x * kQBytes + c * kSlotBytes, &m.q, bar(kBarQFull + x), 64 * c, head0 + hl,
-                            w.t.q_row + 128 * x);
+                tma2_load_3d(sbase + x * kQBytes + c * kQChunk, &m.q, lead(kBarQFull + x), 64 * c, head0 + w.head,
+                             w.t.q_row + 256 * x + 128 * cta);
             }
           }
-          for (int half = 0; half < 2 && ok; ++half) {
-            const uint32_t s = slot(kSlotBytes);
-            if (!ok) break;
-            const uint32_t dst = sbase + kOffRing + s * kSlotBytes;
-            for (int c = 0; c < 2; ++c)
-              tma_load_3d(dst + c * (kSlotBytes / 2), &m.values, bar(kBarFull + s), 64 * c, row + 64 * half, hl);
+          if (!ok || !(ok = mbar_spin(bar(kBarVFree + s), par ^ 1u, abort_flag))) break;
+          ++v_steps;
+          if (cta == 0) mbar_arrive_expect_tx(bar(kBarVFull + s), 2 * kVBytes);
+          tma2_load_3d(dst + kKBytes, &m.values, lead(kBarVFull + s), 64 * cta, row, w.head);
+          if (!drawn && j == 1) {
+            w_next = load_item(next);
+            announce(i + 1, w_next);
+            drawn = true;
           }
         }
-        w = load_item(next);
+        if (!drawn && ok) {
+          w_next = load_item(next);
+          announce(i + 1, w_next);
+        }
       }
       if (!ok) fail();
-      if (*abort_flag) {  // let the copies in flight land (each wait bounded)
-        for (uint32_t i = k > kSlots ? k - kSlots : 0; i < k; ++i)
-          mbar_wait(bar(kBarFull + i % kSlots), (i / kSlots) & 1u, nullptr);
+      if (*abort_flag && cta == 0) {  // let the copies in flight land (each wait bounded)
+        for (uint32_t i = k_steps > kStages ? k_steps - kStages : 0; i < k_steps; ++i) {
+          mbar_wait(bar(kBarKFull + i % kStages), (i / kStages) & 1u, nullptr);
+          if (i < v_steps) mbar_wait(bar(kBarVFull + i % kStages), (i / kStages) & 1u, nullptr);
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (q_use[x]) mbar_wait(bar(kBarQFull + x), (q_use[x] - 1) & 1u, nullptr);
       }
     }
   } else if (warp == kIssueWarp) {
-    constexpr uint32_t idesc_qk = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
-    // Descriptors differ in their address field only (units of 16 bytes).
-    const uint64_t q_desc = sdesc_sw128(sbase, 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(sbase + kOffRing, 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(sbase + kOffRing, kSlotBytes / 2, 1024);
-    uint32_t k = 0;  // first ring slot of the current step
-    uint32_t p_use0 = 0, p_use1 = 0, q_use0 = 0, q_use1 = 0;
-    bool ok = true;
-    auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag)); };
-    auto full = [&](uint32_t i) { wait(bar(kBarFull + i % kSlots), (i / kSlots) & 1u); };
-    // S_x = Q_x K^T of the step at ring slots k .. k + 2.
-    auto qk = [&](int x) {
-#pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        const uint64_t ad = q_desc + ((x * kQBytes + c * kSlotBytes) >> 4);
-        const uint64_t bd = k_desc + ((k + c) % kSlots) * (kSlotBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_bf16_ss(tmem + kColS + 128 * x, ad + 2 * i, bd + 2 * i, idesc_qk, (c | i) != 0);
-          if (c == 2) mma_commit(bar(kBarS + x));
+    // One elected lane of the even block runs the whole role. Between two products
+    // of the chain it does as little as it can: the next unit is worked out, and its
+    // copies are waited for, while the tensor core is busy with the last one's.
+    if (cta == 0 && elect_one()) {
+      constexpr uint32_t idesc_qk = idesc_bf16(256, 128, false, false);
+      constexpr uint32_t idesc_pv = idesc_bf16(256, 128, false, true);
+      const uint32_t q_lo = desc_lo(sbase), ring_lo = desc_lo(sbase + kOffRing);
+      constexpr uint32_t kStageUnits = kStageBytes >> 4, kVUnits = kKBytes >> 4;
+      bool ok = true;
+      auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && mbar_spin(b, parity, abort_flag); };
+      // Generator of units: stream, step and item, with what the products need.
+      uint32_t item_no = 0, stage = kStages - 1, par = 1, q_par = 0;  // (the first step turns to stage 0, parity 0)
+      int j = 0, n = 0, n0 = 0, n1 = 0, left0 = 0, left1 = 0, ux = -1;
+      bool shared = false;
+      auto advance = [&]() -> bool {  // false: no further units
+        if (ux == 0 && !shared && n1 > 0) {
+          ux = 1;  // the same step's second stream
+          return true;
         }
-      }
-    };
-    // O_x += P_x V for the step whose values sit at slots v, v + 1: up to the
-    // last 16 keys below `end`.
-    auto pv = [&](int x, uint32_t v, int left, bool first) {
-      const int ksteps = min(8, (left + 15) / 16);
+        if (ux >= 0) ++j;
+        while (ux < 0 || j >= n) {
+          wait(bar(kBarItem + (item_no & 1u)), (item_no >> 1) & 1u);
+          if (!ok) return false;
+          acquire_item(item_no);
+          const Item& w = board[item_no & 1u];
+          const int head = w.head;
+          n0 = w.n0;
+          n1 = w.n1;
+          shared = w.shared != 0;
+          left0 = end_of(w, 0) - w.t.kv_begin;
+          left1 = end_of(w, 1) - w.t.kv_begin;
+          mbar_arrive_cluster(lead(kBarItemFree + (item_no & 1u)));
+          ++item_no;
+          if (head < 0) return false;
+          n = shared ? n0 + n1 : max(n0, n1);
+          j = 0;
+          ux = 0;
+        }
+        ux = shared ? (j & 1) : (j < n0 ? 0 : 1);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        par ^= stage == 0 ? 1u : 0u;
+        return true;
+      };
+      static_assert(kSched == 2, "item_no & 1");
+      // A unit's P V, kept until its softmax is done.
+      int p_x = -1, p_left = 0;
+      uint32_t p_par = 0, p_v = 0, p_vfull = 0, p_vpar = 0, p_vfree = 0, p_o = 0;  // barriers: 0 is none
+      bool p_acc = false;
+      auto flush = [&] {
+        if (p_x < 0 || !ok) return;
+        if (p_vfull) wait(p_vfull, p_vpar);
+        wait(bar(kBarP + p_x), (p_par >> p_x) & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t d = tmem + kColO + 128 * p_x, p = tmem + kColS + 128 * p_x;
+        if (p_left > 112) {
+          mma2_bf16_ts(d, p, p_v, idesc_pv, p_acc);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint64_t bd = v_desc + ((v + h) % kSlots) * (kSlotBytes >> 4);
-        const uint32_t td = tmem + kColO + 128 * x, ta = tmem + kColS + 128 * x + 32 * h;
-        if (ksteps >= 4 * h + 4) {
-          if (elect_one()) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_bf16_ts(td, ta + 8 * i, bd + i * (2048 >> 4), idesc_pv, !first || (h | i) != 0);
-          }
+          for (int i = 1; i < 8; ++i) mma2_bf16_ts(d, p + 8 * i, p_v + 128 * i, idesc_pv, 1);
         } else {
-          for (int i = 0; i < ksteps - 4 * h; ++i)
-            if (elect_one()) mma_bf16_ts(td, ta + 8 * i, bd + i * (2048 >> 4), idesc_pv, !first || (h | i) != 0);
+#pragma unroll 1
+          for (int i = 0; 16 * i < p_left; ++i) mma2_bf16_ts(d, p + 8 * i, p_v + 128 * i, idesc_pv, p_acc || i > 0);
         }
-      }
-    };
-    // Stream 1's product and the values' release.
-    auto pv1 = [&](const Item& w, int j, uint32_t v) {
-      wait(bar(kBarP + 1), p_use1++ & 1u);
-      full(v);
-      full(v + 1);
-      if (!ok) return;
-      tc_fence_after();
-      pv(1, v, w.t.kv_end - w.t.kv_begin - j * kPfKvTile, j == 0);
-      if (elect_one()) {
-        mma_commit(bar(kBarEmpty + v % kSlots));
-        mma_commit(bar(kBarEmpty + (v + 1) % kSlots));
-        if (j == w.n1 - 1) mma_commit(bar(kBarO + 1));
-      }
-    };
-    Item w;
-    for (uint32_t i = 0; ok; ++i) {
-      ok = read_item(i, w);
-      if (!ok || w.head < 0) break;
-      for (int j = 0; j < w.n && ok; ++j, k += 5) {
-        full(k);
-        full(k + 1);
-        full(k + 2);
-        if (j < w.n0) {
-          if (j == 0) wait(bar(kBarQFull), q_use0++ & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          qk(0);
-          if (j == w.n0 - 1 && elect_one()) mma_commit(bar(kBarQEmpty));
-        }
-        if (w.n1) {
-          if (j > 0) pv1(w, j - 1, k - 2);
-          if (j == 0) wait(bar(kBarQFull + 1), q_use1++ & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          qk(1);
-          if (j == w.n1 - 1 && elect_one()) mma_commit(bar(kBarQEmpty + 1));
+        if (p_vfree) mma2_commit(p_vfree);
+        if (p_o) mma2_commit(p_o);
+        p_par ^= 1u << p_x;
+        p_x = -1;
+      };
+      bool have = advance();
+      while (have && ok) {
+        // The unit: constants of its products and its place in the item.
+        const int x = ux;
+        const bool first_of_step = shared || x == 0 || j >= n0, last_of_step = shared || x == 1 || n1 == 0;
+        const int step_in = shared ? j >> 1 : j;
+        const uint32_t d = tmem + kColS + 128 * x, q = q_lo + (shared ? 0 : x) * (kQBytes >> 4), k = ring_lo + stage * kStageUnits;
+        const bool q_last = shared ? j == n - 1 : j == (x ? n1 : n0) - 1;
+        const uint32_t u_stage = stage, u_par = par;
+        const int u_left = (x ? left1 : left0) - j * kPfKvTile;
+        const bool o_last = step_in == (x ? n1 : n0) - 1;
+        const int q_buf = shared ? 0 : x;
+        const bool q_first = shared ? j == 0 : j == 0;
+        // S_x still holds P of this stream's previous unit where no other came between.
+        if (p_x == x) flush();
+        if (first_of_step) wait(bar(kBarKFull + u_stage), u_par);
+        if (q_first) {
+          wait(bar(kBarQFull + q_buf), (q_par >> q_buf) & 1u);
+          q_par ^= 1u << q_buf;
         }
         if (!ok) break;
-        if (elect_one()) {
+        // (the unit before, if its softmax is done by now or else later)
+        tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 3; ++c) mma_commit(bar(kBarEmpty + (k + c) % kSlots));
-        }
-        if (j < w.n0) {
-          wait(bar(kBarP), p_use0++ & 1u);
-          full(k + 3);
-          full(k + 4);
-          if (!ok) break;
-          tc_fence_after();
-          pv(0, k + 3, w.end0 - w.t.kv_begin - j * kPfKvTile, j == 0);
-          if (j == w.n0 - 1 && elect_one()) mma_commit(bar(kBarO));
-        }
-        if (!w.n1 && elect_one()) {
-          mma_commit(bar(kBarEmpty + (k + 3) % kSlots));
-          mma_commit(bar(kBarEmpty + (k + 4) % kSlots));
-        }
+        for (int c = 0; c < 3; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mma2_bf16_ss(d, q + c * (kQChunk >> 4) + 2 * e, k + c * (kKChunk >> 4) + 2 * e, idesc_qk, (c | e) != 0);
+        mma2_commit(bar(kBarS + x));
+        if (last_of_step) mma2_commit(bar(kBarKFree + u_stage));
+        if (q_last) mma2_commit(bar(kBarQFree + q_buf));
+        have = advance();  // works out the next unit before the wait
+        flush();
+        p_x = x;
+        p_left = u_left;
+        p_v = ring_lo + kVUnits + u_stage * kStageUnits;
+        p_vfull = first_of_step ? bar(kBarVFull + u_stage) : 0;
+        p_vpar = u_par;
+        p_vfree = last_of_step ? bar(kBarVFree + u_stage) : 0;
+        p_o = o_last ? bar(kBarO + x) : 0;
+        p_acc = step_in != 0;
       }
-      if (ok && w.n1) pv1(w, w.n - 1, k - 2);
+      flush();
+      if (!ok) fail();
+      mma2_commit(bar(kBarDrain));
+      mbar_wait(bar(kBarDrain), 0, nullptr);
     }
-    if (!ok && lane == 0) fail();
-    __syncwarp();
-    if (elect_one()) mma_commit(bar(kBarDrain));
-    mbar_wait(bar(kBarDrain), 0, nullptr);
-  } else if (warp < kProducerWarp) {
+  } else if (warp < kSoftmaxWarps) {
     setmaxnreg_inc<kRegsSoftmax>();
     // Warp w works for stream w >> 3 on 16 lanes of TMEM lane quarter w & 3. A
     // row belongs to threads t and t + 16: keys [0, 64) and [64, 128) of every
     // step, value dims [0, 64) and [64, 128) of O.
     const int x = warp >> 3, quarter = warp & 3, th = lane >> 4;
     const int lane0 = quarter * 32 + ((warp >> 2) & 1) * 16;
-    const int r = x * 128 + lane0 + (lane & 15);  // row of the tile
-    const uint32_t tbase = tmem + (static_cast<uint32_t>(lane0) << 16) + 128 * x;
-    const uint32_t tS = tbase + kColS, tO = tbase + kColO;
+    const int lrow = lane0 + (lane & 15);  // row of this block
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(lane0) << 16);
+    const uint32_t tS = tbase + kColS + 128 * x, tO = tbase + kColO + 128 * x;
+    float2* stats = reinterpret_cast<float2*>(smem + kOffBar + kOffStats);
     const float scale = a.scale_log2;
     const uint64_t scale2 = f2_make(scale, scale);
     const float threshold = kRescaleThreshold / scale;  // in units of S
-    uint32_t s_use = 0, o_use = 0;
+    uint32_t s_use = 0, o_use = 0, o1_use = 0, stats_use = 0;
     bool ok = true;
-    Item w;
     for (uint32_t i = 0; ok; ++i) {
-      ok = read_item(i, w);
-      if (!ok || w.head < 0) break;
-      if (w.t.rows <= 128 * x) continue;
+      if (!(ok = warp_wait(bar(kBarItem + i % kSched), (i / kSched) & 1u))) break;
+      acquire_item(i);
+      const Item w = board[i % kSched];
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead(kBarItemFree + i % kSched));
+      if (w.head < 0) break;
+      const int r = 128 * cta + lrow + (w.shared ? 0 : 256 * x);  // row of the tile
       const bool valid = r < w.t.rows;
+      const bool any = r - (lane & 15) < w.t.rows;  // any row of this warp
       const int64_t out_row = (static_cast<int64_t>(w.t.q_row) + r) * a.num_heads + head0 + w.head;
       uint8_t* dst = static_cast<uint8_t*>(a.out) + out_row * (kDimV * 2) + th * kDimV;
       if (w.t.refused) {
@@ -371,102 +448,148 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int n = x ? w.n1 : w.n0;
-      // The row's range, relative to this thread's first key of step 0.
-      const int off = w.t.kv_begin + 64 * th;
-      const int end = min(w.t.first_end + r, x ? w.t.kv_end : w.end0) - off;
+      if (n == 0) continue;
+      // The row's range, relative to this thread's first key of the stream's first step.
+      const int stride = w.shared ? 2 * kPfKvTile : kPfKvTile;
+      const int off = w.t.kv_begin + 64 * th + (w.shared ? kPfKvTile * x : 0);
+      const int end = min(w.t.first_end + r, end_of(w, x)) - off;
       const int begin = a.window > 0 ? max(0, w.t.first_end + r - a.window) - off : -off;
       float mx_ref = -CUDART_INF_F, l = 0.f;  // l: this thread's keys only
       for (int j = 0; j < n; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + x), s_use & 1u, abort_flag));
-        if (!ok) break;
+        if (!(ok = warp_wait(bar(kBarS + x), s_use & 1u))) break;
         ++s_use;
-        tc_fence_after();
-        uint32_t s[64];
-        tmem_ld_h32<64>(tS, s);
-        tmem_ld_h32<64>(tS + 32, s + 32);
-        tmem_wait_ld();
-        const int b0 = begin - j * kPfKvTile, e0 = end - j * kPfKvTile;
-        if (b0 > 0 || e0 < 64) {
+        if (any) {
+          tc_fence_after();
+          uint32_t s[64];
+          tmem_ld_h32<64>(tS, s);
+          tmem_ld_h32<64>(tS + 32, s + 32);
+          tmem_wait_ld();
+          const int b0 = begin - j * stride, e0 = end - j * stride;
+          if (b0 > 0 || e0 < 64) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c < b0 || c >= e0) s[c] = 0xff800000u;
-        }
-        float mxa = -CUDART_INF_F, mxb = -CUDART_INF_F;
+            for (int c = 0; c < 64; ++c)
+              if (c < b0 || c >= e0) s[c] = 0xff800000u;
+          }
+          float mxa = -CUDART_INF_F, mxb = -CUDART_INF_F;
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          mxa = fmax3(mxa, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          mxb = fmax3(mxb, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-        }
-        float mx = fmaxf(mxa, mxb);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        float alpha = 1.f;
-        if (mx > mx_ref + threshold) {
-          alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
-          l *= alpha;
-          mx_ref = mx;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          for (int c = 0; c < 64; c += 4) {
+            mxa = fmax3(mxa, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            mxb = fmax3(mxb, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          }
+          float mx = fmaxf(mxa, mxb);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          float alpha = 1.f;
+          if (mx > mx_ref + threshold) {
+            alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
+            l *= alpha;
+            mx_ref = mx;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[16];
-            tmem_ld_h16<64>(tO + 16 * c, o);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[16];
+              tmem_ld_h16<64>(tO + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+              tmem_st_h16<64>(tO + 16 * c, o);
+            }
+          }
+          const float neg = mx_ref == -CUDART_INF_F ? 0.f : -mx_ref * scale;
+          const uint64_t neg2 = f2_make(neg, neg);
+          uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float t0, t1;
+            f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
+            const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
+            sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
+            s[c] = pack_bf16x2(p0, p1);
+          }
+          tmem_st_h32<32>(tS, s);
+          float s0, s1, s2, s3;
+          f2_split(sum2[0], s0, s1);
+          f2_split(sum2[1], s2, s3);
+          l += (s0 + s1) + (s2 + s3);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_cluster(lead(kBarP + x));
+      }
+      if (!ok) break;
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (x == 1 && w.shared) {
+        // Stream 0 stores the row: hand over its maximum and sum, keep O until read.
+        if (th == 0) stats[lrow] = make_float2(mx_ref, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarStats));
+        if (!(ok = warp_wait(bar(kBarStatsFree), stats_use++ & 1u))) break;
+        if (!(ok = warp_wait(bar(kBarO + 1), o_use++ & 1u))) break;
+        continue;
+      }
+      if (!(ok = warp_wait(bar(kBarO + x), o_use++ & 1u))) break;
+      float f0 = 1.f, f1 = 0.f;  // factors of the streams' O
+      const bool merge = w.shared && w.n1 > 0;
+      if (merge) {
+        if (!(ok = warp_wait(bar(kBarStats), stats_use++ & 1u))) break;
+        if (!(ok = warp_wait(bar(kBarO + 1), o1_use & 1u))) break;
+        const float2 other = stats[lrow];
+        const float both = fmaxf(mx_ref, other.x);
+        // (a stream without a key has -inf and a sum of 0; NaN sums stay NaN)
+        f0 = mx_ref == -CUDART_INF_F ? 0.f : exp2_approx((mx_ref - both) * scale);
+        f1 = other.x == -CUDART_INF_F ? 0.f : exp2_approx((other.x - both) * scale);
+        if (l != l) f0 = l;
+        if (other.y != other.y) f1 = other.y;
+        l = l * f0 + other.y * f1;
+        mx_ref = both;
+      }
+      if (x == 0 && w.n1 > 0) ++o1_use;  // (phases of stream 1's barrier, waited for or not)
+      tc_fence_after();
+      if (any) {
+        const float inv = a.out_scale / l;  // every valid row attends itself: l > 0
+        f0 *= inv;
+        f1 *= inv;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[32];
+          tmem_ld_h32<64>(tO + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * f0);
+          if (merge) {
+            uint32_t o1[32];
+            tmem_ld_h32<64>(tO + 128 + 32 * c, o1);
             tmem_wait_ld();
 #pragma unroll
-            for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
-            tmem_st_h16<64>(tO + 16 * c, o);
+            for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(fmaf(__uint_as_float(o1[v]), f1, __uint_as_float(o[v])));
+          }
+          if (valid) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                pk[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]), __uint_as_float(o[16 * v + 2 * e + 1]));
+              st_global_v8(dst + 64 * c + 32 * v, pk);
+            }
           }
         }
-        const float neg = mx_ref == -CUDART_INF_F ? 0.f : -mx_ref * scale;
-        const uint64_t neg2 = f2_make(neg, neg);
-        uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float t0, t1;
-          f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
-          const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
-          sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
-          s[c] = pack_bf16x2(p0, p1);
-        }
-        tmem_st_h32<32>(tS, s);
-        float s0, s1, s2, s3;
-        f2_split(sum2[0], s0, s1);
-        f2_split(sum2[1], s2, s3);
-        l += (s0 + s1) + (s2 + s3);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + x));
-      }
-      if (!ok) break;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarO + x), o_use & 1u, abort_flag));
-      if (!ok) break;
-      ++o_use;
-      tc_fence_after();
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const float inv = a.out_scale / l;  // every valid row attends itself: l > 0
-      uint32_t o[64];
-      tmem_ld_h32<64>(tO, o);
-      tmem_ld_h32<64>(tO + 32, o + 32);
-      tmem_wait_ld();
-      if (valid) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t pk[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            pk[c] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * c]) * inv, __uint_as_float(o[16 * v + 2 * c + 1]) * inv);
-          st_global_v8(dst + 32 * v, pk);
-        }
-        if (a.lse && th == 0) a.lse[out_row] = (mx_ref * scale + log2f(l)) * 0.69314718055994531f;
+        if (a.lse && valid && th == 0) a.lse[out_row] = (mx_ref * scale + log2f(l)) * 0.69314718055994531f;
       }
       tc_fence_before();
+      if (merge) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarStatsFree));
+      }
     }
     if (!ok) fail();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // no block ends while the other's products or arrivals reach into it
   tc_fence_after();
-  if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp) tmem_dealloc2(tmem, 512);
 }
 
 }  // namespace
@@ -475,11 +598,11 @@ cudaError_t launch_prefill_attn(const PrefillMaps& m, const PrefillArgs& a, int 
   static bool attr_set[kMaxDevices] = {};
   const cudaError_t e = set_smem_once(prefill_attn_kernel, kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int pairs = sm_count() / 2;
+  if (pairs <= 0) return cudaErrorInvalidDevice;
   const int64_t most = a.lay.max_tiles * heads;
-  return launch_pdl(prefill_attn_kernel, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads), kSmemBytes,
-                    stream, m, a, head0, heads);
+  return launch_pdl(prefill_attn_kernel, dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs)), dim3(kThreads),
+                    kSmemBytes, stream, m, a, head0, heads);
 }
 
 }  // namespace mla

@@ -206,10 +206,12 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
                    {64, 1, 128}) ||
       !make_map_2d(&m.rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.ws + a.lay.rows, cap, mla::kDimRow, mla::kDimRow * 2, 64,
                    128) ||
+      !make_map_2d(&m.ropes, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.ws + a.lay.rows, cap, mla::kDimRow, mla::kDimRow * 2, 64,
+                   64) ||
       !make_map_3d(&m.keys, a.ws + a.lay.keys, {mla::kDimNope, cap, static_cast<uint64_t>(per_pass)},
-                   {mla::kDimNope * 2, cap * mla::kDimNope * 2}, {64, 128, 1}) ||
+                   {mla::kDimNope * 2, cap * mla::kDimNope * 2}, {64, 64, 1}) ||
       !make_map_3d(&m.values, a.ws + a.lay.values, {mla::kDimV, cap, static_cast<uint64_t>(per_pass)},
-                   {mla::kDimV * 2, cap * mla::kDimV * 2}, {64, 64, 1}) ||
+                   {mla::kDimV * 2, cap * mla::kDimV * 2}, {64, 128, 1}) ||
       !make_map_2d(&m.w_uk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w_uk, h * mla::kDimNope, mla::kDimCkv, mla::kDimCkv * 2, 64,
                    128) ||
       !make_map_2d(&m.w_uv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w_uv, h * mla::kDimCkv, mla::kDimV, mla::kDimV * 2, 64, 64))

@@ -62,7 +62,7 @@ struct RopeArgs {
 // ---------------------------------------------------------------- chunk attention (prefill)
 constexpr int kDimNope = 128;
 constexpr int kDimQk = 192;
-constexpr int kPfRows = 256;      // query rows of one tile: two row blocks of 128
+constexpr int kPfRows = 512;      // query rows of one tile: two streams of two blocks' 128
 constexpr int kPfKvAlign = 16;    // a request's gathered rows start at a multiple of this (one K step of an MMA)
 constexpr int kPfKvTile = 128;    // key rows per step
 
@@ -156,8 +156,9 @@ struct PrefillArgs {
 struct PrefillMaps {
   CUtensorMap q;        // [T][H][192] as {192, H, T}, box {64, 1, 128}
   CUtensorMap rows;     // gathered rows [kv][576], box {64, 128}
-  CUtensorMap keys;     // [heads][kv][128] as {128, kv, heads}, box {64, 128, 1}
-  CUtensorMap values;   // same, box {64, 64, 1}
+  CUtensorMap ropes;    // same, box {64, 64}
+  CUtensorMap keys;     // [heads][kv][128] as {128, kv, heads}, box {64, 64, 1}
+  CUtensorMap values;   // same, box {64, 128, 1}
   CUtensorMap w_uk;     // [H * 128][512], box {64, 128}
   CUtensorMap w_uv;     // [H * 512][128], box {64, 64}
 };
