@@ -27,10 +27,13 @@
 // to hide under. All products are issued by one thread and complete in order, so S
 // of a stream being complete implies that its previous P V is: softmax warps may
 // rescale O without asking.
-// Softmax: two threads of a warp share a row (64 keys of a step each; eight warps
-// a stream keep the chain from S to P short), base 2, the reference maximum moves
-// only when the running one exceeds it by 2^8 (the final division makes it exact);
-// P is rounded to bf16 for the product, its sum is kept in fp32.
+// Softmax: one thread a row (with 128 scores in registers the exponentials of a
+// step overlap; two threads a row in twice the warps took as long, short of
+// registers), base 2. The reference maximum moves
+// only when a score exceeds it by 8 (the final division makes it exact), so a step
+// takes its exponentials against the reference as it stands and looks at the
+// largest afterwards: above 2^8 the warp does the step again, with a maximum taken
+// first. P is rounded to bf16 for the product, its sum is kept in fp32.
 // Positions beyond a row's range are masked by selection, never by adding, so
 // NaN in them stays out; the last step multiplies only up to the last 16 keys
 // with a valid one, beyond which the buffer may hold another request's rows.
@@ -53,12 +56,12 @@ constexpr int kVBytes = 128 * 128;          // [128 keys][64 value dims]
 constexpr int kStageBytes = kKBytes + kVBytes;
 constexpr int kOffRing = 2 * kQBytes;
 constexpr int kOffBar = kOffRing + kStages * kStageBytes;
-constexpr int kSoftmaxWarps = 16;           // eight a stream
-constexpr int kProducerWarp = 16, kIssueWarp = 17;
-constexpr int kThreads = 640;               // (the last two warps idle)
-// Registers a thread after setmaxnreg; they add up to the launch's 5 x 96.
-constexpr int kRegsSoftmax = 104, kRegsOther = 64;
-static_assert(4 * kRegsSoftmax + kRegsOther == 5 * 96, "register split");
+constexpr int kSoftmaxWarps = 8;            // four a stream
+constexpr int kProducerWarp = 8, kIssueWarp = 9;
+constexpr int kThreads = 384;               // (the last two warps idle)
+// Registers a thread after setmaxnreg; they add up to the launch's 3 x 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "register split");
 constexpr int kSched = 2;                   // items announced ahead
 // Items that a group of heads should have for each cluster: within a group the
 // costly tiles of all its heads come first, groups follow each other so that
@@ -66,6 +69,10 @@ constexpr int kSched = 2;                   // items announced ahead
 constexpr int kGroupItems = 3;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr float kMostWeight = 256.0f;       // 2^kRescaleThreshold
+// The reference of a row that has seen no key: below every score, and finite so
+// that a score of -inf against it is a weight of zero and any other infinite.
+constexpr float kNoMax = -1e30f;
 
 enum {
   // In the even block: a step's copies of both blocks landed.
@@ -157,7 +164,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int count = 1;
-      if (i >= kBarP && i < kBarP + 2) count = kSoftmaxWarps;                            // eight of each block
+      if (i >= kBarP && i < kBarP + 2) count = kSoftmaxWarps;                            // four of each block
       if (i >= kBarItemFree && i < kBarItemFree + kSched) count = 2 * (kSoftmaxWarps + 1);  // + issuer, + odd producer
       if (i == kBarStats || i == kBarStatsFree) count = kSoftmaxWarps / 2;
       mbar_init(bar(i), count);
@@ -183,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // A wait of a whole warp: one lane polls (a poll by 32 lanes takes them in turn).
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
     int done = 1;
-    if (lane == 0) done = mbar_spin(b, parity, abort_flag);
+    if (lane == 0) done = mbar_wait(b, parity, abort_flag);
     done = __shfl_sync(0xffffffffu, done, 0);
     __syncwarp();
     return done != 0;
@@ -412,13 +419,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kSoftmaxWarps) {
     setmaxnreg_inc<kRegsSoftmax>();
-    // Warp w works for stream w >> 3 on 16 lanes of TMEM lane quarter w & 3. A
-    // row belongs to threads t and t + 16: keys [0, 64) and [64, 128) of every
-    // step, value dims [0, 64) and [64, 128) of O.
-    const int x = warp >> 3, quarter = warp & 3, th = lane >> 4;
-    const int lane0 = quarter * 32 + ((warp >> 2) & 1) * 16;
-    const int lrow = lane0 + (lane & 15);  // row of this block
-    const uint32_t tbase = tmem + (static_cast<uint32_t>(lane0) << 16);
+    // Warp w works for stream w >> 2 on TMEM lane quarter w & 3, a row a thread.
+    const int x = warp >> 2;
+    const int lrow = (warp & 3) * 32 + lane;  // row of this block
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(lrow & ~31) << 16);
     const uint32_t tS = tbase + kColS + 128 * x, tO = tbase + kColO + 128 * x;
     float2* stats = reinterpret_cast<float2*>(smem + kOffBar + kOffStats);
     const float scale = a.scale_log2;
@@ -435,78 +439,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (w.head < 0) break;
       const int r = 128 * cta + lrow + (w.shared ? 0 : 256 * x);  // row of the tile
       const bool valid = r < w.t.rows;
-      const bool any = r - (lane & 15) < w.t.rows;  // any row of this warp
-      const int64_t out_row = (static_cast<int64_t>(w.t.q_row) + r) * a.num_heads + head0 + w.head;
-      uint8_t* dst = static_cast<uint8_t*>(a.out) + out_row * (kDimV * 2) + th * kDimV;
+      const bool any = r - lane < w.t.rows;  // any row of this warp
+      const int q_row = w.t.q_row, head = head0 + w.head;
+      auto out_row = [&] { return (static_cast<int64_t>(q_row) + r) * a.num_heads + head; };
+      auto out_ptr = [&] { return static_cast<uint8_t*>(a.out) + out_row() * (kDimV * 2); };
       if (w.t.refused) {
         if (valid) {
           const uint32_t nan8[8] = {0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u,
                                     0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
-          for (int v = 0; v < kDimV / 32; ++v) st_global_v8(dst + 32 * v, nan8);
-          if (a.lse && th == 0) a.lse[out_row] = CUDART_NAN_F;
+          for (int v = 0; v < kDimV * 2 / 32; ++v) st_global_v8(out_ptr() + 32 * v, nan8);
+          if (a.lse) a.lse[out_row()] = CUDART_NAN_F;
         }
         continue;
       }
-      const int n = x ? w.n1 : w.n0;
+      const int n = x ? w.n1 : w.n0, n1 = w.n1;
+      const bool shared = w.shared != 0;
       if (n == 0) continue;
-      // The row's range, relative to this thread's first key of the stream's first step.
+      // The row's range, relative to the first key of the stream's first step.
       const int stride = w.shared ? 2 * kPfKvTile : kPfKvTile;
-      const int off = w.t.kv_begin + 64 * th + (w.shared ? kPfKvTile * x : 0);
+      const int off = w.t.kv_begin + (w.shared ? kPfKvTile * x : 0);
       const int end = min(w.t.first_end + r, end_of(w, x)) - off;
       const int begin = a.window > 0 ? max(0, w.t.first_end + r - a.window) - off : -off;
-      float mx_ref = -CUDART_INF_F, l = 0.f;  // l: this thread's keys only
+      // Steps [full0, full1) after the first have no position to mask in any row
+      // of the warp.
+      const int full0 = __reduce_max_sync(0xffffffffu, begin > 0 ? (begin + stride - 1) / stride : 1);
+      const int full1 = __reduce_min_sync(0xffffffffu, end >= kPfKvTile ? (end - kPfKvTile) / stride + 1 : 0);
+      float mx_ref = kNoMax, l = 0.f;
       for (int j = 0; j < n; ++j) {
         if (!(ok = warp_wait(bar(kBarS + x), s_use & 1u))) break;
         ++s_use;
         if (any) {
           tc_fence_after();
-          uint32_t s[64];
-          tmem_ld_h32<64>(tS, s);
-          tmem_ld_h32<64>(tS + 32, s + 32);
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
           tmem_wait_ld();
-          const int b0 = begin - j * stride, e0 = end - j * stride;
-          if (b0 > 0 || e0 < 64) {
+          // P against the reference maximum as it stands, the sum and maximum of
+          // P beside it: no pass over S before the exponentials.
+          float neg = -mx_ref * scale;
+          uint64_t sum2[2];
+          float top;
+          auto weights = [&] {
+            const uint64_t neg2 = f2_make(neg, neg);
+            float top1 = 0.f;
+            top = 0.f;
+            sum2[0] = sum2[1] = f2_make(0.f, 0.f);
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c < b0 || c >= e0) s[c] = 0xff800000u;
-          }
-          float mxa = -CUDART_INF_F, mxb = -CUDART_INF_F;
+            for (int c = 0; c < 64; ++c) {
+              float t0, t1;
+              f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
+              const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
+              sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
+              if (c & 1) top1 = fmax3(top1, p0, p1);
+              else top = fmax3(top, p0, p1);
+              s[c] = pack_bf16x2(p0, p1);
+            }
+            top = fmaxf(top, top1);
+          };
+          bool plain = j >= full0 && j < full1;
+          if (plain) {
+            weights();
+            plain = !__any_sync(0xffffffffu, top > kMostWeight);
+            if (!plain) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            mxa = fmax3(mxa, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            mxb = fmax3(mxb, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-          }
-          float mx = fmaxf(mxa, mxb);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          float alpha = 1.f;
-          if (mx > mx_ref + threshold) {
-            alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
-            l *= alpha;
-            mx_ref = mx;
-          }
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[16];
-              tmem_ld_h16<64>(tO + 16 * c, o);
+              for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
               tmem_wait_ld();
-#pragma unroll
-              for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
-              tmem_st_h16<64>(tO + 16 * c, o);
             }
           }
-          const float neg = mx_ref == -CUDART_INF_F ? 0.f : -mx_ref * scale;
-          const uint64_t neg2 = f2_make(neg, neg);
-          uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+          if (!plain) {
+            // The stream's first step, one with positions to mask, or one whose
+            // scores outgrow the reference: mask, take the maximum, rescale.
+            const int b0 = begin - j * stride, e0 = end - j * stride;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float t0, t1;
-            f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
-            const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
-            sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
-            s[c] = pack_bf16x2(p0, p1);
+            for (int c = 0; c < 128; ++c)
+              if (c < b0 || c >= e0) s[c] = 0xff800000u;
+            float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+            for (int c = 0; c < 128; c += 4) {
+              mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+            }
+            mx = fmaxf(mx, mx1);
+            float alpha = 1.f;
+            if (mx > mx_ref + threshold) {
+              alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
+              l *= alpha;
+              mx_ref = mx;
+            }
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+                tmem_st16(tO + 16 * c, o);
+              }
+            }
+            neg = -mx_ref * scale;
+            weights();
           }
-          tmem_st_h32<32>(tS, s);
+          tmem_st32(tS, s);
+          tmem_st32(tS + 32, s + 32);
           float s0, s1, s2, s3;
           f2_split(sum2[0], s0, s1);
           f2_split(sum2[1], s2, s3);
@@ -518,10 +553,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(lead(kBarP + x));
       }
       if (!ok) break;
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (x == 1 && w.shared) {
+      if (x == 1 && shared) {
         // Stream 0 stores the row: hand over its maximum and sum, keep O until read.
-        if (th == 0) stats[lrow] = make_float2(mx_ref, l);
+        stats[lrow] = make_float2(mx_ref, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarStats));
         if (!(ok = warp_wait(bar(kBarStatsFree), stats_use++ & 1u))) break;
@@ -530,36 +564,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!(ok = warp_wait(bar(kBarO + x), o_use++ & 1u))) break;
       float f0 = 1.f, f1 = 0.f;  // factors of the streams' O
-      const bool merge = w.shared && w.n1 > 0;
+      const bool merge = shared && n1 > 0;
       if (merge) {
         if (!(ok = warp_wait(bar(kBarStats), stats_use++ & 1u))) break;
         if (!(ok = warp_wait(bar(kBarO + 1), o1_use & 1u))) break;
         const float2 other = stats[lrow];
         const float both = fmaxf(mx_ref, other.x);
-        // (a stream without a key has -inf and a sum of 0; NaN sums stay NaN)
-        f0 = mx_ref == -CUDART_INF_F ? 0.f : exp2_approx((mx_ref - both) * scale);
-        f1 = other.x == -CUDART_INF_F ? 0.f : exp2_approx((other.x - both) * scale);
-        if (l != l) f0 = l;
-        if (other.y != other.y) f1 = other.y;
-        l = l * f0 + other.y * f1;
+        f0 = exp2_approx((mx_ref - both) * scale);
+        f1 = exp2_approx((other.x - both) * scale);
+        l = l * f0 + other.y * f1;  // (a NaN of either stays: 0 * NaN)
         mx_ref = both;
       }
-      if (x == 0 && w.n1 > 0) ++o1_use;  // (phases of stream 1's barrier, waited for or not)
+      if (x == 0 && n1 > 0) ++o1_use;  // (phases of stream 1's barrier, waited for or not)
       tc_fence_after();
       if (any) {
         const float inv = a.out_scale / l;  // every valid row attends itself: l > 0
         f0 *= inv;
         f1 *= inv;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
-          tmem_ld_h32<64>(tO + 32 * c, o);
+          tmem_ld32(tO + 32 * c, o);
           tmem_wait_ld();
 #pragma unroll
           for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * f0);
           if (merge) {
             uint32_t o1[32];
-            tmem_ld_h32<64>(tO + 128 + 32 * c, o1);
+            tmem_ld32(tO + 128 + 32 * c, o1);
             tmem_wait_ld();
 #pragma unroll
             for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(fmaf(__uint_as_float(o1[v]), f1, __uint_as_float(o[v])));
@@ -571,11 +602,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 pk[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]), __uint_as_float(o[16 * v + 2 * e + 1]));
-              st_global_v8(dst + 64 * c + 32 * v, pk);
+              st_global_v8(out_ptr() + 64 * c + 32 * v, pk);
             }
           }
         }
-        if (a.lse && valid && th == 0) a.lse[out_row] = (mx_ref * scale + log2f(l)) * 0.69314718055994531f;
+        if (a.lse && valid) a.lse[out_row()] = (mx_ref * scale + log2f(l)) * 0.69314718055994531f;
       }
       tc_fence_before();
       if (merge) {
