@@ -187,15 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
     atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
   };
-  // A wait of a whole warp: one lane polls (a poll by 32 lanes takes them in turn).
-  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
-    int done = 1;
-    if (lane == 0) done = mbar_wait(b, parity, abort_flag);
-    done = __shfl_sync(0xffffffffu, done, 0);
-    __syncwarp();
-    return done != 0;
-  };
-
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return mbar_spin_warp(b, parity, abort_flag); };
   // The announced item comes from the even block: once its barrier is seen
   // complete (polls have the block's scope), acquire at the cluster's.
   auto acquire_item = [&](uint32_t i) { mbar_test_wait_cluster(bar(kBarItem + i % kSched), (i / kSched) & 1u); };
@@ -546,9 +538,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           f2_split(sum2[0], s0, s1);
           f2_split(sum2[1], s2, s3);
           l += (s0 + s1) + (s2 + s3);
-          tmem_wait_st();
+          tmem_wait_st();  // (of the whole warp: one lane may announce it)
           tc_fence_before();
-          __syncwarp();
         }
         if (lane == 0) mbar_arrive_cluster(lead(kBarP + x));
       }
@@ -568,6 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (merge) {
         if (!(ok = warp_wait(bar(kBarStats), stats_use++ & 1u))) break;
         if (!(ok = warp_wait(bar(kBarO + 1), o1_use & 1u))) break;
+        mbar_test_wait(bar(kBarStats), (stats_use - 1) & 1u);  // (every lane acquires what it reads next)
         const float2 other = stats[lrow];
         const float both = fmaxf(mx_ref, other.x);
         f0 = exp2_approx((mx_ref - both) * scale);

@@ -57,6 +57,31 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// Bounded wait of a whole converged warp: lane 0 polls (32 lanes would be
+// served in turn) under a predicate and votes, so that nothing diverges. All
+// lanes may go on once the phase is complete; what they then read has to be
+// ordered by more than this (a tcgen05 fence and load, or a poll of their own).
+__device__ __forceinline__ bool mbar_spin_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               unsigned long long limit_ns = kWaitLimitNs) {
+  const uint32_t lane = threadIdx.x & 31;
+  unsigned long long t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred l, p;\n\tsetp.ne.u32 p, 0, 0;\n\tsetp.eq.u32 l, %3, 0;\n\t"
+        "@l mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(lane)
+        : "memory");
+    if (__any_sync(0xffffffffu, ok)) return true;
+    if ((n & 1023u) == 0) {
+      const unsigned long long t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (__any_sync(0xffffffffu, (abort && *abort) || t - t0 > limit_ns)) return false;
+    }
+  }
+}
+
 // Arrivals on a barrier of either block of a cluster (address from mapa). The
 // first has the default scope, the block: it announces what tcgen05 fences
 // order (a release at cluster scope waits for the thread's earlier global
