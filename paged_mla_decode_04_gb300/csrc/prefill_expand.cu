@@ -3,13 +3,18 @@
 // a product of [rows x 512] with [512 x 256] per head, rounded to bf16 (the
 // precision at which models keep K and V; attention multiplies them in bf16).
 //
-// A persistent block per SM takes tiles of 128 rows x one head: both halves
-// accumulate side by side in 256 TMEM columns (K in the first 128, V in the
-// others), two such accumulators alternate, so the epilogue of one tile runs
-// under the products of the next. Operands come by TMA in chunks of 64 of the
-// 512 dims: rows (K-major), W_UK (K-major) and W_UV (MN-major), 48 KB a stage.
-// Heads vary fastest over the blocks: a row block is then read by neighbours
-// at the same time and the weights stay in L2.
+// Bound by the tensor core once the operands arrive: per tile of 128 rows x one
+// head an SM would read 128 KB of rows and 256 KB of weights in the 4,096 cycles of
+// its products, more than L2 gives it. So pairs of SMs multiply M = 256 rows
+// (each block holds 128 of them and one half of the weights' N), a block keeps its
+// 128 rows of all 512 dims in shared memory (128 KB) over the heads of its run,
+// and only its half of the weights streams: 128 KB a tile.
+//
+// A cluster takes a run of (256 rows, head) units, heads fastest. Both halves of
+// a unit accumulate side by side in 256 TMEM columns (K in the first 128, V in
+// the others); two such accumulators alternate, so that the epilogue of one unit
+// runs under the products of the next. Weights come by TMA in chunks of 64 of the
+// 512 dims, W_UK K-major and W_UV MN-major, 16 KB a stage and block.
 #include <cuda_bf16.h>
 
 #include "../../include/mla_decode.h"
@@ -19,20 +24,33 @@
 namespace mla {
 namespace {
 
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr int kChunk = 64;
 constexpr int kChunks = kDimCkv / kChunk;          // 8
-constexpr int kABytes = 128 * kChunk * 2;          // [128 rows][64 dims]
-constexpr int kUkBytes = kDimNope * kChunk * 2;    // [128 key dims][64 dims]
-constexpr int kUvBytes = kChunk * 64 * 2;          // [64 dims][64 value dims], two of them
-constexpr int kStageBytes = kABytes + kUkBytes + 2 * kUvBytes;
-constexpr int kOffBar = kStages * kStageBytes;
+constexpr int kABytes = 128 * kChunk * 2;          // a chunk of this block's rows
+constexpr int kWBytes = 64 * kChunk * 2;           // [64 key dims][64 dims], or [64 dims][64 value dims]
+constexpr int kStageBytes = 2 * kWBytes;
+constexpr int kOffRing = kChunks * kABytes;
+constexpr int kOffBar = kOffRing + kStages * kStageBytes;
 constexpr int kSmemBytes = kOffBar + 256 + 1024;
 constexpr int kThreads = 192;  // producer, issuer, four epilogue warps
+static_assert(kSmemBytes <= 232448, "shared memory");
 
-enum { kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccFree = kBarAccFull + 2, kBarDrain = kBarAccFree + 2, kNumBars };
+enum {
+  // In the even block: copies of both blocks landed, accumulator read by both.
+  kBarFull = 0,                       // [stages]
+  kBarRows = kBarFull + kStages,      // [chunks]
+  kBarAccFree = kBarRows + kChunks,   // [2]
+  kBarDrain = kBarAccFree + 2,
+  // In both blocks: products complete.
+  kBarEmpty = kBarDrain + 1,          // [stages]
+  kBarRowsFree = kBarEmpty + kStages,
+  kBarAccFull,                        // [2]
+  kNumBars = kBarAccFull + 2
+};
+static_assert(8 * kNumBars + 8 <= 256, "barrier area");
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_expand_kernel(const __grid_constant__ PrefillMaps m, const __grid_constant__ PrefillArgs a, int head0, int heads) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -43,32 +61,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * kNumBars + 4);
   PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cta = cluster_rank();
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(kBarFull + s), 1);
-      mbar_init(bar(kBarEmpty + s), 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(kBarAccFull + s), 1);
-      mbar_init(bar(kBarAccFree + s), 128);
-    }
-    mbar_init(bar(kBarDrain), 1);
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i >= kBarAccFree && i < kBarAccFree + 2 ? 8 : 1);
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
   if (warp == 1) {
-    tmem_alloc(smem_addr(tmem_slot), 512);
-    tmem_relinquish();
+    tmem_alloc2(smem_addr(tmem_slot), 512);
+    tmem_relinquish2();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const uint32_t lead0 = mapa(bar0, 0);
+  auto lead = [&](int i) -> uint32_t { return lead0 + 8u * i; };
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) hd->next_item = 0;  // for the attention that follows
-  const int row_blocks = (hd->kv_rows + 127) / 128;
-  const int64_t tiles = static_cast<int64_t>(row_blocks) * heads;
+  const int row_blocks = (hd->kv_rows + 255) / 256;
+  const int64_t units = static_cast<int64_t>(row_blocks) * heads;
+  const int64_t clusters = gridDim.x / 2, mine = blockIdx.x / 2;
+  const int64_t u0 = units * mine / clusters, u1 = units * (mine + 1) / clusters;
   auto fail = [&] {
     *abort_flag = 1;
     atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
@@ -76,97 +91,127 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t k = 0;  // chunks issued
+      uint32_t k = 0, loads = 0;  // weight chunks, row blocks
+      int row_block = -1;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const int head = head0 + static_cast<int>(t % heads), row = static_cast<int>(t / heads) * 128;
+      for (int64_t u = u0; u < u1 && ok; ++u) {
+        const int head = head0 + static_cast<int>(u % heads), rb = static_cast<int>(u / heads);
+        const bool fresh = rb != row_block;
+        if (fresh) {
+          if (!(ok = mbar_spin(bar(kBarRowsFree), (loads & 1u) ^ 1u, abort_flag))) break;
+          row_block = rb;
+          ++loads;
+        }
         for (int c = 0; c < kChunks; ++c, ++k) {
-          const uint32_t s = k % kStages, use = k / kStages;
-          if (!(ok = mbar_wait(bar(kBarEmpty + s), (use & 1u) ^ 1u, abort_flag))) break;
-          const uint32_t dst = sbase + s * kStageBytes, fb = bar(kBarFull + s);
-          mbar_arrive_expect_tx(fb, kStageBytes);
-          tma_load_2d(dst, &m.rows, fb, c * kChunk, row);
-          tma_load_2d(dst + kABytes, &m.w_uk, fb, c * kChunk, head * kDimNope);
-          tma_load_2d(dst + kABytes + kUkBytes, &m.w_uv, fb, 0, head * kDimCkv + c * kChunk);
-          tma_load_2d(dst + kABytes + kUkBytes + kUvBytes, &m.w_uv, fb, 64, head * kDimCkv + c * kChunk);
+          if (fresh) {
+            if (cta == 0) mbar_arrive_expect_tx(bar(kBarRows + c), 2 * kABytes);
+            tma2_load_2d(sbase + c * kABytes, &m.rows, lead(kBarRows + c), c * kChunk, rb * 256 + 128 * cta);
+          }
+          const uint32_t s = k % kStages;
+          if (!(ok = mbar_spin(bar(kBarEmpty + s), ((k / kStages) & 1u) ^ 1u, abort_flag))) break;
+          const uint32_t dst = sbase + kOffRing + s * kStageBytes;
+          if (cta == 0) mbar_arrive_expect_tx(bar(kBarFull + s), 2 * kStageBytes);
+          tma2_load_2d(dst, &m.w_uk, lead(kBarFull + s), c * kChunk, head * kDimNope + 64 * cta);
+          tma2_load_2d(dst + kWBytes, &m.w_uv, lead(kBarFull + s), 64 * cta, head * kDimCkv + c * kChunk);
         }
       }
       if (!ok) fail();
-      if (*abort_flag)  // let the copies in flight land (each wait bounded)
+      if (*abort_flag && cta == 0) {  // let the copies in flight land (each wait bounded)
         for (uint32_t i = k > kStages ? k - kStages : 0; i < k; ++i)
           mbar_wait(bar(kBarFull + i % kStages), (i / kStages) & 1u, nullptr);
+        if (loads)
+          for (int c = 0; c < kChunks; ++c) mbar_wait(bar(kBarRows + c), (loads - 1) & 1u, nullptr);
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_k = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idesc_v = idesc_bf16(128, 128, false, true);
-      uint32_t k = 0, n = 0;
+    if (cta == 0 && elect_one()) {
+      constexpr uint32_t idesc_k = idesc_bf16(256, 128, false, false);
+      constexpr uint32_t idesc_v = idesc_bf16(256, 128, false, true);
+      const uint32_t a_lo = desc_lo(sbase), ring_lo = desc_lo(sbase + kOffRing);
+      uint32_t stage = 0, par = 0, n = 0, loads = 0;
+      int row_block = -1;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n) {
-        const uint32_t acc = n & 1u;
-        if (!(ok = mbar_wait(bar(kBarAccFree + acc), ((n >> 1) & 1u) ^ 1u, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t d = tmem + acc * 256;
-        for (int c = 0; c < kChunks; ++c, ++k) {
-          const uint32_t s = k % kStages;
-          if (!(ok = mbar_wait(bar(kBarFull + s), (k / kStages) & 1u, abort_flag))) break;
+      auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && mbar_spin(b, parity, abort_flag); };
+      int64_t left = heads - u0 % heads;  // units until the next row block
+      for (int64_t u = u0; u < u1 && ok; ++u, ++n) {
+        const int rb = static_cast<int>(u / heads);
+        const bool fresh = rb != row_block;
+        if (fresh) {
+          row_block = rb;
+          ++loads;
+        }
+        const uint32_t acc = n & 1u, d = tmem + acc * 256;
+        wait(bar(kBarAccFree + acc), ((n >> 1) & 1u) ^ 1u);
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          if (fresh) wait(bar(kBarRows + c), (loads - 1) & 1u);
+          wait(bar(kBarFull + stage), par);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t st = sbase + s * kStageBytes;
+          const uint32_t ad = a_lo + c * (kABytes >> 4), wd = ring_lo + stage * (kStageBytes >> 4);
 #pragma unroll
           for (int i = 0; i < kChunk / 16; ++i) {
-            const uint64_t ad = sdesc_sw128(st + i * 32, 16, 1024);
-            mma_bf16_ss(d, ad, sdesc_sw128(st + kABytes + i * 32, 16, 1024), idesc_k, (c | i) != 0);
-            mma_bf16_ss(d + 128, ad, sdesc_sw128(st + kABytes + kUkBytes + i * 16 * 128, kUvBytes, 1024), idesc_v,
-                        (c | i) != 0);
+            mma2_bf16_ss(d, ad + 2 * i, wd + 2 * i, idesc_k, (c | i) != 0);
+            mma2_bf16_ss(d + 128, ad + 2 * i, wd + (kWBytes >> 4) + 128 * i, idesc_v, (c | i) != 0);
           }
-          mma_commit(bar(kBarEmpty + s));
+          mma2_commit(bar(kBarEmpty + stage));
+          stage = stage == kStages - 1 ? 0 : stage + 1;
+          par ^= stage == 0 ? 1u : 0u;
         }
-        if (ok) mma_commit(bar(kBarAccFull + acc));
+        if (!ok) break;
+        mma2_commit(bar(kBarAccFull + acc));
+        if (--left == 0) {
+          mma2_commit(bar(kBarRowsFree));
+          left = heads;
+        }
       }
       if (!ok) fail();
-      mma_commit(bar(kBarDrain));
+      mma2_commit(bar(kBarDrain));
       mbar_wait(bar(kBarDrain), 0, nullptr);
     }
   } else {
     const int quarter = warp & 3;
-    const int row_in = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t n = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+    for (int64_t u = u0; u < u1; ++u, ++n) {
       const uint32_t acc = n & 1u;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarAccFull + acc), (n >> 1) & 1u, abort_flag));
-      if (!ok) break;
+      if (!(ok = mbar_spin_warp(bar(kBarAccFull + acc), (n >> 1) & 1u, abort_flag))) break;
       tc_fence_after();
-      const int64_t row = (t / heads) * 128 + row_in;
-      const int64_t out_row = (t % heads) * a.lay.kv_capacity + row;
-      // Rows of the buffer are a multiple of 128: every row of a tile has its place.
+      const int64_t row = (u / heads) * 256 + 128 * cta + quarter * 32 + lane;
+      const bool keep = row < a.lay.kv_capacity;  // (a multiple of 128: whole blocks)
+      const int64_t out_row = (u % heads) * a.lay.kv_capacity + row;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {  // 64 columns each: K, K, V, V
         uint32_t r[64];
         tmem_ld32(tmem + lane_base + acc * 256 + c * 64, r);
         tmem_ld32(tmem + lane_base + acc * 256 + c * 64 + 32, r + 32);
         tmem_wait_ld();
+        if (c == 3) {  // all read: the products may go on
+          tc_fence_before();
+          if (lane == 0) mbar_arrive_cluster(lead(kBarAccFree + acc));
+        }
         __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.ws + (c < 2 ? a.lay.keys : a.lay.values)) +
                              out_row * 128 + (c & 1) * 64;
+        if (keep) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t pk[8];
+          for (int v = 0; v < 4; ++v) {
+            uint32_t pk[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1]));
-          st_global_v8(dst + v * 16, pk);
+            for (int i = 0; i < 8; ++i)
+              pk[i] = pack_bf16x2(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1]));
+            st_global_v8(dst + v * 16, pk);
+          }
         }
       }
-      tc_fence_before();
-      mbar_arrive(bar(kBarAccFree + acc));
     }
     if (!ok) fail();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // no block ends while the other's products or arrivals reach into it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 
 }  // namespace
@@ -175,11 +220,11 @@ cudaError_t launch_prefill_expand(const PrefillMaps& m, const PrefillArgs& a, in
   static bool attr_set[kMaxDevices] = {};
   const cudaError_t e = set_smem_once(prefill_expand_kernel, kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int64_t most = a.lay.kv_capacity / 128 * heads;
-  return launch_pdl(prefill_expand_kernel, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads), kSmemBytes,
-                    stream, m, a, head0, heads);
+  const int pairs = sm_count() / 2;
+  if (pairs <= 0) return cudaErrorInvalidDevice;
+  const int64_t most = (a.lay.kv_capacity + 255) / 256 * heads;
+  return launch_pdl(prefill_expand_kernel, dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs)), dim3(kThreads),
+                    kSmemBytes, stream, m, a, head0, heads);
 }
 
 }  // namespace mla

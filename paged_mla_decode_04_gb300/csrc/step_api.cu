@@ -213,7 +213,7 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
       !make_map_3d(&m.values, a.ws + a.lay.values, {mla::kDimV, cap, static_cast<uint64_t>(per_pass)},
                    {mla::kDimV * 2, cap * mla::kDimV * 2}, {64, 128, 1}) ||
       !make_map_2d(&m.w_uk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w_uk, h * mla::kDimNope, mla::kDimCkv, mla::kDimCkv * 2, 64,
-                   128) ||
+                   64) ||
       !make_map_2d(&m.w_uv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w_uv, h * mla::kDimCkv, mla::kDimV, mla::kDimV * 2, 64, 64))
     return MLA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -159,7 +159,7 @@ struct PrefillMaps {
   CUtensorMap ropes;    // same, box {64, 64}
   CUtensorMap keys;     // [heads][kv][128] as {128, kv, heads}, box {64, 64, 1}
   CUtensorMap values;   // same, box {64, 128, 1}
-  CUtensorMap w_uk;     // [H * 128][512], box {64, 128}
+  CUtensorMap w_uk;     // [H * 128][512], box {64, 64}
   CUtensorMap w_uv;     // [H * 512][128], box {64, 64}
 };
 
