@@ -125,8 +125,10 @@ def _check(rc: int, what: str):
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # (the handle alone: building a Stream object costs as much as a launch)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
@@ -152,13 +154,14 @@ class KVPool:
 
     def _c(self) -> _Pool:
         d = self.data
-        if d.dim() != 4 or d.shape[3] != LATENT_DIM:
+        shape = d.shape
+        if len(shape) != 4 or shape[3] != LATENT_DIM:
             raise ValueError("pool must be [num_layers, num_pages, page_size, 576]")
-        if d.dtype not in (torch.bfloat16, torch.uint8):
+        dtype = d.dtype
+        if dtype is not torch.bfloat16 and dtype is not torch.uint8:
             raise ValueError("pool dtype must be bfloat16 or uint8 (e4m3 codes)")
-        _dev(d, "pool")
-        return _Pool(d.data_ptr(), d.shape[0], d.shape[1], d.shape[2], self.dtype_code,
-                     float(self.kv_scale))
+        return _Pool(_dev(d, "pool"), shape[0], shape[1], shape[2],
+                     DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP8_E4M3, self.kv_scale)
 
 
 def kv_write(pool: KVPool, layer: int, new_rows: torch.Tensor, slot_mapping: torch.Tensor,
@@ -356,12 +359,16 @@ def decode_q(pool: KVPool, layer: int, q: torch.Tensor, context_lens: torch.Tens
 
 # ----------------------------------------------------------------- prefill step
 
+_I32, _I64, _BF16, _F32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
+
+
 def _here(t: torch.Tensor, name: str, dtype, device: int) -> int:
-    """_dev for tensors that have to live on the current device."""
-    p = _dev(t, name, dtype)
-    if t.get_device() != device:
+    """Pointer of a contiguous tensor of `dtype` (None: any) on the current device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or (t.dtype is not dtype and dtype is not None) \
+            or not t.is_contiguous():
+        _dev(t, name, dtype)  # says what is wrong with it
         raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), device))
-    return p
+    return t.data_ptr()
 
 
 def _opt(t: Optional[torch.Tensor], name: str, dtype, device: int):
@@ -380,44 +387,51 @@ def extend_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages
     and the tables as CSR lists. state becomes (free pages left, first request
     refused for want of pages); it may share free_count's memory."""
     dev = torch.cuda.current_device()
-    i32 = torch.int32
-    if context_lens.dim() != 1 or new_lens.shape != context_lens.shape:
+    if context_lens.dim() != 1 or new_lens.dim() != 1 or new_lens.numel() != context_lens.numel():
         raise ValueError("context_lens and new_lens must be [batch]")
-    B = context_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    B = context_lens.numel()
+    if block_table.dim() != 2 or block_table.size(0) != B:
         raise ValueError("block_table must be [batch, max_blocks]")
-    if slot_mapping.dim() != 1 or (positions is not None and positions.shape != slot_mapping.shape):
+    n = slot_mapping.numel()
+    if slot_mapping.dim() != 1 or (positions is not None and (positions.dim() != 1 or positions.numel() != n)):
         raise ValueError("slot_mapping and positions must be [max_tokens]")
-    if q_indptr.shape != (B + 1,) or (page_indptr is not None and page_indptr.shape != (B + 1,)):
-        raise ValueError("q_indptr and page_indptr must be [batch + 1]")
+    if q_indptr.dim() != 1 or q_indptr.numel() != B + 1:
+        raise ValueError("q_indptr must be [batch + 1]")
     if (page_indptr is None) != (page_ids is None):
         raise ValueError("give page_indptr and page_ids together")
+    pi_p = ids_p = None
+    max_ids = 0
+    if page_indptr is not None:
+        if page_indptr.dim() != 1 or page_indptr.numel() != B + 1:
+            raise ValueError("page_indptr must be [batch + 1]")
+        pi_p, ids_p = _here(page_indptr, "page_indptr", _I32, dev), _here(page_ids, "page_ids", _I32, dev)
+        max_ids = page_ids.numel()
     if free_count.numel() < 1 or state.numel() < 2:
         raise ValueError("free_count needs one element and state two")
-    rc = load_library().mla_extend_tables(
-        _here(context_lens, "context_lens", i32, dev), _here(new_lens, "new_lens", i32, dev), B, page_size, num_pages,
-        _here(free_pages, "free_pages", i32, dev), _here(free_count, "free_count", i32, dev), free_pages.numel(),
-        _here(block_table, "block_table", i32, dev), block_table.shape[1],
-        _here(slot_mapping, "slot_mapping", torch.int64, dev), _opt(positions, "positions", i32, dev),
-        slot_mapping.shape[0], _here(q_indptr, "q_indptr", i32, dev), _opt(page_indptr, "page_indptr", i32, dev),
-        _opt(page_ids, "page_ids", i32, dev), 0 if page_ids is None else page_ids.numel(),
-        _here(state, "state", i32, dev), _opt(workspace, "workspace", None, dev), _stream(stream))
-    _check(rc, "mla_extend_tables")
+    rc = (_lib or load_library()).mla_extend_tables(
+        _here(context_lens, "context_lens", _I32, dev), _here(new_lens, "new_lens", _I32, dev), B, page_size, num_pages,
+        _here(free_pages, "free_pages", _I32, dev), _here(free_count, "free_count", _I32, dev), free_pages.numel(),
+        _here(block_table, "block_table", _I32, dev), block_table.size(1),
+        _here(slot_mapping, "slot_mapping", _I64, dev), None if positions is None else
+        _here(positions, "positions", _I32, dev), n, _here(q_indptr, "q_indptr", _I32, dev), pi_p, ids_p, max_ids,
+        _here(state, "state", _I32, dev), None if workspace is None else _here(workspace, "workspace", None, dev),
+        _stream(stream))
+    if rc:
+        _check(rc, "mla_extend_tables")
 
 
-def _head_rows(t: torch.Tensor, name: str, device: int):
-    """Pointer and pitch of the [tokens, heads, 64] rope dims of queries, a view
-    whose (token, head) rows lie at one pitch."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device:
+def _head_rows(t: torch.Tensor, name: str, n: int, device: int):
+    """Pointer, pitch and heads of the [tokens, heads, 64] rope dims of queries, a
+    view whose (token, head) rows lie at one pitch."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
         raise ValueError("%s must be a CUDA tensor on the current device" % name)
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != ROPE_DIM:
+    if t.dtype is not _BF16 or t.dim() != 3 or t.size(0) != n or t.size(2) != ROPE_DIM:
         raise ValueError("%s must be bfloat16 [tokens, heads, 64]" % name)
-    n, h, _ = t.shape
+    h = t.size(1)
     s0, s1, s2 = t.stride()
-    pitch = s1 if h > 1 else s0 if n > 1 else ROPE_DIM
     if s2 != 1 or (h > 1 and n > 1 and s0 != h * s1):
         raise ValueError("%s: the (token, head) rows must lie at one pitch" % name)
-    return t.data_ptr(), pitch
+    return t.data_ptr(), s1 if h > 1 else s0 if n > 1 else ROPE_DIM, h
 
 
 def rope_write(pool: Optional[KVPool], layer: int, rows: Optional[torch.Tensor], slot_mapping: Optional[torch.Tensor],
@@ -432,51 +446,58 @@ def rope_write(pool: Optional[KVPool], layer: int, rows: Optional[torch.Tensor],
     q_out None rotates in place. rows None (with pool and slot_mapping as may
     be) rotates queries only."""
     dev = torch.cuda.current_device()
-    if positions.dim() not in (1, 2):
+    pd = positions.dim()
+    if pd == 2:
+        axes, n = positions.size(0), positions.size(1)
+    elif pd == 1:
+        axes, n = 1, positions.size(0)
+    else:
         raise ValueError("positions must be [tokens] or [axes, tokens]")
-    axes, n = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
-    if rows is None and q_rope is None:
-        raise ValueError("give rows, q_rope or both")
-    if rows is not None and (pool is None or slot_mapping is None or rows.shape != (n, LATENT_DIM)):
-        raise ValueError("rows [tokens, 576] go with pool and slot_mapping")
-    if slot_mapping is not None and slot_mapping.shape != (n,):
-        raise ValueError("slot_mapping must be [tokens]")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != ROPE_DIM:
+    if cos_sin.dim() != 2 or cos_sin.size(1) != ROPE_DIM:
         raise ValueError("cos_sin must be [positions, 64]")
-    if norm_weight is not None and norm_weight.shape != (KV_LORA_RANK,):
-        raise ValueError("norm_weight must be [512]")
-    axis_of = None
-    if pair_axis is not None:
-        if len(pair_axis) != ROPE_DIM // 2 or min(pair_axis) < 0 or max(pair_axis) >= axes:
-            raise ValueError("pair_axis must name an axis for each of the 32 pairs")
-        axis_of = bytes(pair_axis)
-    qp = op = None
+    c = rows_p = slots_p = weight_p = qp = op = axis_of = None
     q_pitch = o_pitch = heads = 0
+    if slot_mapping is not None:
+        if slot_mapping.dim() != 1 or slot_mapping.numel() != n:
+            raise ValueError("slot_mapping must be [tokens]")
+        slots_p = _here(slot_mapping, "slot_mapping", _I64, dev)
+    if rows is not None:
+        if pool is None or slots_p is None or rows.dim() != 2 or rows.size(0) != n or rows.size(1) != LATENT_DIM:
+            raise ValueError("rows [tokens, 576] go with pool and slot_mapping")
+        rows_p = _here(rows, "rows", _BF16, dev)
+        if pool.data.get_device() != dev:
+            raise ValueError("pool is not on the current device")
+        c = ctypes.byref(pool._c())
+    if norm_weight is not None:
+        if norm_weight.numel() != KV_LORA_RANK:
+            raise ValueError("norm_weight must be [512]")
+        weight_p = _here(norm_weight, "norm_weight", _BF16, dev)
+    if pair_axis is not None:
+        axis_of = bytes(pair_axis)
+        if len(axis_of) != ROPE_DIM // 2 or max(axis_of) >= axes:
+            raise ValueError("pair_axis must name an axis for each of the 32 pairs")
     if q_rope is not None:
-        q_out = q_rope if q_out is None else q_out
-        if q_rope.shape[0] != n or q_out.shape != q_rope.shape:
-            raise ValueError("q_rope and q_out must be [tokens, heads, 64]")
-        qp, q_pitch = _head_rows(q_rope, "q_rope", dev)
-        op, o_pitch = _head_rows(q_out, "q_out", dev)
-        heads = q_rope.shape[1]
+        qp, q_pitch, heads = _head_rows(q_rope, "q_rope", n, dev)
+        if q_out is None:
+            op, o_pitch = qp, q_pitch
+        else:
+            op, o_pitch, h2 = _head_rows(q_out, "q_out", n, dev)
+            if h2 != heads:
+                raise ValueError("q_rope and q_out must be [tokens, heads, 64]")
         if heads == 0:
             qp = op = None
     elif q_out is not None:
         raise ValueError("q_out goes with q_rope")
-    c = None
-    if rows is not None:
-        c = pool._c()
-        if pool.data.get_device() != dev:
-            raise ValueError("pool is not on the current device")
-        c = ctypes.byref(c)
-    elif qp is None:
+    elif rows is None:
+        raise ValueError("give rows, q_rope or both")
+    if n == 0 or (qp is None and rows_p is None):
         return
-    rc = load_library().mla_rope_write(
-        c, layer, _opt(rows, "rows", torch.bfloat16, dev), _opt(slot_mapping, "slot_mapping", torch.int64, dev), n,
-        _here(positions, "positions", torch.int32, dev), axes, axis_of, _here(cos_sin, "cos_sin", torch.float32, dev),
-        cos_sin.shape[0], 1 if interleaved else 0, _opt(norm_weight, "norm_weight", torch.bfloat16, dev),
-        float(norm_eps), qp, q_pitch, op, o_pitch, heads, _opt(workspace, "workspace", None, dev), _stream(stream))
-    _check(rc, "mla_rope_write")
+    rc = (_lib or load_library()).mla_rope_write(
+        c, layer, rows_p, slots_p, n, _here(positions, "positions", _I32, dev), axes, axis_of,
+        _here(cos_sin, "cos_sin", _F32, dev), cos_sin.size(0), 1 if interleaved else 0, weight_p, norm_eps, qp, q_pitch,
+        op, o_pitch, heads, None if workspace is None else _here(workspace, "workspace", None, dev), _stream(stream))
+    if rc:
+        _check(rc, "mla_rope_write")
 
 
 def prefill_workspace_size(batch: int, q_rows: int, max_kv_tokens: int, num_heads: int, heads_per_pass: int = 0) -> int:
@@ -506,36 +527,35 @@ def prefill(pool: KVPool, layer: int, q: torch.Tensor, q_indptr: torch.Tensor, c
     128], lse [rows, heads]: causal attention over the paged cache, the new
     tokens' latent rows written beforehand."""
     dev = torch.cuda.current_device()
-    i32, bf16 = torch.int32, torch.bfloat16
-    if q.dim() != 3 or q.shape[2] != QK_HEAD_DIM:
+    if q.dim() != 3 or q.size(2) != QK_HEAD_DIM:
         raise ValueError("q must be [rows, heads, 192]")
-    T, H, _ = q.shape
+    T, H = q.size(0), q.size(1)
     if out.shape != (T, H, V_HEAD_DIM) or (lse is not None and lse.shape != (T, H)):
         raise ValueError("out must be [rows, heads, 128], lse [rows, heads]")
     if context_lens.dim() != 1:
         raise ValueError("context_lens must be [batch]")
-    B = context_lens.shape[0]
-    if q_indptr.shape != (B + 1,):
+    B = context_lens.numel()
+    if q_indptr.dim() != 1 or q_indptr.numel() != B + 1:
         raise ValueError("q_indptr must be [batch + 1]")
     if w_uk.shape != (H, NOPE_DIM, KV_LORA_RANK) or w_uv.shape != (H, KV_LORA_RANK, V_HEAD_DIM):
         raise ValueError("w_uk [heads, 128, 512] and w_uv [heads, 512, 128] expected")
     if block_table is not None:
-        if block_table.dim() != 2 or block_table.shape[0] != B:
+        if block_table.dim() != 2 or block_table.size(0) != B:
             raise ValueError("block_table must be [batch, max_blocks]")
-        indptr_p, ids_p, max_blocks = None, _here(block_table, "block_table", i32, dev), block_table.shape[1]
+        indptr_p, ids_p, max_blocks = None, _here(block_table, "block_table", _I32, dev), block_table.size(1)
     else:
-        if page_indptr is None or page_ids is None or page_indptr.shape != (B + 1,):
+        if page_indptr is None or page_ids is None or page_indptr.dim() != 1 or page_indptr.numel() != B + 1:
             raise ValueError("give block_table, or page_indptr [batch+1] and page_ids")
-        indptr_p, ids_p, max_blocks = _here(page_indptr, "page_indptr", i32, dev), \
-            _here(page_ids, "page_ids", i32, dev), 0
+        indptr_p, ids_p, max_blocks = _here(page_indptr, "page_indptr", _I32, dev), \
+            _here(page_ids, "page_ids", _I32, dev), 0
     if pool.data.get_device() != dev:
         raise ValueError("pool is not on the current device")
-    c = pool._c()
-    rc = load_library().mla_prefill(
-        ctypes.byref(c), layer, _here(q, "q", bf16, dev), _here(q_indptr, "q_indptr", i32, dev), indptr_p, ids_p,
-        max_blocks, _here(context_lens, "context_lens", i32, dev), B, T, max_kv_tokens, H,
-        _here(w_uk, "w_uk", bf16, dev), _here(w_uv, "w_uv", bf16, dev), float(softmax_scale), window,
+    rc = (_lib or load_library()).mla_prefill(
+        ctypes.byref(pool._c()), layer, _here(q, "q", _BF16, dev), _here(q_indptr, "q_indptr", _I32, dev), indptr_p,
+        ids_p, max_blocks, _here(context_lens, "context_lens", _I32, dev), B, T, max_kv_tokens, H,
+        _here(w_uk, "w_uk", _BF16, dev), _here(w_uv, "w_uv", _BF16, dev), softmax_scale, window,
         _here(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
-        _here(out, "out", bf16, dev), _opt(lse, "lse", torch.float32, dev), _stream(stream))
-    _check(rc, "mla_prefill")
+        _here(out, "out", _BF16, dev), _opt(lse, "lse", _F32, dev), _stream(stream))
+    if rc:
+        _check(rc, "mla_prefill")
     return out
