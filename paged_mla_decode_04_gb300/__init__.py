@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -65,6 +66,9 @@ class _Pool(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("kv_scale", ctypes.c_float)]
 
 
+_pack_pool = struct.Struct("@Piiiif0P").pack  # _Pool, its tail padding included
+assert len(_pack_pool(0, 0, 0, 0, 0, 0.0)) == ctypes.sizeof(_Pool)
+
 _lib = None
 
 
@@ -107,10 +111,10 @@ def load_library(path: str = LIB_PATH):
     L = ctypes.c_int64
     lib.mla_extend_tables.argtypes = [P, P, I, I, I, P, P, I, P, I, P, P, I, P, P, P, I, P, P, P]
     lib.mla_extend_tables.restype = I
-    lib.mla_rope_write.argtypes = [ctypes.POINTER(_Pool), I, P, P, I, P, I, ctypes.c_char_p, P, I, I, P,
+    lib.mla_rope_write.argtypes = [ctypes.c_char_p, I, P, P, I, P, I, ctypes.c_char_p, P, I, I, P,
                                    ctypes.c_float, P, L, P, L, I, P, P]
     lib.mla_rope_write.restype = I
-    lib.mla_prefill.argtypes = [ctypes.POINTER(_Pool), I, P, P, P, P, I, P, I, I, L, I, P, P, ctypes.c_float, I,
+    lib.mla_prefill.argtypes = [ctypes.c_char_p, I, P, P, P, P, I, P, I, I, L, I, P, P, ctypes.c_float, I,
                                 P, Z, P, P, P]
     lib.mla_prefill.restype = I
     lib.mla_prefill_workspace_size.argtypes = [I, I, L, I, I]
@@ -162,6 +166,16 @@ class KVPool:
             raise ValueError("pool dtype must be bfloat16 or uint8 (e4m3 codes)")
         return _Pool(_dev(d, "pool"), shape[0], shape[1], shape[2],
                      DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP8_E4M3, self.kv_scale)
+
+    def _packed(self, device: int) -> bytes:
+        """The same structure as bytes (quicker made than a ctypes one)."""
+        d = self.data
+        if d.dim() != 4 or d.size(3) != LATENT_DIM:
+            raise ValueError("pool must be [num_layers, num_pages, page_size, 576]")
+        code = DTYPE_BF16 if d.dtype is torch.bfloat16 else DTYPE_FP8_E4M3
+        if code == DTYPE_FP8_E4M3 and d.dtype is not torch.uint8:
+            raise ValueError("pool dtype must be bfloat16 or uint8 (e4m3 codes)")
+        return _pack_pool(_here(d, "pool", None, device), d.size(0), d.size(1), d.size(2), code, self.kv_scale)
 
 
 def kv_write(pool: KVPool, layer: int, new_rows: torch.Tensor, slot_mapping: torch.Tensor,
@@ -465,16 +479,14 @@ def rope_write(pool: Optional[KVPool], layer: int, rows: Optional[torch.Tensor],
         if pool is None or slots_p is None or rows.dim() != 2 or rows.size(0) != n or rows.size(1) != LATENT_DIM:
             raise ValueError("rows [tokens, 576] go with pool and slot_mapping")
         rows_p = _here(rows, "rows", _BF16, dev)
-        if pool.data.get_device() != dev:
-            raise ValueError("pool is not on the current device")
-        c = ctypes.byref(pool._c())
+        c = pool._packed(dev)
     if norm_weight is not None:
         if norm_weight.numel() != KV_LORA_RANK:
             raise ValueError("norm_weight must be [512]")
         weight_p = _here(norm_weight, "norm_weight", _BF16, dev)
     if pair_axis is not None:
         axis_of = bytes(pair_axis)
-        if len(axis_of) != ROPE_DIM // 2 or max(axis_of) >= axes:
+        if len(axis_of) != ROPE_DIM // 2:
             raise ValueError("pair_axis must name an axis for each of the 32 pairs")
     if q_rope is not None:
         qp, q_pitch, heads = _head_rows(q_rope, "q_rope", n, dev)
@@ -497,6 +509,8 @@ def rope_write(pool: Optional[KVPool], layer: int, rows: Optional[torch.Tensor],
         _here(cos_sin, "cos_sin", _F32, dev), cos_sin.size(0), 1 if interleaved else 0, weight_p, norm_eps, qp, q_pitch,
         op, o_pitch, heads, None if workspace is None else _here(workspace, "workspace", None, dev), _stream(stream))
     if rc:
+        if axis_of is not None and max(axis_of) >= axes:
+            raise ValueError("pair_axis names an axis that positions lacks")
         _check(rc, "mla_rope_write")
 
 
@@ -548,10 +562,8 @@ def prefill(pool: KVPool, layer: int, q: torch.Tensor, q_indptr: torch.Tensor, c
             raise ValueError("give block_table, or page_indptr [batch+1] and page_ids")
         indptr_p, ids_p, max_blocks = _here(page_indptr, "page_indptr", _I32, dev), \
             _here(page_ids, "page_ids", _I32, dev), 0
-    if pool.data.get_device() != dev:
-        raise ValueError("pool is not on the current device")
     rc = (_lib or load_library()).mla_prefill(
-        ctypes.byref(pool._c()), layer, _here(q, "q", _BF16, dev), _here(q_indptr, "q_indptr", _I32, dev), indptr_p,
+        pool._packed(dev), layer, _here(q, "q", _BF16, dev), _here(q_indptr, "q_indptr", _I32, dev), indptr_p,
         ids_p, max_blocks, _here(context_lens, "context_lens", _I32, dev), B, T, max_kv_tokens, H,
         _here(w_uk, "w_uk", _BF16, dev), _here(w_uv, "w_uv", _BF16, dev), softmax_scale, window,
         _here(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),

@@ -72,6 +72,7 @@ int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int 
   a.status = status_of(workspace);
   a.batch = batch;
   a.page_size = page_size;
+  a.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
   a.num_pages = num_pages;
   a.free_capacity = free_capacity;
   a.max_blocks = max_blocks;

@@ -26,6 +26,7 @@ struct TablesArgs {
   int* status;           // or null
   int batch;
   int page_size;
+  int page_shift;  // log2 of it
   int num_pages;
   int free_capacity;
   int max_blocks;

@@ -27,7 +27,7 @@ def pool(mem, **kw):
     import paged_mla_decode_04_gb300 as m
     d = dict(data=mem, num_layers=2, num_pages=4, page_size=16, dtype=0, kv_scale=1.0)
     d.update(kw)
-    return m._Pool(d["data"], d["num_layers"], d["num_pages"], d["page_size"], d["dtype"], d["kv_scale"])
+    return bytes(m._Pool(d["data"], d["num_layers"], d["num_pages"], d["page_size"], d["dtype"], d["kv_scale"]))
 
 
 TABLES = ["context_lens", "new_lens", "batch", "page_size", "num_pages", "free_pages", "free_count", "free_capacity",
@@ -56,7 +56,7 @@ ROPE = ["pool", "layer", "rows", "slot_mapping", "n", "positions", "num_axes", "
 
 def rope(lib, mem, **kw):
     a = {n: mem for n in ROPE}
-    a.update(pool=ctypes.byref(pool(mem)), layer=0, n=3, num_axes=1, pair_axis=None, max_position=8, interleaved=1,
+    a.update(pool=pool(mem), layer=0, n=3, num_axes=1, pair_axis=None, max_position=8, interleaved=1,
              norm_eps=1e-6, q_rope=mem, q_out=mem + 8192, q_pitch=64, q_out_pitch=64, num_heads=2, stream=None)
     a.update(kw)
     return lib.mla_rope_write(*[a[n] for n in ROPE])
@@ -81,7 +81,7 @@ def test_rope_write_alignment_and_overlap(lib, mem):
     assert rope(lib, mem, q_rope=mem, q_out=mem, q_pitch=64, q_out_pitch=128) == ARG
     assert rope(lib, mem, n=0) == 0
     bad = pool(mem, dtype=1, kv_scale=0.0)
-    assert rope(lib, mem, pool=ctypes.byref(bad)) == ARG
+    assert rope(lib, mem, pool=bad) == ARG
 
 
 PREFILL = ["pool", "layer", "q", "q_indptr", "page_indptr", "page_ids", "max_blocks", "context_lens", "batch", "q_rows",
@@ -99,7 +99,7 @@ PREFILL = ["pool", "layer", "q", "q_indptr", "page_indptr", "page_ids", "max_blo
     (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=1000), WORKSPACE)])
 def test_prefill(lib, mem, bad, code):
     a = {n: mem for n in PREFILL}
-    a.update(pool=ctypes.byref(pool(mem)), layer=0, max_blocks=4, batch=2, q_rows=8, max_kv_tokens=64, num_heads=4,
+    a.update(pool=pool(mem), layer=0, max_blocks=4, batch=2, q_rows=8, max_kv_tokens=64, num_heads=4,
              softmax_scale=0.07, window=0, workspace_bytes=1 << 14, stream=None)
     a.update(bad)
     assert lib.mla_prefill(*[a[n] for n in PREFILL]) == code
@@ -108,7 +108,7 @@ def test_prefill(lib, mem, bad, code):
 def test_prefill_alignment_and_empty_calls(lib, mem):
     def call(**kw):
         a = {n: mem for n in PREFILL}
-        a.update(pool=ctypes.byref(pool(mem)), layer=0, max_blocks=4, batch=2, q_rows=8, max_kv_tokens=64, num_heads=4,
+        a.update(pool=pool(mem), layer=0, max_blocks=4, batch=2, q_rows=8, max_kv_tokens=64, num_heads=4,
                  softmax_scale=0.07, window=0, workspace_bytes=1 << 14, stream=None)
         a.update(kw)
         return lib.mla_prefill(*[a[n] for n in PREFILL])
