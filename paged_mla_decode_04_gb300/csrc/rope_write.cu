@@ -11,11 +11,12 @@
 // are rounded to bf16. All arithmetic is fp32.
 //
 // The cost is the bytes: 256 of a (token, head)'s query read and written
-// against 12 multiply-adds per pair. So everything moves in 16-byte pieces:
-// four lanes share one row of 64 rope dims, lane i its pairs 8i .. 8i + 7
-// (two 16-byte pieces in either layout), and keep the token's 16 sines and
-// cosines in registers over all heads that the warp serves. A latent row is one
-// warp's work. Both kinds share a launch: blocks [0, row_blocks) write rows.
+// against 6 multiply-adds per pair, so bytes in flight are what counts: eight
+// lanes share one row of 64 rope dims, lane i its pairs 4i .. 4i + 3 (16 bytes), and
+// keep the token's eight sines and cosines in registers over all heads that the
+// warp serves. (With four lanes a row the angles took 16 registers and half the
+// warps fitted.) A latent row is one warp's work. Both kinds share a launch:
+// blocks [0, row_blocks) write rows.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -27,18 +28,19 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kPairsPerLane = 8;
-constexpr int kRowVecs = kDimRow * 2 / 16;  // 72
-constexpr int kHeadsPerStep = 8;            // 32 lanes / 4 lanes a row
-constexpr int kUnroll = 4;                  // rows a lane has in flight
+constexpr int kPairsPerLane = 4;
+constexpr int kRowLanes = kRopePairs / kPairsPerLane;  // 8 lanes share a row
+constexpr int kRowVecs = kDimRow * 2 / 16;             // 72
+constexpr int kHeadsPerStep = 32 / kRowLanes;
+constexpr int kUnroll = 4;                             // rows a lane has in flight
 
 struct Turn {
   float c[kPairsPerLane], s[kPairsPerLane];
 };
 
 // Row of the table for each axis, or false for a pad row or a position that
-// the table lacks (which sets the status word).
-__device__ __forceinline__ bool token_positions(const RopeArgs& a, int t, int (&pos)[kMaxAxes]) {
+// the table lacks (which sets the status word unless the row is a pad already).
+__device__ __forceinline__ bool token_positions(const RopeArgs& a, int t, int (&pos)[kMaxAxes], bool real) {
   bool pad = false, bad = false;
 #pragma unroll
   for (int x = 0; x < kMaxAxes; ++x) {
@@ -49,25 +51,22 @@ __device__ __forceinline__ bool token_positions(const RopeArgs& a, int t, int (&
       bad |= pos[x] >= a.max_position;
     }
   }
-  if (bad && !pad && a.status) atomicOr(a.status, MLA_STATUS_BAD_POSITION);
+  if (bad && !pad && real && a.status) atomicOr(a.status, MLA_STATUS_BAD_POSITION);
   return !pad && !bad;
 }
 
-// Sines and cosines of pairs 8 sub .. 8 sub + 7.
+// Sines and cosines of pairs 4 sub .. 4 sub + 3.
 __device__ __forceinline__ void load_turn(const RopeArgs& a, const int (&pos)[kMaxAxes], int sub, Turn& r) {
-  const uint32_t axes = static_cast<uint32_t>(a.pair_axis >> (16 * sub)) & 0xffffu;
+  const uint32_t axes = static_cast<uint32_t>(a.pair_axis >> (2 * kPairsPerLane * sub)) & 0xffu;
   auto row = [&](uint32_t axis) {
     const int p = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
-    return a.cos_sin + static_cast<int64_t>(p) * kDimRope + 8 * sub;
+    return a.cos_sin + static_cast<int64_t>(p) * kDimRope + kPairsPerLane * sub;
   };
-  if (axes == (axes & 3u) * 0x5555u) {  // one axis for all eight
+  if (axes == (axes & 3u) * 0x55u) {  // one axis for all four
     const float4* v = reinterpret_cast<const float4*>(row(axes & 3u));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 c = __ldg(v + i), s = __ldg(v + 8 + i);
-      r.c[4 * i] = c.x, r.c[4 * i + 1] = c.y, r.c[4 * i + 2] = c.z, r.c[4 * i + 3] = c.w;
-      r.s[4 * i] = s.x, r.s[4 * i + 1] = s.y, r.s[4 * i + 2] = s.z, r.s[4 * i + 3] = s.w;
-    }
+    const float4 c = __ldg(v), s = __ldg(v + kRopePairs / 4);
+    r.c[0] = c.x, r.c[1] = c.y, r.c[2] = c.z, r.c[3] = c.w;
+    r.s[0] = s.x, r.s[1] = s.y, r.s[2] = s.z, r.s[3] = s.w;
   } else {
 #pragma unroll
     for (int i = 0; i < kPairsPerLane; ++i) {
@@ -81,64 +80,72 @@ __device__ __forceinline__ void load_turn(const RopeArgs& a, const int (&pos)[kM
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Turns the lane's eight pairs: u, v are its two 16-byte pieces. x[], y[]
-// receive the pairs' two values; the caller packs them.
-__device__ __forceinline__ void turn_pairs(const uint4& u, const uint4& v, const Turn& r, bool interleaved,
-                                           float (&x)[kPairsPerLane], float (&y)[kPairsPerLane]) {
-  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+// A lane's four pairs of a row, as 16 bytes: one piece, or (rotated halves) the
+// four first and the four second values.
+template <bool kInterleaved>
+__device__ __forceinline__ uint4 load_pairs(const void* row, int sub) {
+  if (kInterleaved) return static_cast<const uint4*>(row)[sub];
+  const uint2 x = static_cast<const uint2*>(row)[sub], y = static_cast<const uint2*>(row)[sub + kRowLanes];
+  return make_uint4(x.x, x.y, y.x, y.y);
+}
+template <bool kInterleaved>
+__device__ __forceinline__ void store_pairs(void* row, int sub, const uint4& v) {
+  if (kInterleaved) {
+    static_cast<uint4*>(row)[sub] = v;
+  } else {
+    static_cast<uint2*>(row)[sub] = make_uint2(v.x, v.y);
+    static_cast<uint2*>(row)[sub + kRowLanes] = make_uint2(v.z, v.w);
+  }
+}
+
+template <bool kInterleaved>
+__device__ __forceinline__ void turn_pairs(const uint4& v, const Turn& r, float (&x)[kPairsPerLane],
+                                           float (&y)[kPairsPerLane]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < kPairsPerLane; ++i) {
-    const float a = interleaved ? lo_f(w[i]) : (i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1]));
-    const float b = interleaved ? hi_f(w[i]) : (i & 1 ? hi_f(w[4 + (i >> 1)]) : lo_f(w[4 + (i >> 1)]));
+    const float a = kInterleaved ? lo_f(w[i]) : (i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1]));
+    const float b = kInterleaved ? hi_f(w[i]) : (i & 1 ? hi_f(w[2 + (i >> 1)]) : lo_f(w[2 + (i >> 1)]));
     x[i] = a * r.c[i] - b * r.s[i];
     y[i] = a * r.s[i] + b * r.c[i];
   }
 }
 
-// The two 16-byte bf16 pieces of turned pairs.
-__device__ __forceinline__ void pack_pairs(const float (&x)[kPairsPerLane], const float (&y)[kPairsPerLane],
-                                           bool interleaved, uint4& u, uint4& v) {
-  if (interleaved) {
-    u = make_uint4(pack_bf16x2(x[0], y[0]), pack_bf16x2(x[1], y[1]), pack_bf16x2(x[2], y[2]), pack_bf16x2(x[3], y[3]));
-    v = make_uint4(pack_bf16x2(x[4], y[4]), pack_bf16x2(x[5], y[5]), pack_bf16x2(x[6], y[6]), pack_bf16x2(x[7], y[7]));
-  } else {
-    u = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    v = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-  }
+template <bool kInterleaved>
+__device__ __forceinline__ uint4 pack_pairs(const float (&x)[kPairsPerLane], const float (&y)[kPairsPerLane]) {
+  return kInterleaved ? make_uint4(pack_bf16x2(x[0], y[0]), pack_bf16x2(x[1], y[1]), pack_bf16x2(x[2], y[2]),
+                                   pack_bf16x2(x[3], y[3]))
+                      : make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
+                                   pack_bf16x2(y[2], y[3]));
 }
 
 __device__ __forceinline__ uint32_t e4m3(float x, float scale) {
   return static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3));
 }
 
-__device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float scale) {
-  uint2 r;
-  r.x = e4m3(x[0], scale) | e4m3(x[1], scale) << 8 | e4m3(x[2], scale) << 16 | e4m3(x[3], scale) << 24;
-  r.y = e4m3(x[4], scale) | e4m3(x[5], scale) << 8 | e4m3(x[6], scale) << 16 | e4m3(x[7], scale) << 24;
-  return r;
+__device__ __forceinline__ uint32_t e4m3x4(float p, float q, float r, float t, float scale) {
+  return e4m3(p, scale) | e4m3(q, scale) << 8 | e4m3(r, scale) << 16 | e4m3(t, scale) << 24;
 }
 
 // One warp, one latent row.
-template <int kDtype>
+template <int kDtype, bool kInterleaved>
 __device__ __forceinline__ void write_row(const RopeArgs& a, int t, int lane) {
+  // The row and its slot and positions are asked for together; only the angles
+  // have to wait for an answer.
+  const uint4* src = a.rows + static_cast<int64_t>(t) * kRowVecs;
   const int64_t slot = a.slots[t];
-  if (slot < 0) return;  // pad row
+  const uint4 c0 = src[lane], c1 = src[lane + 32];
+  uint4 rope;
+  if (lane < kRowLanes) rope = load_pairs<kInterleaved>(src + 64, lane);
+  int pos[kMaxAxes];
+  const bool here = token_positions(a, t, pos, slot >= 0);
+  if (slot < 0 || !here) return;  // pad row
   if (slot >= a.layer_rows) {
     if (lane == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_SLOT);
     return;
   }
-  int pos[kMaxAxes];
-  if (!token_positions(a, t, pos)) return;
-  const uint4* src = a.rows + static_cast<int64_t>(t) * kRowVecs;
-  const uint4 c0 = src[lane], c1 = src[lane + 32];
-  const bool il = a.interleaved != 0;
-  uint4 ru, rv;
   Turn r;
-  if (lane < 4) {
-    ru = src[64 + (il ? 2 * lane : lane)];
-    rv = src[64 + (il ? 2 * lane + 1 : lane + 4)];
-    load_turn(a, pos, lane, r);
-  }
+  if (lane < kRowLanes) load_turn(a, pos, lane, r);
   float x[2][8];
   const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
@@ -163,83 +170,77 @@ __device__ __forceinline__ void write_row(const RopeArgs& a, int t, int lane) {
     }
   }
   float rx[kPairsPerLane], ry[kPairsPerLane];
-  if (lane < 4) turn_pairs(ru, rv, r, il, rx, ry);
+  if (lane < kRowLanes) turn_pairs<kInterleaved>(rope, r, rx, ry);
   if (kDtype == MLA_DTYPE_BF16) {
     uint4* dst = reinterpret_cast<uint4*>(a.layer_base) + slot * kRowVecs;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       dst[lane + 32 * h] = make_uint4(pack_bf16x2(x[h][0], x[h][1]), pack_bf16x2(x[h][2], x[h][3]),
                                       pack_bf16x2(x[h][4], x[h][5]), pack_bf16x2(x[h][6], x[h][7]));
-    if (lane < 4) {
-      uint4 u, v;
-      pack_pairs(rx, ry, il, u, v);
-      dst[64 + (il ? 2 * lane : lane)] = u;
-      dst[64 + (il ? 2 * lane + 1 : lane + 4)] = v;
-    }
+    if (lane < kRowLanes) store_pairs<kInterleaved>(dst + 64, lane, pack_pairs<kInterleaved>(rx, ry));
   } else {
     uint2* dst = reinterpret_cast<uint2*>(a.layer_base + slot * kDimRow);
-    dst[lane] = e4m3x8(x[0], a.kv_scale);
-    dst[lane + 32] = e4m3x8(x[1], a.kv_scale);
-    if (lane < 4) {
-      float p[8], q[8];
+    const float s = a.kv_scale;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = il ? (i & 1 ? ry[i >> 1] : rx[i >> 1]) : rx[i];
-        q[i] = il ? (i & 1 ? ry[4 + (i >> 1)] : rx[4 + (i >> 1)]) : ry[i];
+    for (int h = 0; h < 2; ++h)
+      dst[lane + 32 * h] = make_uint2(e4m3x4(x[h][0], x[h][1], x[h][2], x[h][3], s), e4m3x4(x[h][4], x[h][5], x[h][6], x[h][7], s));
+    if (lane < kRowLanes) {
+      if (kInterleaved) {
+        dst[64 + lane] = make_uint2(e4m3x4(rx[0], ry[0], rx[1], ry[1], s), e4m3x4(rx[2], ry[2], rx[3], ry[3], s));
+      } else {
+        uint32_t* half = reinterpret_cast<uint32_t*>(dst + 64);
+        half[lane] = e4m3x4(rx[0], rx[1], rx[2], rx[3], s);
+        half[lane + kRowLanes] = e4m3x4(ry[0], ry[1], ry[2], ry[3], s);
       }
-      dst[64 + (il ? 2 * lane : lane)] = e4m3x8(p, a.kv_scale);
-      dst[64 + (il ? 2 * lane + 1 : lane + 4)] = e4m3x8(q, a.kv_scale);
     }
   }
 }
 
-// One warp: heads [h0, h1) of one token's query.
+// One warp: heads [h0, h1) of one token's query. The first rows are asked for
+// together with the token's slot and positions, the next ones before the current
+// ones are turned.
 template <bool kInterleaved>
 __device__ __forceinline__ void turn_query(const RopeArgs& a, int t, int h0, int h1, int lane) {
-  if (a.slots && a.slots[t] < 0) return;  // pad row
+  const int sub = lane % kRowLanes;
+  const int64_t row0 = static_cast<int64_t>(t) * a.num_heads;
+  uint4 u[kUnroll];
+  auto load = [&](int h, int k) {
+    const int hh = h + k * kHeadsPerStep;
+    if (hh < h1) u[k] = load_pairs<kInterleaved>(a.q + (row0 + hh) * a.q_pitch, sub);
+  };
+  int h = h0 + lane / kRowLanes;
+  const int64_t slot = a.slots ? a.slots[t] : 0;
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k) load(h, k);
   int pos[kMaxAxes];
-  if (!token_positions(a, t, pos)) return;
-  const int sub = lane & 3;
+  const bool here = token_positions(a, t, pos, slot >= 0);
+  if (slot < 0 || !here) return;  // pad row
   Turn r;
   load_turn(a, pos, sub, r);
-  const int off0 = kInterleaved ? 16 * sub : 8 * sub;
-  const int off1 = kInterleaved ? 16 * sub + 8 : 8 * sub + 32;
-  const int64_t row0 = static_cast<int64_t>(t) * a.num_heads;
-  for (int h = h0 + (lane >> 2); h < h1; h += kHeadsPerStep * kUnroll) {
-    uint4 u[kUnroll], v[kUnroll];
+  for (; h < h1; h += kHeadsPerStep * kUnroll) {
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       const int hh = h + k * kHeadsPerStep;
-      if (hh < h1) {
-        const uint16_t* src = a.q + (row0 + hh) * a.q_pitch;
-        u[k] = *reinterpret_cast<const uint4*>(src + off0);
-        v[k] = *reinterpret_cast<const uint4*>(src + off1);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int hh = h + k * kHeadsPerStep;
+      const uint4 v = u[k];
+      load(h + kHeadsPerStep * kUnroll, k);
       if (hh < h1) {
         float x[kPairsPerLane], y[kPairsPerLane];
-        turn_pairs(u[k], v[k], r, kInterleaved, x, y);
-        pack_pairs(x, y, kInterleaved, u[k], v[k]);
-        uint16_t* dst = a.q_out + (row0 + hh) * a.q_out_pitch;
-        *reinterpret_cast<uint4*>(dst + off0) = u[k];
-        *reinterpret_cast<uint4*>(dst + off1) = v[k];
+        turn_pairs<kInterleaved>(v, r, x, y);
+        store_pairs<kInterleaved>(a.q_out + (row0 + hh) * a.q_out_pitch, sub, pack_pairs<kInterleaved>(x, y));
       }
     }
   }
 }
 
 template <int kDtype, bool kInterleaved>
-__global__ void __launch_bounds__(32 * kWarps) rope_write_kernel(const RopeArgs a, int row_blocks, int heads_per_warp,
+__global__ void __launch_bounds__(32 * kWarps, 4) rope_write_kernel(const RopeArgs a, int row_blocks, int heads_per_warp,
                                                                  int warps_per_token) {
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) < row_blocks) {
     const int t = blockIdx.x * kWarps + warp;
-    if (t < a.n) write_row<kDtype>(a, t, lane);
+    if (t < a.n) write_row<kDtype, kInterleaved>(a, t, lane);
     return;
   }
   const int64_t w = static_cast<int64_t>(blockIdx.x - row_blocks) * kWarps + warp;
