@@ -95,17 +95,17 @@ enum {
   kNumBars
 };
 
-// What the roles need of an item. Sent to both blocks as three 16-byte words.
+// What the roles need of an item. Sent to both blocks as four 16-byte words.
 struct alignas(16) Item {
   PfTile t;
   int head;    // head within the pass; -1: no further items
   int n0, n1;  // steps of each stream (0: none)
   int shared;  // the streams share the rows and alternate over the steps
 };
-static_assert(sizeof(Item) == 48, "three 16-byte words");
+static_assert(sizeof(Item) == 64, "four 16-byte words");
 
 constexpr int kOffItems = (8 * kNumBars + 8 + 15) / 16 * 16;  // after TMEM address and abort flag
-constexpr int kOffStats = kOffItems + kSched * 48;            // float2 [128]: stream 1's maximum and sum
+constexpr int kOffStats = kOffItems + kSched * 64;            // float2 [128]: stream 1's maximum and sum
 constexpr int kSmemBytes = kOffBar + kOffStats + 1024 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 
@@ -121,7 +121,7 @@ __device__ __forceinline__ Item item_of(const PfTile& t, int head) {
     w.n0 = (n + 1) / 2;
     w.n1 = n / 2;
   } else {
-    w.n0 = pf_steps(t.kv_begin, t.first_end + 255);
+    w.n0 = pf_steps(t.kv_begin, min(t.first_end + 255, t.kv_end));
     w.n1 = pf_steps(t.kv_begin, t.kv_end);
   }
   return w;
@@ -129,7 +129,7 @@ __device__ __forceinline__ Item item_of(const PfTile& t, int head) {
 
 // End of the positions that a stream's rows attend.
 __device__ __forceinline__ int end_of(const Item& w, int x) {
-  return x == 0 && !w.shared ? w.t.first_end + min(w.t.rows, 256) - 1 : w.t.kv_end;
+  return x == 0 && !w.shared ? min(w.t.first_end + 255, w.t.kv_end) : w.t.kv_end;
 }
 
 // Tile rank and head of item `it`: groups of heads one after the other, within
@@ -208,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       auto load_item = [&](int64_t it) {
         int rank, head;
-        if (it >= items) return item_of(PfTile{0, 0, 0, 0, 0, 0, 1, 0}, -1);
+        if (it >= items) return item_of(PfTile{0, 0, 0, 0, 0, 0, 1, -1, {}}, -1);
         split_item(it, num_tiles, heads, groups, &rank, &head);
         return item_of(tiles[order[rank]], head);
       };
@@ -221,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t rb = mapa(bar(kBarItem + i % kSched), r), dst = mapa(smem_addr(&board[i % kSched]), r);
           mbar_arrive_expect_tx_cluster(rb, sizeof(Item));
 #pragma unroll
-          for (int c = 0; c < 3; ++c) st_async_v4(dst + 16 * c, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3], rb);
+          for (int c = 0; c < 4; ++c) st_async_v4(dst + 16 * c, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3], rb);
         }
       };
       Item w, w_next;
@@ -258,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (j == 0) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (!ok || (x == 1 && (w.shared || w.n1 == 0))) continue;
+              if (!ok || (x == 1 ? w.shared || w.n1 == 0 : w.n0 == 0)) continue;
               if (!(ok = mbar_spin(bar(kBarQFree + x), (q_use[x] & 1u) ^ 1u, abort_flag))) continue;
               ++q_use[x];
               if (cta == 0) mbar_arrive_expect_tx(bar(kBarQFull + x), 2 * kQBytes);
@@ -446,7 +446,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const int n = x ? w.n1 : w.n0, n1 = w.n1;
       const bool shared = w.shared != 0;
-      if (n == 0) continue;
+      // Where the row's sums go if this is a piece of a split tile.
+      const int part_row = w.t.part_row;
+      auto part = [&] { return static_cast<int64_t>(head - head0) * a.lay.part_rows + part_row + r; };
+      const bool split = part_row >= 0;
+      if (n == 0) {
+        if (x == 0 && n1 > 0) ++o1_use;
+        if (split && valid && !(x == 1 && shared))
+          reinterpret_cast<float2*>(a.ws + a.lay.part_stats)[part()] = make_float2(kNoMax, 0.f);
+        continue;
+      }
       // The row's range, relative to the first key of the stream's first step.
       const int stride = w.shared ? 2 * kPfKvTile : kPfKvTile;
       const int off = w.t.kv_begin + (w.shared ? kPfKvTile * x : 0);
@@ -570,7 +579,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (x == 0 && n1 > 0) ++o1_use;  // (phases of stream 1's barrier, waited for or not)
       tc_fence_after();
       if (any) {
-        const float inv = a.out_scale / l;  // every valid row attends itself: l > 0
+        // (every valid row attends itself: l > 0; a piece is scaled when joined)
+        const float inv = split ? 1.f : a.out_scale / l;
         f0 *= inv;
         f1 *= inv;
 #pragma unroll
@@ -587,7 +597,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(fmaf(__uint_as_float(o1[v]), f1, __uint_as_float(o[v])));
           }
-          if (valid) {
+          if (valid && split) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) st_global_v8(reinterpret_cast<float*>(a.ws + a.lay.part_o) + part() * kDimV + 32 * c + 8 * v, o + 8 * v);
+          } else if (valid) {
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
               uint32_t pk[8];
@@ -598,7 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (a.lse && valid) a.lse[out_row()] = (mx_ref * scale + log2f(l)) * 0.69314718055994531f;
+        if (split && valid) reinterpret_cast<float2*>(a.ws + a.lay.part_stats)[part()] = make_float2(mx_ref, l);
+        else if (a.lse && valid) a.lse[out_row()] = (mx_ref * scale + log2f(l)) * 0.69314718055994531f;
       }
       tc_fence_before();
       if (merge) {
@@ -623,7 +637,7 @@ cudaError_t launch_prefill_attn(const PrefillMaps& m, const PrefillArgs& a, int 
   if (e != cudaSuccess) return e;
   const int pairs = sm_count() / 2;
   if (pairs <= 0) return cudaErrorInvalidDevice;
-  const int64_t most = a.lay.max_tiles * heads;
+  const int64_t most = (a.lay.max_tiles + (pf_may_split(a.max_kv) ? kPfMostPieces : 0)) * heads;
   return launch_pdl(prefill_attn_kernel, dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs)), dim3(kThreads),
                     kSmemBytes, stream, m, a, head0, heads);
 }

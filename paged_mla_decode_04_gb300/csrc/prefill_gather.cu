@@ -48,6 +48,103 @@ __device__ __forceinline__ int64_t block_exclusive(int64_t x, int64_t* sh, int64
   return x + before - x0;
 }
 
+// Few items: cut tiles along the keys so that every cluster has work. With N(P)
+// pieces of at most P steps a head, all heads' pieces run in w waves if N(P) x
+// heads <= w x clusters, and take about w (P + kPieceSteps), kPieceSteps being what
+// an item costs beyond its steps. The best of up to four waves is taken if it beats
+// the uncut tiles by a tenth. Returns the number of tiles; all threads call it.
+constexpr int kPieceSteps = 6;   // measured: start-up, partial rows and joining, in steps
+constexpr int kLeastPiece = 3;   // steps
+constexpr int kMostWaves = 4;    // pieces a head fit in kPfMostPieces entries: heads >= 2, or waves <= 2
+
+__device__ int split_tiles(const PrefillArgs& a, PfTile* tiles, int nt, int64_t* sh) {
+  constexpr int kFew = kMostWaves * kPfPairs;
+  __shared__ int steps[kFew], found[kMostWaves];
+  const int heads = a.lay.heads;
+  int per = 0;
+  if (pf_may_split(a.max_kv) && static_cast<int64_t>(nt) * heads < kFew) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (static_cast<int>(threadIdx.x) < nt) steps[threadIdx.x] = pf_steps(tiles[threadIdx.x].kv_begin, tiles[threadIdx.x].kv_end);
+    __syncthreads();
+    int longest = 0, all = 0;
+    for (int i = lane; i < nt; i += 32) {
+      longest = max(longest, steps[i]);
+      all += steps[i] + kPieceSteps;
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (warp < kMostWaves) {  // a warp per number of waves: the least P that fits, 32 candidates at a time
+      const int room = min((warp + 1) * kPfPairs / heads, kPfMostPieces);  // pieces a head
+      int lo = kLeastPiece, hi = max(longest, kLeastPiece);
+      while (lo < hi && room > nt) {
+        const int gap = (hi - lo + 31) / 32, p = min(lo + lane * gap, hi);
+        int count = 0;
+        for (int i = 0; i < nt; ++i) count += max(1, (steps[i] + p - 1) / p);
+        const unsigned ok = __ballot_sync(0xffffffffu, count <= room);
+        const int first = ok ? __ffs(ok) - 1 : 32;
+        const int new_hi = min(lo + first * gap, hi);
+        lo = first > 0 ? min(lo + (first - 1) * gap + 1, new_hi) : lo;
+        hi = new_hi;
+      }
+      if (lane == 0) found[warp] = room > nt ? hi : longest;
+    }
+    __syncthreads();
+    const float whole = max(static_cast<float>(longest + kPieceSteps), 1.1f * all * heads / kPfPairs);
+    float least = 0.9f * whole;
+    for (int w = 0; w < kMostWaves; ++w) {
+      const int p = found[w];
+      const float t = static_cast<float>(w + 1) * (p + kPieceSteps);
+      if (t < least && p < longest) {
+        least = t;
+        per = p;
+      }
+    }
+  }
+  PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
+  if (threadIdx.x == 0) hd->num_split = hd->merge_rows = 0;
+  if (per == 0) return nt;
+  // (fewer than kMostWaves x kPfPairs tiles: one round of threads)
+  const int i = threadIdx.x;
+  PfTile t = {};
+  int n = 0, pieces = 1;
+  if (i < nt) {
+    t = tiles[i];
+    n = pf_steps(t.kv_begin, t.kv_end);
+    pieces = max(1, (n + per - 1) / per);
+  }
+  // Partial rows that would not fit leave their tiles whole.
+  int64_t rows = pieces > 1 ? static_cast<int64_t>(pieces) * t.rows : 0, total;
+  const int64_t row0 = block_exclusive(rows, sh, &total);
+  const bool cut = pieces > 1 && row0 + rows <= a.lay.part_rows;
+  // (room for the entries: pieces a head fit in kMostWaves waves of clusters, or
+  // in kPfMostPieces entries beyond the first of each)
+  int64_t extra = cut ? pieces - 1 : 0, split = cut ? 1 : 0, merged = cut ? t.rows : 0, extras, splits, merge_rows;
+  const int64_t to = nt + block_exclusive(extra, sh, &extras);
+  const int64_t at = block_exclusive(split, sh, &splits), merge_row = block_exclusive(merged, sh, &merge_rows);
+  if (cut) {
+    t.part_row = static_cast<int>(row0);
+    const int begin = t.kv_begin, end = t.kv_end;
+    for (int p = 0; p < pieces; ++p) {
+      t.kv_begin = begin + static_cast<int>(static_cast<int64_t>(n) * p / pieces) * kPfKvTile;
+      t.kv_end = p == pieces - 1 ? end : begin + static_cast<int>(static_cast<int64_t>(n) * (p + 1) / pieces) * kPfKvTile;
+      tiles[p == 0 ? i : to + p - 1] = t;
+      t.part_row += t.rows;
+    }
+    PfSplit& s = reinterpret_cast<PfSplit*>(a.ws + a.lay.splits)[at];
+    s.q_row = t.q_row;
+    s.rows = t.rows;
+    s.part_row = static_cast<int>(row0);
+    s.pieces = pieces;
+    s.merge_row = static_cast<int>(merge_row);
+  }
+  if (threadIdx.x == 0) {
+    hd->num_split = static_cast<int>(splits);
+    hd->merge_rows = static_cast<int>(merge_rows);
+  }
+  __syncthreads();
+  return nt + static_cast<int>(extras);
+}
+
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillArgs a) {
   __shared__ int64_t sh[32];
   pdl_launch_dependents();
@@ -99,7 +196,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
         t.kv_end = good ? t.first_end + t.rows - 1 : 0;
         t.kv_begin = good && a.window > 0 ? max(0, t.first_end - a.window) / kPfKvAlign * kPfKvAlign : 0;
         t.refused = good ? 0 : 1;
-        t.pad = 0;
+        t.part_row = -1;
+        t.pad[0] = t.pad[1] = t.pad[2] = t.pad[3] = 0;
         tiles[tile0 + k] = t;
       }
     }
@@ -111,12 +209,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   // short. The order within a class varies from call to call and changes nothing
   // but who computes a tile.
   __shared__ int most, bins[256];
-  const int nt = static_cast<int>(min(tiles_before, a.lay.max_tiles));
+  int nt = static_cast<int>(min(tiles_before, a.lay.max_tiles));
   int* order = reinterpret_cast<int*>(a.ws + a.lay.order);
   if (threadIdx.x < 256) bins[threadIdx.x] = 0;
   if (threadIdx.x == 0) most = 1;
   __syncthreads();  // (also: tiles are written)
   auto cost = [&](int i) { return pf_steps(tiles[i].kv_begin, tiles[i].kv_end); };
+  nt = split_tiles(a, tiles, nt, sh);
   for (int i = threadIdx.x; i < nt; i += kPlanThreads) atomicMax(&most, cost(i));
   __syncthreads();
   auto bin = [&](int i) { return 255 - static_cast<int>(static_cast<int64_t>(cost(i)) * 255 / most); };
@@ -218,6 +317,52 @@ __global__ void __launch_bounds__(32 * kGatherWarps) prefill_gather_kernel(const
   }
 }
 
+// Joins the pieces of split tiles: a warp per (row, head), four value dims a
+// lane. Each piece left its sums O relative to its own maximum m, and l.
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a, int head0, int heads) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const PfHeader* hd = reinterpret_cast<const PfHeader*>(a.ws);
+  const PfSplit* splits = reinterpret_cast<const PfSplit*>(a.ws + a.lay.splits);
+  const int lane = threadIdx.x & 31;
+  const int64_t units = static_cast<int64_t>(hd->merge_rows) * heads, step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += step) {
+    const int row = static_cast<int>(u / heads), head = static_cast<int>(u % heads);
+    int lo = 0, hi = hd->num_split;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (splits[mid].merge_row <= row) lo = mid;
+      else hi = mid;
+    }
+    const PfSplit s = splits[lo];
+    const int r = row - s.merge_row;
+    const int64_t first = static_cast<int64_t>(head) * a.lay.part_rows + s.part_row + r;
+    const float2* stats = reinterpret_cast<const float2*>(a.ws + a.lay.part_stats) + first;
+    const float4* part = reinterpret_cast<const float4*>(a.ws + a.lay.part_o) + first * (kDimV / 4) + lane;
+    float m = -3e38f;
+    for (int p = 0; p < s.pieces; ++p) m = fmaxf(m, stats[static_cast<int64_t>(p) * s.rows].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < s.pieces; ++p) {
+      const float2 st = stats[static_cast<int64_t>(p) * s.rows];
+      const float4 v = part[static_cast<int64_t>(p) * s.rows * (kDimV / 4)];
+      if (st.y == 0.f) continue;  // no key of this row (its sums are not written)
+      const float w = exp2f((st.x - m) * a.scale_log2);
+      l = fmaf(w, st.y, l);
+      o.x = fmaf(w, v.x, o.x);
+      o.y = fmaf(w, v.y, o.y);
+      o.z = fmaf(w, v.z, o.z);
+      o.w = fmaf(w, v.w, o.w);
+    }
+    const float inv = a.out_scale / l;
+    const int64_t out_row = (static_cast<int64_t>(s.q_row) + r) * a.num_heads + head0 + head;
+    reinterpret_cast<uint2*>(a.out)[out_row * (kDimV / 4) + lane] =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[out_row] = (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
 }  // namespace
 
 int sm_count() {
@@ -234,6 +379,10 @@ int sm_count() {
 
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t stream) {
   return launch_pdl(prefill_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+}
+
+cudaError_t launch_prefill_merge(const PrefillArgs& a, int head0, int heads, cudaStream_t stream) {
+  return launch_pdl(prefill_merge_kernel, dim3(152 * 4), dim3(256), 0, stream, a, head0, heads);
 }
 
 cudaError_t launch_prefill_gather(const PrefillArgs& a, cudaStream_t stream) {

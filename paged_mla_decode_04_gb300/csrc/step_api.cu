@@ -188,6 +188,7 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
   a.ws = static_cast<uint8_t*>(workspace);
   a.lay = mla::pf_layout(batch, q_rows, max_kv_tokens, per_pass);
   a.max_blocks = max_blocks;
+  a.max_kv = max_kv_tokens;
   a.batch = batch;
   a.q_rows = q_rows;
   a.num_heads = num_heads;
@@ -224,6 +225,7 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
     const int n = h0 + per_pass <= num_heads ? per_pass : num_heads - h0;
     e = mla::launch_prefill_expand(m, a, h0, n, st);
     if (e == cudaSuccess) e = mla::launch_prefill_attn(m, a, h0, n, st);
+    if (e == cudaSuccess && mla::pf_may_split(max_kv_tokens)) e = mla::launch_prefill_merge(a, h0, n, st);
   }
   return done(e);
 }

@@ -85,7 +85,21 @@ struct PfTile {
   int kv_end;     // end of the last row's range
   int first_end;  // end of row 0's range
   int refused;    // the request's lengths are bad: its rows are written as NaN
-  int pad;
+  // Where items are few, a tile runs as several over consecutive key steps, each
+  // of which leaves its rows' sums in the partial buffers.
+  int part_row;   // partial row (per head) of row 0, or -1: not split
+  int pad[4];
+};
+
+static_assert(sizeof(PfTile) == 48, "three 16-byte words");
+
+constexpr int kPfPairs = 76;         // SM pairs of the GPU: the clusters that run at once
+constexpr int kPfMostPieces = 2 * kPfPairs;  // pieces of all split tiles of a head beyond the first of each
+
+// A split tile: its pieces' partial rows follow each other, `rows` each. Row r of
+// it is row merge_row + r of all split tiles' rows.
+struct PfSplit {
+  int q_row, rows, part_row, pieces, merge_row, pad[3];
 };
 
 struct PfHeader {
@@ -93,7 +107,9 @@ struct PfHeader {
   int kv_rows;     // rows of the row buffer in use
   int num_tiles;
   int next_item;   // items of the current pass handed out beyond the first of each block
-  int pad[60];
+  int num_split;   // split tiles
+  int merge_rows;  // their rows
+  int pad[58];
 };
 
 // Key steps of a tile whose rows attend relative positions [begin, end).
@@ -102,7 +118,8 @@ __host__ __device__ inline int pf_steps(int begin, int end) {
 }
 
 struct PfLayout {
-  size_t requests, tiles, order, rows, keys, values, total;
+  size_t requests, tiles, order, splits, part_stats, part_o, rows, keys, values, total;
+  int64_t part_rows;    // partial rows of each head
   int64_t kv_capacity;  // rows of the row buffer
   int64_t max_tiles;
   int heads;            // heads whose keys and values fit
@@ -114,13 +131,23 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int heads) 
   L.heads = heads;
   L.kv_capacity = (max_kv + static_cast<int64_t>(batch) * kPfKvAlign + kPfKvTile - 1) / kPfKvTile * kPfKvTile;
   L.max_tiles = q_rows / kPfRows + batch;
+  // Partial rows: two tiles' rows for each pair of SMs, no more than the pieces of every row.
+  L.part_rows = 2ll * kPfPairs * kPfRows / heads;
+  if (L.part_rows > kPfMostPieces * q_rows) L.part_rows = kPfMostPieces * q_rows;
+  const int64_t entries = L.max_tiles + kPfMostPieces;
   size_t off = sizeof(PfHeader);
   L.requests = off;
   off = align_up(off + sizeof(PfRequest) * (static_cast<size_t>(batch) + 1), 256);
   L.tiles = off;
-  off = align_up(off + sizeof(PfTile) * static_cast<size_t>(L.max_tiles), 256);
+  off = align_up(off + sizeof(PfTile) * static_cast<size_t>(entries), 256);
   L.order = off;
-  off = align_up(off + sizeof(int) * static_cast<size_t>(L.max_tiles), 256);
+  off = align_up(off + sizeof(int) * static_cast<size_t>(entries), 256);
+  L.splits = off;
+  off = align_up(off + sizeof(PfSplit) * kPfMostPieces, 256);
+  L.part_stats = off;
+  off = align_up(off + 8 * static_cast<size_t>(L.part_rows) * heads, 1024);
+  L.part_o = off;
+  off = align_up(off + 4 * kDimV * static_cast<size_t>(L.part_rows) * heads, 1024);
   L.rows = off;
   off = align_up(off + static_cast<size_t>(L.kv_capacity) * kDimRow * 2, 1024);
   L.keys = off;
@@ -141,6 +168,7 @@ struct PrefillArgs {
   float* lse;
   uint8_t* ws;
   PfLayout lay;
+  int64_t max_kv;
   int max_blocks;
   int batch;
   int q_rows;
@@ -175,6 +203,10 @@ cudaError_t launch_prefill_gather(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_expand(const PrefillMaps& m, const PrefillArgs& a, int head0, int heads, cudaStream_t stream);
 // prefill_attn.cu
 cudaError_t launch_prefill_attn(const PrefillMaps& m, const PrefillArgs& a, int head0, int heads, cudaStream_t stream);
+// prefill_gather.cu: split tiles' partial sums joined
+cudaError_t launch_prefill_merge(const PrefillArgs& a, int head0, int heads, cudaStream_t stream);
+// Whether any tile may be split (its plan decides): too few keys for two pieces otherwise.
+__host__ __device__ inline bool pf_may_split(int64_t max_kv) { return max_kv > 6 * kPfKvTile; }
 // Streaming multiprocessors of the current device (0 on failure).
 int sm_count();
 

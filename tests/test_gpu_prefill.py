@@ -170,6 +170,30 @@ def test_many_requests(lib):
     Case(lib, ctx, new, heads=1, ps=16).run().check()
 
 
+@pytest.mark.parametrize("ctx,new,heads,window,fp8", [
+    ([9000], [1], 2, 0, False), ([9000], [130], 1, 0, True), ([5000], [256], 2, 0, False), ([7000], [257], 2, 0, False),
+    ([3000], [512], 3, 0, False), ([6000], [700], 2, 0, True), ([4000, 100, 2500], [20, 300, 513], 1, 0, False),
+    ([6000, 50], [300, 10], 2, 2500, False), ([0], [2500], 1, 0, False)])
+def test_few_items_are_cut_along_the_keys(lib, ctx, new, heads, window, fp8):
+    """Tiles whose keys several clusters share: all partial sums joined, rows before a piece's keys among them."""
+    c = Case(lib, ctx, new, heads=heads, window=window, fp8=fp8).run().check()
+    assert int(c.ws[:20].view(torch.int32)[4]) > 0 or heads * len(ctx) > 2  # (tiles were split)
+    out = c.out.clone()
+    c.run()
+    assert torch.equal(bits(c.out), bits(out))  # the same order of sums each time
+    b = Case(lib, ctx, new, heads=heads, window=window, fp8=fp8, heads_per_pass=1).run().check()
+    assert b.T == c.T
+
+
+def test_nan_in_cut_tiles(lib):
+    args = dict(ctx=[8000], new=[140], heads=1)
+    a = Case(lib, **args).run()
+    b = Case(lib, **args)
+    pos = 8050
+    b.pool.data[1].view(-1, 576)[int(b.table[0, pos // b.ps]) * b.ps + pos % b.ps, 9] = float("nan")
+    b.run()
+    assert torch.isnan(b.out[50:140].float()).all() and torch.equal(bits(a.out[:50]), bits(b.out[:50]))
+
 def test_no_new_tokens_and_empty_batch(lib):
     c = Case(lib, [10, 50], [0, 0]).run().check()
     assert (c.out == 7).all()
