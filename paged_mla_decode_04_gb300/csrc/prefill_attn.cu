@@ -461,9 +461,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int off = w.t.kv_begin + (w.shared ? kPfKvTile * x : 0);
       const int end = min(w.t.first_end + r, end_of(w, x)) - off;
       const int begin = a.window > 0 ? max(0, w.t.first_end + r - a.window) - off : -off;
-      // Steps [full0, full1) after the first have no position to mask in any row
-      // of the warp.
-      const int full0 = __reduce_max_sync(0xffffffffu, begin > 0 ? (begin + stride - 1) / stride : 1);
+      // Steps [full0, full1) have no position to mask in any row of the warp.
+      const int full0 = __reduce_max_sync(0xffffffffu, begin > 0 ? (begin + stride - 1) / stride : 0);
       const int full1 = __reduce_min_sync(0xffffffffu, end >= kPfKvTile ? (end - kPfKvTile) / stride + 1 : 0);
       float mx_ref = kNoMax, l = 0.f;
       for (int j = 0; j < n; ++j) {
@@ -472,9 +471,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (any) {
           tc_fence_after();
           uint32_t s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
-          tmem_wait_ld();
           // P against the reference maximum as it stands, the sum and maximum of
           // P beside it: no pass over S before the exponentials.
           float neg = -mx_ref * scale;
@@ -497,49 +493,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             top = fmaxf(top, top1);
           };
-          bool plain = j >= full0 && j < full1;
-          if (plain) {
-            weights();
-            plain = !__any_sync(0xffffffffu, top > kMostWeight);
-            if (!plain) {
+          const bool full = j >= full0 && j < full1;
+          for (bool anew = j == 0;; anew = true) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
-              tmem_wait_ld();
-            }
-          }
-          if (!plain) {
-            // The stream's first step, one with positions to mask, or one whose
-            // scores outgrow the reference: mask, take the maximum, rescale.
-            const int b0 = begin - j * stride, e0 = end - j * stride;
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
+            tmem_wait_ld();
+            if (!full) {  // positions outside [b0, e0) of this step
+              const int b0 = begin - j * stride, e0 = end - j * stride;
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c < b0 || c >= e0) s[c] = 0xff800000u;
-            float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+              for (int g = 0; g < 4; ++g) {
+                const uint32_t above = e0 >= 32 * g + 32 ? ~0u : (1u << max(e0 - 32 * g, 0)) - 1u;
+                const uint32_t below = b0 >= 32 * g + 32 ? ~0u : (1u << max(b0 - 32 * g, 0)) - 1u;
+                const uint32_t keep = above & ~below;
 #pragma unroll
-            for (int c = 0; c < 128; c += 4) {
-              mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-              mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-            }
-            mx = fmaxf(mx, mx1);
-            float alpha = 1.f;
-            if (mx > mx_ref + threshold) {
-              alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
-              l *= alpha;
-              mx_ref = mx;
-            }
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
-                tmem_st16(tO + 16 * c, o);
+                for (int c = 0; c < 32; ++c)
+                  if (!(keep & (1u << c))) s[32 * g + c] = 0xff800000u;
               }
             }
-            neg = -mx_ref * scale;
+            if (anew) {
+              // The stream's first step, or scores that outgrow the reference: take
+              // the maximum, rescale what there is.
+              float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+              for (int c = 0; c < 128; c += 4) {
+                mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+              }
+              mx = fmaxf(mx, mx1);
+              float alpha = 1.f;
+              if (mx > mx_ref + threshold) {
+                alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
+                l *= alpha;
+                mx_ref = mx;
+              }
+              if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 16 * c, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+                  tmem_st16(tO + 16 * c, o);
+                }
+              }
+              neg = -mx_ref * scale;
+            }
             weights();
+            if (anew || !__any_sync(0xffffffffu, top > kMostWeight)) break;
           }
           tmem_st32(tS, s);
           tmem_st32(tS + 32, s + 32);
