@@ -17,8 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla_decode.so")
 SOURCES = ["mla_api.cu", "kv_write.cu", "plan_merge.cu", "decode_sm103.cu", "uv_project.cu", "selftest.cu",
-           "step_api.cu", "step_tables.cu", "rope_write.cu", "prefill_gather.cu", "prefill_expand.cu", "prefill_attn.cu"]
-HEADERS = ["ptx.cuh", "mla_internal.h", "trace.cuh", "host_util.h", "step_internal.h", "ptx_prefill.cuh"]
+           "step_api.cu", "step_tables.cu", "rope_write.cu", "prefill_gather.cu", "prefill_expand.cu", "prefill_attn.cu",
+           "prefill_absorb.cu"]
+HEADERS = ["ptx.cuh", "mla_internal.h", "trace.cuh", "host_util.h", "step_internal.h", "ptx_prefill.cuh", "scan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

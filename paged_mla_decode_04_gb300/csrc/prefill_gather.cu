@@ -19,6 +19,7 @@
 
 #include "../../include/mla_decode.h"
 #include "ptx.cuh"
+#include "scan.cuh"
 #include "step_internal.h"
 
 namespace mla {
@@ -28,24 +29,10 @@ constexpr int kPlanThreads = 512;
 constexpr int kRowVecs = kDimRow * 2 / 16;  // 72
 
 __device__ __forceinline__ int64_t block_exclusive(int64_t x, int64_t* sh, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t x0 = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += u;
-  }
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-    const int64_t u = sh[w];
-    if (w < warp) before += u;
-    all += u;
-  }
-  __syncthreads();
-  *total = all;
-  return x + before - x0;
+  int64_t v[1] = {x}, t[1];
+  block_scan(v, t, sh);
+  *total = t[0];
+  return v[0];
 }
 
 // Few items: cut tiles along the keys so that every cluster has work. With N(P)
@@ -145,64 +132,222 @@ __device__ int split_tiles(const PrefillArgs& a, PfTile* tiles, int nt, int64_t*
   return nt + static_cast<int>(extras);
 }
 
+// The decode kernel's schedule for the groups of small requests: their 64-row
+// blocks, each group weighing kGroupCost more for its start and end, laid out in a
+// row and cut into equal ranges, one a cluster; a group across a cut leaves partial
+// sums that the decode's merge joins. All threads call it.
+constexpr int kGroupCost = 4;
+
+__device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t* sh) {
+  const PfLayout& lay = a.lay;
+  const PfGroup* gs = reinterpret_cast<const PfGroup*>(a.ws + lay.groups);
+  uint8_t* ws = a.ws + lay.decode;
+  WsHeader* hd = reinterpret_cast<WsHeader*>(ws);
+  WorkItem* items = reinterpret_cast<WorkItem*>(ws + lay.decode_lay.items);
+  int* cstart = reinterpret_cast<int*>(ws + lay.decode_lay.cluster_start);
+  SplitRequest* split = reinterpret_cast<SplitRequest*>(ws + lay.decode_lay.split);
+  const int tid = threadIdx.x, step = blockDim.x;
+  auto first_token = [&](const PfGroup& g) { return a.window > 0 ? max(0, g.first + 1 - a.window) : 0; };
+  auto blocks_of = [&](const PfGroup& g) {
+    return (g.first + g.tokens - 1) / kBlockTokens - first_token(g) / kBlockTokens + 1;
+  };
+  int64_t total = 0;
+  for (int i0 = 0; i0 < groups; i0 += step) {
+    int64_t sum;
+    block_exclusive(i0 + tid < groups ? blocks_of(gs[i0 + tid]) + kGroupCost : 0, sh, &sum);
+    total += sum;
+  }
+  const int64_t clusters = max(static_cast<int64_t>(1), min(total, static_cast<int64_t>(a.clusters)));
+  auto cut = [&](int64_t c) { return c * total / clusters; };  // first unit of cluster c
+  auto cluster_of = [&](int64_t x) { return ((x + 1) * clusters + total - 1) / total - 1; };
+  int64_t carry[4] = {0, 0, 0, 0};  // units, items, partial slots, split groups
+  for (int i0 = 0; i0 < groups; i0 += step) {
+    const int i = i0 + tid;
+    PfGroup g = {};
+    int n = 0;
+    if (i < groups) {
+      g = gs[i];
+      n = blocks_of(g);
+    }
+    int64_t units;
+    const int64_t off = carry[0] + block_exclusive(n ? n + kGroupCost : 0, sh, &units) + kGroupCost;
+    const int64_t cf = n ? cluster_of(off) : 0, cl = n ? cluster_of(off + n - 1) : -1;
+    const int64_t pieces = cl - cf + 1;
+    int64_t v[3] = {pieces, pieces > 1 ? pieces : 0, pieces > 1 ? 1 : 0}, sums[3];
+    block_scan(v, sums, sh);
+    for (int64_t k = 0; k < pieces; ++k) {
+      WorkItem w;
+      const int64_t lo = max(off, cut(cf + k)), hi = min(off + n, cut(cf + k + 1));
+      const int blk0 = first_token(g) / kBlockTokens;
+      w.b = i;
+      w.blk_begin = blk0 + static_cast<int>(lo - off);
+      w.blk_end = blk0 + static_cast<int>(hi - off);
+      w.slot = pieces > 1 ? static_cast<int>(carry[2] + v[1] + k) : -1;
+      w.tok_lo = first_token(g);
+      w.tok_hi = g.first + lay.group_tokens;  // (as if the group were full: its rows count from here)
+      w.cluster = static_cast<int>(cf + k);
+      w.row0 = 0;
+      items[carry[1] + v[0] + k] = w;
+    }
+    if (pieces > 1) {
+      SplitRequest r;
+      r.b = i;
+      r.num_splits = static_cast<int>(pieces);
+      r.first_partial = static_cast<int>(carry[2] + v[1]);
+      r.row0 = 0;
+      split[carry[3] + v[2]] = r;
+    }
+    carry[0] += units;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) carry[k + 1] += sums[k];
+  }
+  __syncthreads();
+  const int num_items = static_cast<int>(carry[1]);
+  for (int c = tid; c <= a.clusters; c += step) {
+    int lo = 0, hi = num_items;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (items[mid].cluster < c) lo = mid + 1;
+      else hi = mid;
+    }
+    cstart[c] = lo;
+  }
+  if (tid == 0) {
+    hd->status = 0;
+    hd->batch = lay.max_groups;
+    hd->num_heads = a.num_heads;
+    hd->q_len = lay.group_tokens;
+    hd->page_size = kBlockTokens;
+    hd->window = a.window;
+    hd->num_clusters = static_cast<int>(clusters);
+    hd->total_blocks = static_cast<int>(total);
+    hd->num_items = num_items;
+    hd->num_partials = static_cast<int>(carry[2]);
+    hd->num_split = static_cast<int>(carry[3]);
+    hd->schedule = kScheduleCut;
+    hd->planned = 1;
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillArgs a) {
-  __shared__ int64_t sh[32];
+  __shared__ int64_t sh[32 * 5];
   pdl_launch_dependents();
   pdl_wait();
   PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
   PfRequest* reqs = reinterpret_cast<PfRequest*>(a.ws + a.lay.requests);
   PfTile* tiles = reinterpret_cast<PfTile*>(a.ws + a.lay.tiles);
-  int64_t rows_before = 0, tiles_before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
-    const int b = b0 + threadIdx.x;
-    int64_t len = 0, n = 0, q0 = 0, lo = 0;
-    bool ok = true;
-    if (b < a.batch) {
-      len = a.context_lens[b];
-      q0 = a.q_indptr[b];
-      n = a.q_indptr[b + 1] - q0;
-      // Row pointers outside q leave nothing that could be written.
-      if (q0 < 0 || n < 0 || q0 + n > a.q_rows) {
-        n = 0;
-        ok = false;
-      }
-      const int64_t nb = a.page_indptr ? a.page_indptr[b + 1] - a.page_indptr[b] : a.max_blocks;
-      if (len < 0 || len + n > nb * a.page_size || len + n > INT32_MAX) ok = ok && n == 0;
-      lo = a.window > 0 ? max(static_cast<int64_t>(0), len + 1 - a.window) : 0;
+  PfGroup* groups = reinterpret_cast<PfGroup*>(a.ws + a.lay.groups);
+  const bool absorb = a.lay.absorb != 0;
+  const int per_group = a.lay.group_tokens;
+  // Sums over the requests so far: rows of the expanded ones, rows of the small ones,
+  // requests that are not small, tiles, groups. With small requests a first pass
+  // finds where their rows start, after all others'.
+  int64_t sum[5] = {0, 0, 0, 0, 0}, small_start = 0, small_first = 0;
+  for (int pass = absorb ? 0 : 1; pass < 2; ++pass) {
+    if (pass == 1) {
+      small_start = (sum[0] + 255) / 256 * 256;
+      small_first = sum[2];
     }
-    const int64_t want = ok && n > 0 ? len + n - lo : 0;
-    const int64_t span = (want + kPfKvAlign - 1) / kPfKvAlign * kPfKvAlign;
-    int64_t round_rows, round_tiles;
-    const int64_t base = rows_before + block_exclusive(span, sh, &round_rows);
-    bool fits = base + span <= a.lay.kv_capacity;
-    const int64_t nt = (n + kPfRows - 1) / kPfRows;
-    const int64_t tile0 = tiles_before + block_exclusive(nt, sh, &round_tiles);
-    if (b < a.batch) {
-      const bool good = ok && fits;
-      if (!good) atomicOr(&hd->status, MLA_STATUS_BAD_LENGTH);
-      PfRequest r;
-      r.base = static_cast<int>(min(base, a.lay.kv_capacity));
-      r.rows = good ? static_cast<int>(want) : 0;
-      r.lo = static_cast<int>(lo);
-      r.pad = 0;
-      reqs[b] = r;
-      for (int64_t k = 0; k < nt && tile0 + k < a.lay.max_tiles; ++k) {
-        PfTile t;
-        const int64_t i0 = k * kPfRows;
-        t.q_row = static_cast<int>(q0 + i0);
-        t.rows = static_cast<int>(min(n - i0, static_cast<int64_t>(kPfRows)));
-        t.base = r.base;
-        t.first_end = good ? static_cast<int>(len + i0 + 1 - lo) : 0;
-        t.kv_end = good ? t.first_end + t.rows - 1 : 0;
-        t.kv_begin = good && a.window > 0 ? max(0, t.first_end - a.window) / kPfKvAlign * kPfKvAlign : 0;
-        t.refused = good ? 0 : 1;
-        t.part_row = -1;
-        t.pad[0] = t.pad[1] = t.pad[2] = t.pad[3] = 0;
-        tiles[tile0 + k] = t;
+    int64_t wished = 0, spanned = 0;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) sum[k] = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+      const int b = b0 + threadIdx.x;
+      int64_t len = 0, n = 0, q0 = 0, lo = 0;
+      bool ok = true;
+      if (b < a.batch) {
+        len = a.context_lens[b];
+        q0 = a.q_indptr[b];
+        n = a.q_indptr[b + 1] - q0;
+        // Row pointers outside q leave nothing that could be written.
+        if (q0 < 0 || n < 0 || q0 + n > a.q_rows) {
+          n = 0;
+          ok = false;
+        }
+        const int64_t nb = a.page_indptr ? a.page_indptr[b + 1] - a.page_indptr[b] : a.max_blocks;
+        if (len < 0 || len + n > nb * a.page_size || len + n > INT32_MAX) ok = ok && n == 0;
+        lo = a.window > 0 ? max(static_cast<int64_t>(0), len + 1 - a.window) : 0;
       }
+      const int64_t want = ok && n > 0 ? len + n - lo : 0;
+      bool small = false;
+      int64_t ng = 0;
+      if (absorb) {
+        ng = want > 0 && n <= kPfSmallTokens ? (n + per_group - 1) / per_group : 0;
+        int64_t round;
+        const int64_t before = wished + block_exclusive(ng, sh, &round);
+        small = ng > 0 && before + ng <= a.lay.max_groups;
+        wished += round;
+      }
+      const int align = small ? kBlockTokens : kPfKvAlign;
+      const int64_t span = (want + align - 1) / align * align;
+      int64_t round;
+      const int64_t upto = spanned + block_exclusive(span, sh, &round) + span;
+      spanned += round;
+      const bool good = ok && upto + (absorb ? 256 : 0) <= a.lay.kv_capacity;
+      small = small && good;
+      const int64_t nt = small ? 0 : (n + kPfRows - 1) / kPfRows;
+      int64_t v[5] = {small || !good ? 0 : span, small ? span : 0, b < a.batch && !small ? 1 : 0, nt, small ? ng : 0}, total[5];
+      block_scan(v, total, sh);
+      if (pass == 1 && b < a.batch) {
+        if (!good) atomicOr(&hd->status, MLA_STATUS_BAD_LENGTH);
+        PfRequest r;
+        r.base = static_cast<int>(small ? small_start + sum[1] + v[1] : sum[0] + v[0]);
+        r.rows = good ? static_cast<int>(want) : 0;
+        r.lo = static_cast<int>(lo);
+        r.b = b;
+        // (v[2] counts the others before this one: the rest before it are small)
+        reqs[small ? small_first + b - (sum[2] + v[2]) : sum[2] + v[2]] = r;
+        const int64_t tile0 = sum[3] + v[3];
+        for (int64_t k = 0; k < nt && tile0 + k < a.lay.max_tiles; ++k) {
+          PfTile t;
+          const int64_t i0 = k * kPfRows;
+          t.q_row = static_cast<int>(q0 + i0);
+          t.rows = static_cast<int>(min(n - i0, static_cast<int64_t>(kPfRows)));
+          t.base = r.base;
+          t.first_end = good ? static_cast<int>(len + i0 + 1 - lo) : 0;
+          t.kv_end = good ? t.first_end + t.rows - 1 : 0;
+          t.kv_begin = good && a.window > 0 ? max(0, t.first_end - a.window) / kPfKvAlign * kPfKvAlign : 0;
+          t.refused = good ? 0 : 1;
+          t.part_row = -1;
+          t.pad[0] = t.pad[1] = t.pad[2] = t.pad[3] = 0;
+          tiles[tile0 + k] = t;
+        }
+        if (small)
+          for (int64_t k = 0; k < ng; ++k) {
+            PfGroup g = {};
+            g.base = r.base;
+            g.first = static_cast<int>(len + k * per_group - lo);
+            g.q_row = static_cast<int>(q0 + k * per_group);
+            g.tokens = static_cast<int>(min(n - k * per_group, static_cast<int64_t>(per_group)));
+            g.pages = (g.first + g.tokens - 1) / kBlockTokens + 1;
+            groups[sum[4] + v[4] + k] = g;
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < 5; ++k) sum[k] += total[k];
     }
-    rows_before += round_rows;
-    tiles_before += round_tiles;
+  }
+  const int64_t tiles_before = sum[3];
+  if (absorb) {
+    __syncthreads();  // groups are written
+    const int count = static_cast<int>(sum[4]);
+    int32_t* indptr = reinterpret_cast<int32_t*>(a.ws + a.lay.group_indptr);
+    int64_t pages = 0;
+    for (int i0 = 0; i0 < count; i0 += kPlanThreads) {
+      const int i = i0 + threadIdx.x;
+      int64_t round;
+      const int64_t at = pages + block_exclusive(i < count ? groups[i].pages : 0, sh, &round);
+      if (i < count) {
+        groups[i].page0 = static_cast<int>(at);
+        indptr[i] = static_cast<int>(at);
+      }
+      pages += round;
+    }
+    if (threadIdx.x == 0) {
+      indptr[count] = static_cast<int>(pages);
+      hd->num_groups = count;
+    }
+    schedule_groups(a, count, sh);
   }
   // Tiles by falling cost (key steps, in 256 classes of the most expensive
   // one's): blocks draw them in this order, so that what is drawn last is
@@ -227,9 +372,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   __syncthreads();
   for (int i = threadIdx.x; i < nt; i += kPlanThreads) order[atomicAdd(&bins[bin(i)], 1)] = i;
   if (threadIdx.x == 0) {
-    const int64_t used = min(rows_before, a.lay.kv_capacity);
-    reqs[a.batch] = {static_cast<int>(used), 0, 0, 0};
-    hd->kv_rows = static_cast<int>(used);
+    hd->kv_rows = static_cast<int>(sum[0]);
+    hd->all_rows = static_cast<int>(absorb && sum[1] > 0 ? small_start + sum[1] : sum[0]);
     hd->num_tiles = nt;
     if (tiles_before > a.lay.max_tiles) atomicOr(&hd->status, MLA_STATUS_BAD_LENGTH);
   }
@@ -267,8 +411,17 @@ __global__ void __launch_bounds__(32 * kGatherWarps) prefill_gather_kernel(const
   PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
   const PfRequest* reqs = reinterpret_cast<const PfRequest*>(a.ws + a.lay.requests);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int used = hd->kv_rows;
+  const int used = hd->all_rows;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (a.lay.absorb) {  // page lists of the groups: their rows lie one after the other
+    const PfGroup* groups = reinterpret_cast<const PfGroup*>(a.ws + a.lay.groups);
+    int32_t* pages = reinterpret_cast<int32_t*>(a.ws + a.lay.group_pages);
+    const int num_groups = hd->num_groups;
+    for (int g = blockIdx.x * kGatherWarps + warp; g < num_groups; g += gridDim.x * kGatherWarps) {
+      const PfGroup p = groups[g];
+      for (int j = lane; j < p.pages; j += 32) pages[p.page0 + j] = p.base / kBlockTokens + j;
+    }
+  }
   for (int64_t run = blockIdx.x; run * kPfKvAlign < used; run += gridDim.x) {
     const int row0 = static_cast<int>(run) * kPfKvAlign;
     int lo = 0, hi = a.batch;  // the last request with base <= row0
@@ -278,8 +431,9 @@ __global__ void __launch_bounds__(32 * kGatherWarps) prefill_gather_kernel(const
       else hi = mid;
     }
     const PfRequest r = reqs[lo];
-    const int nb = a.page_indptr ? a.page_indptr[lo + 1] - a.page_indptr[lo] : a.max_blocks;
-    const int32_t* ids = a.page_indptr ? a.page_ids + a.page_indptr[lo] : a.page_ids + static_cast<int64_t>(lo) * a.max_blocks;
+    const int b = r.b;
+    const int nb = a.page_indptr ? a.page_indptr[b + 1] - a.page_indptr[b] : a.max_blocks;
+    const int32_t* ids = a.page_indptr ? a.page_ids + a.page_indptr[b] : a.page_ids + static_cast<int64_t>(b) * a.max_blocks;
 #pragma unroll
     for (int k = 0; k < kPfKvAlign / kGatherWarps; ++k) {
       const int row = row0 + warp + k * kGatherWarps;

@@ -34,10 +34,56 @@ bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], co
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Small requests through the decode kernel: their queries into the latent space,
+// one decode over the gathered rows as its pool (pages of 64 rows, a request per
+// row group), the result out of it.
+int attend_small(const mla::PrefillMaps& m, const mla::PrefillArgs& a, const void* q, cudaStream_t st) {
+  const mla::PfLayout& lay = a.lay;
+  const uint64_t rows = static_cast<uint64_t>(lay.kv_capacity), h = a.num_heads;
+  const uint64_t q_rows = static_cast<uint64_t>(lay.max_groups) * mla::kGroupRows;
+  constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  uint8_t *pool = a.ws + lay.rows, *qs = a.ws + lay.q_latent, *out = a.ws + lay.latent;
+  CUtensorMap maps[5], latent;
+  if (!make_map_2d(&maps[0], bf16, pool, rows, mla::kDimRow, mla::kDimRow * 2, 64, 64) ||
+      !make_map_2d(&maps[1], bf16, pool, rows, mla::kDimRow, mla::kDimRow * 2, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_map_2d(&maps[2], bf16, qs, q_rows, mla::kDimRow, mla::kDimRow * 2, 64, 128) ||
+      !make_map_2d(&maps[3], bf16, qs, q_rows, mla::kDimRow, mla::kDimRow * 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_map_3d(&maps[4], pool, {64, rows, 8}, {mla::kDimRow * 2ull, 128}, {64, 64, 4}) ||
+      !make_map_3d(&latent, out, {mla::kDimCkv, h, static_cast<uint64_t>(lay.max_groups) * lay.group_tokens},
+                   {mla::kDimCkv * 2ull, h * mla::kDimCkv * 2ull}, {64, 1, 128}))
+    return MLA_ERR_CUDA;
+  mla::DecodeArgs d = {};
+  d.pool = pool;
+  d.page_indptr = reinterpret_cast<const int32_t*>(a.ws + lay.group_indptr);
+  d.page_ids = reinterpret_cast<const int32_t*>(a.ws + lay.group_pages);
+  d.out = out;
+  d.lse = reinterpret_cast<float*>(a.ws + lay.latent_lse);
+  d.ws = a.ws + lay.decode;
+  d.lay = lay.decode_lay;
+  d.batch = lay.max_groups;
+  d.num_heads = a.num_heads;
+  d.q_len = lay.group_tokens;
+  d.rows = d.group_rows = mla::kGroupRows;
+  d.groups = 1;
+  d.page_size = mla::kBlockTokens;
+  d.window = a.window;
+  d.num_pages = static_cast<int>(rows / mla::kBlockTokens);
+  d.num_layers = 1;
+  d.dtype = MLA_DTYPE_BF16;
+  d.kv_scale = 1.f;
+  d.scale_log2 = a.scale_log2;
+  d.out_scale = a.out_scale;
+  cudaError_t e = mla::launch_prefill_q_latent(m.w_uk, a, q, st);
+  if (e == cudaSuccess) e = mla::launch_decode(maps, d, a.clusters, st);
+  if (e == cudaSuccess) e = mla::launch_merge(d, a.clusters, st);
+  if (e == cudaSuccess) e = mla::launch_prefill_v_latent(latent, m.w_uv, a, st);
+  return done(e);
+}
+
 bool prefill_sizes_ok(int batch, int q_rows, int64_t max_kv, int heads) {
   if (batch < 0 || q_rows < 0 || max_kv < 0 || heads < 1 || heads > 1024) return false;
   if (static_cast<int64_t>(q_rows) * heads >= (1ll << 31)) return false;
-  return max_kv + static_cast<int64_t>(batch) * mla::kPfKvAlign + mla::kPfKvTile < (1ll << 31);
+  return max_kv + static_cast<int64_t>(batch) * mla::kBlockTokens + 512 < (1ll << 31);
 }
 
 }  // namespace
@@ -146,13 +192,13 @@ size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, 
   if (!prefill_sizes_ok(batch, q_rows, max_kv_tokens, num_heads) || heads_per_pass < 0) return 0;
   int h = heads_per_pass;
   if (h == 0) {
-    const mla::PfLayout one = mla::pf_layout(batch, q_rows, max_kv_tokens, 1);
+    const mla::PfLayout one = mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, 1);
     const size_t per_head = static_cast<size_t>(one.kv_capacity) * (mla::kDimNope + mla::kDimV) * 2;
     h = per_head * num_heads <= kExpandedBytes ? num_heads : static_cast<int>(kExpandedBytes / per_head);
     if (h < 1) h = 1;
   }
   if (h > num_heads) h = num_heads;
-  return mla::pf_layout(batch, q_rows, max_kv_tokens, h).total;
+  return mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, h).total;
 }
 
 int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t* q_indptr, const int32_t* page_indptr,
@@ -170,7 +216,7 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
   int lo = 0, hi = num_heads;  // the most heads whose keys and values fit
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (mla::pf_layout(batch, q_rows, max_kv_tokens, mid).total <= workspace_bytes) lo = mid;
+    if (mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, mid).total <= workspace_bytes) lo = mid;
     else hi = mid - 1;
   }
   if (lo == 0) return MLA_ERR_WORKSPACE;
@@ -186,7 +232,7 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
   a.out = out;
   a.lse = lse;
   a.ws = static_cast<uint8_t*>(workspace);
-  a.lay = mla::pf_layout(batch, q_rows, max_kv_tokens, per_pass);
+  a.lay = mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, per_pass);
   a.max_blocks = max_blocks;
   a.max_kv = max_kv_tokens;
   a.batch = batch;
@@ -219,8 +265,17 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
       !make_map_2d(&m.w_uv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w_uv, h * mla::kDimCkv, mla::kDimV, mla::kDimV * 2, 64, 64))
     return MLA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.lay.absorb) {
+    const int c = mla::decode_max_active_clusters();
+    if (c <= 0) return MLA_ERR_CUDA;
+    a.clusters = c < mla::kPfPairs ? c : mla::kPfPairs;
+  }
   cudaError_t e = mla::launch_prefill_plan(a, st);
   if (e == cudaSuccess) e = mla::launch_prefill_gather(a, st);
+  if (e == cudaSuccess && a.lay.absorb) {
+    const int rc = attend_small(m, a, q, st);
+    if (rc != MLA_OK) return rc;
+  }
   for (int h0 = 0; h0 < num_heads && e == cudaSuccess; h0 += per_pass) {
     const int n = h0 + per_pass <= num_heads ? per_pass : num_heads - h0;
     e = mla::launch_prefill_expand(m, a, h0, n, st);

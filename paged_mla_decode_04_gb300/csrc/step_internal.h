@@ -70,8 +70,9 @@ constexpr int kPfKvTile = 128;    // key rows per step
 // Request b as the plan sees it. Gathered positions are [lo, lo + rows); they
 // sit at rows base .. of the workspace's row buffer, followed by zero rows up
 // to a multiple of kPfKvAlign.
+// Requests lie in the order of their rows: expanded ones first, then small ones.
 struct PfRequest {
-  int base, rows, lo, pad;
+  int base, rows, lo, b;
 };
 
 // One query tile of one request, the same for every head. Positions below are
@@ -102,14 +103,34 @@ struct PfSplit {
   int q_row, rows, part_row, pieces, merge_row, pad[3];
 };
 
+// Requests with few new tokens are attended in the latent space (the absorbed
+// form: 2,176 flops a pair and head instead of 640, but no keys and values to
+// make) by the decode kernel, in row groups of up to kGroupRows (token, head)
+// rows that are requests of their own to it. Their rows start at multiples of its
+// 64-token blocks, so that the row buffer is its pool, with pages of 64 rows.
+constexpr int kPfSmallTokens = 64;
+constexpr int kPfSmallRows = 1 << 17;  // (token, head) rows of all small requests at most
+
+struct PfGroup {
+  int base;      // workspace row of the request's relative position 0
+  int first;     // relative position of the group's first token
+  int q_row;     // its row of q and out
+  int tokens;    // 1 .. tokens a full group has
+  int page0;     // first entry of its page list
+  int pages;
+  int pad[2];
+};
+
 struct PfHeader {
   int status;  // sticky MLA_STATUS_* bits
-  int kv_rows;     // rows of the row buffer in use
+  int kv_rows;     // rows of the row buffer whose keys and values are made
   int num_tiles;
   int next_item;   // items of the current pass handed out beyond the first of each block
   int num_split;   // split tiles
   int merge_rows;  // their rows
-  int pad[58];
+  int all_rows;    // rows of the row buffer in use
+  int num_groups;
+  int pad[56];
 };
 
 // Key steps of a tile whose rows attend relative positions [begin, end).
@@ -120,16 +141,30 @@ __host__ __device__ inline int pf_steps(int begin, int end) {
 struct PfLayout {
   size_t requests, tiles, order, splits, part_stats, part_o, rows, keys, values, total;
   int64_t part_rows;    // partial rows of each head
+  // Small requests in the latent space (absorb: whether the call may have any).
+  size_t groups, group_indptr, group_pages, q_latent, latent, latent_lse, decode;
+  int absorb;
+  int group_tokens;     // tokens of a full group
+  int max_groups;
+  WsLayout decode_lay;
   int64_t kv_capacity;  // rows of the row buffer
   int64_t max_tiles;
   int heads;            // heads whose keys and values fit
 };
 
-// Workspace regions for `heads` heads at a time.
-inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int heads) {
-  PfLayout L;
+// Calls whose keys and values of all heads would take more than about 30 us to make
+// look for small requests (the five launches of that path cost about 15).
+inline bool pf_may_absorb(int64_t max_kv, int num_heads) {
+  return (num_heads == 16 || num_heads == 32 || num_heads == 64 || num_heads == 128) && max_kv * num_heads >= 200000;
+}
+
+// Workspace regions for `heads` of num_heads heads at a time.
+inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_heads, int heads) {
+  PfLayout L = {};
   L.heads = heads;
-  L.kv_capacity = (max_kv + static_cast<int64_t>(batch) * kPfKvAlign + kPfKvTile - 1) / kPfKvTile * kPfKvTile;
+  L.absorb = pf_may_absorb(max_kv, num_heads);
+  const int64_t slack = static_cast<int64_t>(batch) * (L.absorb ? kBlockTokens : kPfKvAlign) + (L.absorb ? 256 : 0);
+  L.kv_capacity = (max_kv + slack + kPfKvTile - 1) / kPfKvTile * kPfKvTile;
   L.max_tiles = q_rows / kPfRows + batch;
   // Partial rows: two tiles' rows for each pair of SMs, no more than the pieces of every row.
   L.part_rows = 2ll * kPfPairs * kPfRows / heads;
@@ -154,6 +189,30 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int heads) 
   off = align_up(off + static_cast<size_t>(L.kv_capacity) * kDimNope * 2 * heads, 1024);
   L.values = off;
   off = align_up(off + static_cast<size_t>(L.kv_capacity) * kDimV * 2 * heads, 1024);
+  if (L.absorb) {
+    L.group_tokens = kGroupRows / num_heads;
+    const int64_t per_request = (kPfSmallTokens + L.group_tokens - 1) / L.group_tokens;
+    int64_t g = (q_rows + L.group_tokens - 1) / L.group_tokens + batch;
+    if (g > per_request * batch) g = per_request * batch;
+    if (g > kPfSmallRows / kGroupRows) g = kPfSmallRows / kGroupRows;
+    L.max_groups = static_cast<int>(g);
+    const size_t rows = static_cast<size_t>(g) * kGroupRows;
+    L.groups = off;
+    off = align_up(off + sizeof(PfGroup) * g, 256);
+    L.group_indptr = off;
+    off = align_up(off + sizeof(int32_t) * (g + 1), 256);
+    L.group_pages = off;
+    off = align_up(off + sizeof(int32_t) * (static_cast<size_t>(L.kv_capacity / kBlockTokens) * per_request + g), 1024);
+    L.q_latent = off;
+    off = align_up(off + rows * kDimRow * 2, 1024);
+    L.latent = off;
+    off = align_up(off + rows * kDimCkv * 2, 1024);
+    L.latent_lse = off;
+    off = align_up(off + rows * 4, 1024);
+    L.decode = off;
+    L.decode_lay = ws_layout(L.max_groups, kGroupRows, kPfPairs);
+    off = align_up(off + L.decode_lay.total, 1024);
+  }
   L.total = off;
   return L;
 }
@@ -178,6 +237,7 @@ struct PrefillArgs {
   int layer;
   int dtype;
   int window;
+  int clusters;      // of the decode kernel (small requests)
   float scale_log2;  // softmax_scale * log2(e) (* kv_scale for fp8 pools)
   float out_scale;   // 1, or kv_scale for fp8 pools
 };
@@ -207,6 +267,10 @@ cudaError_t launch_prefill_attn(const PrefillMaps& m, const PrefillArgs& a, int 
 cudaError_t launch_prefill_merge(const PrefillArgs& a, int head0, int heads, cudaStream_t stream);
 // Whether any tile may be split (its plan decides): too few keys for two pieces otherwise.
 __host__ __device__ inline bool pf_may_split(int64_t max_kv) { return max_kv > 6 * kPfKvTile; }
+// prefill_absorb.cu: small requests' queries into the latent space, and their
+// attention output out of it
+cudaError_t launch_prefill_q_latent(const CUtensorMap& w_uk, const PrefillArgs& a, const void* q, cudaStream_t stream);
+cudaError_t launch_prefill_v_latent(const CUtensorMap& latent, const CUtensorMap& w_uv, const PrefillArgs& a, cudaStream_t stream);
 // Streaming multiprocessors of the current device (0 on failure).
 int sm_count();
 

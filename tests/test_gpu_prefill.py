@@ -82,7 +82,11 @@ class Case:
         vals, table = self.values(), self.table.cpu().numpy()
         return step_ref.prefill(lambda b, at: vals[table[b][at // self.ps], at % self.ps], f64(self.q),
                                 self.indptr.cpu().numpy(), self.ctx.cpu().numpy(), f64(self.w_uk), f64(self.w_uv),
-                                self.scale, self.window)
+                                self.scale, self.window, lambda n: self.latent() and n <= 64)
+
+    def latent(self):
+        """Calls of this size attend requests of up to 64 new tokens in the latent space."""
+        return self.heads in (16, 32, 64, 128) and self.max_kv * self.heads >= 200000
 
     def check(self, norm=6e-3, status=0):
         ref, lse, tol, tol_lse = self.reference()
@@ -362,6 +366,100 @@ def test_graph_replay_with_changed_lengths(lib):
         torch.cuda.synchronize()
         c.check()
 
+
+@pytest.mark.parametrize("heads,ctx,new,window,fp8", [
+    (16, [4000, 3000, 5000, 100, 2000], [1, 64, 7, 300, 65], 0, False),
+    (16, [4000, 3000, 5000, 100, 2000], [1, 64, 9, 300, 65], 0, True),
+    (16, [9000, 63, 64, 0, 4000], [8, 1, 64, 40, 16], 0, False),
+    (16, [9000, 3000, 4500, 0, 4000], [33, 700, 5, 64, 2], 3500, False),
+    (16, [9000, 3000, 4500, 5000, 200], [33, 12, 5, 64, 2], 70, False),
+    (32, [2500, 1, 3900], [10, 64, 3], 0, False),
+    (64, [1100, 2100], [5, 64], 0, True),
+    (128, [900, 800, 10], [3, 130, 64], 0, False),
+    (128, [1700], [1], 0, False)])
+def test_small_requests_in_the_latent_space(lib, heads, ctx, new, window, fp8):
+    """Few new tokens over long caches, alone and beside chunks; every token group, partly filled ones among them."""
+    c = Case(lib, ctx, new, heads=heads, window=window, fp8=fp8, seed=heads, spare_kv=0 if not window else 20000)
+    assert c.latent()
+    c.run().check()
+    assert int(c.ws[:32].view(torch.int32)[7]) > 0
+    out = c.out.clone()
+    c.run()
+    assert torch.equal(bits(out), bits(c.out))
+
+
+def test_small_requests_with_csr_and_passes_and_no_lse(lib):
+    args = dict(ctx=[4500, 3000, 5000, 100], new=[1, 64, 7, 300], heads=16)
+    a = Case(lib, **args).run().check()
+    b = Case(lib, **args, csr=True, heads_per_pass=3)
+    assert a.latent()
+    b.run(lse=None)
+    assert torch.equal(bits(a.out[:72]), bits(b.out[:72])) and (b.lse == 7).all()
+    b.run().check()  # (heads a pass may cut the chunk's keys elsewhere)
+
+
+def test_many_small_requests_past_the_room_for_them(lib):
+    """More groups than the latent form has room for: the others are expanded."""
+    n = 1100
+    new = [1 + (i % 7 == 0) for i in range(n)]
+    c = Case(lib, [11] * n, new, heads=16, ps=16, extra_rows=2)
+    assert c.latent()
+    c.run()
+    assert 1000 < int(c.ws[:32].view(torch.int32)[7]) <= 1024
+    vals, table, m = c.values(), c.table.cpu().numpy(), sum(new)
+    tols = []
+    for form in (lambda n: True, lambda n: False):  # (which requests are expanded is the plan's choice)
+        ref, _, tol, _ = step_ref.prefill(lambda b, at: vals[table[b][at // c.ps], at % c.ps], f64(c.q),
+                                          c.indptr.cpu().numpy(), c.ctx.cpu().numpy(), f64(c.w_uk), f64(c.w_uv),
+                                          c.scale, 0, form)
+        tols.append(tol)
+    assert (np.abs(f64(c.out)[:m] - ref[:m]) <= np.maximum(*tols)[:m]).all()
+    assert lib.get_error(c.ws) == 0
+
+
+def test_nan_and_bad_requests_among_small_ones(lib):
+    args = dict(ctx=[4000, 3000, 6000, 50], new=[6, 40, 64, 20], heads=16)
+    a = Case(lib, **args).run()
+    b = Case(lib, **args)
+    pos = 3000 + 20
+    b.pool.data[1].view(-1, 576)[int(b.table[1, pos // b.ps]) * b.ps + pos % b.ps, 77] = float("nan")
+    used = torch.zeros(b.num_pages, dtype=torch.bool, device="cuda")
+    used[b.table[b.table >= 0].long()] = True
+    b.pool.data[1][~used] = float("nan")
+    b.run()
+    hit = torch.zeros(b.T, dtype=torch.bool, device="cuda")
+    hit[6 + 20:6 + 40] = True
+    assert torch.isnan(b.out[hit].float()).all()
+    assert torch.equal(bits(a.out[~hit]), bits(b.out[~hit])) and lib.get_error(b.ws) == 0
+    c = Case(lib, **args)
+    c.ctx[3] = 5000  # more than its pages hold
+    ref, _, tol, _ = a.reference()
+    c.run()
+    assert lib.get_error(c.ws) == lib.STATUS_BAD_LENGTH
+    assert torch.isnan(c.out[110:130].float()).all() and (np.abs(f64(c.out) - ref) <= tol)[:110].all()
+
+
+def test_graph_replay_of_mixed_steps(lib):
+    """A captured call whose requests change between small and large, present and absent."""
+    rng = np.random.default_rng(6)
+    B, T, H, most = 5, 500, 16, 16000
+    c = Case(lib, [3000] * B, [40] * B, heads=H, ps=64, extra_rows=T - 40 * B)
+    c.max_kv = most
+    c.ws = lib.alloc_prefill_workspace(B, T, most, H)
+    c.run()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.prefill(c.pool, 1, c.q, c.indptr, c.ctx, c.scale, c.w_uk, c.w_uv, c.ws, c.out, most, block_table=c.table,
+                    lse=c.lse)
+    for new in ([1, 1, 1, 1, 1], [300, 0, 64, 65, 3], [0, 0, 0, 0, 0], [0, 400, 0, 0, 1], [20, 30, 40, 50, 60]):
+        ctx = [int(rng.integers(0, 3040 - n)) for n in new]
+        c.indptr.copy_(torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32))
+        c.ctx.copy_(torch.tensor(ctx, dtype=torch.int32))
+        c.out.fill_(7.0)
+        c.lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        c.check()
 
 def test_on_another_stream_beside_a_second_call(lib):
     """Two calls at once on two streams, each with a workspace of its own."""
