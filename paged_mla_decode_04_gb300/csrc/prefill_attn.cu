@@ -17,7 +17,7 @@
 // and [256, 512), both over every 128-key step. With fewer they share the rows and
 // take the even and the odd steps; their two results are merged at the end.
 //   TMEM of a block (512 columns): S0 [0, 128) S1 [128, 256) O0 [256, 384)
-//   O1 [384, 512), 128 rows each; a stream's P (bf16 pairs, 64 columns)
+//   O1 [384, 512), 128 rows each; a stream's P (f16 pairs, 64 columns)
 //   overwrites its S.
 //   Shared memory of a block: its 128 rows of each stream's Q (2 x 48 KB) and three
 //   stages of a step: keys [64][192] (K-major, 24 KB), values [128][64]
@@ -33,7 +33,8 @@
 // only when a score exceeds it by 8 (the final division makes it exact), so a step
 // takes its exponentials against the reference as it stands and looks at the
 // largest afterwards: above 2^8 the warp does the step again, with a maximum taken
-// first. P is rounded to bf16 for the product, its sum is kept in fp32.
+// first. P is rounded to f16 for the product, as V is (see the expansion); its sum is
+// kept in fp32.
 // Positions beyond a row's range are masked by selection, never by adding, so
 // NaN in them stays out; the last step multiplies only up to the last 16 keys
 // with a valid one, beyond which the buffer may hold another request's rows.
@@ -299,7 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // copies are waited for, while the tensor core is busy with the last one's.
     if (cta == 0 && elect_one()) {
       constexpr uint32_t idesc_qk = idesc_bf16(256, 128, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16(256, 128, false, true);
+      constexpr uint32_t idesc_pv = idesc_f16(256, 128, false, true);  // P and V are f16
       const uint32_t q_lo = desc_lo(sbase), ring_lo = desc_lo(sbase + kOffRing);
       constexpr uint32_t kStageUnits = kStageBytes >> 4, kVUnits = kKBytes >> 4;
       bool ok = true;
@@ -489,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
               if (c & 1) top1 = fmax3(top1, p0, p1);
               else top = fmax3(top, p0, p1);
-              s[c] = pack_bf16x2(p0, p1);
+              s[c] = pack_f16x2(p0, p1);
             }
             top = fmaxf(top, top1);
           };

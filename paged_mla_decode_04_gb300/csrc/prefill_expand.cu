@@ -1,7 +1,11 @@
 // Keys and values of the gathered rows, for every head h of a pass:
 //   K[h][t][0:128] = c_kv[t] W_UK[h]^T,   V[h][t][0:128] = c_kv[t] W_UV[h],
-// a product of [rows x 512] with [512 x 256] per head, rounded to bf16 (the
-// precision at which models keep K and V; attention multiplies them in bf16).
+// a product of [rows x 512] with [512 x 256] per head. Keys are rounded to bf16, as
+// models keep them: their errors reach the result through the scores alone, damped
+// by the softmax scale, and they may be as large as the queries. Values and softmax
+// weights are errors of the result itself, so they are f16, three bits more: with bf16
+// the result was off by 2.9e-3 (2-norm) where its own rounding to bf16 is 1.7e-3, with
+// f16 by 2.1e-3. Values beyond +-65504 saturate.
 //
 // Bound by the tensor core once the operands arrive: per tile of 128 rows x one
 // head an SM would read 128 KB of rows and 256 KB of weights in the 4,096 cycles of
@@ -198,8 +202,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int v = 0; v < 4; ++v) {
             uint32_t pk[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              pk[i] = pack_bf16x2(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1]));
+            for (int i = 0; i < 8; ++i) {
+              const float x = __uint_as_float(r[16 * v + 2 * i]), y = __uint_as_float(r[16 * v + 2 * i + 1]);
+              pk[i] = c < 2 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+            }
             st_global_v8(dst + v * 16, pk);
           }
         }
