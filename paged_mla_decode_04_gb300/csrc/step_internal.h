@@ -166,9 +166,13 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_hea
   const int64_t slack = static_cast<int64_t>(batch) * (L.absorb ? kBlockTokens : kPfKvAlign) + (L.absorb ? 256 : 0);
   L.kv_capacity = (max_kv + slack + kPfKvTile - 1) / kPfKvTile * kPfKvTile;
   L.max_tiles = q_rows / kPfRows + batch;
-  // Partial rows: two tiles' rows for each pair of SMs, no more than the pieces of every row.
-  L.part_rows = 2ll * kPfPairs * kPfRows / heads;
-  if (L.part_rows > kPfMostPieces * q_rows) L.part_rows = kPfMostPieces * q_rows;
+  // Partial rows of all heads: two tiles' rows for each pair of SMs, no more than the
+  // pieces of every row. (The remainder of the division is kept, so that fewer heads
+  // never take more room: a call cuts its heads into equal passes after it has found
+  // how many fit.)
+  int64_t part_rows = 2ll * kPfPairs * kPfRows;
+  if (part_rows > kPfMostPieces * q_rows * heads) part_rows = kPfMostPieces * q_rows * heads;
+  L.part_rows = part_rows / heads;
   const int64_t entries = L.max_tiles + kPfMostPieces;
   size_t off = sizeof(PfHeader);
   L.requests = off;
@@ -180,9 +184,9 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_hea
   L.splits = off;
   off = align_up(off + sizeof(PfSplit) * kPfMostPieces, 256);
   L.part_stats = off;
-  off = align_up(off + 8 * static_cast<size_t>(L.part_rows) * heads, 1024);
+  off = align_up(off + 8 * static_cast<size_t>(part_rows), 1024);
   L.part_o = off;
-  off = align_up(off + 4 * kDimV * static_cast<size_t>(L.part_rows) * heads, 1024);
+  off = align_up(off + 4 * kDimV * static_cast<size_t>(part_rows), 1024);
   L.rows = off;
   off = align_up(off + static_cast<size_t>(L.kv_capacity) * kDimRow * 2, 1024);
   L.keys = off;

@@ -131,3 +131,11 @@ def test_prefill_workspace_size(lib):
     # the default keeps keys and values within 8 GiB, beside the rows themselves and the partial sums
     assert size(1, 8, 1 << 20, 128, 0) <= (8 << 30) + (1 << 20) * 1152 + (64 << 20)
     assert size(0, 0, 0, 1, 0) > 0
+
+
+@pytest.mark.parametrize("batch,q_rows,max_kv", [(1, 1, 1), (3, 700, 100), (2, 64, 2000)])
+def test_prefill_workspace_grows_with_heads(lib, batch, q_rows, max_kv):
+    # A call finds the most heads that fit, then cuts its heads into equal passes: fewer
+    # heads a pass must never need more room.
+    sizes = [lib.mla_prefill_workspace_size(batch, q_rows, max_kv, 1024, h) for h in range(1, 1025)]
+    assert all(a < b for a, b in zip(sizes, sizes[1:]))
