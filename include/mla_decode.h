@@ -249,7 +249,9 @@ int mla_uv_project(const void* attn_out, const void* w_uv, void* y, int batch,
  * beyond max_page_ids are not written (MLA_STATUS_BAD_LENGTH).
  *   workspace:    whose status word records this (a decode or prefill
  *                 workspace), or NULL.
- * page_size is 16, 32, 64 or 128 and max_blocks * page_size below 2^31. */
+ * Outputs share no memory with each other or with inputs (but for state).
+ * page_size is 16, 32, 64 or 128; max_blocks * page_size and batch * max_blocks
+ * are below 2^31. */
 int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int batch, int page_size, int num_pages,
                       const int32_t* free_pages, const int32_t* free_count, int free_capacity, int32_t* block_table,
                       int max_blocks, int64_t* slot_mapping, int32_t* positions, int max_tokens, int32_t* q_indptr,

@@ -99,6 +99,7 @@ int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int 
     return MLA_ERR_ARG;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return MLA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks) * page_size > INT_MAX) return MLA_ERR_ARG;  // positions are int32
+  if (static_cast<int64_t>(batch) * max_blocks > INT_MAX) return MLA_ERR_ARG;  // so are the CSR lists' pointers
   if (!free_count || !q_indptr || !state || (free_capacity > 0 && !free_pages)) return MLA_ERR_ARG;
   if (batch > 0 && (!context_lens || !new_lens || !block_table)) return MLA_ERR_ARG;
   if (max_tokens > 0 && !slot_mapping) return MLA_ERR_ARG;

@@ -166,6 +166,7 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_hea
   const int64_t slack = static_cast<int64_t>(batch) * (L.absorb ? kBlockTokens : kPfKvAlign) + (L.absorb ? 256 : 0);
   L.kv_capacity = (max_kv + slack + kPfKvTile - 1) / kPfKvTile * kPfKvTile;
   L.max_tiles = q_rows / kPfRows + batch;
+  if (L.max_tiles > q_rows) L.max_tiles = q_rows;  // (a tile has a row)
   // Partial rows of all heads: two tiles' rows for each pair of SMs, no more than the
   // pieces of every row. (The remainder of the division is kept, so that fewer heads
   // never take more room: a call cuts its heads into equal passes after it has found

@@ -99,7 +99,8 @@ def test_edges_of_pages(lib, ps):
     run(lib, make(np.random.default_rng(ps), ctx, new, ps))
 
 
-@pytest.mark.parametrize("batch,new_hi", [(1, 1), (1, 5000), (3, 2000), (128, 1), (700, 9), (1024, 1), (1025, 3), (3000, 2)])
+@pytest.mark.parametrize("batch,new_hi", [(1, 1), (1, 5000), (3, 2000), (128, 1), (700, 9), (1024, 1), (1025, 3), (3000, 2), (3840, 1),
+                                          (3841, 3), (9000, 2)])
 def test_batches_of_both_launch_forms(lib, batch, new_hi):
     rng = np.random.default_rng(batch + new_hi)
     ctx = rng.integers(0, 400, batch)

@@ -461,6 +461,49 @@ def test_graph_replay_of_mixed_steps(lib):
         torch.cuda.synchronize()
         c.check()
 
+def test_most_heads_and_a_workspace_cut_to_fit_half(lib):
+    """1024 heads, at once and in two passes with a workspace sized for one head more than a pass has."""
+    a = Case(lib, [40, 3], [20, 1], heads=1024).run().check()
+    b = Case(lib, [40, 3], [20, 1], heads=1024, heads_per_pass=513)
+    guard = torch.full((b.ws.numel() + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    guard[:256] = 0
+    size = b.ws.numel()
+    b.ws = guard[:size]
+    b.run()
+    assert torch.equal(bits(a.out), bits(b.out)) and bool((guard[size:] == 0x5a).all())
+
+
+@pytest.mark.parametrize("heads,per_pass,new", [(2, 0, 1), (16, 2, 65)])
+def test_rows_past_32_bit_offsets(lib, heads, per_pass, new):
+    """A request behind one of 3.84 million tokens, whose gathered rows take 4.4 GB. The long one's pages are one
+    page over and over, so that with one new token it is attention over that page's 128 rows."""
+    long = 30000 * 128
+    c = Case(lib, [200], [30], heads=heads, ps=128)
+    one = Case(lib, [127], [1], heads=heads, ps=128)
+    c.max_kv = long + 230
+    ref, lse, tol, tol_lse = c.reference()
+    one.pool, one.table = c.pool, c.table[:, 1:2].contiguous()
+    one.w_uk, one.w_uv = c.w_uk, c.w_uv
+    ref1, lse1, _, tol1 = one.reference()
+    table = torch.empty(2, long // 128, dtype=torch.int32, device="cuda")
+    table[0] = c.table[0, 1]
+    table[1, :2] = c.table[0]
+    c.q = torch.cat([one.q[:1].expand(new, heads, 192), c.q])
+    c.T = c.q.shape[0]
+    c.table, c.ctx = table, torch.tensor([long - new, 200], dtype=torch.int32, device="cuda")
+    c.indptr = torch.tensor([0, new, new + 30], dtype=torch.int32, device="cuda")
+    c.ws = lib.alloc_prefill_workspace(2, c.T, c.max_kv, heads, per_pass)
+    c.out, c.lse = c.out.new_empty(c.T, heads, 128), c.lse.new_empty(c.T, heads)
+    c.run()
+    assert lib.get_error(c.ws) == 0
+    assert (np.abs(f64(c.out[new:new + 30]) - ref[:30]) <= tol[:30]).all()
+    assert (np.abs(f64(c.lse[new:new + 30]) - lse[:30]) <= tol_lse[:30]).all()
+    # (the last row attends the page 30,000 times, in pieces of at most 400 steps: their sums add 400 2^-23 to its lse)
+    got = f64(c.out[new - 1])
+    assert np.linalg.norm(got - ref1[0]) <= 6e-3 * np.linalg.norm(ref1[0])
+    assert (np.abs(f64(c.lse[new - 1]) - lse1[0] - np.log(30000)) <= tol1[0] + 400 * 2.0 ** -23).all()
+
+
 def test_on_another_stream_beside_a_second_call(lib):
     """Two calls at once on two streams, each with a workspace of its own."""
     a = Case(lib, [500, 64], [300, 257], heads=6, seed=1)

@@ -202,6 +202,34 @@ def test_rows_alone_and_queries_alone(lib):
     assert torch.equal(e.o_all, d.o_all) and torch.equal(e.pool.data, pool)
 
 
+def test_offsets_past_32_bits(lib):
+    """Slots of a layer that starts beyond 4 GB, and queries whose last rows lie beyond 2^31 elements."""
+    c = Case(lib, 70, 3, ps=128)
+    c.run()
+    pages = 31000
+    pool = torch.empty(2, pages, 128, 576, dtype=torch.bfloat16, device="cuda")
+    pool[1, -2:] = 0
+    first = (pages - 1) * 128 + 20
+    slots = torch.arange(first, first + 70, device="cuda")
+    n, heads = 90000, 128
+    q = torch.empty(n, heads, 192, dtype=torch.bfloat16, device="cuda")
+    q[-70:, :3] = c.q_all
+    pos = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    pos[-70:] = c.pos[0]
+    assert q[-70:].storage_offset() + q.stride(0) * (n - 70) > 2 ** 31
+    want = torch.empty(70, 3, 64, dtype=torch.bfloat16, device="cuda")
+    lib.rope_write(None, 0, None, None, c.pos[0].contiguous(), c.cos_sin, q_rope=c.q, q_out=want)
+    lib.rope_write(lib.KVPool(pool), 1, c.rows, slots, c.pos[0].contiguous(), c.cos_sin, norm_weight=c.weight)
+    lib.rope_write(None, 0, None, None, pos, c.cos_sin, q_rope=q[:, :, 128:])
+    small = torch.zeros(2, 2, 128, 576, dtype=torch.bfloat16, device="cuda")
+    lib.rope_write(lib.KVPool(small), 1, c.rows, slots - (pages - 2) * 128, c.pos[0].contiguous(), c.cos_sin,
+                   norm_weight=c.weight)
+    torch.cuda.synchronize()
+    assert small[1].any() and torch.equal(pool[1, -2:].view(torch.int16), small[1].view(torch.int16))
+    assert torch.equal(q[-70:, :3, 128:].view(torch.int16), want.view(torch.int16))
+    assert torch.equal(q[-70:, :3, :128].view(torch.int16), c.q_all[:, :, :128].view(torch.int16))
+
+
 def test_nan_and_infinity_stay_in_their_row(lib):
     c = Case(lib, 10, 4)
     c.rows[3, 100] = float("inf")

@@ -38,7 +38,7 @@ TABLES = ["context_lens", "new_lens", "batch", "page_size", "num_pages", "free_p
 @pytest.mark.parametrize("bad,code", [
     (dict(batch=-1), ARG), (dict(num_pages=0), ARG), (dict(max_blocks=0), ARG), (dict(free_capacity=-1), ARG),
     (dict(max_tokens=-1), ARG), (dict(max_page_ids=-1), ARG), (dict(page_size=48), UNSUPPORTED),
-    (dict(max_blocks=1 << 27, page_size=16), ARG), (dict(context_lens=None), ARG), (dict(new_lens=None), ARG),
+    (dict(max_blocks=1 << 27, page_size=16), ARG), (dict(batch=1 << 16, max_blocks=1 << 15), ARG), (dict(context_lens=None), ARG), (dict(new_lens=None), ARG),
     (dict(free_pages=None), ARG), (dict(free_count=None), ARG), (dict(block_table=None), ARG),
     (dict(slot_mapping=None), ARG), (dict(q_indptr=None), ARG), (dict(state=None), ARG), (dict(page_indptr=None), ARG),
     (dict(page_ids=None), ARG)])
