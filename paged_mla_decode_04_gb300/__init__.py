@@ -1,6 +1,7 @@
 """Paged MLA decode for GB300: thin Python binding of libmla_decode.so.
 
-Argument marshalling only: every step runs in the library's CUDA kernels.
+Argument marshalling only: every step runs in the library's CUDA kernels. (The
+prefill step's calls go through a compiled binding, the others through ctypes.)
 PyTorch supplies device memory and streams. If the library is missing or
 cannot be loaded this module raises; there is no fallback path.
 
@@ -20,8 +21,8 @@ Calls (same names as the C ABI in include/mla_decode.h):
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -29,6 +30,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla_decode.so")
+BINDING_PATH = os.path.join(_HERE, "_step_binding.so")
 
 MLA_OK = 0
 ERRORS = {-1: "MLA_ERR_ARG", -2: "MLA_ERR_UNSUPPORTED", -3: "MLA_ERR_WORKSPACE", -4: "MLA_ERR_CUDA"}
@@ -65,9 +67,6 @@ class _Pool(ctypes.Structure):
                 ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("kv_scale", ctypes.c_float)]
 
-
-_pack_pool = struct.Struct("@Piiiif0P").pack  # _Pool, its tail padding included
-assert len(_pack_pool(0, 0, 0, 0, 0, 0.0)) == ctypes.sizeof(_Pool)
 
 _lib = None
 
@@ -166,16 +165,6 @@ class KVPool:
             raise ValueError("pool dtype must be bfloat16 or uint8 (e4m3 codes)")
         return _Pool(_dev(d, "pool"), shape[0], shape[1], shape[2],
                      DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP8_E4M3, self.kv_scale)
-
-    def _packed(self, device: int) -> bytes:
-        """The same structure as bytes (quicker made than a ctypes one)."""
-        d = self.data
-        if d.dim() != 4 or d.size(3) != LATENT_DIM:
-            raise ValueError("pool must be [num_layers, num_pages, page_size, 576]")
-        code = DTYPE_BF16 if d.dtype is torch.bfloat16 else DTYPE_FP8_E4M3
-        if code == DTYPE_FP8_E4M3 and d.dtype is not torch.uint8:
-            raise ValueError("pool dtype must be bfloat16 or uint8 (e4m3 codes)")
-        return _pack_pool(_here(d, "pool", None, device), d.size(0), d.size(1), d.size(2), code, self.kv_scale)
 
 
 def kv_write(pool: KVPool, layer: int, new_rows: torch.Tensor, slot_mapping: torch.Tensor,
@@ -373,20 +362,22 @@ def decode_q(pool: KVPool, layer: int, q: torch.Tensor, context_lens: torch.Tens
 
 # ----------------------------------------------------------------- prefill step
 
-_I32, _I64, _BF16, _F32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
+_binding = None
 
 
-def _here(t: torch.Tensor, name: str, dtype, device: int) -> int:
-    """Pointer of a contiguous tensor of `dtype` (None: any) on the current device."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or (t.dtype is not dtype and dtype is not None) \
-            or not t.is_contiguous():
-        _dev(t, name, dtype)  # says what is wrong with it
-        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), device))
-    return t.data_ptr()
-
-
-def _opt(t: Optional[torch.Tensor], name: str, dtype, device: int):
-    return None if t is None else _here(t, name, dtype, device)
+def _step():
+    """The compiled binding of these calls (see csrc/step_binding.cpp)."""
+    global _binding
+    if _binding is None:
+        lib = load_library()
+        if not os.path.exists(BINDING_PATH):
+            raise MlaError("_step_binding.so not built; run paged_mla_decode_04_gb300._build.build()")
+        spec = importlib.util.spec_from_file_location("_step_binding", BINDING_PATH)
+        b = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(b)
+        b.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.mla_extend_tables, lib.mla_rope_write, lib.mla_prefill)])
+        _binding = b
+    return _binding
 
 
 def extend_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -400,52 +391,11 @@ def extend_tables(context_lens: torch.Tensor, new_lens: torch.Tensor, free_pages
     positions of the tokens (-1 behind the last), their row pointers q_indptr,
     and the tables as CSR lists. state becomes (free pages left, first request
     refused for want of pages); it may share free_count's memory."""
-    dev = torch.cuda.current_device()
-    if context_lens.dim() != 1 or new_lens.dim() != 1 or new_lens.numel() != context_lens.numel():
-        raise ValueError("context_lens and new_lens must be [batch]")
-    B = context_lens.numel()
-    if block_table.dim() != 2 or block_table.size(0) != B:
-        raise ValueError("block_table must be [batch, max_blocks]")
-    n = slot_mapping.numel()
-    if slot_mapping.dim() != 1 or (positions is not None and (positions.dim() != 1 or positions.numel() != n)):
-        raise ValueError("slot_mapping and positions must be [max_tokens]")
-    if q_indptr.dim() != 1 or q_indptr.numel() != B + 1:
-        raise ValueError("q_indptr must be [batch + 1]")
-    if (page_indptr is None) != (page_ids is None):
-        raise ValueError("give page_indptr and page_ids together")
-    pi_p = ids_p = None
-    max_ids = 0
-    if page_indptr is not None:
-        if page_indptr.dim() != 1 or page_indptr.numel() != B + 1:
-            raise ValueError("page_indptr must be [batch + 1]")
-        pi_p, ids_p = _here(page_indptr, "page_indptr", _I32, dev), _here(page_ids, "page_ids", _I32, dev)
-        max_ids = page_ids.numel()
-    if free_count.numel() < 1 or state.numel() < 2:
-        raise ValueError("free_count needs one element and state two")
-    rc = (_lib or load_library()).mla_extend_tables(
-        _here(context_lens, "context_lens", _I32, dev), _here(new_lens, "new_lens", _I32, dev), B, page_size, num_pages,
-        _here(free_pages, "free_pages", _I32, dev), _here(free_count, "free_count", _I32, dev), free_pages.numel(),
-        _here(block_table, "block_table", _I32, dev), block_table.size(1),
-        _here(slot_mapping, "slot_mapping", _I64, dev), None if positions is None else
-        _here(positions, "positions", _I32, dev), n, _here(q_indptr, "q_indptr", _I32, dev), pi_p, ids_p, max_ids,
-        _here(state, "state", _I32, dev), None if workspace is None else _here(workspace, "workspace", None, dev),
-        _stream(stream))
+    rc = (_binding or _step()).extend_tables(
+        context_lens, new_lens, free_pages, free_count, block_table, page_size, num_pages, slot_mapping, q_indptr, state,
+        positions, page_indptr, page_ids, workspace, stream)
     if rc:
         _check(rc, "mla_extend_tables")
-
-
-def _head_rows(t: torch.Tensor, name: str, n: int, device: int):
-    """Pointer, pitch and heads of the [tokens, heads, 64] rope dims of queries, a
-    view whose (token, head) rows lie at one pitch."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device:
-        raise ValueError("%s must be a CUDA tensor on the current device" % name)
-    if t.dtype is not _BF16 or t.dim() != 3 or t.size(0) != n or t.size(2) != ROPE_DIM:
-        raise ValueError("%s must be bfloat16 [tokens, heads, 64]" % name)
-    h = t.size(1)
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (h > 1 and n > 1 and s0 != h * s1):
-        raise ValueError("%s: the (token, head) rows must lie at one pitch" % name)
-    return t.data_ptr(), s1 if h > 1 else s0 if n > 1 else ROPE_DIM, h
 
 
 def rope_write(pool: Optional[KVPool], layer: int, rows: Optional[torch.Tensor], slot_mapping: Optional[torch.Tensor],
@@ -459,58 +409,11 @@ def rope_write(pool: Optional[KVPool], layer: int, rows: Optional[torch.Tensor],
     q_rope and q_out are views [tokens, heads, 64] of the queries' rope dims;
     q_out None rotates in place. rows None (with pool and slot_mapping as may
     be) rotates queries only."""
-    dev = torch.cuda.current_device()
-    pd = positions.dim()
-    if pd == 2:
-        axes, n = positions.size(0), positions.size(1)
-    elif pd == 1:
-        axes, n = 1, positions.size(0)
-    else:
-        raise ValueError("positions must be [tokens] or [axes, tokens]")
-    if cos_sin.dim() != 2 or cos_sin.size(1) != ROPE_DIM:
-        raise ValueError("cos_sin must be [positions, 64]")
-    c = rows_p = slots_p = weight_p = qp = op = axis_of = None
-    q_pitch = o_pitch = heads = 0
-    if slot_mapping is not None:
-        if slot_mapping.dim() != 1 or slot_mapping.numel() != n:
-            raise ValueError("slot_mapping must be [tokens]")
-        slots_p = _here(slot_mapping, "slot_mapping", _I64, dev)
-    if rows is not None:
-        if pool is None or slots_p is None or rows.dim() != 2 or rows.size(0) != n or rows.size(1) != LATENT_DIM:
-            raise ValueError("rows [tokens, 576] go with pool and slot_mapping")
-        rows_p = _here(rows, "rows", _BF16, dev)
-        c = pool._packed(dev)
-    if norm_weight is not None:
-        if norm_weight.numel() != KV_LORA_RANK:
-            raise ValueError("norm_weight must be [512]")
-        weight_p = _here(norm_weight, "norm_weight", _BF16, dev)
-    if pair_axis is not None:
-        axis_of = bytes(pair_axis)
-        if len(axis_of) != ROPE_DIM // 2:
-            raise ValueError("pair_axis must name an axis for each of the 32 pairs")
-    if q_rope is not None:
-        qp, q_pitch, heads = _head_rows(q_rope, "q_rope", n, dev)
-        if q_out is None:
-            op, o_pitch = qp, q_pitch
-        else:
-            op, o_pitch, h2 = _head_rows(q_out, "q_out", n, dev)
-            if h2 != heads:
-                raise ValueError("q_rope and q_out must be [tokens, heads, 64]")
-        if heads == 0:
-            qp = op = None
-    elif q_out is not None:
-        raise ValueError("q_out goes with q_rope")
-    elif rows is None:
-        raise ValueError("give rows, q_rope or both")
-    if n == 0 or (qp is None and rows_p is None):
-        return
-    rc = (_lib or load_library()).mla_rope_write(
-        c, layer, rows_p, slots_p, n, _here(positions, "positions", _I32, dev), axes, axis_of,
-        _here(cos_sin, "cos_sin", _F32, dev), cos_sin.size(0), 1 if interleaved else 0, weight_p, norm_eps, qp, q_pitch,
-        op, o_pitch, heads, None if workspace is None else _here(workspace, "workspace", None, dev), _stream(stream))
+    data, scale = (None, 1.0) if pool is None else (pool.data, pool.kv_scale)
+    rc = (_binding or _step()).rope_write(
+        data, scale, layer, rows, slot_mapping, positions, cos_sin, norm_weight, norm_eps, q_rope, q_out,
+        None if pair_axis is None else bytes(pair_axis), interleaved, workspace, stream)
     if rc:
-        if axis_of is not None and max(axis_of) >= axes:
-            raise ValueError("pair_axis names an axis that positions lacks")
         _check(rc, "mla_rope_write")
 
 
@@ -540,34 +443,9 @@ def prefill(pool: KVPool, layer: int, q: torch.Tensor, q_indptr: torch.Tensor, c
     q_indptr[b + 1], at positions from context_lens[b]) -> out [rows, heads,
     128], lse [rows, heads]: causal attention over the paged cache, the new
     tokens' latent rows written beforehand."""
-    dev = torch.cuda.current_device()
-    if q.dim() != 3 or q.size(2) != QK_HEAD_DIM:
-        raise ValueError("q must be [rows, heads, 192]")
-    T, H = q.size(0), q.size(1)
-    if out.shape != (T, H, V_HEAD_DIM) or (lse is not None and lse.shape != (T, H)):
-        raise ValueError("out must be [rows, heads, 128], lse [rows, heads]")
-    if context_lens.dim() != 1:
-        raise ValueError("context_lens must be [batch]")
-    B = context_lens.numel()
-    if q_indptr.dim() != 1 or q_indptr.numel() != B + 1:
-        raise ValueError("q_indptr must be [batch + 1]")
-    if w_uk.shape != (H, NOPE_DIM, KV_LORA_RANK) or w_uv.shape != (H, KV_LORA_RANK, V_HEAD_DIM):
-        raise ValueError("w_uk [heads, 128, 512] and w_uv [heads, 512, 128] expected")
-    if block_table is not None:
-        if block_table.dim() != 2 or block_table.size(0) != B:
-            raise ValueError("block_table must be [batch, max_blocks]")
-        indptr_p, ids_p, max_blocks = None, _here(block_table, "block_table", _I32, dev), block_table.size(1)
-    else:
-        if page_indptr is None or page_ids is None or page_indptr.dim() != 1 or page_indptr.numel() != B + 1:
-            raise ValueError("give block_table, or page_indptr [batch+1] and page_ids")
-        indptr_p, ids_p, max_blocks = _here(page_indptr, "page_indptr", _I32, dev), \
-            _here(page_ids, "page_ids", _I32, dev), 0
-    rc = (_lib or load_library()).mla_prefill(
-        pool._packed(dev), layer, _here(q, "q", _BF16, dev), _here(q_indptr, "q_indptr", _I32, dev), indptr_p,
-        ids_p, max_blocks, _here(context_lens, "context_lens", _I32, dev), B, T, max_kv_tokens, H,
-        _here(w_uk, "w_uk", _BF16, dev), _here(w_uv, "w_uv", _BF16, dev), softmax_scale, window,
-        _here(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
-        _here(out, "out", _BF16, dev), _opt(lse, "lse", _F32, dev), _stream(stream))
+    rc = (_binding or _step()).prefill(
+        pool.data, pool.kv_scale, layer, q, q_indptr, context_lens, softmax_scale, w_uk, w_uv, workspace, out,
+        max_kv_tokens, block_table, page_indptr, page_ids, window, lse, stream)
     if rc:
         _check(rc, "mla_prefill")
     return out

@@ -1,4 +1,6 @@
-"""Build libmla_decode.so in-tree with nvcc for sm_103a (no cmake, no torch).
+"""Build libmla_decode.so in-tree with nvcc for sm_103a (no cmake, no torch), and
+beside it _step_binding.so, the compiled Python binding of the prefill step's
+calls (the host compiler, PyTorch's headers).
 
 Each .cu file compiles to an object in parallel; the objects link into one
 shared library with the CUDA runtime linked statically, so the library loads
@@ -11,6 +13,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -20,6 +23,7 @@ SOURCES = ["mla_api.cu", "kv_write.cu", "plan_merge.cu", "decode_sm103.cu", "uv_
            "step_api.cu", "step_tables.cu", "rope_write.cu", "prefill_gather.cu", "prefill_expand.cu", "prefill_attn.cu",
            "prefill_absorb.cu"]
 HEADERS = ["ptx.cuh", "mla_internal.h", "trace.cuh", "host_util.h", "step_internal.h", "ptx_prefill.cuh", "scan.cuh"]
+BINDING = os.path.join(HERE, "_step_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,9 +46,20 @@ def _stale(target, inputs):
     return any(os.path.getmtime(i) > t for i in inputs)
 
 
+def _binding_command(target: str):
+    import torch
+    root = os.path.dirname(torch.__file__)
+    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(nvcc()), "..", "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            *[x for d in dirs for x in ("-isystem", d)], os.path.join(CSRC, "step_binding.cpp"), "-o", target,
+            "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, defines=(),
           lib_path: str = LIB, build_dir: str = BUILD) -> str:
-    """Compile every kernel file and link libmla_decode.so (only what is stale).
+    """Compile every kernel file, link libmla_decode.so and build the binding (only what is stale).
     `defines` (e.g. ["-DMLA_TRACE"] for the event-traced build) go with
     their own lib_path and build_dir."""
     os.makedirs(build_dir, exist_ok=True)
@@ -61,17 +76,25 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
         if force or ptxas_info or _stale(o, [s] + deps):
             jobs.append([nvcc(), *flags, "-c", s, "-o", o])
 
+    binding_tmp = BINDING + ".tmp.%d" % os.getpid()
+    binding = lib_path == LIB and (force or _stale(BINDING, [os.path.join(CSRC, "step_binding.cpp")] + deps[-2:]))
+    link = force or bool(jobs)
+    if binding:
+        jobs.insert(0, _binding_command(binding_tmp))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+            raise RuntimeError("compiler failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
         return r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4) or 1) as ex:
         for log in ex.map(run, jobs):
             if verbose and log:
                 print(log)
-    if force or jobs or _stale(lib_path, objs):
+    if binding:
+        os.replace(binding_tmp, BINDING)
+    if link or _stale(lib_path, objs):
         tmp = lib_path + ".tmp.%d" % os.getpid()
         run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"])
         os.replace(tmp, lib_path)
