@@ -270,7 +270,7 @@ int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int 
  * rounded once from fp32. Queries (q_rope != NULL): the 64 rope dims of every
  * head turn and are rounded to bf16.
  *   rows:         device, [n][576] bf16, 16-byte aligned.
- *   slot_mapping: device, [n] int64; required with rows. A row with a negative
+ *   slot_mapping: device, [n] int64, no slot twice; required with rows. A row with a negative
  *                 slot is a pad row: neither its latent nor its queries are
  *                 touched. A slot beyond the layer sets MLA_STATUS_BAD_SLOT and
  *                 its latent row is skipped.
@@ -286,7 +286,7 @@ int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int 
  *                 multiples of 8 and at least 64, pointers 16-byte aligned.
  *                 q_out may be q_rope (in place) or rows that share no element
  *                 with it; other overlaps are refused with MLA_ERR_ARG.
- *   pool, layer:  used with rows only. workspace: for the status word, or NULL. */
+ *   pool, layer:  used with rows only; rows are not the pool's. workspace: for the status word, or NULL. */
 int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const int64_t* slot_mapping, int n,
                    const int32_t* positions, int num_axes, const uint8_t* pair_axis, const float* cos_sin,
                    int max_position, int interleaved, const void* norm_weight, float norm_eps, const void* q_rope,
@@ -302,10 +302,12 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *         over t in [0 or max(0, L_b + i + 1 - window), L_b + i],
  *   out = sum_t softmax(s)_t v_t,  lse = log(sum_t exp(s_t)).
  * Keys and values of all heads are made once (512 bytes per head and attended
- * position, in the workspace) and then attended at 640 flops a pair where the
- * absorbed form costs 2,176. Making them costs as much as 410 queries'
- * attention, so from about 170 new tokens a request this call does less work,
- * and mla_decode / mla_decode_q serve shorter chunks and single tokens better.
+ * position, in the workspace) and then attended at 640 flops a pair; making
+ * them costs as much as 410 queries' attention. So requests of up to 64 new
+ * tokens (single tokens among chunks) are attended in the latent space instead,
+ * by the kernel of mla_decode, at 2,176 flops a pair: in calls of 16, 32, 64 or
+ * 128 heads with max_kv_tokens * num_heads >= 200,000. A step of single tokens
+ * alone is mla_decode's.
  *   q:        device, [q_rows][num_heads][192] bf16 (nope 128 || rope 64).
  *   q_indptr: device, [batch + 1] int32, non-decreasing, within [0, q_rows].
  *             Rows of out outside [q_indptr[0], q_indptr[batch]) stay as they were.
@@ -319,15 +321,22 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *             num_heads, heads_per_pass) bytes, 256-byte aligned, its first 256
  *             zeroed once before the first use. Of its own: not a decode
  *             workspace, and not shared by calls that overlap on the GPU.
- * num_heads is 1 to 1024. Arithmetic: fp32 accumulation, keys, values and
- * softmax weights rounded to bf16 for the tensor core. fp8 pools: the codes
- * are widened exactly and kv_scale multiplies the scores and the output.
+ * num_heads is 1 to 1024. Arithmetic: fp32 accumulation and softmax sums; for
+ * the tensor core keys are rounded to bf16, values and softmax weights to f16
+ * (values beyond +-65504 saturate). In the latent space the query there and
+ * the latent result are rounded to bf16, scores as in mla_decode. fp8 pools:
+ * the codes are widened exactly and kv_scale multiplies the scores and the
+ * output. A call repeated gives the same bits; with other requests, capacities
+ * or heads a pass beside it a request's sums may be taken in another order.
+ * out and lse share no memory with each other or with inputs.
  * On the device: a bad page id sets MLA_STATUS_BAD_PAGE and its rows read as
  * zero; a request with a bad length (negative, beyond its page list, or beyond
  * max_kv_tokens in the sum) sets MLA_STATUS_BAD_LENGTH and its rows of out and
  * lse are NaN; row pointers outside q set it and nothing is written. A cached
  * row with an infinity or NaN in c_kv gives NaN to the rows that attend it
- * and to no others. */
+ * and to no others (finite c_kv whose product with w_uv overflows fp32 may
+ * reach others of its request). After MLA_STATUS_TIMEOUT out and lse are
+ * unspecified. */
 int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t* q_indptr, const int32_t* page_indptr,
                 const int32_t* page_ids, int max_blocks, const int32_t* context_lens, int batch, int q_rows,
                 int64_t max_kv_tokens, int num_heads, const void* w_uk, const void* w_uv, float softmax_scale,

@@ -25,7 +25,8 @@
 namespace mla {
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 512;  // at most
+constexpr int kCostBins = 128;     // (the least number of threads)
 constexpr int kRowVecs = kDimRow * 2 / 16;  // 72
 
 __device__ __forceinline__ int64_t block_exclusive(int64_t x, int64_t* sh, int64_t* total) {
@@ -105,9 +106,9 @@ __device__ int split_tiles(const PrefillArgs& a, PfTile* tiles, int nt, int64_t*
   const bool cut = pieces > 1 && row0 + rows <= a.lay.part_rows;
   // (room for the entries: pieces a head fit in kMostWaves waves of clusters, or
   // in kPfMostPieces entries beyond the first of each)
-  int64_t extra = cut ? pieces - 1 : 0, split = cut ? 1 : 0, merged = cut ? t.rows : 0, extras, splits, merge_rows;
-  const int64_t to = nt + block_exclusive(extra, sh, &extras);
-  const int64_t at = block_exclusive(split, sh, &splits), merge_row = block_exclusive(merged, sh, &merge_rows);
+  int64_t v[3] = {cut ? pieces - 1 : 0, cut ? 1 : 0, cut ? t.rows : 0}, sums[3];  // further entries, split tiles, their rows
+  block_scan(v, sums, sh);
+  const int64_t to = nt + v[0], at = v[1], merge_row = v[2];
   if (cut) {
     t.part_row = static_cast<int>(row0);
     const int begin = t.kv_begin, end = t.kv_end;
@@ -125,20 +126,28 @@ __device__ int split_tiles(const PrefillArgs& a, PfTile* tiles, int nt, int64_t*
     s.merge_row = static_cast<int>(merge_row);
   }
   if (threadIdx.x == 0) {
-    hd->num_split = static_cast<int>(splits);
-    hd->merge_rows = static_cast<int>(merge_rows);
+    hd->num_split = static_cast<int>(sums[1]);
+    hd->merge_rows = static_cast<int>(sums[2]);
   }
   __syncthreads();
-  return nt + static_cast<int>(extras);
+  return nt + static_cast<int>(sums[0]);
+}
+
+// Decode blocks of a group of a small request.
+__device__ __forceinline__ int group_first(const PfGroup& g, int window) { return window > 0 ? max(0, g.first + 1 - window) : 0; }
+__device__ __forceinline__ int group_blocks(const PfGroup& g, int window) {
+  return (g.first + g.tokens - 1) / kBlockTokens - group_first(g, window) / kBlockTokens + 1;
 }
 
 // The decode kernel's schedule for the groups of small requests: their 64-row
-// blocks, each group weighing kGroupCost more for its start and end, laid out in a
-// row and cut into equal ranges, one a cluster; a group across a cut leaves partial
-// sums that the decode's merge joins. All threads call it.
+// blocks, each group weighing kGroupCost more for its start and end, `total` in all,
+// laid out in a row and cut into equal ranges, one a cluster; a group across a cut
+// leaves partial sums that the decode's merge joins. All threads call it.
 constexpr int kGroupCost = 4;
+constexpr int kMostItems = kPfSmallRows / kGroupRows + kPfPairs;
 
-__device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t* sh) {
+__device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t total, int64_t* sh) {
+  __shared__ uint8_t cluster_of_item[kMostItems];
   const PfLayout& lay = a.lay;
   const PfGroup* gs = reinterpret_cast<const PfGroup*>(a.ws + lay.groups);
   uint8_t* ws = a.ws + lay.decode;
@@ -147,19 +156,7 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t* sh) {
   int* cstart = reinterpret_cast<int*>(ws + lay.decode_lay.cluster_start);
   SplitRequest* split = reinterpret_cast<SplitRequest*>(ws + lay.decode_lay.split);
   const int tid = threadIdx.x, step = blockDim.x;
-  auto first_token = [&](const PfGroup& g) { return a.window > 0 ? max(0, g.first + 1 - a.window) : 0; };
-  auto blocks_of = [&](const PfGroup& g) {
-    return (g.first + g.tokens - 1) / kBlockTokens - first_token(g) / kBlockTokens + 1;
-  };
-  int64_t total = 0;
-  for (int i0 = 0; i0 < groups; i0 += step) {
-    int64_t sum;
-    block_exclusive(i0 + tid < groups ? blocks_of(gs[i0 + tid]) + kGroupCost : 0, sh, &sum);
-    total += sum;
-  }
-  const int64_t clusters = max(static_cast<int64_t>(1), min(total, static_cast<int64_t>(a.clusters)));
-  auto cut = [&](int64_t c) { return c * total / clusters; };  // first unit of cluster c
-  auto cluster_of = [&](int64_t x) { return ((x + 1) * clusters + total - 1) / total - 1; };
+  const int64_t per = max(static_cast<int64_t>(1), (total + a.clusters - 1) / a.clusters);  // units of a cluster
   int64_t carry[4] = {0, 0, 0, 0};  // units, items, partial slots, split groups
   for (int i0 = 0; i0 < groups; i0 += step) {
     const int i = i0 + tid;
@@ -167,32 +164,33 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t* sh) {
     int n = 0;
     if (i < groups) {
       g = gs[i];
-      n = blocks_of(g);
+      n = group_blocks(g, a.window);
     }
     int64_t units;
     const int64_t off = carry[0] + block_exclusive(n ? n + kGroupCost : 0, sh, &units) + kGroupCost;
-    const int64_t cf = n ? cluster_of(off) : 0, cl = n ? cluster_of(off + n - 1) : -1;
-    const int64_t pieces = cl - cf + 1;
+    const int cf = n ? static_cast<int>(off / per) : 0, cl = n ? static_cast<int>((off + n - 1) / per) : -1;
+    const int pieces = cl - cf + 1;
     int64_t v[3] = {pieces, pieces > 1 ? pieces : 0, pieces > 1 ? 1 : 0}, sums[3];
     block_scan(v, sums, sh);
-    for (int64_t k = 0; k < pieces; ++k) {
+    for (int k = 0; k < pieces; ++k) {
       WorkItem w;
-      const int64_t lo = max(off, cut(cf + k)), hi = min(off + n, cut(cf + k + 1));
-      const int blk0 = first_token(g) / kBlockTokens;
+      const int64_t lo = max(off, (cf + k) * per), hi = min(off + n, (cf + k + 1) * per);
+      const int first = group_first(g, a.window), blk0 = first / kBlockTokens;
       w.b = i;
       w.blk_begin = blk0 + static_cast<int>(lo - off);
       w.blk_end = blk0 + static_cast<int>(hi - off);
       w.slot = pieces > 1 ? static_cast<int>(carry[2] + v[1] + k) : -1;
-      w.tok_lo = first_token(g);
+      w.tok_lo = first;
       w.tok_hi = g.first + lay.group_tokens;  // (as if the group were full: its rows count from here)
-      w.cluster = static_cast<int>(cf + k);
+      w.cluster = cf + k;
       w.row0 = 0;
       items[carry[1] + v[0] + k] = w;
+      cluster_of_item[carry[1] + v[0] + k] = static_cast<uint8_t>(cf + k);
     }
     if (pieces > 1) {
       SplitRequest r;
       r.b = i;
-      r.num_splits = static_cast<int>(pieces);
+      r.num_splits = pieces;
       r.first_partial = static_cast<int>(carry[2] + v[1]);
       r.row0 = 0;
       split[carry[3] + v[2]] = r;
@@ -207,7 +205,7 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t* sh) {
     int lo = 0, hi = num_items;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (items[mid].cluster < c) lo = mid + 1;
+      if (cluster_of_item[mid] < c) lo = mid + 1;
       else hi = mid;
     }
     cstart[c] = lo;
@@ -219,8 +217,8 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t* sh) {
     hd->q_len = lay.group_tokens;
     hd->page_size = kBlockTokens;
     hd->window = a.window;
-    hd->num_clusters = static_cast<int>(clusters);
-    hd->total_blocks = static_cast<int>(total);
+    hd->num_clusters = static_cast<int>(max(static_cast<int64_t>(1), (total + per - 1) / per));
+    hd->total_blocks = static_cast<int>(min(total, static_cast<int64_t>(INT32_MAX)));
     hd->num_items = num_items;
     hd->num_partials = static_cast<int>(carry[2]);
     hd->num_split = static_cast<int>(carry[3]);
@@ -228,6 +226,7 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t* sh) {
     hd->planned = 1;
   }
 }
+static_assert(kPfPairs < 256, "clusters in a byte");
 
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillArgs a) {
   __shared__ int64_t sh[32 * 5];
@@ -238,12 +237,15 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   PfTile* tiles = reinterpret_cast<PfTile*>(a.ws + a.lay.tiles);
   PfGroup* groups = reinterpret_cast<PfGroup*>(a.ws + a.lay.groups);
   const bool absorb = a.lay.absorb != 0;
-  const int per_group = a.lay.group_tokens;
+  const int per_group = a.lay.group_tokens, group_shift = absorb ? 31 - __clz(per_group) : 0;  // (a power of two)
   // Sums over the requests so far: rows of the expanded ones, rows of the small ones,
   // requests that are not small, tiles, groups. With small requests a first pass
-  // finds where their rows start, after all others'.
+  // finds where their rows start, after all others'
+  // (unless one round of threads serves all requests: its own sums tell).
   int64_t sum[5] = {0, 0, 0, 0, 0}, small_start = 0, small_first = 0;
-  for (int pass = absorb ? 0 : 1; pass < 2; ++pass) {
+  const int threads = blockDim.x;
+  const bool one_round = a.batch <= threads;
+  for (int pass = absorb && !one_round ? 0 : 1; pass < 2; ++pass) {
     if (pass == 1) {
       small_start = (sum[0] + 255) / 256 * 256;
       small_first = sum[2];
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
     int64_t wished = 0, spanned = 0;
 #pragma unroll
     for (int k = 0; k < 5; ++k) sum[k] = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 < a.batch; b0 += threads) {
       const int b = b0 + threadIdx.x;
       int64_t len = 0, n = 0, q0 = 0, lo = 0;
       bool ok = true;
@@ -272,14 +274,14 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
       bool small = false;
       int64_t ng = 0;
       if (absorb) {
-        ng = want > 0 && n <= kPfSmallTokens ? (n + per_group - 1) / per_group : 0;
+        ng = want > 0 && n <= kPfSmallTokens ? (n + per_group - 1) >> group_shift : 0;
         int64_t round;
         const int64_t before = wished + block_exclusive(ng, sh, &round);
         small = ng > 0 && before + ng <= a.lay.max_groups;
         wished += round;
       }
       const int align = small ? kBlockTokens : kPfKvAlign;
-      const int64_t span = (want + align - 1) / align * align;
+      const int64_t span = (want + align - 1) & -static_cast<int64_t>(align);
       int64_t round;
       const int64_t upto = spanned + block_exclusive(span, sh, &round) + span;
       spanned += round;
@@ -288,6 +290,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
       const int64_t nt = small ? 0 : (n + kPfRows - 1) / kPfRows;
       int64_t v[5] = {small || !good ? 0 : span, small ? span : 0, b < a.batch && !small ? 1 : 0, nt, small ? ng : 0}, total[5];
       block_scan(v, total, sh);
+      if (one_round) {
+        small_start = (total[0] + 255) / 256 * 256;
+        small_first = total[2];
+      }
       if (pass == 1 && b < a.batch) {
         if (!good) atomicOr(&hd->status, MLA_STATUS_BAD_LENGTH);
         PfRequest r;
@@ -332,45 +338,55 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
     __syncthreads();  // groups are written
     const int count = static_cast<int>(sum[4]);
     int32_t* indptr = reinterpret_cast<int32_t*>(a.ws + a.lay.group_indptr);
-    int64_t pages = 0;
-    for (int i0 = 0; i0 < count; i0 += kPlanThreads) {
+    int64_t pages = 0, units = 0;
+    for (int i0 = 0; i0 < count; i0 += threads) {
       const int i = i0 + threadIdx.x;
-      int64_t round;
-      const int64_t at = pages + block_exclusive(i < count ? groups[i].pages : 0, sh, &round);
+      PfGroup g = {};
+      if (i < count) g = groups[i];
+      int64_t v[2] = {g.pages, i < count ? group_blocks(g, a.window) + kGroupCost : 0}, total[2];
+      block_scan(v, total, sh);
       if (i < count) {
-        groups[i].page0 = static_cast<int>(at);
-        indptr[i] = static_cast<int>(at);
+        groups[i].page0 = static_cast<int>(pages + v[0]);
+        indptr[i] = static_cast<int>(pages + v[0]);
       }
-      pages += round;
+      pages += total[0];
+      units += total[1];
     }
     if (threadIdx.x == 0) {
       indptr[count] = static_cast<int>(pages);
       hd->num_groups = count;
     }
-    schedule_groups(a, count, sh);
+    schedule_groups(a, count, units, sh);
   }
-  // Tiles by falling cost (key steps, in 256 classes of the most expensive
+  // Tiles by falling cost (key steps, in kCostBins classes of the most expensive
   // one's): blocks draw them in this order, so that what is drawn last is
   // short. The order within a class varies from call to call and changes nothing
   // but who computes a tile.
-  __shared__ int most, bins[256];
+  __shared__ int most, bins[kCostBins];
   int nt = static_cast<int>(min(tiles_before, a.lay.max_tiles));
   int* order = reinterpret_cast<int*>(a.ws + a.lay.order);
-  if (threadIdx.x < 256) bins[threadIdx.x] = 0;
+  if (threadIdx.x < kCostBins) bins[threadIdx.x] = 0;
   if (threadIdx.x == 0) most = 1;
   __syncthreads();  // (also: tiles are written)
   auto cost = [&](int i) { return pf_steps(tiles[i].kv_begin, tiles[i].kv_end); };
   nt = split_tiles(a, tiles, nt, sh);
-  for (int i = threadIdx.x; i < nt; i += kPlanThreads) atomicMax(&most, cost(i));
+  // (a thread's first tile's cost is read once)
+  const int mine = threadIdx.x < nt ? cost(threadIdx.x) : 0;
+  auto cost_of = [&](int i) { return i == static_cast<int>(threadIdx.x) ? mine : cost(i); };
+  int top = mine;
+  for (int i = threadIdx.x + threads; i < nt; i += threads) top = max(top, cost(i));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0) atomicMax(&most, top);
   __syncthreads();
-  auto bin = [&](int i) { return 255 - static_cast<int>(static_cast<int64_t>(cost(i)) * 255 / most); };
-  for (int i = threadIdx.x; i < nt; i += kPlanThreads) atomicAdd(&bins[bin(i)], 1);
+  const uint32_t scale = most;  // (steps are fewer than 2^24)
+  auto bin = [&](int i) { return kCostBins - 1 - static_cast<int>(static_cast<uint32_t>(cost_of(i)) * (kCostBins - 1) / scale); };
+  for (int i = threadIdx.x; i < nt; i += threads) atomicAdd(&bins[bin(i)], 1);
   __syncthreads();
-  int64_t first = threadIdx.x < 256 ? bins[threadIdx.x] : 0, ignored;
+  int64_t first = threadIdx.x < kCostBins ? bins[threadIdx.x] : 0, ignored;
   first = block_exclusive(first, sh, &ignored);
-  if (threadIdx.x < 256) bins[threadIdx.x] = static_cast<int>(first);
+  if (threadIdx.x < kCostBins) bins[threadIdx.x] = static_cast<int>(first);
   __syncthreads();
-  for (int i = threadIdx.x; i < nt; i += kPlanThreads) order[atomicAdd(&bins[bin(i)], 1)] = i;
+  for (int i = threadIdx.x; i < nt; i += threads) order[atomicAdd(&bins[bin(i)], 1)] = i;
   if (threadIdx.x == 0) {
     hd->kv_rows = static_cast<int>(sum[0]);
     hd->all_rows = static_cast<int>(absorb && sum[1] > 0 ? small_start + sum[1] : sum[0]);
@@ -532,7 +548,9 @@ int sm_count() {
 }
 
 cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t stream) {
-  return launch_pdl(prefill_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+  int threads = kCostBins;  // no more warps than requests and tiles: scans cost by the warp
+  while (threads < kPlanThreads && threads < max(static_cast<int64_t>(a.batch), a.lay.max_tiles)) threads *= 2;
+  return launch_pdl(prefill_plan_kernel, dim3(1), dim3(threads), 0, stream, a);
 }
 
 cudaError_t launch_prefill_merge(const PrefillArgs& a, int head0, int heads, cudaStream_t stream) {

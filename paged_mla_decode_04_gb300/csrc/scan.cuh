@@ -7,7 +7,8 @@
 namespace mla {
 
 // Exclusive prefix sums over the block of kN 64-bit values; total[] receives the
-// block's sums. `sh`: 32 * kN values of shared memory. Two barriers.
+// block's sums. `sh`: 32 * kN values of shared memory. Three barriers. (Shuffles pass
+// one a cycle, so the warps' sums are scanned by one warp a value, not by all.)
 template <int kN>
 __device__ __forceinline__ void block_scan(int64_t (&v)[kN], int64_t (&total)[kN], int64_t* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -25,17 +26,19 @@ __device__ __forceinline__ void block_scan(int64_t (&v)[kN], int64_t (&total)[kN
 #pragma unroll
     for (int i = 0; i < kN; ++i) sh[32 * i + warp] = v[i];
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {  // every warp scans the warps' sums
+  for (int i = warp; i < kN; i += warps) {
     int64_t w = lane < warps ? sh[32 * i + lane] : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+    for (int d = 1; d < warps; d <<= 1) {
       const int64_t u = __shfl_up_sync(0xffffffffu, w, d);
       if (lane >= d) w += u;
     }
-    total[i] = __shfl_sync(0xffffffffu, w, 31);
-    const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-    v[i] += (warp > 0 ? before : 0) - own[i];
+    sh[32 * i + lane] = w;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    total[i] = sh[32 * i + warps - 1];
+    v[i] += (warp > 0 ? sh[32 * i + warp - 1] : 0) - own[i];
   }
   __syncthreads();
 }
