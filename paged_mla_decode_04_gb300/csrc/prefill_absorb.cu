@@ -6,7 +6,9 @@
 // t tokens a full group); slots without a token are left out. Per head these are
 // products over all slots, [slots x 128] x [128 x 512] and [slots x 512] x
 // [512 x 128], bound by reading the weights (256 KB a head) for the few hundred
-// slots of a step: one block per (head, 128 slots), one pass over the weights.
+// slots of a step: one block per (head, 128 slots), one pass over the weights. With
+// about 600 slots of 16 heads they take 11 and 7.6 us beside 40 us of the decode; in a
+// call that turns out to have no small request, the path's four launches cost 10 to 13.
 #include <cuda_bf16.h>
 
 #include "../../include/mla_decode.h"

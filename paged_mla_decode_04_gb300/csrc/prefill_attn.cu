@@ -35,6 +35,12 @@
 // largest afterwards: above 2^8 the warp does the step again, with a maximum taken
 // first. P is rounded to f16 for the product, as V is (see the expansion); its sum is
 // kept in fp32.
+// 2,048 new tokens behind 14,336 cached, 128 heads: 1,531 us alone, 1.68 PFLOP/s (87 % of
+// the library product's burst rate); calls in a row run into the power limit (1,790 us).
+// Three prompts of 4,500 to 8,192 tokens, 16 heads: 452 us, 1.56 (the diagonal's masked
+// halves, and each item's start and end, about five units of (stream, step)). A window of
+// 4,096 and chunks of 300 to 1,024 tokens, 128 heads: 719 us, 1.24 (86 % of the rows of
+// its tiles are real, and a tile's rows span 511 keys more than each attends).
 // Positions beyond a row's range are masked by selection, never by adding, so
 // NaN in them stays out; the last step multiplies only up to the last 16 keys
 // with a valid one, beyond which the buffer may hold another request's rows.
@@ -64,10 +70,12 @@ constexpr int kThreads = 384;               // (the last two warps idle)
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "register split");
 constexpr int kSched = 2;                   // items announced ahead
-// Items that a group of heads should have for each cluster: within a group the
-// costly tiles of all its heads come first, groups follow each other so that
-// their keys and values stay in L2.
-constexpr int kGroupItems = 3;
+// Items are drawn head after head, so that the clusters at work share few heads' keys
+// and values in L2 (2,048 new tokens over 16,384, 128 heads: 2,060 us a call; 2,160 with
+// the tiles of 57 heads interleaved). Where tiles differ in cost, the last heads, with
+// this many items for each cluster, go together, costly tiles first, so that the last
+// items are short (three prompts, 16 heads: 577 us; 618 to 627 without).
+constexpr int kTailItems = 3;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr float kMostWeight = 256.0f;       // 2^kRescaleThreshold
@@ -133,19 +141,17 @@ __device__ __forceinline__ int end_of(const Item& w, int x) {
   return x == 0 && !w.shared ? min(w.t.first_end + 255, w.t.kv_end) : w.t.kv_end;
 }
 
-// Tile rank and head of item `it`: groups of heads one after the other, within
-// a group all heads' tiles of one rank before the next rank's.
-__device__ __forceinline__ void split_item(int64_t it, int num_tiles, int heads, int groups, int* rank, int* head) {
-  int g = static_cast<int>(it * groups / (static_cast<int64_t>(num_tiles) * heads));
-  int h0 = heads * g / groups, h1 = heads * (g + 1) / groups;
-  if (it >= static_cast<int64_t>(h1) * num_tiles) {
-    ++g;
-    h0 = h1;
-    h1 = heads * (g + 1) / groups;
+// Tile rank and head of item `it`: head by head up to head `tail`, from there all
+// heads' tiles of one rank before the next rank's.
+__device__ __forceinline__ void split_item(int64_t it, int num_tiles, int heads, int tail, int* rank, int* head) {
+  const int64_t in = it - static_cast<int64_t>(tail) * num_tiles;
+  if (in < 0) {
+    *head = static_cast<int>(it / num_tiles);
+    *rank = static_cast<int>(it % num_tiles);
+  } else {
+    *rank = static_cast<int>(in / (heads - tail));
+    *head = tail + static_cast<int>(in % (heads - tail));
   }
-  const int64_t in = it - static_cast<int64_t>(h0) * num_tiles;
-  *rank = static_cast<int>(in / (h1 - h0));
-  *head = h0 + static_cast<int>(in % (h1 - h0));
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -201,16 +207,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int clusters = gridDim.x / 2;
       const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + a.lay.tiles);
       const int* order = reinterpret_cast<const int*>(a.ws + a.lay.order);
-      const int group_heads = static_cast<int>(
-          min(static_cast<int64_t>(heads), (static_cast<int64_t>(kGroupItems) * clusters + num_tiles - 1) / max(num_tiles, 1)));
-      const int groups = max(1, heads / max(group_heads, 1));
+      const int tail_heads = (kTailItems * clusters + num_tiles - 1) / max(num_tiles, 1);
+      const int tail = hd->even ? heads : max(0, heads - tail_heads);
       uint32_t k_steps = 0, v_steps = 0;  // steps whose copies are issued
       uint32_t q_use[2] = {0, 0};
       bool ok = true;
       auto load_item = [&](int64_t it) {
         int rank, head;
         if (it >= items) return item_of(PfTile{0, 0, 0, 0, 0, 0, 1, -1, {}}, -1);
-        split_item(it, num_tiles, heads, groups, &rank, &head);
+        split_item(it, num_tiles, heads, tail, &rank, &head);
         return item_of(tiles[order[rank]], head);
       };
       // The even block announces an item to both.

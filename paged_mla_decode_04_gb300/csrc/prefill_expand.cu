@@ -19,6 +19,13 @@
 // the others); two such accumulators alternate, so that the epilogue of one unit
 // runs under the products of the next. Weights come by TMA in chunks of 64 of the
 // 512 dims, W_UK K-major and W_UV MN-major, 16 KB a stage and block.
+//
+// 16,384 rows for 128 heads: 331 us, 1.66 PFLOP/s (86 % of the library product's burst
+// rate, 95 % of what it sustains); 19,799 rows for 16 heads: 55 us, 1.50, where a
+// cluster's last run is short and each run's rows arrive before its first product. Of
+// the rest the tensor core waits 26 % (active 74 %): at a run's start, and for power.
+// Stores through shared memory and TMA instead of 32 bytes a thread: no gain, or 10 %
+// lost where they took two of the five stages.
 #include <cuda_bf16.h>
 
 #include "../../include/mla_decode.h"
