@@ -47,6 +47,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   pdl_wait();
   const int num_groups = hd->num_groups;
+  {  // page lists of the groups, for the decode kernel: their rows lie one after the other
+    const PfGroup* groups = reinterpret_cast<const PfGroup*>(a.ws + a.lay.groups);
+    int32_t* pages = reinterpret_cast<int32_t*>(a.ws + a.lay.group_pages);
+    const int warps = kThreads / 32, first = blockIdx.y * gridDim.x + blockIdx.x;
+    for (int g = first * warps + warp; g < num_groups; g += gridDim.x * gridDim.y * warps) {
+      const PfGroup p = groups[g];
+      for (int j = tid & 31; j < p.pages; j += 32) pages[p.page0 + j] = p.base / kBlockTokens + j;
+    }
+  }
   if (blockIdx.y * 128 >= num_groups * a.lay.group_tokens) return;
   if (tid == 0) {
     mbar_init(full, 1);

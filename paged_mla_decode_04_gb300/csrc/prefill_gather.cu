@@ -1,9 +1,9 @@
 // First half of the chunk attention's preparation: which query tiles there
 // are, and the cache rows that they attend, gathered from their pages.
 //
-// plan: one block, bound by the latency of its scans (6 us for three prompts, 8.5 for
-// 24 mixed requests, 12,000 to 16,500 cycles; with 512 threads and two passes always it
-// was 24,000 to 35,000). Request b has n = q_indptr[b + 1] - q_indptr[b] new tokens
+// plan: one block, bound by the latency of its scans (12,000 cycles for three prompts,
+// 16,500 for 24 mixed requests; with 512 threads and two passes always it was 24,000 to
+// 35,000). The gather runs beside it where every block can place the requests itself. Request b has n = q_indptr[b + 1] - q_indptr[b] new tokens
 // at positions L .. L + n - 1; its rows attend positions [lo, L + n) with
 // lo = max(0, L + 1 - window), the first row's start. Those rows are packed
 // request after request into a buffer, every request starting at a multiple of
@@ -233,16 +233,59 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t total,
 }
 static_assert(kPfPairs < 256, "clusters in a byte");
 
-__global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillArgs a) {
-  __shared__ int64_t sh[32 * 5];
-  pdl_launch_dependents();
-  pdl_wait();
+// Request b (a thread's) of one round. Carries what earlier rounds wished for and
+// spanned. All threads call it.
+struct Request {
+  int64_t len, n, q0, lo, want, groups, span;
+  bool small, good;
+};
+
+__device__ __forceinline__ Request request_of(const PrefillArgs& a, int b, int64_t* wished, int64_t* spanned, int64_t* sh) {
+  Request r = {};
+  const bool absorb = a.lay.absorb != 0;
+  bool ok = true;
+  if (b < a.batch) {
+    r.len = a.context_lens[b];
+    r.q0 = a.q_indptr[b];
+    r.n = a.q_indptr[b + 1] - r.q0;
+    // Row pointers outside q leave nothing that could be written.
+    if (r.q0 < 0 || r.n < 0 || r.q0 + r.n > a.q_rows) {
+      r.n = 0;
+      ok = false;
+    }
+    const int64_t nb = a.page_indptr ? a.page_indptr[b + 1] - a.page_indptr[b] : a.max_blocks;
+    if (r.len < 0 || r.len + r.n > nb * a.page_size || r.len + r.n > INT32_MAX) ok = ok && r.n == 0;
+    r.lo = a.window > 0 ? max(static_cast<int64_t>(0), r.len + 1 - a.window) : 0;
+  }
+  r.want = ok && r.n > 0 ? r.len + r.n - r.lo : 0;
+  int64_t round;
+  if (absorb) {
+    const int per_group = a.lay.group_tokens;  // (a power of two)
+    r.groups = r.want > 0 && r.n <= kPfSmallTokens ? (r.n + per_group - 1) >> (31 - __clz(per_group)) : 0;
+    const int64_t before = *wished + block_exclusive(r.groups, sh, &round);
+    r.small = r.groups > 0 && before + r.groups <= a.lay.max_groups;
+    *wished += round;
+  }
+  const int align = r.small ? kBlockTokens : kPfKvAlign;
+  r.span = (r.want + align - 1) & -static_cast<int64_t>(align);
+  const int64_t upto = *spanned + block_exclusive(r.span, sh, &round) + r.span;
+  *spanned += round;
+  r.good = ok && upto + (absorb ? 256 : 0) <= a.lay.kv_capacity;
+  r.small = r.small && r.good;
+  return r;
+}
+
+// Where small requests' rows start, behind `rows` of the expanded ones.
+__device__ __forceinline__ int64_t small_rows_start(int64_t rows) { return (rows + 255) / 256 * 256; }
+
+// The plan, by one block.
+__device__ __forceinline__ void plan(const PrefillArgs& a, int64_t* sh) {
   PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
   PfRequest* reqs = reinterpret_cast<PfRequest*>(a.ws + a.lay.requests);
   PfTile* tiles = reinterpret_cast<PfTile*>(a.ws + a.lay.tiles);
   PfGroup* groups = reinterpret_cast<PfGroup*>(a.ws + a.lay.groups);
   const bool absorb = a.lay.absorb != 0;
-  const int per_group = a.lay.group_tokens, group_shift = absorb ? 31 - __clz(per_group) : 0;  // (a power of two)
+  const int per_group = a.lay.group_tokens;
   // Sums over the requests so far: rows of the expanded ones, rows of the small ones,
   // requests that are not small, tiles, groups. With small requests a first pass
   // finds where their rows start, after all others'
@@ -252,7 +295,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   const bool one_round = a.batch <= threads;
   for (int pass = absorb && !one_round ? 0 : 1; pass < 2; ++pass) {
     if (pass == 1) {
-      small_start = (sum[0] + 255) / 256 * 256;
+      small_start = small_rows_start(sum[0]);
       small_first = sum[2];
     }
     int64_t wished = 0, spanned = 0;
@@ -260,61 +303,32 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
     for (int k = 0; k < 5; ++k) sum[k] = 0;
     for (int b0 = 0; b0 < a.batch; b0 += threads) {
       const int b = b0 + threadIdx.x;
-      int64_t len = 0, n = 0, q0 = 0, lo = 0;
-      bool ok = true;
-      if (b < a.batch) {
-        len = a.context_lens[b];
-        q0 = a.q_indptr[b];
-        n = a.q_indptr[b + 1] - q0;
-        // Row pointers outside q leave nothing that could be written.
-        if (q0 < 0 || n < 0 || q0 + n > a.q_rows) {
-          n = 0;
-          ok = false;
-        }
-        const int64_t nb = a.page_indptr ? a.page_indptr[b + 1] - a.page_indptr[b] : a.max_blocks;
-        if (len < 0 || len + n > nb * a.page_size || len + n > INT32_MAX) ok = ok && n == 0;
-        lo = a.window > 0 ? max(static_cast<int64_t>(0), len + 1 - a.window) : 0;
-      }
-      const int64_t want = ok && n > 0 ? len + n - lo : 0;
-      bool small = false;
-      int64_t ng = 0;
-      if (absorb) {
-        ng = want > 0 && n <= kPfSmallTokens ? (n + per_group - 1) >> group_shift : 0;
-        int64_t round;
-        const int64_t before = wished + block_exclusive(ng, sh, &round);
-        small = ng > 0 && before + ng <= a.lay.max_groups;
-        wished += round;
-      }
-      const int align = small ? kBlockTokens : kPfKvAlign;
-      const int64_t span = (want + align - 1) & -static_cast<int64_t>(align);
-      int64_t round;
-      const int64_t upto = spanned + block_exclusive(span, sh, &round) + span;
-      spanned += round;
-      const bool good = ok && upto + (absorb ? 256 : 0) <= a.lay.kv_capacity;
-      small = small && good;
+      const Request r = request_of(a, b, &wished, &spanned, sh);
+      const bool small = r.small, good = r.good;
+      const int64_t len = r.len, n = r.n, q0 = r.q0, lo = r.lo, span = r.span, ng = r.groups;
       const int64_t nt = small ? 0 : (n + kPfRows - 1) / kPfRows;
       int64_t v[5] = {small || !good ? 0 : span, small ? span : 0, b < a.batch && !small ? 1 : 0, nt, small ? ng : 0}, total[5];
       block_scan(v, total, sh);
       if (one_round) {
-        small_start = (total[0] + 255) / 256 * 256;
+        small_start = small_rows_start(total[0]);
         small_first = total[2];
       }
       if (pass == 1 && b < a.batch) {
         if (!good) atomicOr(&hd->status, MLA_STATUS_BAD_LENGTH);
-        PfRequest r;
-        r.base = static_cast<int>(small ? small_start + sum[1] + v[1] : sum[0] + v[0]);
-        r.rows = good ? static_cast<int>(want) : 0;
-        r.lo = static_cast<int>(lo);
-        r.b = b;
+        PfRequest p;
+        p.base = static_cast<int>(small ? small_start + sum[1] + v[1] : sum[0] + v[0]);
+        p.rows = good ? static_cast<int>(r.want) : 0;
+        p.lo = static_cast<int>(lo);
+        p.b = b;
         // (v[2] counts the others before this one: the rest before it are small)
-        reqs[small ? small_first + b - (sum[2] + v[2]) : sum[2] + v[2]] = r;
+        reqs[small ? small_first + b - (sum[2] + v[2]) : sum[2] + v[2]] = p;
         const int64_t tile0 = sum[3] + v[3];
         for (int64_t k = 0; k < nt && tile0 + k < a.lay.max_tiles; ++k) {
           PfTile t;
           const int64_t i0 = k * kPfRows;
           t.q_row = static_cast<int>(q0 + i0);
           t.rows = static_cast<int>(min(n - i0, static_cast<int64_t>(kPfRows)));
-          t.base = r.base;
+          t.base = p.base;
           t.first_end = good ? static_cast<int>(len + i0 + 1 - lo) : 0;
           t.kv_end = good ? t.first_end + t.rows - 1 : 0;
           t.kv_begin = good && a.window > 0 ? max(0, t.first_end - a.window) / kPfKvAlign * kPfKvAlign : 0;
@@ -326,7 +340,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
         if (small)
           for (int64_t k = 0; k < ng; ++k) {
             PfGroup g = {};
-            g.base = r.base;
+            g.base = p.base;
             g.first = static_cast<int>(len + k * per_group - lo);
             g.q_row = static_cast<int>(q0 + k * per_group);
             g.tokens = static_cast<int>(min(n - k * per_group, static_cast<int64_t>(per_group)));
@@ -411,6 +425,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   }
 }
 
+__global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillArgs a) {
+  __shared__ int64_t sh[32 * 5];
+  pdl_launch_dependents();
+  pdl_wait();
+  plan(a, sh);
+}
+
 // Two e4m3 codes to a bf16 pair (exact: bf16 has e4m3's values).
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t v) {
   const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(v));
@@ -433,28 +454,44 @@ __device__ __forceinline__ bool has_nonfinite(const uint4& v) {
   return has_nonfinite(v.x) || has_nonfinite(v.y) || has_nonfinite(v.z) || has_nonfinite(v.w);
 }
 
-constexpr int kGatherWarps = 8;
+constexpr int kGatherWarps = 8, kGatherThreads = 32 * kGatherWarps;
 
-// A block takes runs of kPfKvAlign rows (all of one request), two a warp.
-template <int kDtype>
-__global__ void __launch_bounds__(32 * kGatherWarps) prefill_gather_kernel(const PrefillArgs a) {
+// A block takes runs of kPfKvAlign rows (all of one request), two a warp. kFused: up to
+// kGatherThreads requests, whose places every block works out for itself while one
+// more block, the first, makes the plan.
+template <int kDtype, bool kFused>
+__global__ void __launch_bounds__(kGatherThreads, 4) prefill_gather_kernel(const PrefillArgs a) {
+  __shared__ PfRequest placed[kFused ? kGatherThreads : 1];
   pdl_launch_dependents();
   pdl_wait();
   PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
   const PfRequest* reqs = reinterpret_cast<const PfRequest*>(a.ws + a.lay.requests);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int used = hd->all_rows;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  if (a.lay.absorb) {  // page lists of the groups: their rows lie one after the other
-    const PfGroup* groups = reinterpret_cast<const PfGroup*>(a.ws + a.lay.groups);
-    int32_t* pages = reinterpret_cast<int32_t*>(a.ws + a.lay.group_pages);
-    const int num_groups = hd->num_groups;
-    for (int g = blockIdx.x * kGatherWarps + warp; g < num_groups; g += gridDim.x * kGatherWarps) {
-      const PfGroup p = groups[g];
-      for (int j = lane; j < p.pages; j += 32) pages[p.page0 + j] = p.base / kBlockTokens + j;
+  int used;
+  if (kFused) {
+    __shared__ int64_t sh[32 * 5];
+    if (blockIdx.x == 0) {
+      plan(a, sh);
+      return;
     }
+    const int b = threadIdx.x;
+    int64_t wished = 0, spanned = 0;
+    const Request r = request_of(a, b, &wished, &spanned, sh);
+    int64_t v[3] = {r.small || !r.good ? 0 : r.span, r.small ? r.span : 0, b < a.batch && !r.small ? 1 : 0}, total[3];
+    block_scan(v, total, sh);
+    const int64_t start = small_rows_start(total[0]);
+    if (b < a.batch)
+      placed[r.small ? total[2] + b - v[2] : v[2]] = {static_cast<int>(r.small ? start + v[1] : v[0]),
+                                                      r.good ? static_cast<int>(r.want) : 0, static_cast<int>(r.lo), b};
+    used = static_cast<int>(total[1] > 0 ? start + total[1] : total[0]);
+    reqs = placed;
+    __syncthreads();
+  } else {
+    used = hd->all_rows;
   }
-  for (int64_t run = blockIdx.x; run * kPfKvAlign < used; run += gridDim.x) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int first = blockIdx.x - (kFused ? 1 : 0), step = gridDim.x - (kFused ? 1 : 0);
+  for (int64_t run = first; run * kPfKvAlign < used; run += step) {
     const int row0 = static_cast<int>(run) * kPfKvAlign;
     int lo = 0, hi = a.batch;  // the last request with base <= row0
     while (hi - lo > 1) {
@@ -564,22 +601,28 @@ int sm_count() {
   return count[dev];
 }
 
-cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t stream) {
-  int threads = kCostBins;  // no more warps than requests and tiles: scans cost by the warp
-  while (threads < kPlanThreads && threads < max(static_cast<int64_t>(a.batch), a.lay.max_tiles)) threads *= 2;
-  return launch_pdl(prefill_plan_kernel, dim3(1), dim3(threads), 0, stream, a);
-}
-
 cudaError_t launch_prefill_merge(const PrefillArgs& a, int head0, int heads, cudaStream_t stream) {
   return launch_pdl(prefill_merge_kernel, dim3(152 * 4), dim3(256), 0, stream, a, head0, heads);
 }
 
+// One launch for both where a block's threads are enough for the requests and tiles,
+// else two. The smallest call takes 21.3 us so, 24.9 with two launches; a mixed step of
+// 24 requests 195 and 202 (210 with 2 blocks an SM instead of 4, 198 with 6).
 cudaError_t launch_prefill_gather(const PrefillArgs& a, cudaStream_t stream) {
-  const int64_t runs = a.lay.kv_capacity / kPfKvAlign;
-  const dim3 grid(static_cast<unsigned>(runs < 152 * 8 ? runs : 152 * 8)), block(32 * kGatherWarps);
-  if (a.dtype == MLA_DTYPE_BF16)
-    return launch_pdl(prefill_gather_kernel<MLA_DTYPE_BF16>, grid, block, 0, stream, a);
-  return launch_pdl(prefill_gather_kernel<MLA_DTYPE_FP8_E4M3>, grid, block, 0, stream, a);
+  const bool bf16 = a.dtype == MLA_DTYPE_BF16;
+  const int64_t runs = a.lay.kv_capacity / kPfKvAlign, most = max(static_cast<int64_t>(a.batch), a.lay.max_tiles);
+  const int64_t blocks = 152 * 4;
+  if (most <= kGatherThreads) {
+    const dim3 grid(static_cast<unsigned>(1 + min(runs, blocks)));
+    return launch_pdl(bf16 ? prefill_gather_kernel<MLA_DTYPE_BF16, true> : prefill_gather_kernel<MLA_DTYPE_FP8_E4M3, true>, grid,
+                      dim3(kGatherThreads), 0, stream, a);
+  }
+  int threads = kCostBins;  // no more warps than requests and tiles: scans cost by the warp
+  while (threads < kPlanThreads && threads < most) threads *= 2;
+  const cudaError_t e = launch_pdl(prefill_plan_kernel, dim3(1), dim3(threads), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(bf16 ? prefill_gather_kernel<MLA_DTYPE_BF16, false> : prefill_gather_kernel<MLA_DTYPE_FP8_E4M3, false>,
+                    dim3(static_cast<unsigned>(min(runs, blocks))), dim3(kGatherThreads), 0, stream, a);
 }
 
 }  // namespace mla

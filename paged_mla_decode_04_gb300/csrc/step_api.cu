@@ -271,8 +271,7 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
     if (c <= 0) return MLA_ERR_CUDA;
     a.clusters = c < mla::kPfPairs ? c : mla::kPfPairs;
   }
-  cudaError_t e = mla::launch_prefill_plan(a, st);
-  if (e == cudaSuccess) e = mla::launch_prefill_gather(a, st);
+  cudaError_t e = mla::launch_prefill_gather(a, st);
   if (e == cudaSuccess && a.lay.absorb) {
     const int rc = attend_small(m, a, q, st);
     if (rc != MLA_OK) return rc;

@@ -267,8 +267,7 @@ struct PrefillMaps {
 cudaError_t launch_extend_tables(const TablesArgs& a, cudaStream_t stream);
 // rope_write.cu
 cudaError_t launch_rope_write(const RopeArgs& a, int dtype, cudaStream_t stream);
-// prefill_gather.cu: tiles and row numbers, then the rows themselves
-cudaError_t launch_prefill_plan(const PrefillArgs& a, cudaStream_t stream);
+// prefill_gather.cu: tiles and row numbers, and the rows themselves
 cudaError_t launch_prefill_gather(const PrefillArgs& a, cudaStream_t stream);
 // prefill_expand.cu: keys and values of heads [head0, head0 + heads)
 cudaError_t launch_prefill_expand(const PrefillMaps& m, const PrefillArgs& a, int head0, int heads, cudaStream_t stream);
