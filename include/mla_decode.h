@@ -304,7 +304,7 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  * Keys and values of all heads are made once (512 bytes per head and attended
  * position, in the workspace) and then attended at 640 flops a pair; making
  * them costs as much as 410 queries' attention. So requests of up to 64 new
- * tokens (single tokens among chunks) are attended in the latent space instead,
+ * tokens (112 over 3,000 positions and more) are attended in the latent space,
  * by the kernel of mla_decode, at 2,176 flops a pair: in calls of 16, 32, 64 or
  * 128 heads with max_kv_tokens * num_heads >= 200,000. A step of single tokens
  * alone is mla_decode's.

@@ -261,7 +261,8 @@ __device__ __forceinline__ Request request_of(const PrefillArgs& a, int b, int64
   int64_t round;
   if (absorb) {
     const int per_group = a.lay.group_tokens;  // (a power of two)
-    r.groups = r.want > 0 && r.n <= kPfSmallTokens ? (r.n + per_group - 1) >> (31 - __clz(per_group)) : 0;
+    const int most = r.want >= kPfSmallSpan ? kPfSmallTokens : kPfSmallTokensShort;
+    r.groups = r.want > 0 && r.n <= most ? (r.n + per_group - 1) >> (31 - __clz(per_group)) : 0;
     const int64_t before = *wished + block_exclusive(r.groups, sh, &round);
     r.small = r.groups > 0 && before + r.groups <= a.lay.max_groups;
     *wished += round;

@@ -109,9 +109,13 @@ struct PfSplit {
 // rows that are requests of their own to it. Their rows start at multiples of its
 // 64-token blocks, so that the row buffer is its pool, with pages of 64 rows.
 // Latent / expanded, us a call, 8 requests of n new tokens over 4,000: 128 heads, n = 1
-// 87 / 1089, 16 212 / 1093, 32 359 / 1097, 64 650 / 1126; 16 heads, n = 16 93 / 184,
-// 32 113 / 183, 64 151 / 188, and beyond 64 a tie.
-constexpr int kPfSmallTokens = 64;
+// 87 / 1089, 16 212 / 1093, 64 635 / 1126, 112 1093 / 1331, 128 1252 / 1329; 16 heads,
+// 16 93 / 184, 64 130 / 188, 112 181 / 192, 128 196 / 193. Where there are few positions
+// the expanded form starts no later: 4 requests over 1,000, 128 heads, 64 157 / 190, 96
+// 220 / 207, 112 251 / 209; one over 1,600, 96 104 / 105, 112 111 / 104.
+constexpr int kPfSmallTokens = 112;    // at most, from kPfSmallSpan attended positions on
+constexpr int kPfSmallSpan = 3000;
+constexpr int kPfSmallTokensShort = 64;  // with fewer
 constexpr int kPfSmallRows = 1 << 17;  // (token, head) rows of all small requests at most
 
 struct PfGroup {
@@ -159,7 +163,7 @@ struct PfLayout {
 // Calls whose keys and values of all heads would take more than about 30 us to make
 // look for small requests: the four launches of that path cost 10 to 13 us where there
 // are none (404 / 392 us with and without), and one request of 8 new tokens over 1,600, 128
-// heads, takes 57 us there against 100, of 64 new tokens 98 against 101.
+// heads, takes 57 us there against 100, of 64 new tokens 86 against 100.
 inline bool pf_may_absorb(int64_t max_kv, int num_heads) {
   return (num_heads == 16 || num_heads == 32 || num_heads == 64 || num_heads == 128) && max_kv * num_heads >= 200000;
 }

@@ -87,13 +87,13 @@ def norm(ckv, weight, eps):
     return ckv / np.sqrt((ckv ** 2).mean(-1, keepdims=True) + eps) * weight.astype(np.float64)
 
 
-def prefill(rows_of, q, indptr, ctx, w_uk, w_uv, scale, window, latent=lambda n: False):
+def prefill(rows_of, q, indptr, ctx, w_uk, w_uv, scale, window, latent=lambda n, m: False):
     """rows_of(b, positions) -> latent rows [m, 576] in float64. Returns out
     [T, H, 128], lse [T, H] and the largest change that the kernel's roundings
     can make to each output (and to lse): keys, values, softmax weights and
     output are rounded to bf16 (2^-8 of each), products summed in fp32 over at
     most 576 + n terms (2^-24 each, doubled for the approximate 2^x).
-    latent(n): whether a request of n new tokens is attended in the latent space:
+    latent(n, m): whether a request of n new tokens over m positions is attended in the latent space:
     there the query brought into it (512 dims) and the latent output are rounded
     to bf16 instead of keys and values, and each half of a score to fp16 (2^-11)."""
     T, H, _ = q.shape
@@ -120,7 +120,7 @@ def prefill(rows_of, q, indptr, ctx, w_uk, w_uv, scale, window, latent=lambda n:
         v_sum = lat[None, :, :CKV].abs() @ wv.abs()
         ds = mag * BF16_HALF + mag_all * 2 * QK * F32_HALF
         ds += (qb[:, :, :NOPE].abs() @ k_sum.transpose(1, 2)) * scale * CKV * F32_HALF
-        if latent(n):
+        if latent(n, len(at)):
             qa = qb[:, :, :NOPE] @ wk                                         # [H, n, 512]
             c_abs, r_abs = lat[:, :CKV].abs(), lat[:, CKV:].abs()
             whole = qa.abs() @ c_abs.T + qb[:, :, NOPE:].abs() @ r_abs.T       # of both halves' sizes
@@ -140,7 +140,7 @@ def prefill(rows_of, q, indptr, ctx, w_uk, w_uv, scale, window, latent=lambda n:
         # (also in their sum's place), values by 2^-8, all of it relative to sum p |v|
         weight = torch.expm1(2 * d) + 2 * BF16_HALF + (len(at) + 64) * 2 * F32_HALF
         e = (p @ v.abs()) * (weight * (1 + BF16_HALF) + BF16_HALF) + o.abs() * BF16_HALF + (p @ v_sum) * CKV * F32_HALF
-        if latent(n):
+        if latent(n, len(at)):
             # Latent sums off like the values' above, rounded, then multiplied into 128 dims.
             c_abs = lat[:, :CKV].abs()
             d_lat = (p @ c_abs) * weight + (p @ lat[:, :CKV]).abs() * BF16_HALF * (1 + weight)

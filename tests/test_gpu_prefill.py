@@ -82,10 +82,10 @@ class Case:
         vals, table = self.values(), self.table.cpu().numpy()
         return step_ref.prefill(lambda b, at: vals[table[b][at // self.ps], at % self.ps], f64(self.q),
                                 self.indptr.cpu().numpy(), self.ctx.cpu().numpy(), f64(self.w_uk), f64(self.w_uv),
-                                self.scale, self.window, lambda n: self.latent() and n <= 64)
+                                self.scale, self.window, lambda n, m: self.latent() and n <= (112 if m >= 3000 else 64))
 
     def latent(self):
-        """Calls of this size attend requests of up to 64 new tokens in the latent space."""
+        """Calls of this size attend requests of up to 64 new tokens (112 over 3,000 positions) in the latent space."""
         return self.heads in (16, 32, 64, 128) and self.max_kv * self.heads >= 200000
 
     def check(self, norm=6e-3, status=0):
@@ -376,7 +376,10 @@ def test_graph_replay_with_changed_lengths(lib):
     (32, [2500, 1, 3900], [10, 64, 3], 0, False),
     (64, [1100, 2100], [5, 64], 0, True),
     (128, [900, 800, 10], [3, 130, 64], 0, False),
-    (128, [1700], [1], 0, False)])
+    (128, [1700], [1], 0, False),
+    (16, [4000, 2935, 2935, 2999, 5000], [112, 64, 65, 65, 113], 0, True),
+    (16, [4000, 9000, 5000], [112, 80, 112], 2900, False),
+    (64, [3300], [100], 0, False)])
 def test_small_requests_in_the_latent_space(lib, heads, ctx, new, window, fp8):
     """Few new tokens over long caches, alone and beside chunks; every token group, partly filled ones among them."""
     c = Case(lib, ctx, new, heads=heads, window=window, fp8=fp8, seed=heads, spare_kv=0 if not window else 20000)
@@ -408,7 +411,7 @@ def test_many_small_requests_past_the_room_for_them(lib):
     assert 1000 < int(c.ws[:32].view(torch.int32)[7]) <= 1024
     vals, table, m = c.values(), c.table.cpu().numpy(), sum(new)
     tols = []
-    for form in (lambda n: True, lambda n: False):  # (which requests are expanded is the plan's choice)
+    for form in (lambda n, m: True, lambda n, m: False):  # (which requests are expanded is the plan's choice)
         ref, _, tol, _ = step_ref.prefill(lambda b, at: vals[table[b][at // c.ps], at % c.ps], f64(c.q),
                                           c.indptr.cpu().numpy(), c.ctx.cpu().numpy(), f64(c.w_uk), f64(c.w_uv),
                                           c.scale, 0, form)
@@ -473,7 +476,7 @@ def test_most_heads_and_a_workspace_cut_to_fit_half(lib):
     assert torch.equal(bits(a.out), bits(b.out)) and bool((guard[size:] == 0x5a).all())
 
 
-@pytest.mark.parametrize("heads,per_pass,new", [(2, 0, 1), (16, 2, 65)])
+@pytest.mark.parametrize("heads,per_pass,new", [(2, 0, 1), (16, 2, 113)])
 def test_rows_past_32_bit_offsets(lib, heads, per_pass, new):
     """A request behind one of 3.84 million tokens, whose gathered rows take 4.4 GB. The long one's pages are one
     page over and over, so that with one new token it is attention over that page's 128 rows."""
