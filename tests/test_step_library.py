@@ -139,3 +139,13 @@ def test_prefill_workspace_grows_with_heads(lib, batch, q_rows, max_kv):
     # heads a pass must never need more room.
     sizes = [lib.mla_prefill_workspace_size(batch, q_rows, max_kv, 1024, h) for h in range(1, 1025)]
     assert all(a < b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_compiled_binding(lib):
+    import paged_mla_decode_04_gb300 as m
+    b = m._step()
+    for name, n in (("extend_tables", 15), ("rope_write", 15), ("prefill", 18), ("bind", 3)):
+        with pytest.raises(TypeError, match="%d arguments expected" % n):
+            getattr(b, name)()
+    with pytest.raises(ValueError, match="entry point"):
+        b.bind(0, 0, 0)
