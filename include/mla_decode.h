@@ -303,9 +303,9 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *   out = sum_t softmax(s)_t v_t,  lse = log(sum_t exp(s_t)).
  * Keys and values of all heads are made once (512 bytes per head and attended
  * position, in the workspace) and then attended at 640 flops a pair; making
- * them costs as much as 410 queries' attention. So requests of up to 64 new
- * tokens (112 over 3,000 positions and more) are attended in the latent space,
- * by the kernel of mla_decode, at 2,176 flops a pair: in calls of 16, 32, 64 or
+ * them costs as much as 410 queries' attention. So requests of up to 32 new
+ * tokens (56 over 3,000 positions and more) are attended in the latent space, by
+ * the kernel of mla_decode, at 2 x 2,176 flops a pair: in calls of 16, 32, 64 or
  * 128 heads with max_kv_tokens * num_heads >= 200,000. A step of single tokens
  * alone is mla_decode's.
  *   q:        device, [q_rows][num_heads][192] bf16 (nope 128 || rope 64).
@@ -323,8 +323,10 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *             workspace, and not shared by calls that overlap on the GPU.
  * num_heads is 1 to 1024. Arithmetic: fp32 accumulation and softmax sums; for
  * the tensor core keys are rounded to bf16, values and softmax weights to f16
- * (values beyond +-65504 saturate). In the latent space the query there and
- * the latent result are rounded to bf16, scores as in mla_decode. fp8 pools:
+ * (values beyond +-65504 saturate). In the latent space a pair of bf16
+ * queries stands for the exact one, scores and softmax weights are
+ * mla_decode's. The result is off by 1.7e-3 to 2.1e-3 (2-norm, of independent
+ * normal values; 1.7e-3 is its own rounding to bf16). fp8 pools:
  * the codes are widened exactly and kv_scale multiplies the scores and the
  * output. A call repeated gives the same bits; with other requests, capacities
  * or heads a pass beside it a request's sums may be taken in another order.

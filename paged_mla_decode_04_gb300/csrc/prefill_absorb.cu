@@ -2,14 +2,19 @@
 // that attends them in the latent space:
 //   q_latent[slot][h] = (q_nope W_UK[h], q_rope)      [512 + 64], rounded to bf16,
 //   out[row][h]       = latent[slot][h] W_UV[h]       [128].
-// A slot is a token's place in its group (group g holds slots g t .. g t + t - 1,
-// t tokens a full group); slots without a token are left out. Per head these are
+// The decode leaves every item's sums in fp32 (one rounding of the result to bf16, not
+// two), which a kernel between joins, weighed by their lse, into a pair of bf16 rows,
+// the value and what rounding took from it: both are multiplied.
+// A slot is a token's place in its pair of groups (pair g holds slots g t .. g t + t - 1,
+// t tokens a full group); slots without a token are left out. The query is stored
+// twice, rounded one way and the other (see PfGroup). Per head these are
 // products over all slots, [slots x 128] x [128 x 512] and [slots x 512] x
 // [512 x 128], bound by reading the weights (256 KB a head) for the few hundred
 // slots of a step: one block per (head, 128 slots), one pass over the weights. With
 // about 600 slots of 16 heads they take 11 and 7.6 us beside 40 us of the decode; in a
 // call that turns out to have no small request, the path's four launches cost 10 to 13.
 #include <cuda_bf16.h>
+#include <math_constants.h>
 
 #include "../../include/mla_decode.h"
 #include "ptx_prefill.cuh"
@@ -24,8 +29,8 @@ constexpr int kChunk = 128 * 128;  // [128 rows][64 columns] of bf16, swizzled
 // The token of a slot, or false.
 __device__ __forceinline__ bool slot_token(const PrefillArgs& a, int slot, int num_groups, int* row) {
   const int t = a.lay.group_tokens, g = slot / t, i = slot - g * t;
-  if (g >= num_groups) return false;
-  const PfGroup& group = reinterpret_cast<const PfGroup*>(a.ws + a.lay.groups)[g];
+  if (2 * g >= num_groups) return false;
+  const PfGroup& group = reinterpret_cast<const PfGroup*>(a.ws + a.lay.groups)[2 * g];
   *row = group.q_row + i;
   return i < group.tokens;
 }
@@ -56,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = tid & 31; j < p.pages; j += 32) pages[p.page0 + j] = p.base / kBlockTokens + j;
     }
   }
-  if (blockIdx.y * 128 >= num_groups * a.lay.group_tokens) return;
+  if (blockIdx.y * 128 >= num_groups / 2 * a.lay.group_tokens) return;
   if (tid == 0) {
     mbar_init(full, 1);
     mbar_init(done, 1);
@@ -105,7 +110,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (!ready && (tid & 31) == 0) atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
   if (ready) {
-    uint8_t* dst = a.ws + a.lay.q_latent + (static_cast<int64_t>(slot) * heads + h) * (kDimRow * 2);
+    const int t = a.lay.group_tokens, first = slot + slot / t * t;  // the slot's place in the pair's first group
+    uint8_t* dst = a.ws + a.lay.q_latent + (static_cast<int64_t>(first) * heads + h) * (kDimRow * 2);
+    uint8_t* dst2 = dst + static_cast<int64_t>(t) * heads * (kDimRow * 2);
 #pragma unroll 1
     for (int c = 0; c < 16; ++c) {
       uint32_t r[32];
@@ -114,16 +121,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (valid) {
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          uint32_t pk[8];
+          uint32_t pk[8], other[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1]));
+          for (int i = 0; i < 8; ++i) {
+            const float x = __uint_as_float(r[16 * v + 2 * i]), y = __uint_as_float(r[16 * v + 2 * i + 1]);
+            pk[i] = pack_bf16x2(x, y);
+            other[i] = pack_bf16x2(2.f * x - __uint_as_float(pk[i] << 16), 2.f * y - __uint_as_float(pk[i] & 0xffff0000u));
+          }
           st_global_v8(dst + 64 * c + 32 * v, pk);
+          st_global_v8(dst2 + 64 * c + 32 * v, other);
         }
       }
     }
     if (valid)
-      for (int j = 0; j < 8; ++j) reinterpret_cast<uint4*>(dst + kDimCkv * 2)[j] = src[16 + j];
+      for (int j = 0; j < 8; ++j)
+        reinterpret_cast<uint4*>(dst + kDimCkv * 2)[j] = reinterpret_cast<uint4*>(dst2 + kDimCkv * 2)[j] = src[16 + j];
   }
   tc_fence_before();
   __syncthreads();
@@ -131,8 +143,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-constexpr int kStages = 6;
-constexpr int kVStage = 2 * kChunk;  // 64 of the 512 dims: [128 slots][64], W_UV [64][2 x 64]
+// A warp joins the partial sums of one (slot, head), 16 dims a lane.
+constexpr int kJoinWarps = 8;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) prefill_latent_kernel(const PrefillArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const PfHeader* hd = reinterpret_cast<const PfHeader*>(a.ws);
+  const int lane = threadIdx.x & 31, heads = a.num_heads;
+  const PfGroup* groups = reinterpret_cast<const PfGroup*>(a.ws + a.lay.groups);
+  const float* lses = reinterpret_cast<const float*>(a.ws + a.lay.decode + a.lay.decode_lay.partial_lse);
+  const float4* sums = reinterpret_cast<const float4*>(a.ws + a.lay.decode + a.lay.decode_lay.partial_o);
+  uint2* out = reinterpret_cast<uint2*>(a.ws + a.lay.latent);
+  const int64_t rest = static_cast<int64_t>(a.lay.max_pairs) * kGroupRows * (kDimCkv / 4);  // of a row's remainder, in uint2
+  const int rows = hd->num_groups / 2 * kGroupRows;
+  for (int r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5); r < rows; r += gridDim.x * kJoinWarps) {
+    const int row = r % kGroupRows, token = row / heads;  // of the group
+    const PfGroup g = groups[2 * (r / kGroupRows)];
+    if (token >= g.tokens) continue;
+    const int items = g.items + groups[2 * (r / kGroupRows) + 1].items;  // (the pair's lie one after the other)
+    const int64_t first = static_cast<int64_t>(g.first_item) * kGroupRows + row;
+    float m = -3e38f;
+    for (int p = 0; p < items; ++p) m = fmaxf(m, lses[first + static_cast<int64_t>(p) * kGroupRows]);
+    float4 o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int p = 0; p < items; ++p) {
+      const int64_t at = first + static_cast<int64_t>(p) * kGroupRows;
+      const float lse = lses[at];
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = sums[at * (kDimCkv / 4) + lane + 32 * j];
+      const float w = exp2f(lse - m);  // 0 (of zeros) where the row has no position in the item; NaN sums stay NaN
+      l += w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[j].x = fmaf(w, v[j].x, o[j].x);
+        o[j].y = fmaf(w, v[j].y, o[j].y);
+        o[j].z = fmaf(w, v[j].z, o[j].z);
+        o[j].w = fmaf(w, v[j].w, o[j].w);
+      }
+    }
+    const float inv = 1.f / l;
+    auto rounded = [](float x) { return __bfloat162float(__float2bfloat16_rn(x)); };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x[4] = {o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv};
+      const int64_t at = static_cast<int64_t>(r) * (kDimCkv / 4) + lane + 32 * j;
+      out[at] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      out[rest + at] = make_uint2(pack_bf16x2(x[0] - rounded(x[0]), x[1] - rounded(x[1])),
+                                  pack_bf16x2(x[2] - rounded(x[2]), x[3] - rounded(x[3])));
+    }
+    if (a.lse && lane == 0)  // (a row without a NaN attends itself: l > 0)
+      a.lse[(static_cast<int64_t>(g.q_row) + token) * heads + row % heads] =
+          l > 0.f && o[0].x == o[0].x ? (m + log2f(l) - 1.f) * 0.69314718055994531f : CUDART_NAN_F;
+  }
+}
+
+constexpr int kStages = 4;
+constexpr int kVStage = 3 * kChunk;  // 64 of the 512 dims: [128 slots][64] twice, W_UV [64][2 x 64]
 constexpr int kVOffBar = kStages * kVStage;
 constexpr int kVSmem = kVOffBar + 256 + 1024;
 
@@ -156,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bits = reinterpret_cast<const WsHeader*>(a.ws + a.lay.decode)->status;  // (of the decode kernel)
     if (bits) atomicOr(&hd->status, bits);
   }
-  if (slot0 >= num_groups * a.lay.group_tokens) return;
+  if (slot0 >= num_groups / 2 * a.lay.group_tokens) return;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full(s), 1);
@@ -182,8 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dst = sbase + s * kVStage;
       mbar_arrive_expect_tx(full(s), kVStage);
       tma_load_3d(dst, &latent, full(s), 64 * k, h, slot0);
-      tma_load_2d(dst + kChunk, &w_uv, full(s), 0, h * kDimCkv + 64 * k);
-      tma_load_2d(dst + kChunk + kChunk / 2, &w_uv, full(s), 64, h * kDimCkv + 64 * k);
+      tma_load_3d(dst + kChunk, &latent, full(s), 64 * k, h, a.lay.max_pairs * a.lay.group_tokens + slot0);
+      tma_load_2d(dst + 2 * kChunk, &w_uv, full(s), 0, h * kDimCkv + 64 * k);
+      tma_load_2d(dst + 2 * kChunk + kChunk / 2, &w_uv, full(s), 64, h * kDimCkv + 64 * k);
     }
   } else if (warp == 1 && lane == 0) {
     constexpr uint32_t idesc = idesc_bf16(128, 128, false, true);
@@ -193,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t st = sbase + s * kVStage;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mma_bf16_ss(tmem, sdesc_sw128(st + i * 32, 16, 1024), sdesc_sw128(st + kChunk + i * 2048, kChunk / 2, 1024), idesc,
-                    (k | i) != 0);
+      for (int i = 0; i < 8; ++i)
+        mma_bf16_ss(tmem, sdesc_sw128(st + (i >> 2) * kChunk + (i & 3) * 32, 16, 1024),
+                    sdesc_sw128(st + 2 * kChunk + (i & 3) * 2048, kChunk / 2, 1024), idesc, (k | i) != 0);
       mma_commit(empty(s));
       if (k == kSteps - 1) mma_commit(done);
     }
@@ -224,8 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (a.lse && valid)
-      a.lse[out_row] = reinterpret_cast<const float*>(a.ws + a.lay.latent_lse)[static_cast<int64_t>(slot0 + tid) * heads + h];
   }
   tc_fence_before();
   __syncthreads();
@@ -234,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 dim3 slots_grid(const PrefillArgs& a) {
-  return dim3(a.num_heads, (a.lay.max_groups * a.lay.group_tokens + 127) / 128);
+  return dim3(a.num_heads, (a.lay.max_pairs * a.lay.group_tokens + 127) / 128);
 }
 
 }  // namespace
@@ -245,6 +314,12 @@ cudaError_t launch_prefill_q_latent(const CUtensorMap& w_uk, const PrefillArgs& 
   if (e != cudaSuccess) return e;
   return launch_pdl(prefill_q_latent_kernel, slots_grid(a), dim3(kThreads), kQSmem, stream, w_uk, a,
                     static_cast<const uint4*>(q));
+}
+
+cudaError_t launch_prefill_latent(const PrefillArgs& a, cudaStream_t stream) {
+  const int64_t most = static_cast<int64_t>(a.lay.max_pairs) * (kGroupRows / kJoinWarps);
+  return launch_pdl(prefill_latent_kernel, dim3(static_cast<unsigned>(most < 152 * 4 ? most : 152 * 4)), dim3(32 * kJoinWarps),
+                    0, stream, a);
 }
 
 cudaError_t launch_prefill_v_latent(const CUtensorMap& latent, const CUtensorMap& w_uv, const PrefillArgs& a,

@@ -146,23 +146,22 @@ __device__ __forceinline__ int group_blocks(const PfGroup& g, int window) {
 
 // The decode kernel's schedule for the groups of small requests: their 64-row
 // blocks, each group weighing kGroupCost more for its start and end, `total` in all,
-// laid out in a row and cut into equal ranges, one a cluster; a group across a cut
-// leaves partial sums that the decode's merge joins. All threads call it.
+// laid out in a row and cut into equal ranges, one a cluster; a group across a cut has
+// several items. All threads call it.
 constexpr int kGroupCost = 4;
 constexpr int kMostItems = kPfSmallRows / kGroupRows + kPfPairs;
 
 __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t total, int64_t* sh) {
   __shared__ uint8_t cluster_of_item[kMostItems];
   const PfLayout& lay = a.lay;
-  const PfGroup* gs = reinterpret_cast<const PfGroup*>(a.ws + lay.groups);
+  PfGroup* gs = reinterpret_cast<PfGroup*>(a.ws + lay.groups);
   uint8_t* ws = a.ws + lay.decode;
   WsHeader* hd = reinterpret_cast<WsHeader*>(ws);
   WorkItem* items = reinterpret_cast<WorkItem*>(ws + lay.decode_lay.items);
   int* cstart = reinterpret_cast<int*>(ws + lay.decode_lay.cluster_start);
-  SplitRequest* split = reinterpret_cast<SplitRequest*>(ws + lay.decode_lay.split);
   const int tid = threadIdx.x, step = blockDim.x;
   const int64_t per = max(static_cast<int64_t>(1), (total + a.clusters - 1) / a.clusters);  // units of a cluster
-  int64_t carry[4] = {0, 0, 0, 0};  // units, items, partial slots, split groups
+  int64_t carry[2] = {0, 0};  // units, items
   for (int i0 = 0; i0 < groups; i0 += step) {
     const int i = i0 + tid;
     PfGroup g = {};
@@ -171,12 +170,11 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t total,
       g = gs[i];
       n = group_blocks(g, a.window);
     }
-    int64_t units;
+    int64_t units, round;
     const int64_t off = carry[0] + block_exclusive(n ? n + kGroupCost : 0, sh, &units) + kGroupCost;
     const int cf = n ? static_cast<int>(off / per) : 0, cl = n ? static_cast<int>((off + n - 1) / per) : -1;
     const int pieces = cl - cf + 1;
-    int64_t v[3] = {pieces, pieces > 1 ? pieces : 0, pieces > 1 ? 1 : 0}, sums[3];
-    block_scan(v, sums, sh);
+    const int item0 = static_cast<int>(carry[1] + block_exclusive(pieces, sh, &round));
     for (int k = 0; k < pieces; ++k) {
       WorkItem w;
       const int64_t lo = max(off, (cf + k) * per), hi = min(off + n, (cf + k + 1) * per);
@@ -184,25 +182,20 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t total,
       w.b = i;
       w.blk_begin = blk0 + static_cast<int>(lo - off);
       w.blk_end = blk0 + static_cast<int>(hi - off);
-      w.slot = pieces > 1 ? static_cast<int>(carry[2] + v[1] + k) : -1;
+      w.slot = item0 + k;  // (even a whole group's sums stay in fp32)
       w.tok_lo = first;
       w.tok_hi = g.first + lay.group_tokens;  // (as if the group were full: its rows count from here)
       w.cluster = cf + k;
       w.row0 = 0;
-      items[carry[1] + v[0] + k] = w;
-      cluster_of_item[carry[1] + v[0] + k] = static_cast<uint8_t>(cf + k);
+      items[item0 + k] = w;
+      cluster_of_item[item0 + k] = static_cast<uint8_t>(cf + k);
     }
-    if (pieces > 1) {
-      SplitRequest r;
-      r.b = i;
-      r.num_splits = pieces;
-      r.first_partial = static_cast<int>(carry[2] + v[1]);
-      r.row0 = 0;
-      split[carry[3] + v[2]] = r;
+    if (i < groups) {
+      gs[i].first_item = item0;
+      gs[i].items = pieces;
     }
     carry[0] += units;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) carry[k + 1] += sums[k];
+    carry[1] += round;
   }
   __syncthreads();
   const int num_items = static_cast<int>(carry[1]);
@@ -217,7 +210,7 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t total,
   }
   if (tid == 0) {
     hd->status = 0;
-    hd->batch = lay.max_groups;
+    hd->batch = 2 * lay.max_pairs;
     hd->num_heads = a.num_heads;
     hd->q_len = lay.group_tokens;
     hd->page_size = kBlockTokens;
@@ -225,8 +218,8 @@ __device__ void schedule_groups(const PrefillArgs& a, int groups, int64_t total,
     hd->num_clusters = static_cast<int>(max(static_cast<int64_t>(1), (total + per - 1) / per));
     hd->total_blocks = static_cast<int>(min(total, static_cast<int64_t>(INT32_MAX)));
     hd->num_items = num_items;
-    hd->num_partials = static_cast<int>(carry[2]);
-    hd->num_split = static_cast<int>(carry[3]);
+    hd->num_partials = num_items;
+    hd->num_split = 0;
     hd->schedule = kScheduleCut;
     hd->planned = 1;
   }
@@ -262,9 +255,9 @@ __device__ __forceinline__ Request request_of(const PrefillArgs& a, int b, int64
   if (absorb) {
     const int per_group = a.lay.group_tokens;  // (a power of two)
     const int most = r.want >= kPfSmallSpan ? kPfSmallTokens : kPfSmallTokensShort;
-    r.groups = r.want > 0 && r.n <= most ? (r.n + per_group - 1) >> (31 - __clz(per_group)) : 0;
+    r.groups = r.want > 0 && r.n <= most ? (r.n + per_group - 1) >> (31 - __clz(per_group)) << 1 : 0;
     const int64_t before = *wished + block_exclusive(r.groups, sh, &round);
-    r.small = r.groups > 0 && before + r.groups <= a.lay.max_groups;
+    r.small = r.groups > 0 && before + r.groups <= 2 * a.lay.max_pairs;
     *wished += round;
   }
   const int align = r.small ? kBlockTokens : kPfKvAlign;
@@ -339,14 +332,15 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, int64_t* sh) {
           tiles[tile0 + k] = t;
         }
         if (small)
-          for (int64_t k = 0; k < ng; ++k) {
+          for (int64_t k = 0; 2 * k < ng; ++k) {
             PfGroup g = {};
             g.base = p.base;
             g.first = static_cast<int>(len + k * per_group - lo);
             g.q_row = static_cast<int>(q0 + k * per_group);
             g.tokens = static_cast<int>(min(n - k * per_group, static_cast<int64_t>(per_group)));
             g.pages = (g.first + g.tokens - 1) / kBlockTokens + 1;
-            groups[sum[4] + v[4] + k] = g;
+            groups[sum[4] + v[4] + 2 * k] = g;
+            groups[sum[4] + v[4] + 2 * k + 1] = g;
           }
       }
 #pragma unroll

@@ -36,11 +36,12 @@ bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], co
 
 // Small requests through the decode kernel: their queries into the latent space,
 // one decode over the gathered rows as its pool (pages of 64 rows, a request per
-// row group), the result out of it.
+// row group), its sums joined, the result out of the latent space.
 int attend_small(const mla::PrefillMaps& m, const mla::PrefillArgs& a, const void* q, cudaStream_t st) {
   const mla::PfLayout& lay = a.lay;
   const uint64_t rows = static_cast<uint64_t>(lay.kv_capacity), h = a.num_heads;
-  const uint64_t q_rows = static_cast<uint64_t>(lay.max_groups) * mla::kGroupRows;
+  const int groups = 2 * lay.max_pairs;
+  const uint64_t q_rows = static_cast<uint64_t>(groups) * mla::kGroupRows;
   constexpr auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   uint8_t *pool = a.ws + lay.rows, *qs = a.ws + lay.q_latent, *out = a.ws + lay.latent;
   CUtensorMap maps[5], latent;
@@ -49,7 +50,7 @@ int attend_small(const mla::PrefillMaps& m, const mla::PrefillArgs& a, const voi
       !make_map_2d(&maps[2], bf16, qs, q_rows, mla::kDimRow, mla::kDimRow * 2, 64, 128) ||
       !make_map_2d(&maps[3], bf16, qs, q_rows, mla::kDimRow, mla::kDimRow * 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
       !make_map_3d(&maps[4], pool, {64, rows, 8}, {mla::kDimRow * 2ull, 128}, {64, 64, 4}) ||
-      !make_map_3d(&latent, out, {mla::kDimCkv, h, static_cast<uint64_t>(lay.max_groups) * lay.group_tokens},
+      !make_map_3d(&latent, out, {mla::kDimCkv, h, 2ull * lay.max_pairs * lay.group_tokens},
                    {mla::kDimCkv * 2ull, h * mla::kDimCkv * 2ull}, {64, 1, 128}))
     return MLA_ERR_CUDA;
   mla::DecodeArgs d = {};
@@ -57,10 +58,9 @@ int attend_small(const mla::PrefillMaps& m, const mla::PrefillArgs& a, const voi
   d.page_indptr = reinterpret_cast<const int32_t*>(a.ws + lay.group_indptr);
   d.page_ids = reinterpret_cast<const int32_t*>(a.ws + lay.group_pages);
   d.out = out;
-  d.lse = reinterpret_cast<float*>(a.ws + lay.latent_lse);
   d.ws = a.ws + lay.decode;
   d.lay = lay.decode_lay;
-  d.batch = lay.max_groups;
+  d.batch = groups;
   d.num_heads = a.num_heads;
   d.q_len = lay.group_tokens;
   d.rows = d.group_rows = mla::kGroupRows;
@@ -75,7 +75,7 @@ int attend_small(const mla::PrefillMaps& m, const mla::PrefillArgs& a, const voi
   d.out_scale = a.out_scale;
   cudaError_t e = mla::launch_prefill_q_latent(m.w_uk, a, q, st);
   if (e == cudaSuccess) e = mla::launch_decode(maps, d, a.clusters, st);
-  if (e == cudaSuccess) e = mla::launch_merge(d, a.clusters, st);
+  if (e == cudaSuccess) e = mla::launch_prefill_latent(a, st);
   if (e == cudaSuccess) e = mla::launch_prefill_v_latent(latent, m.w_uv, a, st);
   return done(e);
 }

@@ -109,15 +109,21 @@ struct PfSplit {
 // rows that are requests of their own to it. Their rows start at multiples of its
 // 64-token blocks, so that the row buffer is its pool, with pages of 64 rows.
 // Latent / expanded, us a call, 8 requests of n new tokens over 4,000: 128 heads, n = 1
-// 87 / 1089, 16 212 / 1093, 64 635 / 1126, 112 1093 / 1331, 128 1252 / 1329; 16 heads,
-// 16 93 / 184, 64 130 / 188, 112 181 / 192, 128 196 / 193. Where there are few positions
-// the expanded form starts no later: 4 requests over 1,000, 128 heads, 64 157 / 190, 96
-// 220 / 207, 112 251 / 209; one over 1,600, 96 104 / 105, 112 111 / 104.
-constexpr int kPfSmallTokens = 112;    // at most, from kPfSmallSpan attended positions on
+// 86 / 1089, 16 350 / 1093, 56 1114 / 1300, 64 1273 / 1301; 32 heads, 56 313 / 327, 64
+// 349 / 328; 16 heads, 16 105 / 184, 48 173 / 187, 56 191 / 187. Where there are few
+// positions the expanded form starts no later: 4 requests over 1,000, 128 heads, 32
+// 169 / 190, 40 206 / 195; one over 1,600, 32 87 / 100, 48 109 / 102.
+constexpr int kPfSmallTokens = 56;       // at most, from kPfSmallSpan attended positions on
 constexpr int kPfSmallSpan = 3000;
-constexpr int kPfSmallTokensShort = 64;  // with fewer
-constexpr int kPfSmallRows = 1 << 17;  // (token, head) rows of all small requests at most
+constexpr int kPfSmallTokensShort = 32;  // with fewer
+constexpr int kPfSmallRows = 1 << 17;  // rows of all groups at most
 
+// Groups come in pairs of the same tokens: rounding the latent query to bf16 alone
+// would cost 1.5e-3 of the result, nearly as much as the result's own rounding. The
+// second group's query is what is left of twice the exact one, rounded: their mean
+// is on a grid twice as fine, and their sums are joined into one, which averages the
+// softmax weights' roundings as well. The result is off by about 2.0e-3 (2-norm); with
+// single groups it was 2.6e-3, and with a rounded latent result 3.0e-3.
 struct PfGroup {
   int base;      // workspace row of the request's relative position 0
   int first;     // relative position of the group's first token
@@ -125,7 +131,7 @@ struct PfGroup {
   int tokens;    // 1 .. tokens a full group has
   int page0;     // first entry of its page list
   int pages;
-  int pad[2];
+  int first_item, items;  // its work items of the decode, each of which leaves partial sums
 };
 
 struct PfHeader {
@@ -150,10 +156,10 @@ struct PfLayout {
   size_t requests, tiles, order, splits, part_stats, part_o, rows, keys, values, total;
   int64_t part_rows;    // partial rows of each head
   // Small requests in the latent space (absorb: whether the call may have any).
-  size_t groups, group_indptr, group_pages, q_latent, latent, latent_lse, decode;
+  size_t groups, group_indptr, group_pages, q_latent, latent, decode;
   int absorb;
   int group_tokens;     // tokens of a full group
-  int max_groups;
+  int max_pairs;        // groups come in pairs (see PfGroup)
   WsLayout decode_lay;
   int64_t kv_capacity;  // rows of the row buffer
   int64_t max_tiles;
@@ -163,7 +169,7 @@ struct PfLayout {
 // Calls whose keys and values of all heads would take more than about 30 us to make
 // look for small requests: the four launches of that path cost 10 to 13 us where there
 // are none (404 / 392 us with and without), and one request of 8 new tokens over 1,600, 128
-// heads, takes 57 us there against 100, of 64 new tokens 86 against 100.
+// heads, takes 60 us there against 100, of 32 new tokens 87 against 100.
 inline bool pf_may_absorb(int64_t max_kv, int num_heads) {
   return (num_heads == 16 || num_heads == 32 || num_heads == 64 || num_heads == 128) && max_kv * num_heads >= 200000;
 }
@@ -209,23 +215,26 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_hea
     const int64_t per_request = (kPfSmallTokens + L.group_tokens - 1) / L.group_tokens;
     int64_t g = (q_rows + L.group_tokens - 1) / L.group_tokens + batch;
     if (g > per_request * batch) g = per_request * batch;
-    if (g > kPfSmallRows / kGroupRows) g = kPfSmallRows / kGroupRows;
-    L.max_groups = static_cast<int>(g);
+    if (g > kPfSmallRows / kGroupRows / 2) g = kPfSmallRows / kGroupRows / 2;
+    L.max_pairs = static_cast<int>(g);
+    const int groups = 2 * L.max_pairs;
     const size_t rows = static_cast<size_t>(g) * kGroupRows;
     L.groups = off;
-    off = align_up(off + sizeof(PfGroup) * g, 256);
+    off = align_up(off + sizeof(PfGroup) * groups, 256);
     L.group_indptr = off;
-    off = align_up(off + sizeof(int32_t) * (g + 1), 256);
+    off = align_up(off + sizeof(int32_t) * (groups + 1), 256);
     L.group_pages = off;
-    off = align_up(off + sizeof(int32_t) * (static_cast<size_t>(L.kv_capacity / kBlockTokens) * per_request + g), 1024);
+    off = align_up(off + sizeof(int32_t) * (static_cast<size_t>(L.kv_capacity / kBlockTokens) * 2 * per_request + groups), 1024);
     L.q_latent = off;
-    off = align_up(off + rows * kDimRow * 2, 1024);
+    off = align_up(off + 2 * rows * kDimRow * 2, 1024);
     L.latent = off;
-    off = align_up(off + rows * kDimCkv * 2, 1024);
-    L.latent_lse = off;
-    off = align_up(off + rows * 4, 1024);
+    off = align_up(off + rows * kDimCkv * 4, 1024);
     L.decode = off;
-    L.decode_lay = ws_layout(L.max_groups, kGroupRows, kPfPairs);
+    // (with room for partial sums of every item: a group has one, and one more a cut)
+    L.decode_lay = ws_layout(groups, kGroupRows, kPfPairs);
+    const size_t items = static_cast<size_t>(groups) + kPfPairs;
+    L.decode_lay.partial_o = align_up(L.decode_lay.partial_lse + sizeof(float) * items * kGroupRows, 256);
+    L.decode_lay.total = align_up(L.decode_lay.partial_o + sizeof(float) * items * kGroupRows * kDimCkv, 256);
     off = align_up(off + L.decode_lay.total, 1024);
   }
   L.total = off;
@@ -284,6 +293,8 @@ __host__ __device__ inline bool pf_may_split(int64_t max_kv) { return max_kv > 6
 // prefill_absorb.cu: small requests' queries into the latent space, and their
 // attention output out of it
 cudaError_t launch_prefill_q_latent(const CUtensorMap& w_uk, const PrefillArgs& a, const void* q, cudaStream_t stream);
+// (partial sums of the decode joined into pairs of bf16 rows)
+cudaError_t launch_prefill_latent(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_v_latent(const CUtensorMap& latent, const CUtensorMap& w_uv, const PrefillArgs& a, cudaStream_t stream);
 // Streaming multiprocessors of the current device (0 on failure).
 int sm_count();

@@ -82,10 +82,10 @@ class Case:
         vals, table = self.values(), self.table.cpu().numpy()
         return step_ref.prefill(lambda b, at: vals[table[b][at // self.ps], at % self.ps], f64(self.q),
                                 self.indptr.cpu().numpy(), self.ctx.cpu().numpy(), f64(self.w_uk), f64(self.w_uv),
-                                self.scale, self.window, lambda n, m: self.latent() and n <= (112 if m >= 3000 else 64))
+                                self.scale, self.window, lambda n, m: self.latent() and n <= (56 if m >= 3000 else 32))
 
     def latent(self):
-        """Calls of this size attend requests of up to 64 new tokens (112 over 3,000 positions) in the latent space."""
+        """Calls of this size attend requests of up to 32 new tokens (56 over 3,000 positions) in the latent space."""
         return self.heads in (16, 32, 64, 128) and self.max_kv * self.heads >= 200000
 
     def check(self, norm=6e-3, status=0):
@@ -377,9 +377,9 @@ def test_graph_replay_with_changed_lengths(lib):
     (64, [1100, 2100], [5, 64], 0, True),
     (128, [900, 800, 10], [3, 130, 64], 0, False),
     (128, [1700], [1], 0, False),
-    (16, [4000, 2935, 2935, 2999, 5000], [112, 64, 65, 65, 113], 0, True),
-    (16, [4000, 9000, 5000], [112, 80, 112], 2900, False),
-    (64, [3300], [100], 0, False)])
+    (16, [4000, 2935, 2935, 2967, 5000], [56, 32, 33, 33, 57], 0, True),
+    (16, [4000, 9000, 5000], [56, 50, 32], 2900, False),
+    (64, [3300], [50], 0, False)])
 def test_small_requests_in_the_latent_space(lib, heads, ctx, new, window, fp8):
     """Few new tokens over long caches, alone and beside chunks; every token group, partly filled ones among them."""
     c = Case(lib, ctx, new, heads=heads, window=window, fp8=fp8, seed=heads, spare_kv=0 if not window else 20000)
@@ -397,8 +397,11 @@ def test_small_requests_with_csr_and_passes_and_no_lse(lib):
     b = Case(lib, **args, csr=True, heads_per_pass=3)
     assert a.latent()
     b.run(lse=None)
-    assert torch.equal(bits(a.out[:72]), bits(b.out[:72])) and (b.lse == 7).all()
-    b.run().check()  # (heads a pass may cut the chunk's keys elsewhere)
+    # (requests 0 and 2 are attended in the latent space; 64 and 300 tokens' keys may be cut elsewhere with other heads a pass)
+    for r in (slice(0, 1), slice(65, 72)):
+        assert torch.equal(bits(a.out[r]), bits(b.out[r]))
+    assert (b.lse == 7).all()
+    b.run().check()
 
 
 def test_many_small_requests_past_the_room_for_them(lib):
