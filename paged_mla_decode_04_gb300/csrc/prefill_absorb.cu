@@ -10,9 +10,10 @@
 // twice, rounded one way and the other (see PfGroup). Per head these are
 // products over all slots, [slots x 128] x [128 x 512] and [slots x 512] x
 // [512 x 128], bound by reading the weights (256 KB a head) for the few hundred
-// slots of a step: one block per (head, 128 slots), one pass over the weights. With
-// about 600 slots of 16 heads they take 11 and 7.6 us beside 40 us of the decode; in a
-// call that turns out to have no small request, the path's four launches cost 10 to 13.
+// slots of a step: one or two blocks per (head, 128 slots), one pass over the weights.
+// For the small requests of a step of 24 mixed ones, 16 heads, they take 11 and 9 us, the
+// join 7, the decode between 60; in a call that turns out to have no small request, the
+// path's four launches cost 10 to 13.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -35,10 +36,11 @@ __device__ __forceinline__ bool slot_token(const PrefillArgs& a, int slot, int n
   return i < group.tokens;
 }
 
-constexpr int kQOffB = 2 * kChunk;             // A: 128 slots x 128 dims; B: W_UK[h], 8 chunks of 64 columns
-constexpr int kQOffBar = kQOffB + 8 * kChunk;
+constexpr int kQOffB = 2 * kChunk;             // A: 128 slots x 128 dims; B: half of W_UK[h], 4 chunks of 64 columns
+constexpr int kQOffBar = kQOffB + 4 * kChunk;
 constexpr int kQSmem = kQOffBar + 64 + 1024;
 
+// Half of the 512 columns a block: a step's slots are too few to fill the GPU.
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q_latent_kernel(const __grid_constant__ CUtensorMap w_uk, const __grid_constant__ PrefillArgs a,
                             const uint4* __restrict__ q) {
@@ -48,7 +50,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kQOffBar + 16);
   const int tid = threadIdx.x, warp = tid >> 5;
   PfHeader* hd = reinterpret_cast<PfHeader*>(a.ws);
-  const int h = blockIdx.x, slot = blockIdx.y * 128 + tid, heads = a.num_heads;
+  const int h = blockIdx.x >> 1, half = blockIdx.x & 1, slot = blockIdx.y * 128 + tid, heads = a.num_heads;
   pdl_launch_dependents();
   pdl_wait();
   const int num_groups = hd->num_groups;
@@ -68,17 +70,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init_cluster();
   }
   if (warp == 0) {
-    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_alloc(smem_addr(tmem_slot), 256);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (tid == 0) {
-    mbar_arrive_expect_tx(full, 8 * kChunk);
-    for (int c = 0; c < 8; ++c)
+    mbar_arrive_expect_tx(full, 4 * kChunk);
+    for (int c = 0; c < 4; ++c)
       for (int k = 0; k < 2; ++k)
-        tma_load_2d(sbase + kQOffB + c * kChunk + k * (kChunk / 2), &w_uk, full, 64 * c, h * kDimNope + 64 * k);
+        tma_load_2d(sbase + kQOffB + c * kChunk + k * (kChunk / 2), &w_uk, full, 256 * half + 64 * c, h * kDimNope + 64 * k);
   }
   // A row a thread: 256 bytes into the swizzled layout.
   int row = 0;
@@ -97,11 +99,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc = idesc_bf16(128, 256, false, true);
     if (mbar_wait(full, 0, nullptr)) {
       tc_fence_after();
-      for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ss(tmem + 256 * half, sdesc_sw128(sbase + (k >> 2) * kChunk + (k & 3) * 32, 16, 1024),
-                      sdesc_sw128(sbase + kQOffB + 4 * half * kChunk + k * 2048, kChunk, 1024), idesc, k != 0);
+      for (int k = 0; k < 8; ++k)
+        mma_bf16_ss(tmem, sdesc_sw128(sbase + (k >> 2) * kChunk + (k & 3) * 32, 16, 1024),
+                    sdesc_sw128(sbase + kQOffB + k * 2048, kChunk, 1024), idesc, k != 0);
       mma_commit(done);
     }
   }
@@ -111,10 +112,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ready && (tid & 31) == 0) atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
   if (ready) {
     const int t = a.lay.group_tokens, first = slot + slot / t * t;  // the slot's place in the pair's first group
-    uint8_t* dst = a.ws + a.lay.q_latent + (static_cast<int64_t>(first) * heads + h) * (kDimRow * 2);
+    uint8_t* dst = a.ws + a.lay.q_latent + (static_cast<int64_t>(first) * heads + h) * (kDimRow * 2) + 512 * half;
     uint8_t* dst2 = dst + static_cast<int64_t>(t) * heads * (kDimRow * 2);
 #pragma unroll 1
-    for (int c = 0; c < 16; ++c) {
+    for (int c = 0; c < 8; ++c) {
       uint32_t r[32];
       tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + 32 * c, r);
       tmem_wait_ld();
@@ -133,14 +134,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (valid)
+    if (valid && half)
       for (int j = 0; j < 8; ++j)
-        reinterpret_cast<uint4*>(dst + kDimCkv * 2)[j] = reinterpret_cast<uint4*>(dst2 + kDimCkv * 2)[j] = src[16 + j];
+        reinterpret_cast<uint4*>(dst + 512)[j] = reinterpret_cast<uint4*>(dst2 + 512)[j] = src[16 + j];
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
 // A warp joins the partial sums of one (slot, head), 16 dims a lane.
@@ -302,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 128);
 }
 
-dim3 slots_grid(const PrefillArgs& a) {
-  return dim3(a.num_heads, (a.lay.max_pairs * a.lay.group_tokens + 127) / 128);
+dim3 slots_grid(const PrefillArgs& a, int blocks_a_head) {
+  return dim3(a.num_heads * blocks_a_head, (a.lay.max_pairs * a.lay.group_tokens + 127) / 128);
 }
 
 }  // namespace
@@ -312,7 +313,7 @@ cudaError_t launch_prefill_q_latent(const CUtensorMap& w_uk, const PrefillArgs& 
   static bool attr_set[kMaxDevices] = {};
   const cudaError_t e = set_smem_once(prefill_q_latent_kernel, kQSmem, attr_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_q_latent_kernel, slots_grid(a), dim3(kThreads), kQSmem, stream, w_uk, a,
+  return launch_pdl(prefill_q_latent_kernel, slots_grid(a, 2), dim3(kThreads), kQSmem, stream, w_uk, a,
                     static_cast<const uint4*>(q));
 }
 
@@ -327,7 +328,7 @@ cudaError_t launch_prefill_v_latent(const CUtensorMap& latent, const CUtensorMap
   static bool attr_set[kMaxDevices] = {};
   const cudaError_t e = set_smem_once(prefill_v_latent_kernel, kVSmem, attr_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_v_latent_kernel, slots_grid(a), dim3(kThreads), kVSmem, stream, latent, w_uv, a);
+  return launch_pdl(prefill_v_latent_kernel, slots_grid(a, 1), dim3(kThreads), kVSmem, stream, latent, w_uv, a);
 }
 
 }  // namespace mla
