@@ -467,6 +467,23 @@ def test_graph_replay_of_mixed_steps(lib):
         torch.cuda.synchronize()
         c.check()
 
+@pytest.mark.parametrize("heads,ctx,new,fp8,latent", [
+    (16, [4000, 3500, 9000], [20, 1, 55], False, True), (128, [4000], [3], False, True), (32, [4000, 3100], [40, 9], True, True),
+    (2, [4000, 500], [300, 64], False, False), (16, [3000], [200], True, False)])
+def test_nearly_as_exact_as_the_results_own_rounding(lib, heads, ctx, new, fp8, latent):
+    """Normal values, scores of standard deviation 1. Rounded to bf16, a value is off by 1.67e-3 (root mean square,
+    taken from the reference itself below).
+    Expanded, only the keys add to it: 128 of 192 products a score, so 1.67e-3 sqrt(2 / 3) = 1.36e-3 of each weight,
+    together sqrt(1.67^2 + 1.36^2) = 1.29 of the rounding. In the latent space the pair of queries leaves half of
+    that, 0.7e-3, and the weights' two roundings 1.1e-3 / sqrt(2): 1.19. Bounded by 1.4 of it."""
+    c = Case(lib, ctx, new, heads=heads, fp8=fp8, seed=7).run()
+    assert (int(c.ws[:32].view(torch.int32)[7]) > 0) == latent
+    ref, _, _, _ = c.reference()
+    n = sum(new)
+    own = f64(torch.from_numpy(ref[:n]).to(torch.bfloat16)) - ref[:n]
+    assert np.linalg.norm(f64(c.out)[:n] - ref[:n]) <= 1.4 * np.linalg.norm(own)
+
+
 def test_most_heads_and_a_workspace_cut_to_fit_half(lib):
     """1024 heads, at once and in two passes with a workspace sized for one head more than a pass has."""
     a = Case(lib, [40, 3], [20, 1], heads=1024).run().check()
