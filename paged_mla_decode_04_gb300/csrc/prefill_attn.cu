@@ -205,8 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int num_tiles = hd->num_tiles;
       const int64_t items = static_cast<int64_t>(num_tiles) * heads;
       const int clusters = gridDim.x / 2;
-      const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + a.lay.tiles);
-      const int* order = reinterpret_cast<const int*>(a.ws + a.lay.order);
+      const PfTile* tiles = reinterpret_cast<const PfTile*>(a.ws + a.lay.sorted);
       const int tail_heads = (kTailItems * clusters + num_tiles - 1) / max(num_tiles, 1);
       const int tail = hd->even ? heads : max(0, heads - tail_heads);
       uint32_t k_steps = 0, v_steps = 0;  // steps whose copies are issued
@@ -216,7 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int rank, head;
         if (it >= items) return item_of(PfTile{0, 0, 0, 0, 0, 0, 1, -1, {}}, -1);
         split_item(it, num_tiles, heads, tail, &rank, &head);
-        return item_of(tiles[order[rank]], head);
+        return item_of(tiles[rank], head);
       };
       // The even block announces an item to both.
       auto announce = [&](uint32_t i, const Item& w) {

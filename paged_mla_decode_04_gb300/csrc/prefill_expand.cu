@@ -61,6 +61,11 @@ enum {
 };
 static_assert(8 * kNumBars + 8 <= 256, "barrier area");
 
+// halves == 2: so few units that half the clusters would do, and keys and values are
+// units of their own, at most one a cluster (the smallest call, 95 rows of 16 heads, takes
+// 19.7 us so, 21.2 with whole units; in larger ones the choice would sit in the loops of
+// all, which costs 1 to 2 %, hence the template).
+template <int halves>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_expand_kernel(const __grid_constant__ PrefillMaps m, const __grid_constant__ PrefillArgs a, int head0, int heads) {
   extern __shared__ uint8_t smem_raw[];
@@ -92,8 +97,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) hd->next_item = 0;  // for the attention that follows
   const int row_blocks = (hd->kv_rows + 255) / 256;
-  const int64_t units = static_cast<int64_t>(row_blocks) * heads;
   const int64_t clusters = gridDim.x / 2, mine = blockIdx.x / 2;
+  const int64_t units = static_cast<int64_t>(row_blocks) * heads * halves;
   const int64_t u0 = units * mine / clusters, u1 = units * (mine + 1) / clusters;
   auto fail = [&] {
     *abort_flag = 1;
@@ -106,7 +111,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int row_block = -1;
       bool ok = true;
       for (int64_t u = u0; u < u1 && ok; ++u) {
-        const int head = head0 + static_cast<int>(u % heads), rb = static_cast<int>(u / heads);
+        const int head = head0 + static_cast<int>(u / halves % heads), rb = static_cast<int>(u / halves / heads);
+        const bool with_k = halves == 1 || !(u & 1), with_v = halves == 1 || (u & 1);
         const bool fresh = rb != row_block;
         if (fresh) {
           if (!(ok = mbar_spin(bar(kBarRowsFree), (loads & 1u) ^ 1u, abort_flag))) break;
@@ -121,9 +127,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t s = k % kStages;
           if (!(ok = mbar_spin(bar(kBarEmpty + s), ((k / kStages) & 1u) ^ 1u, abort_flag))) break;
           const uint32_t dst = sbase + kOffRing + s * kStageBytes;
-          if (cta == 0) mbar_arrive_expect_tx(bar(kBarFull + s), 2 * kStageBytes);
-          tma2_load_2d(dst, &m.w_uk, lead(kBarFull + s), c * kChunk, head * kDimNope + 64 * cta);
-          tma2_load_2d(dst + kWBytes, &m.w_uv, lead(kBarFull + s), 64 * cta, head * kDimCkv + c * kChunk);
+          if (cta == 0) mbar_arrive_expect_tx(bar(kBarFull + s), 2 * kStageBytes / halves);
+          if (with_k) tma2_load_2d(dst, &m.w_uk, lead(kBarFull + s), c * kChunk, head * kDimNope + 64 * cta);
+          if (with_v) tma2_load_2d(dst + kWBytes, &m.w_uv, lead(kBarFull + s), 64 * cta, head * kDimCkv + c * kChunk);
         }
       }
       if (!ok) fail();
@@ -143,9 +149,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int row_block = -1;
       bool ok = true;
       auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && mbar_spin(b, parity, abort_flag); };
-      int64_t left = heads - u0 % heads;  // units until the next row block
+      int64_t left = heads - u0 % heads;  // units until the next row block (with halves a cluster has one unit)
       for (int64_t u = u0; u < u1 && ok; ++u, ++n) {
-        const int rb = static_cast<int>(u / heads);
+        const int rb = static_cast<int>(u / halves / heads);
+        const bool with_k = halves == 1 || !(u & 1), with_v = halves == 1 || (u & 1);
         const bool fresh = rb != row_block;
         if (fresh) {
           row_block = rb;
@@ -162,8 +169,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t ad = a_lo + c * (kABytes >> 4), wd = ring_lo + stage * (kStageBytes >> 4);
 #pragma unroll
           for (int i = 0; i < kChunk / 16; ++i) {
-            mma2_bf16_ss(d, ad + 2 * i, wd + 2 * i, idesc_k, (c | i) != 0);
-            mma2_bf16_ss(d + 128, ad + 2 * i, wd + (kWBytes >> 4) + 128 * i, idesc_v, (c | i) != 0);
+            if (with_k) mma2_bf16_ss(d, ad + 2 * i, wd + 2 * i, idesc_k, (c | i) != 0);
+            if (with_v) mma2_bf16_ss(d + 128, ad + 2 * i, wd + (kWBytes >> 4) + 128 * i, idesc_v, (c | i) != 0);
           }
           mma2_commit(bar(kBarEmpty + stage));
           stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -189,11 +196,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t acc = n & 1u;
       if (!(ok = mbar_spin_warp(bar(kBarAccFull + acc), (n >> 1) & 1u, abort_flag))) break;
       tc_fence_after();
-      const int64_t row = (u / heads) * 256 + 128 * cta + quarter * 32 + lane;
+      const int64_t row = (u / halves / heads) * 256 + 128 * cta + quarter * 32 + lane;
       const bool keep = row < a.lay.kv_capacity;  // (a multiple of 128: whole blocks)
-      const int64_t out_row = (u % heads) * a.lay.kv_capacity + row;
+      const int64_t out_row = (u / halves % heads) * a.lay.kv_capacity + row;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {  // 64 columns each: K, K, V, V
+        if (halves == 2 && (u & 1) != (c >> 1)) continue;
         uint32_t r[64];
         tmem_ld32(tmem + lane_base + acc * 256 + c * 64, r);
         tmem_ld32(tmem + lane_base + acc * 256 + c * 64 + 32, r + 32);
@@ -230,14 +238,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t launch_prefill_expand(const PrefillMaps& m, const PrefillArgs& a, int head0, int heads, cudaStream_t stream) {
-  static bool attr_set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_once(prefill_expand_kernel, kSmemBytes, attr_set);
-  if (e != cudaSuccess) return e;
+  static bool attr_set[2][kMaxDevices] = {};
   const int pairs = sm_count() / 2;
   if (pairs <= 0) return cudaErrorInvalidDevice;
   const int64_t most = (a.lay.kv_capacity + 255) / 256 * heads;
-  return launch_pdl(prefill_expand_kernel, dim3(2 * static_cast<unsigned>(most < pairs ? most : pairs)), dim3(kThreads),
-                    kSmemBytes, stream, m, a, head0, heads);
+  const bool halves = 2 * most <= pairs;
+  const auto kernel = halves ? prefill_expand_kernel<2> : prefill_expand_kernel<1>;
+  const cudaError_t e = set_smem_once(kernel, kSmemBytes, attr_set[halves]);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = halves ? 4 * most : 2 * (most < pairs ? most : pairs);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kSmemBytes, stream, m, a, head0, heads);
 }
 
 }  // namespace mla

@@ -378,7 +378,7 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, int64_t* sh) {
   // but who computes a tile.
   __shared__ int most, least, bins[kCostBins];
   int nt = static_cast<int>(min(tiles_before, a.lay.max_tiles));
-  int* order = reinterpret_cast<int*>(a.ws + a.lay.order);
+  PfTile* sorted = reinterpret_cast<PfTile*>(a.ws + a.lay.sorted);
   if (threadIdx.x < kCostBins) bins[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     most = 1;
@@ -410,7 +410,7 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, int64_t* sh) {
   first = block_exclusive(first, sh, &ignored);
   if (threadIdx.x < kCostBins) bins[threadIdx.x] = static_cast<int>(first);
   __syncthreads();
-  for (int i = threadIdx.x; i < nt; i += threads) order[atomicAdd(&bins[bin(i)], 1)] = i;
+  for (int i = threadIdx.x; i < nt; i += threads) sorted[atomicAdd(&bins[bin(i)], 1)] = tiles[i];
   if (threadIdx.x == 0) {
     hd->kv_rows = static_cast<int>(sum[0]);
     hd->all_rows = static_cast<int>(absorb && sum[1] > 0 ? small_start + sum[1] : sum[0]);

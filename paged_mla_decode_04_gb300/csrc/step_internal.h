@@ -153,7 +153,7 @@ __host__ __device__ inline int pf_steps(int begin, int end) {
 }
 
 struct PfLayout {
-  size_t requests, tiles, order, splits, part_stats, part_o, rows, keys, values, total;
+  size_t requests, tiles, sorted, splits, part_stats, part_o, rows, keys, values, total;
   int64_t part_rows;    // partial rows of each head
   // Small requests in the latent space (absorb: whether the call may have any).
   size_t groups, group_indptr, group_pages, q_latent, latent, decode;
@@ -196,8 +196,8 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_hea
   off = align_up(off + sizeof(PfRequest) * (static_cast<size_t>(batch) + 1), 256);
   L.tiles = off;
   off = align_up(off + sizeof(PfTile) * static_cast<size_t>(entries), 256);
-  L.order = off;
-  off = align_up(off + sizeof(int) * static_cast<size_t>(entries), 256);
+  L.sorted = off;
+  off = align_up(off + sizeof(PfTile) * static_cast<size_t>(entries), 256);
   L.splits = off;
   off = align_up(off + sizeof(PfSplit) * kPfMostPieces, 256);
   L.part_stats = off;
