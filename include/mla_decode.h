@@ -306,8 +306,9 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  * them costs as much as 410 queries' attention. So requests of up to 32 new
  * tokens (56 over 3,000 positions and more) are attended in the latent space, by
  * the kernel of mla_decode, at 2 x 2,176 flops a pair: in calls of 16, 32, 64 or
- * 128 heads with max_kv_tokens * num_heads >= 200,000. A step of single tokens
- * alone is mla_decode's.
+ * 128 heads with max_kv_tokens * num_heads >= 200,000 (where q_rows <= 8 * batch
+ * also from 100,000 or from batch * num_heads >= 400 on). A step of single
+ * tokens alone is mla_decode's.
  *   q:        device, [q_rows][num_heads][192] bf16 (nope 128 || rope 64).
  *   q_indptr: device, [batch + 1] int32, non-decreasing, within [0, q_rows].
  *             Rows of out outside [q_indptr[0], q_indptr[batch]) stay as they were.

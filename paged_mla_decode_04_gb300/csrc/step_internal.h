@@ -166,19 +166,26 @@ struct PfLayout {
   int heads;            // heads whose keys and values fit
 };
 
-// Calls whose keys and values of all heads would take more than about 30 us to make
-// look for small requests: the four launches of that path cost 10 to 13 us where there
-// are none (404 / 392 us with and without), and one request of 8 new tokens over 1,600, 128
-// heads, takes 60 us there against 100, of 32 new tokens 87 against 100.
-inline bool pf_may_absorb(int64_t max_kv, int num_heads) {
-  return (num_heads == 16 || num_heads == 32 || num_heads == 64 || num_heads == 128) && max_kv * num_heads >= 200000;
+// Calls look for small requests if the keys and values of all heads would take more than
+// about 30 us to make: the four launches of that path cost 10 to 13 us where there are
+// none (404 / 392 us with and without). Calls of few tokens a request (8 on average) from
+// half of that on, or with so many (request, head) items that their starts count. Latent
+// / expanded, us a call: 14 requests of one token over 60, 64 heads, 43 / 73; 4 of 4 over
+// 200, 128 heads, 48 / 72; 30 of one over 50, 16 heads, 45 / 48; one of 8 over 1,000, 128
+// heads, 52 / 63; below, 16 of one over 100, 16 heads, 45 / 41; 7 of one over 200 45 / 32;
+// one of 16 over 2,000, 32 heads, 55 / 43. With more tokens: 2 of 20 over 400, 64 heads,
+// 53 / 41.
+inline bool pf_may_absorb(int64_t batch, int64_t q_rows, int64_t max_kv, int64_t num_heads) {
+  if (num_heads != 16 && num_heads != 32 && num_heads != 64 && num_heads != 128) return false;
+  if (max_kv * num_heads >= 200000) return true;
+  return q_rows <= 8 * batch && (max_kv * num_heads >= 100000 || batch * num_heads >= 400);
 }
 
 // Workspace regions for `heads` of num_heads heads at a time.
 inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_heads, int heads) {
   PfLayout L = {};
   L.heads = heads;
-  L.absorb = pf_may_absorb(max_kv, num_heads);
+  L.absorb = pf_may_absorb(batch, q_rows, max_kv, num_heads);
   const int64_t slack = static_cast<int64_t>(batch) * (L.absorb ? kBlockTokens : kPfKvAlign) + (L.absorb ? 256 : 0);
   L.kv_capacity = (max_kv + slack + kPfKvTile - 1) / kPfKvTile * kPfKvTile;
   L.max_tiles = q_rows / kPfRows + batch;

@@ -86,7 +86,9 @@ class Case:
 
     def latent(self):
         """Calls of this size attend requests of up to 32 new tokens (56 over 3,000 positions) in the latent space."""
-        return self.heads in (16, 32, 64, 128) and self.max_kv * self.heads >= 200000
+        size, few = self.max_kv * self.heads, self.T <= 8 * len(self.ctx)
+        return self.heads in (16, 32, 64, 128) and (
+            size >= 200000 or few and (size >= 100000 or len(self.ctx) * self.heads >= 400))
 
     def check(self, norm=6e-3, status=0):
         ref, lse, tol, tol_lse = self.reference()
@@ -379,7 +381,9 @@ def test_graph_replay_with_changed_lengths(lib):
     (128, [1700], [1], 0, False),
     (16, [4000, 2935, 2935, 2967, 5000], [56, 32, 33, 33, 57], 0, True),
     (16, [4000, 9000, 5000], [56, 50, 32], 2900, False),
-    (64, [3300], [50], 0, False)])
+    (64, [3300], [50], 0, False),
+    (64, [60, 0, 17, 100, 64, 63, 200], [1, 1, 2, 9, 1, 1, 1], 0, True),
+    (128, [1000], [5], 600, False)])
 def test_small_requests_in_the_latent_space(lib, heads, ctx, new, window, fp8):
     """Few new tokens over long caches, alone and beside chunks; every token group, partly filled ones among them."""
     c = Case(lib, ctx, new, heads=heads, window=window, fp8=fp8, seed=heads, spare_kv=0 if not window else 20000)
