@@ -22,7 +22,7 @@
 // Sums are 64-bit: none of int32 lengths overflows.
 //
 // Bound by latency: lengths, scan, search, table entry and store wait for one another.
-// 128 requests with a token each take 5.4 us a call (6.5 alone), 1,024 requests with
+// 128 requests with a token each take 5.2 us a call (6.5 alone), 1,024 requests with
 // 1.05 million listed pages 10.0 us, of which their 10.5 MB need 1.6.
 #include "../../include/mla_decode.h"
 #include "ptx.cuh"
