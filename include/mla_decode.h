@@ -312,7 +312,8 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *   q:        device, [q_rows][num_heads][192] bf16 (nope 128 || rope 64).
  *   q_indptr: device, [batch + 1] int32, non-decreasing, within [0, q_rows].
  *             Rows of out outside [q_indptr[0], q_indptr[batch]) stay as they were.
- *   page_indptr / page_ids / max_blocks: the pages, as for mla_decode.
+ *   page_indptr / page_ids / max_blocks: the pages, as for mla_decode. With
+ *             page_indptr, NULL page_ids are lists without a page.
  *   max_kv_tokens: at least the sum over requests of attended positions,
  *             L_b + n_b - (0 or max(0, L_b + 1 - window)) where n_b > 0.
  *   w_uk:     device, [num_heads][128][512] bf16; w_uv: [num_heads][512][128].

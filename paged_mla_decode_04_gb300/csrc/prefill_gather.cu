@@ -246,7 +246,8 @@ __device__ __forceinline__ Request request_of(const PrefillArgs& a, int b, int64
       r.n = 0;
       ok = false;
     }
-    const int64_t nb = a.page_indptr ? a.page_indptr[b + 1] - a.page_indptr[b] : a.max_blocks;
+    // (no ids at all: every list is empty)
+    const int64_t nb = !a.page_ids ? 0 : a.page_indptr ? a.page_indptr[b + 1] - a.page_indptr[b] : a.max_blocks;
     if (r.len < 0 || r.len + r.n > nb * a.page_size || r.len + r.n > INT32_MAX) ok = ok && r.n == 0;
     r.lo = a.window > 0 ? max(static_cast<int64_t>(0), r.len + 1 - a.window) : 0;
   }

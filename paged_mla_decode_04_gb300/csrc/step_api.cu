@@ -210,7 +210,7 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
   if (!prefill_sizes_ok(batch, q_rows, max_kv_tokens, num_heads)) return MLA_ERR_ARG;
   if (!(softmax_scale > 0.f)) return MLA_ERR_ARG;
   if (batch == 0 || q_rows == 0) return MLA_OK;
-  if (!q || !q_indptr || !page_ids || !context_lens || !w_uk || !w_uv || !out) return MLA_ERR_ARG;
+  if (!q || !q_indptr || (!page_ids && !page_indptr) || !context_lens || !w_uk || !w_uv || !out) return MLA_ERR_ARG;
   if (!aligned(q, 16) || !aligned(w_uk, 16) || !aligned(w_uv, 16) || !aligned(out, 32)) return MLA_ERR_ARG;
   if (!page_indptr && (max_blocks <= 0 || static_cast<int64_t>(max_blocks) * pool->page_size > INT_MAX)) return MLA_ERR_ARG;
   if (!workspace || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;

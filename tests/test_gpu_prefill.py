@@ -208,6 +208,18 @@ def test_no_new_tokens_and_empty_batch(lib):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_csr_without_a_page(lib, fp8):
+    """Requests without tokens, cached or new, and an empty list of ids; where one has tokens it is refused."""
+    c = Case(lib, [0, 0], [0, 0], csr=True, fp8=fp8).run().check()
+    assert c.ids.numel() == 0 and (c.out == 7).all()
+    c = Case(lib, [0, 0], [0, 3], csr=True, fp8=fp8)
+    c.ids = c.ids[:0]
+    c.run()
+    assert torch.isnan(c.out[:3].float()).all() and (c.out[3:] == 7).all()
+    assert lib.get_error(c.ws) == lib.STATUS_BAD_LENGTH
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_csr_lists_equal_block_tables(lib, fp8):
     a = Case(lib, [333, 0, 12], [100, 300, 1], fp8=fp8).run()
     b = Case(lib, [333, 0, 12], [100, 300, 1], fp8=fp8, csr=True).run()

@@ -93,7 +93,7 @@ PREFILL = ["pool", "layer", "q", "q_indptr", "page_indptr", "page_ids", "max_blo
     (dict(pool=None), ARG), (dict(layer=2), ARG), (dict(window=-1), ARG), (dict(batch=-1), ARG), (dict(q_rows=-1), ARG),
     (dict(max_kv_tokens=-1), ARG), (dict(max_kv_tokens=1 << 31), ARG), (dict(num_heads=0), ARG),
     (dict(num_heads=1025), ARG), (dict(q_rows=1 << 28, num_heads=16), ARG), (dict(softmax_scale=0.0), ARG),
-    (dict(softmax_scale=float("nan")), ARG), (dict(q=None), ARG), (dict(q_indptr=None), ARG), (dict(page_ids=None), ARG),
+    (dict(softmax_scale=float("nan")), ARG), (dict(q=None), ARG), (dict(q_indptr=None), ARG), (dict(page_ids=None, page_indptr=None), ARG),
     (dict(context_lens=None), ARG), (dict(w_uk=None), ARG), (dict(w_uv=None), ARG), (dict(out=None), ARG),
     (dict(page_indptr=None, max_blocks=0), ARG), (dict(page_indptr=None, max_blocks=1 << 28), ARG),
     (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=1000), WORKSPACE)])
