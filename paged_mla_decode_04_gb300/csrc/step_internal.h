@@ -116,7 +116,7 @@ struct PfSplit {
 constexpr int kPfSmallTokens = 56;       // at most, from kPfSmallSpan attended positions on
 constexpr int kPfSmallSpan = 3000;
 constexpr int kPfSmallTokensShort = 32;  // with fewer
-constexpr int kPfSmallRows = 1 << 17;  // rows of all groups at most
+constexpr int kPfSmallRows = 1 << 18;  // rows of all groups at most: 1,024 tokens of 128 heads, 1.1 GB of workspace
 
 // Groups come in pairs of the same tokens: rounding the latent query to bf16 alone
 // would cost 1.5e-3 of the result, nearly as much as the result's own rounding. The
