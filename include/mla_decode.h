@@ -325,7 +325,8 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *             workspace, and not shared by calls that overlap on the GPU.
  * num_heads is 1 to 1024. Arithmetic: fp32 accumulation and softmax sums; for
  * the tensor core keys are rounded to bf16, values and softmax weights to f16
- * (values beyond +-65504 saturate). In the latent space a pair of bf16
+ * (values beyond +-65504 saturate; weights lose bits below 2^-21 of the row's
+ * largest and are zero below 2^-32 of it). In the latent space a pair of bf16
  * queries stands for the exact one, scores and softmax weights are
  * mla_decode's. The result is off by 1.7e-3 to 2.1e-3 (2-norm, of independent
  * normal values; 1.7e-3 is its own rounding to bf16). fp8 pools:

@@ -34,7 +34,10 @@
 // takes its exponentials against the reference as it stands and looks at the
 // largest afterwards: above 2^8 the warp does the step again, with a maximum taken
 // first. P is rounded to f16 for the product, as V is (see the expansion); its sum is
-// kept in fp32.
+// kept in fp32. P is taken 2^7 times as large as against the reference, so that with
+// the 2^8 of above it fills f16's range: weights keep all eleven bits down to 2^-21 of
+// the row's largest (2^-14 without), some down to 2^-31. The result's division takes the
+// factor out again.
 // 2,048 new tokens behind 14,336 cached, 128 heads: 1,531 us alone, 1.68 PFLOP/s (87 % of
 // the library product's burst rate); calls in a row run into the power limit (1,790 us).
 // Three prompts of 4,500 to 8,192 tokens, 16 heads: 452 us, 1.56 (the diagonal's masked
@@ -78,7 +81,7 @@ constexpr int kSched = 2;                   // items announced ahead
 constexpr int kTailItems = 3;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
-constexpr float kMostWeight = 256.0f;       // 2^kRescaleThreshold
+constexpr float kMostWeight = 32768.0f;     // 2^(kRescaleThreshold + kWeightShift)
 // The reference of a row that has seen no key: below every score, and finite so
 // that a score of -inf against it is a weight of zero and any other infinite.
 constexpr float kNoMax = -1e30f;
@@ -478,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t s[128];
           // P against the reference maximum as it stands, the sum and maximum of
           // P beside it: no pass over S before the exponentials.
-          float neg = -mx_ref * scale;
+          float neg = kWeightShift - mx_ref * scale;
           uint64_t sum2[2];
           float top;
           auto weights = [&] {
@@ -542,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   tmem_st16(tO + 16 * c, o);
                 }
               }
-              neg = -mx_ref * scale;
+              neg = kWeightShift - mx_ref * scale;
             }
             weights();
             if (anew || !__any_sync(0xffffffffu, top > kMostWeight)) break;
@@ -618,7 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (split && valid) reinterpret_cast<float2*>(a.ws + a.lay.part_stats)[part()] = make_float2(mx_ref, l);
-        else if (a.lse && valid) a.lse[out_row()] = (mx_ref * scale + log2f(l)) * 0.69314718055994531f;
+        else if (a.lse && valid) a.lse[out_row()] = (mx_ref * scale + log2f(l * kWeightUnit)) * 0.69314718055994531f;
       }
       tc_fence_before();
       if (merge) {

@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kGatherThreads, 4) prefill_gather_kernel(const
 }
 
 // Joins the pieces of split tiles: a warp per (row, head), four value dims a
-// lane. Each piece left its sums O relative to its own maximum m, and l. 2.3 us where
+// lane. Each piece left its sums O and l, 2^kWeightShift of what they are relative to
+// its own maximum m. 2.3 us where
 // nothing or little was cut, most of it the launch.
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a, int head0, int heads) {
   pdl_launch_dependents();
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillArgs a,
     const int64_t out_row = (static_cast<int64_t>(s.q_row) + r) * a.num_heads + head0 + head;
     reinterpret_cast<uint2*>(a.out)[out_row * (kDimV / 4) + lane] =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (a.lse && lane == 0) a.lse[out_row] = (m * a.scale_log2 + log2f(l)) * 0.69314718055994531f;
+    if (a.lse && lane == 0) a.lse[out_row] = (m * a.scale_log2 + log2f(l * kWeightUnit)) * 0.69314718055994531f;
   }
 }
 

@@ -66,6 +66,9 @@ constexpr int kDimQk = 192;
 constexpr int kPfRows = 512;      // query rows of one tile: two streams of two blocks' 128
 constexpr int kPfKvAlign = 16;    // a request's gathered rows start at a multiple of this (one K step of an MMA)
 constexpr int kPfKvTile = 128;    // key rows per step
+// The expanded path's softmax weights and their sums are 2^7 of what they are against
+// the reference maximum (see the attention kernel).
+constexpr float kWeightShift = 7.f, kWeightUnit = 1.f / 128;
 
 // Request b as the plan sees it. Gathered positions are [lo, lo + rows); they
 // sit at rows base .. of the workspace's row buffer, followed by zero rows up
