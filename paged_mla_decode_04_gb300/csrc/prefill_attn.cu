@@ -38,6 +38,15 @@
 // the 2^8 of above it fills f16's range: weights keep all eleven bits down to 2^-21 of
 // the row's largest (2^-14 without), some down to 2^-31. The result's division takes the
 // factor out again.
+// V of a key t is stored times 2^(-e_t), e_t = 20 k_t by the size of its row (see the
+// expansion), so P holds weights times 2^(e_t): what a key adds to O, whose largest sets
+// the reference, not the weight alone. The row's sum takes 2^(-e_t) again:
+//   P_t = 2^(S_t + e_t - m),  O = sum P_t V_t 2^(-e_t),  l = sum P_t 2^(-e_t).
+// Nearly always e is 0 throughout, which the workspace's header says. Else steps take a
+// loop of their own, 32 keys at a time in two passes, for little code: the long chunk
+// below takes 3.2 ms where all rows have one other e, 4.3 where each step's differ, and
+// 1.9 with e = 0, within a percent of what it took without any of this (6 % more with
+// both kinds of step in one loop, unrolled over the 128 keys).
 // 2,048 new tokens behind 14,336 cached, 128 heads: 1,531 us alone, 1.68 PFLOP/s (87 % of
 // the library product's burst rate); calls in a row run into the power limit (1,790 us).
 // Three prompts of 4,500 to 8,192 tokens, 16 heads: 452 us, 1.56 (the diagonal's masked
@@ -49,6 +58,8 @@
 // with a valid one, beyond which the buffer may hold another request's rows.
 #include <cuda_bf16.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "../../include/mla_decode.h"
 #include "ptx_prefill.cuh"
@@ -81,6 +92,7 @@ constexpr int kSched = 2;                   // items announced ahead
 constexpr int kTailItems = 3;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr float kBinSteps = kBinBits / kRescaleThreshold;
 constexpr float kMostWeight = 32768.0f;     // 2^(kRescaleThreshold + kWeightShift)
 // The reference of a row that has seen no key: below every score, and finite so
 // that a score of -inf against it is a weight of zero and any other infinite.
@@ -428,6 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const float scale = a.scale_log2;
     const uint64_t scale2 = f2_make(scale, scale);
     const float threshold = kRescaleThreshold / scale;  // in units of S
+    const bool odd_bins = hd->odd_bins != 0;
     uint32_t s_use = 0, o_use = 0, o1_use = 0, stats_use = 0;
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
@@ -473,7 +486,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int full0 = __reduce_max_sync(0xffffffffu, begin > 0 ? (begin + stride - 1) / stride : 0);
       const int full1 = __reduce_min_sync(0xffffffffu, end >= kPfKvTile ? (end - kPfKvTile) / stride + 1 : 0);
       float mx_ref = kNoMax, l = 0.f;
-      for (int j = 0; j < n; ++j) {
+      // The kept positions among keys [32 g, 32 g + 32) of step j, a bit each.
+      auto kept = [&](int j, int g) {
+        const int b0 = begin - j * stride, e0 = end - j * stride;
+        const uint32_t above = e0 >= 32 * g + 32 ? ~0u : (1u << max(e0 - 32 * g, 0)) - 1u;
+        const uint32_t below = b0 >= 32 * g + 32 ? ~0u : (1u << max(b0 - 32 * g, 0)) - 1u;
+        return above & ~below;
+      };
+      // Takes mx as the reference if it exceeds the one of now by the threshold.
+      auto move_reference = [&](int j, float mx) {
+        float alpha = 1.f;
+        if (mx > mx_ref + threshold) {
+          alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
+          l *= alpha;
+          mx_ref = mx;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+            tmem_st16(tO + 16 * c, o);
+          }
+        }
+      };
+      // (uniform: all keys of the step have the bin k0)
+      auto weights_of_odd_bins = [&](int j, uint32_t bins, int k0, auto uniform) {
+        constexpr bool kUniform = uniform.value;
+        auto bin_at = [&](int key) {
+          if constexpr (kUniform) return k0;
+          else return static_cast<int>(static_cast<int8_t>(__shfl_sync(0xffffffffu, bins, key >> 2) >> (8 * (key & 3))));
+        };
+        const float per_bin = fminf(threshold * kBinSteps, 1e38f);  // kBinBits in units of S
+        uint32_t s[32];
+        auto scores = [&](int g) {  // with their keys' e
+          tmem_ld32(tS + 32 * g, s);
+          tmem_wait_ld();
+          const uint32_t keep = kept(j, g);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float e = fmaf(static_cast<float>(bin_at(32 * g + c)), per_bin, __uint_as_float(s[c]));
+            s[c] = keep & (1u << c) ? __float_as_uint(e) : 0xff800000u;
+          }
+        };
+        float mx = -CUDART_INF_F;
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          scores(g);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        }
+        move_reference(j, mx);
+        const float neg = kWeightShift - mx_ref * scale;
+        const uint64_t neg2 = f2_make(neg, neg);
+        uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+        auto unit = [](int k) { return __int_as_float((127 - kBinBits * k) << 23); };  // 2^(-e)
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          scores(g);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float t0, t1;
+            f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
+            const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
+            const uint64_t units = f2_make(unit(bin_at(32 * g + 2 * c)), unit(bin_at(32 * g + 2 * c + 1)));
+            sum2[c & 1] = f2_fma(f2_make(p0, p1), units, sum2[c & 1]);
+            s[c] = pack_f16x2(p0, p1);
+          }
+          tmem_st16(tS + 16 * g, s);  // (over scores that are read already)
+        }
+        float s0, s1, s2, s3;
+        f2_split(sum2[0], s0, s1);
+        f2_split(sum2[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+      };
+      auto step_of_odd_bins = [&](int j) {
+        // The bins of keys 4 lane .. 4 lane + 3. (Keys behind the request's have any byte; they are masked.)
+        // (rows x heads x 513 bytes lie in the workspace: 32 bits are enough)
+        const uint32_t at = static_cast<uint32_t>(w.head * a.lay.kv_capacity) + w.t.base + off + j * stride + 4 * lane;
+        const uint32_t bytes = *reinterpret_cast<const uint32_t*>(a.ws + a.lay.bins + at);
+        uint32_t bins = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          bins |= (min(max(static_cast<int8_t>(bytes >> (8 * i)), -kMostBin), kMostBin) & 0xff) << (8 * i);
+        const int k0 = static_cast<int8_t>(__shfl_sync(0xffffffffu, bins, 0));
+        if (__all_sync(0xffffffffu, bins == (k0 & 0xff) * 0x01010101u)) weights_of_odd_bins(j, bins, k0, std::true_type{});
+        else weights_of_odd_bins(j, bins, k0, std::false_type{});
+      };
+      if (odd_bins) {
+        for (int j = 0; j < n; ++j) {
+          if (!(ok = warp_wait(bar(kBarS + x), s_use & 1u))) break;
+          ++s_use;
+          if (any) {
+            tc_fence_after();
+            step_of_odd_bins(j);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          if (lane == 0) mbar_arrive_cluster(lead(kBarP + x));
+        }
+      }
+      for (int j = odd_bins ? n : 0; j < n; ++j) {
         if (!(ok = warp_wait(bar(kBarS + x), s_use & 1u))) break;
         ++s_use;
         if (any) {
@@ -506,13 +622,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
             tmem_wait_ld();
-            if (!full) {  // positions outside [b0, e0) of this step
-              const int b0 = begin - j * stride, e0 = end - j * stride;
+            if (!full) {
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
-                const uint32_t above = e0 >= 32 * g + 32 ? ~0u : (1u << max(e0 - 32 * g, 0)) - 1u;
-                const uint32_t below = b0 >= 32 * g + 32 ? ~0u : (1u << max(b0 - 32 * g, 0)) - 1u;
-                const uint32_t keep = above & ~below;
+                const uint32_t keep = kept(j, g);
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                   if (!(keep & (1u << c))) s[32 * g + c] = 0xff800000u;
@@ -527,24 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
                 mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
               }
-              mx = fmaxf(mx, mx1);
-              float alpha = 1.f;
-              if (mx > mx_ref + threshold) {
-                alpha = exp2_approx((mx_ref - mx) * scale);  // 0 on the first step with a key
-                l *= alpha;
-                mx_ref = mx;
-              }
-              if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                  uint32_t o[16];
-                  tmem_ld16(tO + 16 * c, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
-                  tmem_st16(tO + 16 * c, o);
-                }
-              }
+              move_reference(j, fmaxf(mx, mx1));
               neg = kWeightShift - mx_ref * scale;
             }
             weights();

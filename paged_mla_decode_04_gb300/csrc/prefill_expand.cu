@@ -5,7 +5,10 @@
 // by the softmax scale, and they may be as large as the queries. Values and softmax
 // weights are errors of the result itself, so they are f16, three bits more: with bf16
 // the result was off by 2.9e-3 (2-norm) where its own rounding to bf16 is 1.7e-3, with
-// f16 by 2.1e-3. Values beyond +-65504 saturate.
+// f16 by 2.1e-3. f16 has few exponents: a row's 128 values of a head are stored times
+// 2^(-20 k), k being the bin of the largest (0 for values of usual sizes), and k beside
+// them for the attention, which takes it into the row's score (the header says whether
+// any row has another k than 0).
 //
 // Bound by the tensor core once the operands arrive: per tile of 128 rows x one
 // head an SM would read 128 KB of rows and 256 KB of weights in the 4,096 cycles of
@@ -61,6 +64,12 @@ enum {
 };
 static_assert(8 * kNumBars + 8 <= 256, "barrier area");
 
+// Bin of a row whose largest value has this size (zero: the lowest).
+__device__ __forceinline__ int bin_of(float most) {
+  const int e = (__float_as_int(most) >> 23) - 127;  // -127 .. 128
+  return min(max((e - kBinLow + 10 * kBinBits) / kBinBits - 10, -kMostBin), kMostBin);
+}
+
 // halves == 2: so few units that half the clusters would do, and keys and values are
 // units of their own, at most one a cluster (the smallest call, 95 rows of 16 heads, takes
 // 19.7 us so, 21.2 with whole units; in larger ones the choice would sit in the loops of
@@ -95,8 +104,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t lead0 = mapa(bar0, 0);
   auto lead = [&](int i) -> uint32_t { return lead0 + 8u * i; };
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) hd->next_item = 0;  // for the attention that follows
-  const int row_blocks = (hd->kv_rows + 255) / 256;
+  if (blockIdx.x == 0 && threadIdx.x == kThreads - 1) {  // for the attention that follows (by a thread that has time)
+    hd->next_item = 0;
+    if (hd->zero_rows) hd->odd_bins = 1;
+    hd->zero_rows = 0;
+  }
+  const int kv_rows = hd->kv_rows, row_blocks = (kv_rows + 255) / 256;
   const int64_t clusters = gridDim.x / 2, mine = blockIdx.x / 2;
   const int64_t units = static_cast<int64_t>(row_blocks) * heads * halves;
   const int64_t u0 = units * mine / clusters, u1 = units * (mine + 1) / clusters;
@@ -199,30 +212,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int64_t row = (u / halves / heads) * 256 + 128 * cta + quarter * 32 + lane;
       const bool keep = row < a.lay.kv_capacity;  // (a multiple of 128: whole blocks)
       const int64_t out_row = (u / halves % heads) * a.lay.kv_capacity + row;
+      const bool with_k = halves == 1 || !(u & 1), with_v = halves == 1 || (u & 1);
+      const uint32_t acc_k = tmem + lane_base + acc * 256, acc_v = acc_k + 128;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // 64 columns each: K, K, V, V
-        if (halves == 2 && (u & 1) != (c >> 1)) continue;
+      for (int c = 0; c < 2; ++c) {
+        if (!with_k) break;
         uint32_t r[64];
-        tmem_ld32(tmem + lane_base + acc * 256 + c * 64, r);
-        tmem_ld32(tmem + lane_base + acc * 256 + c * 64 + 32, r + 32);
+        tmem_ld32(acc_k + c * 64, r);
+        tmem_ld32(acc_k + c * 64 + 32, r + 32);
         tmem_wait_ld();
-        if (c == 3) {  // all read: the products may go on
-          tc_fence_before();
-          if (lane == 0) mbar_arrive_cluster(lead(kBarAccFree + acc));
-        }
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.ws + (c < 2 ? a.lay.keys : a.lay.values)) +
-                             out_row * 128 + (c & 1) * 64;
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.ws + a.lay.keys) + out_row * 128 + c * 64;
         if (keep) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint32_t pk[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float x = __uint_as_float(r[16 * v + 2 * i]), y = __uint_as_float(r[16 * v + 2 * i + 1]);
-              pk[i] = c < 2 ? pack_bf16x2(x, y) : pack_f16x2(x, y);
-            }
+            for (int i = 0; i < 8; ++i)
+              pk[i] = pack_bf16x2(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1]));
             st_global_v8(dst + v * 16, pk);
           }
+        }
+      }
+      uint32_t r[128];
+      if (with_v) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(acc_v + c * 32, r + 32 * c);
+        tmem_wait_ld();
+      }
+      tc_fence_before();  // all read: the products may go on
+      if (lane == 0) mbar_arrive_cluster(lead(kBarAccFree + acc));
+      if (with_v && keep) {
+        float most[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 128; i += 4)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            most[e] = fmax3(most[e], fabsf(__uint_as_float(r[i + 2 * e])), fabsf(__uint_as_float(r[i + 2 * e + 1])));
+        const int k = bin_of(fmaxf(most[0], most[1]));
+        const float f = __int_as_float((127 - kBinBits * k) << 23);
+        a.ws[a.lay.bins + out_row] = static_cast<uint8_t>(k);
+        if (k != 0 && row < kv_rows && (most[0] > 0.f || most[1] > 0.f)) hd->odd_bins = 1;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(a.ws + a.lay.values) + out_row * 128;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x, y;
+            f2_split(f2_mul(f2_make(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1])), f2_make(f, f)), x, y);
+            pk[i] = pack_f16x2(x, y);
+          }
+          st_global_v8(dst + v * 16, pk);
         }
       }
     }

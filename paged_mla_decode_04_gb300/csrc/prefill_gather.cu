@@ -413,6 +413,7 @@ __device__ __forceinline__ void plan(const PrefillArgs& a, int64_t* sh) {
   __syncthreads();
   for (int i = threadIdx.x; i < nt; i += threads) sorted[atomicAdd(&bins[bin(i)], 1)] = tiles[i];
   if (threadIdx.x == 0) {
+    hd->odd_bins = 0;
     hd->kv_rows = static_cast<int>(sum[0]);
     hd->all_rows = static_cast<int>(absorb && sum[1] > 0 ? small_start + sum[1] : sum[0]);
     hd->num_tiles = nt;
@@ -449,6 +450,8 @@ __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
 __device__ __forceinline__ bool has_nonfinite(const uint4& v) {
   return has_nonfinite(v.x) || has_nonfinite(v.y) || has_nonfinite(v.z) || has_nonfinite(v.w);
 }
+
+__device__ __forceinline__ bool has_value(const uint4& v) { return ((v.x | v.y | v.z | v.w) & 0x7fff7fffu) != 0; }
 
 constexpr int kGatherWarps = 8, kGatherThreads = 32 * kGatherWarps;
 
@@ -504,7 +507,8 @@ __global__ void __launch_bounds__(kGatherThreads, 4) prefill_gather_kernel(const
       const int row = row0 + warp + k * kGatherWarps;
       const int rel = row - r.base;
       uint4 v[3] = {zero, zero, zero};
-      if (rel < r.rows) {
+      const bool real = rel < r.rows;
+      if (real) {
         const int pos = r.lo + rel, j = pos / a.page_size;
         const int id = j < nb ? ids[j] : -1;
         if (id < 0 || id >= a.num_pages) {
@@ -528,6 +532,7 @@ __global__ void __launch_bounds__(kGatherThreads, 4) prefill_gather_kernel(const
           }
         }
       }
+      if (real && !__any_sync(0xffffffffu, has_value(v[0]) || has_value(v[1])) && lane == 0) hd->zero_rows = 1;
       uint4* dst = reinterpret_cast<uint4*>(a.ws + a.lay.rows) + static_cast<int64_t>(row) * kRowVecs;
       dst[lane] = v[0];
       dst[lane + 32] = v[1];

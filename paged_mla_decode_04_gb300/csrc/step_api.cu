@@ -194,7 +194,7 @@ size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, 
   int h = heads_per_pass;
   if (h == 0) {
     const mla::PfLayout one = mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, 1);
-    const size_t per_head = static_cast<size_t>(one.kv_capacity) * (mla::kDimNope + mla::kDimV) * 2;
+    const size_t per_head = static_cast<size_t>(one.kv_capacity) * ((mla::kDimNope + mla::kDimV) * 2 + 1);
     h = per_head * num_heads <= kExpandedBytes ? num_heads : static_cast<int>(kExpandedBytes / per_head);
     if (h < 1) h = 1;
   }

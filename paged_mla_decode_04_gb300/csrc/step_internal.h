@@ -69,6 +69,11 @@ constexpr int kPfKvTile = 128;    // key rows per step
 // The expanded path's softmax weights and their sums are 2^7 of what they are against
 // the reference maximum (see the attention kernel).
 constexpr float kWeightShift = 7.f, kWeightUnit = 1.f / 128;
+// Values are kept in f16 with a power of two of their own for each row and head,
+// 2^(kBinBits k): bin k is that of the row's largest value, from 2^(kBinBits k + kBinLow)
+// up, with no bins beyond +-kMostBin. Wide bins, so that the rows of a key step hardly
+// ever differ; values between 2^-8 and 2^12 have bin 0 and are kept as they are.
+constexpr int kBinBits = 20, kBinLow = -8, kMostBin = 3;
 
 // Request b as the plan sees it. Gathered positions are [lo, lo + rows); they
 // sit at rows base .. of the workspace's row buffer, followed by zero rows up
@@ -147,7 +152,9 @@ struct PfHeader {
   int all_rows;    // rows of the row buffer in use
   int num_groups;
   int even;        // no tile costs more than twice what another does
-  int pad[55];
+  int zero_rows;   // (gather) a row that is attended has c_kv zero; taken over by the expansion
+  int odd_bins;    // any value row attended may have another bin than 0
+  int pad[53];
 };
 
 // Key steps of a tile whose rows attend relative positions [begin, end).
@@ -156,7 +163,7 @@ __host__ __device__ inline int pf_steps(int begin, int end) {
 }
 
 struct PfLayout {
-  size_t requests, tiles, sorted, splits, part_stats, part_o, rows, keys, values, total;
+  size_t requests, tiles, sorted, splits, part_stats, part_o, rows, keys, values, bins, total;
   int64_t part_rows;    // partial rows of each head
   // Small requests in the latent space (absorb: whether the call may have any).
   size_t groups, group_indptr, group_pages, q_latent, latent, decode;
@@ -220,6 +227,8 @@ inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_hea
   off = align_up(off + static_cast<size_t>(L.kv_capacity) * kDimNope * 2 * heads, 1024);
   L.values = off;
   off = align_up(off + static_cast<size_t>(L.kv_capacity) * kDimV * 2 * heads, 1024);
+  L.bins = off;  // a byte a row and head; steps read whole, past the last row
+  off = align_up(off + static_cast<size_t>(L.kv_capacity) * heads + kPfKvTile, 1024);
   if (L.absorb) {
     L.group_tokens = kGroupRows / num_heads;
     const int64_t per_request = (kPfSmallTokens + L.group_tokens - 1) / L.group_tokens;

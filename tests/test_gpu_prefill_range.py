@@ -1,10 +1,11 @@
-"""Chunk attention (prefill) far from scores of a few units:
-softmax weights far below a row's largest."""
+"""Chunk attention (prefill) far from values of size one and scores of a few units:
+values of any scale and softmax weights far below a row's largest, expanded and in the
+latent space alike."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_prefill import Case, f64
+from test_gpu_prefill import Case, bits, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -49,11 +50,38 @@ def exact_enough(c, ref, n, factor=1.4):
     assert (err <= 6 * 1.67e-3 * unit + 1e-300).all()
 
 
-@pytest.mark.parametrize("nats", [0.0, 8.0, 12.0, 14.0, 16.0])
+# heads, cached, new, e4m3: expanded with split tiles, with two streams, many heads; in the latent space
+FORMS = [(2, [4000, 500], [300, 64], False), (3, [200], [600], True), (16, [3000], [200], False),
+         (16, [9000, 4500], [20, 1], False), (128, [2000], [3], True)]
+
+
+@pytest.mark.parametrize("power", [-50, -35, -20, -12, 12, 16, 30, 50])
+@pytest.mark.parametrize("form", range(len(FORMS)))
+def test_values_of_any_scale(lib, form, power):
+    """w_uv times a power of two: the result times it, as exact as ever."""
+    heads, ctx, new, fp8 = FORMS[form]
+    c = Case(lib, ctx, new, heads=heads, fp8=fp8, seed=form)
+    c.w_uv.mul_(2.0 ** power)
+    exact_enough(c, check(c.run()), sum(new))
+    assert (groups(c) > 0) == (form >= 3)
+
+
+@pytest.mark.parametrize("power", [-40, -20, 15, 40])
+@pytest.mark.parametrize("form", [0, 2, 3])
+def test_cached_rows_of_any_scale(lib, form, power):
+    """c_kv times a power of two and w_uk divided by it: the scores stay, the result grows."""
+    heads, ctx, new, fp8 = FORMS[form]
+    c = Case(lib, ctx, new, heads=heads, seed=form)
+    c.pool.data[..., :512].mul_(2.0 ** power)
+    c.w_uk.mul_(2.0 ** -power)
+    exact_enough(c, check(c.run()), sum(new))
+
+
+@pytest.mark.parametrize("nats", [0.0, 8.0, 12.0, 14.0, 16.0, 17.0, 20.0, 25.0, 30.0])
 @pytest.mark.parametrize("heads,ctx,new", [(2, 2000, 30), (2, 700, 400), (1, 9000, 130), (16, 2000, 200)])
 def test_a_first_key_without_value_takes_nearly_all_weight(lib, heads, ctx, new, nats):
     """An attention sink: c_kv of the first position is zero and its score `nats` above the others' mean. The result is
-    made of the other weights alone, which are small, and is as exact as without the sink."""
+    made of the other weights alone, however small they are, and is as exact as without the sink."""
     c = Case(lib, [ctx], [new], heads=heads, seed=3)
     flat = c.pool.data[1].view(-1, 576)
     flat[:, 512] = 0
@@ -63,3 +91,68 @@ def test_a_first_key_without_value_takes_nearly_all_weight(lib, heads, ctx, new,
     c.q[:, :, 128] = 8
     exact_enough(c, check(c.run()), new)
     assert groups(c) == 0
+
+
+@pytest.mark.parametrize("nats", [8.0, 14.0, 17.0, 25.0])
+@pytest.mark.parametrize("heads,new", [(16, 20), (128, 3)])
+def test_such_a_key_in_the_latent_space(lib, heads, new, nats):
+    """The same there, where each half of a score is rounded to fp16 before the sum, as in decode: half a step of a
+    score x in log2 units is 2^-11 x at most, and that factor is common to all of a row's result."""
+    c = Case(lib, [13000 if heads == 16 else 4000], [new], heads=heads, seed=3)
+    flat = c.pool.data[1].view(-1, 576)
+    flat[:, 512] = 0
+    s = slot(c, 0, 0)
+    flat[s] = 0
+    flat[s, 512] = nats / c.scale / 8
+    c.q[:, :, 128] = 8
+    ref = check(c.run(), 2e-2)
+    assert groups(c) > 0
+    common = 2.0 ** -11 * nats  # (nats: 2^-11 x log2 units times ln 2)
+    assert np.linalg.norm(f64(c.out)[:new] - ref[:new]) <= (1.4 * 1.67e-3 + common) * np.linalg.norm(ref[:new])
+
+
+@pytest.mark.parametrize("heads,ctx,new,window", [
+    (2, [0], [700], 0), (2, [500], [200], 0), (1, [6000], [150], 0), (2, [3000], [513], 1200), (16, [900, 17], [120, 300], 0),
+    (16, [9000, 4000], [20, 300], 0)])
+@pytest.mark.parametrize("step", [0.02, 0.06, -0.02, 0.5])
+def test_values_that_grow_or_shrink_along_the_positions(lib, heads, ctx, new, window, step):
+    """c_kv times 2^(step x position), up to 2^+-40: rows see values of many sizes at once, and a row's result depends
+    on those that it attends alone. Scores come from the rope part (w_uk is zero), so that they stay of a few units."""
+    c = Case(lib, ctx, new, heads=heads, window=window, seed=9)
+    c.w_uk.zero_()
+    flat = c.pool.data[1].view(-1, 576)
+    for b, n in enumerate(a + m for a, m in zip(ctx, new)):
+        at = torch.arange(n, device="cuda")
+        rows = c.table[b].long()[at // c.ps] * c.ps + at % c.ps
+        power = torch.clamp((at - n // 2) * step, -40, 40).floor()
+        flat[rows, :512] *= torch.exp2(power).to(torch.bfloat16)[:, None]
+    exact_enough(c, check(c.run()), sum(new))
+
+
+@pytest.mark.parametrize("big", [2.0 ** 30, 2.0 ** 55])
+@pytest.mark.parametrize("heads,ctx,new", [(2, 100, 300), (1, 5000, 120), (16, 13000, 30)])
+def test_one_huge_row_changes_those_that_attend_it_only(lib, heads, ctx, new, big):
+    args = dict(ctx=[ctx, 90], new=[new, 40], heads=heads, seed=4)
+    a, b = Case(lib, **args), Case(lib, **args)
+    for c in (a, b):
+        c.w_uk.zero_()
+    pos = ctx + 20
+    b.pool.data[1].view(-1, 576)[slot(b, 0, pos), :512] *= big
+    a.run()
+    b.run()
+    hit = torch.zeros(b.T, dtype=torch.bool, device="cuda")
+    hit[20:new] = True
+    assert torch.equal(bits(a.out[~hit]), bits(b.out[~hit])) and torch.equal(bits(a.lse[~hit]), bits(b.lse[~hit]))
+    exact_enough(b, check(b), new + 40)
+
+
+def test_zero_values(lib):
+    """All values zero, and half of them: zero results, the same lse."""
+    c = Case(lib, [300], [200], heads=2)
+    c.w_uv.zero_()
+    c.run().check()
+    assert not c.out[:200].any()
+    c = Case(lib, [300], [200], heads=2)
+    c.w_uv[0].zero_()
+    c.run().check()
+    assert not c.out[:200, 0].any() and c.out[:200, 1].any()
