@@ -444,14 +444,12 @@ __device__ __forceinline__ uint4 widen(uint2 c) {
                     e4m3x2_to_bf16x2(c.y >> 16));
 }
 
-__device__ __forceinline__ bool has_nonfinite(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// The largest sizes among the low and among the high halves of bf16 pairs, as their bits.
+__device__ __forceinline__ uint32_t sizes(uint32_t w) { return w & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t sizes(const uint4& v) {
+  return __vmaxu2(__vmaxu2(sizes(v.x), sizes(v.y)), __vmaxu2(sizes(v.z), sizes(v.w)));
 }
-__device__ __forceinline__ bool has_nonfinite(const uint4& v) {
-  return has_nonfinite(v.x) || has_nonfinite(v.y) || has_nonfinite(v.z) || has_nonfinite(v.w);
-}
-
-__device__ __forceinline__ bool has_value(const uint4& v) { return ((v.x | v.y | v.z | v.w) & 0x7fff7fffu) != 0; }
+__device__ __forceinline__ bool reach(uint32_t sizes, uint32_t bits) { return (sizes & 0xffffu) >= bits || sizes >> 16 >= bits; }
 
 constexpr int kGatherWarps = 8, kGatherThreads = 32 * kGatherWarps;
 
@@ -507,8 +505,8 @@ __global__ void __launch_bounds__(kGatherThreads, 4) prefill_gather_kernel(const
       const int row = row0 + warp + k * kGatherWarps;
       const int rel = row - r.base;
       uint4 v[3] = {zero, zero, zero};
-      const bool real = rel < r.rows;
-      if (real) {
+      if (rel < r.rows) {
+        bool zeros = true;
         const int pos = r.lo + rel, j = pos / a.page_size;
         const int id = j < nb ? ids[j] : -1;
         if (id < 0 || id >= a.num_pages) {
@@ -526,13 +524,16 @@ __global__ void __launch_bounds__(kGatherThreads, 4) prefill_gather_kernel(const
             v[1] = widen(s[lane + 32]);
             if (lane < 8) v[2] = widen(s[lane + 64]);
           }
-          if (__any_sync(0xffffffffu, has_nonfinite(v[0]) || has_nonfinite(v[1]))) {
+          const uint32_t ckv = __vmaxu2(sizes(v[0]), sizes(v[1]));
+          zeros = !__any_sync(0xffffffffu, ckv);
+          if (__any_sync(0xffffffffu, reach(ckv, 0x7f80u))) {
+            zeros = true;
             v[0] = v[1] = zero;
             v[2] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
           }
         }
+        if (zeros && lane == 0) hd->zero_rows = 1;
       }
-      if (real && !__any_sync(0xffffffffu, has_value(v[0]) || has_value(v[1])) && lane == 0) hd->zero_rows = 1;
       uint4* dst = reinterpret_cast<uint4*>(a.ws + a.lay.rows) + static_cast<int64_t>(row) * kRowVecs;
       dst[lane] = v[0];
       dst[lane + 32] = v[1];
