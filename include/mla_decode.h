@@ -331,7 +331,7 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  * is zero). Values with rows whose largest is outside [2^-8, 2^12), and attended
  * rows whose c_kv is zero, cost the call up to 2.3 times its time. In the latent space a pair of bf16
  * queries stands for the exact one, scores and softmax weights are
- * mla_decode's. The result is off by 1.7e-3 to 2.1e-3 (2-norm, of independent
+ * mla_decode's, but half scores beyond 65504 log2 units are infinite. The result is off by 1.7e-3 to 2.1e-3 (2-norm, of independent
  * normal values; 1.7e-3 is its own rounding to bf16). fp8 pools:
  * the codes are widened exactly and kv_scale multiplies the scores and the
  * output. A call repeated gives the same bits; with other requests, capacities

@@ -147,7 +147,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-template <bool kFp8>
+// kInfinite: half scores beyond f16's range cross the exchange as infinities, so that a row
+// with an infinite score gets what a plain softmax gives (weight zero, or NaN). Without it
+// they saturate to 65504, and +inf looks like a key that takes all weight.
+template <bool kFp8, bool kInfinite>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
     mla_decode_kernel(const __grid_constant__ Params p) {
   using C = Cfg<kFp8>;
@@ -729,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         for (int i = 0; i < kHalf / 2; ++i) {
           float s0, s1;
           f2_split(f2_mul(f2_make(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sc2), s0, s1);
-          xp[i] = pack_f16x2(s0, s1);
+          xp[i] = kInfinite ? pack_f16x2_inf(s0, s1) : pack_f16x2(s0, s1);
         }
       }
       tc_fence_before();
@@ -924,10 +927,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
   if (threadIdx.x == 0) MLA_TRACE_EVENT(trc5, 5, kEvGlobalExit, 0);
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kInfinite>
 int max_active_clusters_of() {
   using C = Cfg<kFp8>;
-  if (cudaFuncSetAttribute(mla_decode_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
+  if (cudaFuncSetAttribute(mla_decode_kernel<kFp8, kInfinite>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
       cudaSuccess)
     return -1;
   cudaLaunchConfig_t cfg = {};
@@ -945,15 +948,15 @@ int max_active_clusters_of() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_kernel<kFp8>, &cfg) != cudaSuccess || n <= 0) return -1;
+  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_kernel<kFp8, kInfinite>, &cfg) != cudaSuccess || n <= 0) return -1;
   return n;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kInfinite>
 cudaError_t launch_variant(const CUtensorMap* maps, const DecodeArgs& a, int clusters, cudaStream_t stream) {
   using C = Cfg<kFp8>;
   static bool attr_set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_once(mla_decode_kernel<kFp8>, C::kSmemBytes, attr_set);
+  const cudaError_t e = set_smem_once(mla_decode_kernel<kFp8, kInfinite>, C::kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
   Params p;
   p.kv_wide = maps[0];
@@ -962,28 +965,31 @@ cudaError_t launch_variant(const CUtensorMap* maps, const DecodeArgs& a, int clu
   p.q_narrow = maps[3];
   p.kv_chunks = maps[4];
   p.a = a;
-  return launch_pdl(mla_decode_kernel<kFp8>, dim3(2 * clusters), dim3(C::kThreads), C::kSmemBytes, stream, p);
+  return launch_pdl(mla_decode_kernel<kFp8, kInfinite>, dim3(2 * clusters), dim3(C::kThreads), C::kSmemBytes, stream, p);
 }
 
 }  // namespace
 
-// Co-resident clusters on the current device: the smaller of the two
-// variants' counts, so that one plan serves either pool type (cached per
+// Co-resident clusters on the current device: the smallest of the
+// variants' counts, so that one plan serves any of them (cached per
 // device).
 int decode_max_active_clusters() {
   static int cached[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return -1;
   if (cached[dev] > 0) return cached[dev];
-  const int a = max_active_clusters_of<false>(), b = max_active_clusters_of<true>();
-  if (a <= 0 || b <= 0) return -1;
-  cached[dev] = a < b ? a : b;
+  const int a = max_active_clusters_of<false, false>(), b = max_active_clusters_of<true, false>(),
+            c = max_active_clusters_of<false, true>();
+  if (a <= 0 || b <= 0 || c <= 0) return -1;
+  const int least = a < b ? a : b;
+  cached[dev] = least < c ? least : c;
   return cached[dev];
 }
 
 cudaError_t launch_decode(const CUtensorMap* maps, const DecodeArgs& a, int clusters, cudaStream_t stream) {
-  return a.dtype == MLA_DTYPE_FP8_E4M3 ? launch_variant<true>(maps, a, clusters, stream)
-                                       : launch_variant<false>(maps, a, clusters, stream);
+  if (a.dtype == MLA_DTYPE_FP8_E4M3) return launch_variant<true, false>(maps, a, clusters, stream);
+  return a.infinite_scores ? launch_variant<false, true>(maps, a, clusters, stream)
+                           : launch_variant<false, false>(maps, a, clusters, stream);
 }
 
 }  // namespace mla

@@ -128,6 +128,7 @@ struct DecodeArgs {
   float kv_scale;
   float scale_log2;  // softmax_scale * log2(e) (* kv_scale for fp8 pools)
   float out_scale;   // 1, or kv_scale for fp8 pools (codes are dequantised by scaling O)
+  bool infinite_scores;  // (bf16 pools) half scores beyond 65504 are infinite instead of saturated
 };
 
 // Index of the current device for per-device caches (kMaxDevices entries),

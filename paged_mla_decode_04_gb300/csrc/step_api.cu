@@ -73,6 +73,7 @@ int attend_small(const mla::PrefillMaps& m, const mla::PrefillArgs& a, const voi
   d.kv_scale = 1.f;
   d.scale_log2 = a.scale_log2;
   d.out_scale = a.out_scale;
+  d.infinite_scores = true;  // (as in the expanded path)
   cudaError_t e = mla::launch_prefill_q_latent(m.w_uk, a, q, st);
   if (e == cudaSuccess) e = mla::launch_decode(maps, d, a.clusters, st);
   if (e == cudaSuccess) e = mla::launch_prefill_latent(a, st);

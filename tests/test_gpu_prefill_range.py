@@ -1,6 +1,6 @@
 """Chunk attention (prefill) far from values of size one and scores of a few units:
-values of any scale and softmax weights far below a row's largest, expanded and in the
-latent space alike."""
+values of any scale, softmax weights far below a row's largest, infinite and large
+scores, expanded and in the latent space alike."""
 import numpy as np
 import pytest
 import torch
@@ -156,3 +156,69 @@ def test_zero_values(lib):
     c.w_uv[0].zero_()
     c.run().check()
     assert not c.out[:200, 0].any() and c.out[:200, 1].any()
+
+
+# heads, cached, new, in the latent space
+SCORES = [(2, [90], [20], False), (2, [2000], [300], False), (16, [13000], [20], True), (16, [9000, 4000], [33, 2], True),
+          (128, [2000], [5], True)]
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("dim", [514, 570])
+@pytest.mark.parametrize("heads,ctx,new,latent", SCORES)
+def test_infinite_rope_value(lib, heads, ctx, new, latent, value, dim):
+    """A score of -inf is a weight of zero; one of +inf gives NaN to the rows that attend it and to no others."""
+    args = dict(ctx=ctx, new=new, heads=heads, seed=5)
+    a, b = Case(lib, **args), Case(lib, **args)
+    for c in (a, b):
+        c.q[:, :, 128:] = 0
+        c.q[:, :, 128 + dim - 512] = 1.0
+    pos = ctx[0] + new[0] // 2
+    b.pool.data[1].view(-1, 576)[slot(b, 0, pos), dim] = value
+    a.run()
+    b.run()
+    assert (groups(b) > 0) == latent
+    if value < 0:
+        b.check()
+        return
+    hit = torch.zeros(b.T, dtype=torch.bool, device="cuda")
+    hit[new[0] // 2:new[0]] = True
+    assert torch.isnan(b.out[hit].float()).all() and torch.isnan(b.lse[hit]).all()
+    assert torch.equal(bits(a.out[~hit]), bits(b.out[~hit])) and torch.equal(bits(a.lse[~hit]), bits(b.lse[~hit]))
+
+
+@pytest.mark.parametrize("heads,ctx,new", [(2, [0], [40]), (16, [0, 13000], [1, 3])])
+def test_a_row_whose_only_score_is_minus_infinity(lib, heads, ctx, new):
+    """Position 0 attends itself alone: no weight at all is NaN, as in a plain softmax, and has no finite lse."""
+    c = Case(lib, ctx, new, heads=heads)
+    c.q[:, :, 128:] = 0
+    c.q[:, :, 130] = 1.0
+    c.pool.data[1].view(-1, 576)[slot(c, 0, 0), 514] = -float("inf")
+    c.run()
+    assert (groups(c) > 0) == (heads == 16)
+    assert torch.isnan(c.out[0].float()).all() and not torch.isfinite(c.lse[0]).any()
+    assert torch.isfinite(c.out[1:sum(new)].float()).all() and torch.isfinite(c.lse[1:sum(new)]).all()
+
+
+@pytest.mark.parametrize("q_std", [6.0, 0.0])
+@pytest.mark.parametrize("heads,ctx,new,latent", SCORES)
+def test_peaked_and_equal_scores(lib, heads, ctx, new, latent, q_std):
+    c = Case(lib, ctx, new, heads=heads, q_std=q_std).run().check(3e-2 if q_std else 6e-3)
+    assert (groups(c) > 0) == latent
+
+
+@pytest.mark.parametrize("heads,ctx,new,latent", SCORES)
+def test_growing_scores(lib, heads, ctx, new, latent):
+    """Scores that climb by hundreds along the positions. In the latent space each half of a score is off by up to 2^-11
+    of it, which the bounds of every output hold; all outputs together are then off by as much."""
+    c = Case(lib, ctx, new, heads=heads)
+    for b, n in enumerate(a + m for a, m in zip(ctx, new)):
+        at = torch.arange(n, device="cuda")
+        flat = c.pool.data[1].view(-1, 576)
+        slots = c.table[b].long()[at // c.ps] * c.ps + at % c.ps
+        flat[slots, 512:] = 0
+        flat[slots, 512] = torch.linspace(0, 60, n, device="cuda").to(torch.bfloat16)
+    c.q[:, :, 128:] = 0
+    c.q[:, :, 128] = 60.0
+    c.run().check(0.3 if latent else 6e-3)
+    assert (groups(c) > 0) == latent
