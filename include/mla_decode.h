@@ -351,9 +351,11 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
                 int window, void* workspace, size_t workspace_bytes, void* out, float* lse, void* stream);
 
 /* Bytes of workspace for mla_prefill with room for the keys and values of
- * heads_per_pass heads (0: of all heads, or of as many as 8 GiB hold). A
- * workspace of another size is used for as many heads a pass as fit; below
- * one head's mla_prefill returns MLA_ERR_WORKSPACE. 0 on bad arguments. */
+ * heads_per_pass heads (0: of all heads, or of as many as 8 GiB hold). It does
+ * for every call of as many heads with no more requests, rows and positions, in
+ * no more passes. A workspace of another size is used for as many heads a pass
+ * as fit, without the latent space where that does not fit; below one head's
+ * mla_prefill returns MLA_ERR_WORKSPACE. 0 on bad arguments. */
 size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, int num_heads, int heads_per_pass);
 
 /* Reads the status word of `workspace` into *code (MLA_STATUS_* bits) and, if

@@ -81,6 +81,19 @@ int attend_small(const mla::PrefillMaps& m, const mla::PrefillArgs& a, const voi
   return done(e);
 }
 
+// The layout with the most heads at a time that `bytes` hold, none: heads = 0.
+mla::PfLayout fit(int batch, int q_rows, int64_t max_kv, int num_heads, bool absorb, size_t bytes) {
+  int lo = 0, hi = num_heads;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (mla::pf_layout(batch, q_rows, max_kv, num_heads, mid, absorb).total <= bytes) lo = mid;
+    else hi = mid - 1;
+  }
+  if (lo == 0) return mla::PfLayout{};
+  const int passes = (num_heads + lo - 1) / lo;
+  return mla::pf_layout(batch, q_rows, max_kv, num_heads, (num_heads + passes - 1) / passes, absorb);
+}
+
 bool prefill_sizes_ok(int batch, int q_rows, int64_t max_kv, int heads) {
   if (batch < 0 || q_rows < 0 || max_kv < 0 || heads < 1 || heads > 1024) return false;
   if (static_cast<int64_t>(q_rows) * heads >= (1ll << 31)) return false;
@@ -192,15 +205,21 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
 
 size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, int num_heads, int heads_per_pass) {
   if (!prefill_sizes_ok(batch, q_rows, max_kv_tokens, num_heads) || heads_per_pass < 0) return 0;
+  // The most rows with which a call of no more requests and positions may take the latent path.
+  int64_t latent_rows = q_rows;
+  if (!mla::pf_may_absorb(batch, latent_rows, max_kv_tokens, num_heads) && latent_rows > 8ll * batch) latent_rows = 8ll * batch;
+  const bool latent = mla::pf_may_absorb(batch, latent_rows, max_kv_tokens, num_heads);
   int h = heads_per_pass;
   if (h == 0) {
-    const mla::PfLayout one = mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, 1);
+    const mla::PfLayout one = mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, 1, latent);
     const size_t per_head = static_cast<size_t>(one.kv_capacity) * ((mla::kDimNope + mla::kDimV) * 2 + 1);
     h = per_head * num_heads <= kExpandedBytes ? num_heads : static_cast<int>(kExpandedBytes / per_head);
     if (h < 1) h = 1;
   }
   if (h > num_heads) h = num_heads;
-  return mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, h).total;
+  const size_t expanded = mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, h, false).total;
+  const size_t both = latent ? mla::pf_layout(batch, latent_rows, max_kv_tokens, num_heads, h, true).total : 0;
+  return expanded > both ? expanded : both;
 }
 
 int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t* q_indptr, const int32_t* page_indptr,
@@ -215,17 +234,14 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
   if (!aligned(q, 16) || !aligned(w_uk, 16) || !aligned(w_uv, 16) || !aligned(out, 32)) return MLA_ERR_ARG;
   if (!page_indptr && (max_blocks <= 0 || static_cast<int64_t>(max_blocks) * pool->page_size > INT_MAX)) return MLA_ERR_ARG;
   if (!workspace || !aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
-  int lo = 0, hi = num_heads;  // the most heads whose keys and values fit
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, mid).total <= workspace_bytes) lo = mid;
-    else hi = mid - 1;
-  }
-  if (lo == 0) return MLA_ERR_WORKSPACE;
-  const int passes = (num_heads + lo - 1) / lo;
-  const int per_pass = (num_heads + passes - 1) / passes;
-
+  // (a workspace of another call's size may lack the room for the latent path)
+  const bool absorb = mla::pf_may_absorb(batch, q_rows, max_kv_tokens, num_heads);
   mla::PrefillArgs a = {};
+  a.lay = fit(batch, q_rows, max_kv_tokens, num_heads, absorb, workspace_bytes);
+  if (absorb && a.lay.heads == 0) a.lay = fit(batch, q_rows, max_kv_tokens, num_heads, false, workspace_bytes);
+  if (a.lay.heads == 0) return MLA_ERR_WORKSPACE;
+  const int per_pass = a.lay.heads;
+
   a.pool = pool->data;
   a.page_indptr = page_indptr;
   a.page_ids = page_ids;
@@ -234,7 +250,6 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
   a.out = out;
   a.lse = lse;
   a.ws = static_cast<uint8_t*>(workspace);
-  a.lay = mla::pf_layout(batch, q_rows, max_kv_tokens, num_heads, per_pass);
   a.max_blocks = max_blocks;
   a.max_kv = max_kv_tokens;
   a.batch = batch;

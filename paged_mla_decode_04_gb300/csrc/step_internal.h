@@ -191,11 +191,12 @@ inline bool pf_may_absorb(int64_t batch, int64_t q_rows, int64_t max_kv, int64_t
   return q_rows <= 8 * batch && (max_kv * num_heads >= 100000 || batch * num_heads >= 400);
 }
 
-// Workspace regions for `heads` of num_heads heads at a time.
-inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_heads, int heads) {
+// Workspace regions for `heads` of num_heads heads at a time, with or without the latent
+// path. Every region grows with each of the arguments.
+inline PfLayout pf_layout(int batch, int64_t q_rows, int64_t max_kv, int num_heads, int heads, bool absorb) {
   PfLayout L = {};
   L.heads = heads;
-  L.absorb = pf_may_absorb(batch, q_rows, max_kv, num_heads);
+  L.absorb = absorb;
   const int64_t slack = static_cast<int64_t>(batch) * (L.absorb ? kBlockTokens : kPfKvAlign) + (L.absorb ? 256 : 0);
   L.kv_capacity = (max_kv + slack + kPfKvTile - 1) / kPfKvTile * kPfKvTile;
   L.max_tiles = q_rows / kPfRows + batch;
