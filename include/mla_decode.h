@@ -248,7 +248,7 @@ int mla_uv_project(const void* attn_out, const void* w_uv, void* y, int batch,
  * as -1 and gives slot and position -1. Tokens beyond max_tokens and ids
  * beyond max_page_ids are not written (MLA_STATUS_BAD_LENGTH).
  *   workspace:    whose status word records this (a decode or prefill
- *                 workspace), or NULL.
+ *                 workspace, 256-byte aligned), or NULL.
  * Outputs share no memory with each other or with inputs (but for state).
  * page_size is 16, 32, 64 or 128; max_blocks * page_size and batch * max_blocks
  * are below 2^31. */
@@ -286,7 +286,8 @@ int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int 
  *                 multiples of 8 and at least 64, pointers 16-byte aligned.
  *                 q_out may be q_rope (in place) or rows that share no element
  *                 with it; other overlaps are refused with MLA_ERR_ARG.
- *   pool, layer:  used with rows only; rows are not the pool's. workspace: for the status word, or NULL. */
+ *   pool, layer:  used with rows only; rows are not the pool's. workspace: for the status word
+ *                 (256-byte aligned), or NULL. */
 int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const int64_t* slot_mapping, int n,
                    const int32_t* positions, int num_axes, const uint8_t* pair_axis, const float* cos_sin,
                    int max_position, int interleaved, const void* norm_weight, float norm_eps, const void* q_rope,

@@ -118,6 +118,7 @@ int mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int 
   if (batch > 0 && (!context_lens || !new_lens || !block_table)) return MLA_ERR_ARG;
   if (max_tokens > 0 && !slot_mapping) return MLA_ERR_ARG;
   if (page_indptr ? !page_ids && max_page_ids > 0 : page_ids != nullptr) return MLA_ERR_ARG;
+  if (!aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
   mla::TablesArgs a = {};
   a.context_lens = context_lens;
   a.new_lens = new_lens;
@@ -176,6 +177,7 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
       if (off < mla::kDimRope * 2 || off > pitch - mla::kDimRope * 2) return MLA_ERR_ARG;
     }
   }
+  if (!aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
   int dtype = MLA_DTYPE_BF16;
   if (rows) {
     dtype = pool->dtype;

@@ -66,8 +66,13 @@ T* here_or_none(PyObject* o, const char* name, at::ScalarType type, int device) 
   return o == Py_None ? nullptr : here<T>(o, name, type, device);
 }
 
-void* any_or_none(PyObject* o, const char* name, int device) {
-  return o == Py_None ? nullptr : here(tensor(o, name), name, device);
+// A workspace for the status word alone: decode's and prefill's begin with it.
+void* status_workspace(PyObject* o, int device) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, "workspace");
+  void* p = here(t, "workspace", device);
+  if (t.nbytes() < 256) refuse("workspace must hold 256 bytes at least");
+  return p;
 }
 
 int int_of(int64_t v, const char* name) {
@@ -178,7 +183,7 @@ PyObject* extend_tables(PyObject*, PyObject* const* v, Py_ssize_t n) {
     auto* page_indptr_p = here_or_none<int32_t>(v[11], "page_indptr", kI32, dev);
     auto* ids_p = here_or_none<int32_t>(v[12], "page_ids", kI32, dev);
     auto* state_p = here<int32_t>(state, "state", kI32, dev);
-    void* ws = any_or_none(v[13], "workspace", dev);
+    void* ws = status_workspace(v[13], dev);
     void* stream = stream_of(v[14], dev);
     const int b = int_of(batch, "batch"), capacity = int_of(free.numel(), "free_pages"), width = int_of(table.size(1), "max_blocks"),
               t = int_of(tokens, "max_tokens"), ids = int_of(max_ids, "max_page_ids");
@@ -266,7 +271,7 @@ PyObject* rope_write(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const float eps = real(v[8]);
     const auto* pos_p = here<int32_t>(pos, "positions", kI32, dev);
     const auto* cs_p = here<float>(cos_sin, "cos_sin", kF32, dev);
-    void* ws = any_or_none(v[13], "workspace", dev);
+    void* ws = status_workspace(v[13], dev);
     void* stream = stream_of(v[14], dev);
     const int t = int_of(tokens, "tokens"), ax = int_of(axes, "axes"), table = int_of(cos_sin.size(0), "positions"),
               heads = int_of(q.heads, "heads");
