@@ -28,9 +28,11 @@ from typing import Optional
 
 import torch
 
+from ._build import binding_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla_decode.so")
-BINDING_PATH = os.path.join(_HERE, "_step_binding.so")
+BINDING_PATH = binding_path()
 
 MLA_OK = 0
 ERRORS = {-1: "MLA_ERR_ARG", -2: "MLA_ERR_UNSUPPORTED", -3: "MLA_ERR_WORKSPACE", -4: "MLA_ERR_CUDA"}
@@ -371,7 +373,7 @@ def _step():
     if _binding is None:
         lib = load_library()
         if not os.path.exists(BINDING_PATH):
-            raise MlaError("_step_binding.so not built; run paged_mla_decode_04_gb300._build.build()")
+            raise MlaError("%s not built; run paged_mla_decode_04_gb300._build.build()" % os.path.basename(BINDING_PATH))
         spec = importlib.util.spec_from_file_location("_step_binding", BINDING_PATH)
         b = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(b)

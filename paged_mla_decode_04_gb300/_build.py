@@ -1,6 +1,6 @@
-"""Build libmla_decode.so in-tree with nvcc for sm_103a (no cmake, no torch), and
-beside it _step_binding.so, the compiled Python binding of the prefill step's
-calls (the host compiler, PyTorch's headers).
+"""Build libmla_decode.so in-tree with nvcc for sm_103a (no cmake, no torch). Where
+PyTorch is there, also the compiled Python binding of the prefill step's calls (the
+host compiler, PyTorch's headers), in a file named after the versions that it is for.
 
 Each .cu file compiles to an object in parallel; the objects link into one
 shared library with the CUDA runtime linked statically, so the library loads
@@ -13,6 +13,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,7 +24,6 @@ SOURCES = ["mla_api.cu", "kv_write.cu", "plan_merge.cu", "decode_sm103.cu", "uv_
            "step_api.cu", "step_tables.cu", "rope_write.cu", "prefill_gather.cu", "prefill_expand.cu", "prefill_attn.cu",
            "prefill_absorb.cu"]
 HEADERS = ["ptx.cuh", "mla_internal.h", "trace.cuh", "host_util.h", "step_internal.h", "ptx_prefill.cuh", "scan.cuh"]
-BINDING = os.path.join(HERE, "_step_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,6 +46,19 @@ def _stale(target, inputs):
     return any(os.path.getmtime(i) > t for i in inputs)
 
 
+def _run(cmd) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compiler failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    return r.stderr
+
+
+def binding_path() -> str:
+    """The binding for this Python and this PyTorch (their ABIs change between versions)."""
+    import torch
+    return os.path.join(HERE, "_step_binding.%s-torch%s.so" % (sys.implementation.cache_tag, torch.__version__))
+
+
 def _binding_command(target: str):
     import torch
     root = os.path.dirname(torch.__file__)
@@ -57,11 +70,18 @@ def _binding_command(target: str):
             "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
+def _make_binding(target: str) -> None:
+    tmp = target + ".tmp.%d" % os.getpid()
+    _run(_binding_command(tmp))
+    os.replace(tmp, target)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, defines=(),
           lib_path: str = LIB, build_dir: str = BUILD) -> str:
     """Compile every kernel file, link libmla_decode.so and build the binding (only what is stale).
     `defines` (e.g. ["-DMLA_TRACE"] for the event-traced build) go with
-    their own lib_path and build_dir."""
+    their own lib_path and build_dir. The library does not wait for the binding: it is there
+    even where the binding could not be made (an error) or PyTorch is missing (none)."""
     os.makedirs(build_dir, exist_ok=True)
     deps = _deps()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -76,31 +96,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
         if force or ptxas_info or _stale(o, [s] + deps):
             jobs.append([nvcc(), *flags, "-c", s, "-o", o])
 
-    binding_tmp = BINDING + ".tmp.%d" % os.getpid()
-    binding = lib_path == LIB and (force or _stale(BINDING, [os.path.join(CSRC, "step_binding.cpp")] + deps[-2:]))
-    link = force or bool(jobs)
-    if binding:
-        jobs.insert(0, _binding_command(binding_tmp))
+    binding = None
+    if lib_path == LIB:
+        try:
+            binding = binding_path()
+        except ImportError:
+            pass
+    if binding and not force and not _stale(binding, [os.path.join(CSRC, "step_binding.cpp")] + deps[-2:]):
+        binding = None
 
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("compiler failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
-        return r.stderr
-
-    with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4) or 1) as ex:
-        for log in ex.map(run, jobs):
+    with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+        made = ex.submit(_make_binding, binding) if binding else None
+        for log in ex.map(_run, jobs):
             if verbose and log:
                 print(log)
-    if binding:
-        os.replace(binding_tmp, BINDING)
-    if link or _stale(lib_path, objs):
-        tmp = lib_path + ".tmp.%d" % os.getpid()
-        run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"])
-        os.replace(tmp, lib_path)
+        if force or jobs or _stale(lib_path, objs):
+            tmp = lib_path + ".tmp.%d" % os.getpid()
+            _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"])
+            os.replace(tmp, lib_path)
+        if made:
+            try:
+                made.result()
+            except (RuntimeError, OSError) as e:
+                raise RuntimeError("%s is built, its Python binding is not: %s" % (os.path.basename(lib_path), e)) from e
     return lib_path
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True, ptxas_info="--ptxas" in sys.argv))
