@@ -365,7 +365,7 @@ cudaError_t launch_extend_tables(const TablesArgs& a, cudaStream_t stream) {
   }
   const cudaError_t e = launch_pdl(tables_scan_kernel, dim3(1), dim3(1024), 0, stream, a);
   if (e != cudaSuccess) return e;
-  const int token_blocks = (a.max_tokens + kFillThreads - 1) / kFillThreads;
+  const int token_blocks = static_cast<int>((static_cast<int64_t>(a.max_tokens) + kFillThreads - 1) / kFillThreads);
   const int id_span = kFillThreads * kIdsPerThread;
   const int64_t id_blocks = (ids + id_span - 1) / id_span;
   if (token_blocks + id_blocks == 0) return cudaSuccess;

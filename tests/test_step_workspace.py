@@ -48,3 +48,19 @@ def test_short_workspaces_are_refused(short):
     assert m.get_error(ws) == m.STATUS_BAD_PAGE | m.STATUS_BAD_POSITION  # (request 1's cached pages are -1)
     with pytest.raises(m.MlaError, match="WORKSPACE"):
         m.extend_tables(**tables, workspace=torch.zeros(512, dtype=torch.uint8, device="cuda")[4:])
+
+
+@pytest.mark.gpu
+def test_as_many_tokens_as_an_int_holds():
+    """Slots for 2^31 - 1 tokens, of which 4,000 requests (two launches) use 8,000: the others are pad entries."""
+    import paged_mla_decode_04_gb300 as m
+    B, most = 4000, (1 << 31) - 1
+    z = lambda n, v=0: torch.full((n,), v, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots = torch.full((most,), 7, dtype=torch.int64, device="cuda")
+    table, state, indptr = torch.full((B, 1), -1, dtype=torch.int32, device="cuda"), z(2), z(B + 1)
+    m.extend_tables(z(B), z(B, 2), torch.arange(B, dtype=torch.int32, device="cuda"), z(1, B), table, 16, B, slots, indptr, state)
+    assert state.tolist() == [0, B] and indptr[-1] == 2 * B
+    want = (torch.arange(B - 1, -1, -1, device="cuda")[:, None] * 16 + torch.arange(2, device="cuda")).flatten()
+    assert torch.equal(slots[:2 * B], want)
+    for part in slots[2 * B:].split(1 << 28):
+        assert bool((part == -1).all())
