@@ -235,17 +235,21 @@ int mla_uv_project(const void* attn_out, const void* w_uv, void* y, int batch,
  *   page_indptr, page_ids: device, [batch + 1] and [max_page_ids] int32: the
  *                 tables as CSR lists, of ceil((L + n) / page_size) pages each;
  *                 or both NULL. Entries behind the last page are left as they were.
- *   state:        device, [2] int32, written last: the free pages left, and the
- *                 first request that was refused for want of pages (batch if
- *                 none). state may be free_count's own address: the count is
- *                 then updated in place.
+ *   state:        device, [2] int32: the free pages left, and the first request
+ *                 that was refused for want of pages (batch if none). state may
+ *                 be free_count's own address: the count is then updated in place.
+ * All outputs are complete when the call is, in the order of the stream; state
+ * is written before the others and says nothing of them.
  * A request whose pages do not all remain (MLA_STATUS_NO_PAGES) takes none: its
  * new tokens have slot and position -1, its CSR list only the pages it held.
  * Requests after it that need pages are refused too, those that need none are
  * served. A request with a negative length or more tokens than max_blocks
  * blocks hold (MLA_STATUS_BAD_LENGTH) is refused alike; a negative n counts as
- * no tokens. A page id outside [0, num_pages) (MLA_STATUS_BAD_PAGE) is stored
- * as -1 and gives slot and position -1. Tokens beyond max_tokens and ids
+ * no tokens. A free page outside [0, num_pages) (MLA_STATUS_BAD_PAGE) is stored
+ * as -1 in the table and its list. Such an id among the pages held already stays
+ * as it is in both, and sets the status only where a new token lies in its page
+ * (entries before a window, which nothing reads, may hold anything). Either gives
+ * the tokens slot and position -1. Tokens beyond max_tokens and ids
  * beyond max_page_ids are not written (MLA_STATUS_BAD_LENGTH).
  *   workspace:    whose status word records this (a decode or prefill
  *                 workspace, 256-byte aligned), or NULL.

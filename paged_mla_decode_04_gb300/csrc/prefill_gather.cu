@@ -28,8 +28,8 @@
 namespace mla {
 namespace {
 
-constexpr int kPlanThreads = 512;  // at most
-constexpr int kCostBins = 128;     // (the least number of threads)
+constexpr int kPlanThreads = 512;  // in a launch of its own (kGatherThreads beside the gather)
+constexpr int kCostBins = 128;     // (no more than threads)
 constexpr int kRowVecs = kDimRow * 2 / 16;  // 72
 
 __device__ __forceinline__ int64_t block_exclusive(int64_t x, int64_t* sh, int64_t* total) {
@@ -620,9 +620,7 @@ cudaError_t launch_prefill_gather(const PrefillArgs& a, cudaStream_t stream) {
     return launch_pdl(bf16 ? prefill_gather_kernel<MLA_DTYPE_BF16, true> : prefill_gather_kernel<MLA_DTYPE_FP8_E4M3, true>, grid,
                       dim3(kGatherThreads), 0, stream, a);
   }
-  int threads = kCostBins;  // no more warps than requests and tiles: scans cost by the warp
-  while (threads < kPlanThreads && threads < most) threads *= 2;
-  const cudaError_t e = launch_pdl(prefill_plan_kernel, dim3(1), dim3(threads), 0, stream, a);
+  const cudaError_t e = launch_pdl(prefill_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(bf16 ? prefill_gather_kernel<MLA_DTYPE_BF16, false> : prefill_gather_kernel<MLA_DTYPE_FP8_E4M3, false>,
                     dim3(static_cast<unsigned>(min(runs, blocks))), dim3(kGatherThreads), 0, stream, a);
