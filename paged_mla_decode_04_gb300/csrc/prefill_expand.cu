@@ -64,8 +64,9 @@ enum {
 };
 static_assert(8 * kNumBars + 8 <= 256, "barrier area");
 
-// Bin of a row whose largest value has this size (zero: the lowest).
+// Bin of a row whose largest value has this size.
 __device__ __forceinline__ int bin_of(float most) {
+  if (most == 0.f) return kZeroBin;
   const int e = (__float_as_int(most) >> 23) - 127;  // -127 .. 128
   return min(max((e - kBinLow + 10 * kBinBits) / kBinBits - 10, -kMostBin), kMostBin);
 }

@@ -72,8 +72,11 @@ constexpr float kWeightShift = 7.f, kWeightUnit = 1.f / 128;
 // Values are kept in f16 with a power of two of their own for each row and head,
 // 2^(kBinBits k): bin k is that of the row's largest value, from 2^(kBinBits k + kBinLow)
 // up, with no bins beyond +-kMostBin. Wide bins, so that the rows of a key step hardly
-// ever differ; values between 2^-8 and 2^12 have bin 0 and are kept as they are.
-constexpr int kBinBits = 20, kBinLow = -8, kMostBin = 3;
+// ever differ; values between 2^-8 and 2^12 have bin 0 and are kept as they are. Rows of
+// zeros may have any; kZeroBin leaves room for weights 2^40 times the others'. (A score
+// takes its key's power, which rounds it to 2^-24 of that: a log of the sum is off by up
+// to 2e-6 with 40, 4e-6 with 60.)
+constexpr int kBinBits = 20, kBinLow = -8, kMostBin = 3, kZeroBin = -2;
 
 // Request b as the plan sees it. Gathered positions are [lo, lo + rows); they
 // sit at rows base .. of the workspace's row buffer, followed by zero rows up

@@ -102,3 +102,12 @@ def test_many_requests_each_of_its_own_scale(lib, n):
     d.run()
     e.run()
     assert torch.equal(bits(d.out), bits(e.out)) and torch.equal(bits(d.lse), bits(e.lse))
+
+
+@pytest.mark.parametrize("window", [1, 2, 0])
+def test_lse_of_rows_without_values(lib, window):
+    """c_kv zero and queries zero: lse is the log of the number of attended positions, to the bounds of other rows."""
+    c = Case(lib, [170, 60], [56, 300], heads=3, window=window, q_std=0.0)
+    c.pool.data[1].view(-1, 576)[:, :512] = 0
+    c.run().check()
+    assert not c.out[:356].any()
