@@ -44,14 +44,14 @@
 //   P_t = 2^(S_t + e_t - m),  O = sum P_t V_t 2^(-e_t),  l = sum P_t 2^(-e_t).
 // Nearly always e is 0 throughout, which the workspace's header says. Else steps take a
 // loop of their own, 32 keys at a time in two passes, for little code: the long chunk
-// below takes 3.2 ms where all rows have one other e, 4.3 where each step's differ, and
+// below takes 3.1 ms where all rows have one other e, 4.3 where each step's differ, and
 // 1.9 with e = 0, within a percent of what it took without any of this (6 % more with
 // both kinds of step in one loop, unrolled over the 128 keys).
-// 2,048 new tokens behind 14,336 cached, 128 heads: 1,531 us alone, 1.68 PFLOP/s (87 % of
+// 2,048 new tokens behind 14,336 cached, 128 heads: 1,510 us alone, 1.70 PFLOP/s (88 % of
 // the library product's burst rate); calls in a row run into the power limit (1,790 us).
-// Three prompts of 4,500 to 8,192 tokens, 16 heads: 452 us, 1.56 (the diagonal's masked
+// Three prompts of 4,500 to 8,192 tokens, 16 heads: 465 us, 1.52 (the diagonal's masked
 // halves, and each item's start and end, about five units of (stream, step)). A window of
-// 4,096 and chunks of 300 to 1,024 tokens, 128 heads: 719 us, 1.24 (86 % of the rows of
+// 4,096 and chunks of 300 to 1,024 tokens, 128 heads: 741 us, 1.20 (86 % of the rows of
 // its tiles are real, and a tile's rows span 511 keys more than each attends).
 // Positions beyond a row's range are masked by selection, never by adding, so
 // NaN in them stays out; the last step multiplies only up to the last 16 keys

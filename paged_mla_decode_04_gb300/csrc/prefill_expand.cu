@@ -23,7 +23,7 @@
 // runs under the products of the next. Weights come by TMA in chunks of 64 of the
 // 512 dims, W_UK K-major and W_UV MN-major, 16 KB a stage and block.
 //
-// 16,384 rows for 128 heads: 331 us, 1.66 PFLOP/s (86 % of the library product's burst
+// 16,384 rows for 128 heads: 334 us, 1.65 PFLOP/s (85 % of the library product's burst
 // rate, 95 % of what it sustains); 19,799 rows for 16 heads: 55 us, 1.50, where a
 // cluster's last run is short and each run's rows arrive before its first product. Of
 // the rest the tensor core waits 26 % (active 74 %): at a run's start, and for power.
@@ -72,8 +72,8 @@ __device__ __forceinline__ int bin_of(float most) {
 }
 
 // halves == 2: so few units that half the clusters would do, and keys and values are
-// units of their own, at most one a cluster (the smallest call, 95 rows of 16 heads, takes
-// 19.7 us so, 21.2 with whole units; in larger ones the choice would sit in the loops of
+// units of their own, at most one a cluster (the smallest call, 95 rows of 16 heads, became
+// 1.5 us shorter by it, of 21; in larger ones the choice would sit in the loops of
 // all, which costs 1 to 2 %, hence the template).
 template <int halves>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -205,7 +205,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t n = 0;
-    bool ok = true;
+    bool ok = true, told = false;
     for (int64_t u = u0; u < u1; ++u, ++n) {
       const uint32_t acc = n & 1u;
       if (!(ok = mbar_spin_warp(bar(kBarAccFull + acc), (n >> 1) & 1u, abort_flag))) break;
@@ -252,7 +252,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int k = bin_of(fmaxf(most[0], most[1]));
         const float f = __int_as_float((127 - kBinBits * k) << 23);
         a.ws[a.lay.bins + out_row] = static_cast<uint8_t>(k);
-        if (k != 0 && row < kv_rows && (most[0] > 0.f || most[1] > 0.f)) hd->odd_bins = 1;
+        if (!told && k != 0 && row < kv_rows && (most[0] > 0.f || most[1] > 0.f)) {
+          hd->odd_bins = 1;
+          told = true;  // (a store a unit and thread to the one address cost 30 % of the time)
+        }
         uint16_t* dst = reinterpret_cast<uint16_t*>(a.ws + a.lay.values) + out_row * 128;
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
