@@ -329,18 +329,19 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *             zeroed once before the first use. Of its own: not a decode
  *             workspace, and not shared by calls that overlap on the GPU.
  * num_heads is 1 to 1024. Arithmetic: fp32 accumulation and softmax sums; for
- * the tensor core keys are rounded to bf16, values and softmax weights to f16:
- * the values of a row and head with a power of two between them (beyond 2^76 in
- * size they saturate, below 2^-74 they lose bits), weights as they are times
- * that power (what lies 2^-21 below a row's largest loses bits, below 2^-32 it
- * is zero). Values with rows whose largest is outside [2^-8, 2^12), and attended
- * rows whose c_kv is zero, cost the call up to 2.3 times its time. In the latent space a pair of bf16
- * queries stands for the exact one, scores and softmax weights are
- * mla_decode's, but half scores beyond 65504 log2 units are infinite. The result is off by 1.7e-3 to 2.1e-3 (2-norm, of independent
- * normal values; 1.7e-3 is its own rounding to bf16). fp8 pools:
- * the codes are widened exactly and kv_scale multiplies the scores and the
- * output. A call repeated gives the same bits; with other requests, capacities
- * or heads a pass beside it a request's sums may be taken in another order.
+ * the tensor core keys are rounded to bf16, values and softmax weights to f16,
+ * the values of a row and head with a power of two of their own (beyond 2^76 in
+ * size they saturate, below 2^-74 they lose bits), the weights times that power
+ * (what lies 2^-21 below a row's largest loses bits, below 2^-32 it is zero).
+ * Rows whose largest value of a head lies outside [2^-8, 2^12), and attended
+ * rows whose c_kv is zero, cost the call up to 2.3 times its time. In the
+ * latent space a pair of bf16 queries stands for the exact one, scores and
+ * softmax weights are mla_decode's, but half scores beyond 65504 log2 units are
+ * infinite. The result is off by 1.7e-3 to 2.1e-3 (2-norm, of independent
+ * normal values; 1.7e-3 is its own rounding to bf16). fp8 pools: the codes are
+ * widened exactly and kv_scale multiplies the scores and the output. A call
+ * repeated gives the same bits; with other requests, capacities or heads a pass
+ * beside it a request's sums may be taken in another order.
  * out and lse share no memory with each other or with inputs.
  * On the device: a bad page id sets MLA_STATUS_BAD_PAGE and its rows read as
  * zero; a request with a bad length (negative, beyond its page list, or beyond
