@@ -306,7 +306,7 @@ int mla_rope_write(const mla_kv_pool* pool, int layer, const void* rows, const i
  *   s_t = softmax_scale * q[q_indptr[b] + i, h, :] . k_t
  *         over t in [0 or max(0, L_b + i + 1 - window), L_b + i],
  *   out = sum_t softmax(s)_t v_t,  lse = log(sum_t exp(s_t)).
- * Keys and values of all heads are made once (512 bytes per head and attended
+ * Keys and values of all heads are made once (513 bytes per head and attended
  * position, in the workspace) and then attended at 640 flops a pair; making
  * them costs as much as 410 queries' attention. So requests of up to 32 new
  * tokens (56 over 3,000 positions and more) are attended in the latent space, by
