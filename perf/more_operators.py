@@ -247,7 +247,7 @@ def run(s):
 
 
 def _own_shared(s):
-    s["lib"].decode_shared(s["kv"], 1, s["q"], s["ctx"], s["softmax_scale"], s["ws"], s["out"], s["case"]["prefixes"],
+    s["lib"].decode_shared(s["kv"], 1, s["q"], s["case"]["prefixes"], s["softmax_scale"], s["ws"], s["out"],
                            block_table=s["table"], lse=s["lse"])
     return {"out": s["out"], "lse": s["lse"]}
 
