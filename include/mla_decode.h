@@ -364,6 +364,102 @@ int mla_prefill(const mla_kv_pool* pool, int layer, const void* q, const int32_t
  * mla_prefill returns MLA_ERR_WORKSPACE. 0 on bad arguments. */
 size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, int num_heads, int heads_per_pass);
 
+/* ---------------------------------------------------------------- shared prefixes
+ * Decode of a batch whose requests share their first positions in groups (one
+ * system prompt or document for many requests): a group's prefix is read and
+ * attended once for all its requests. The operation is mla_decode_q's with
+ * window = 0: request b has context_lens[b] = L_b tokens cached and q_len new
+ * ones, written beforehand, and its query i attends [0, L_b + i]. Prefix g
+ * belongs to requests prefix_indptr[g] to prefix_indptr[g + 1]: their first
+ * P = min(prefix_lens[g], every L_b of theirs) positions are read through the
+ * block table row (or page list) of the first of them, the positions from P on
+ * through each request's own. So a request's entries of pages that end before P
+ * are used of the first request alone, and P need not end a page. A request that
+ * has its group to itself is read through its own pages throughout.
+ * Requests before prefix_indptr[0] or from prefix_indptr[num_prefixes] on are
+ * pad requests: their rows of out and lse stay as they were.
+ * Rows of a request do not see another's: a cached row of one request's own
+ * positions with an infinity or NaN leaves the results of all others as they are.
+ *
+ * The plan goes by the lengths alone and serves any number of mla_decode_shared
+ * calls (every layer of a step) with the same batch, q_len, num_heads,
+ * num_prefixes and page_size; other values set MLA_STATUS_PLAN_MISMATCH and
+ * nothing is written.
+ *   context_lens, prefix_lens: device, [batch] and [num_prefixes] int32. Lengths
+ *             below 0 or from 2^29 on set MLA_STATUS_BAD_LENGTH and count as 0.
+ *   prefix_indptr: device, [num_prefixes + 1] int32, non-decreasing, within
+ *             [0, batch]; otherwise MLA_STATUS_BAD_LENGTH is set and the plan is
+ *             empty (decode calls with it write nothing).
+ *   num_clusters: as for mla_decode_plan, of the clusters of this kernel.
+ *   page_size is 16, 32, 64 or 128, num_heads 1 to 1024; batch * q_len *
+ *   num_heads stays below 2^31 (q_len * num_heads below 2^30). */
+size_t mla_decode_workspace_size_shared(int batch, int q_len, int num_heads, int num_prefixes);
+int mla_decode_plan_shared(const int32_t* context_lens, const int32_t* prefix_indptr, const int32_t* prefix_lens, int batch,
+                           int num_prefixes, int q_len, int num_heads, int page_size, int num_clusters, void* workspace,
+                           size_t workspace_bytes, void* stream);
+/*   q:   device [batch][q_len][num_heads][576] bf16, 16-byte aligned.
+ *   page_indptr / page_ids / max_blocks: the pages, as for mla_decode. With
+ *        page_indptr, NULL page_ids are lists without a page. A page id outside
+ *        [0, num_pages), or a position beyond the request's list, sets
+ *        MLA_STATUS_BAD_PAGE and its rows read as zero.
+ *   out: device [batch][q_len][num_heads][512] bf16, 32-byte aligned;
+ *   lse: device [batch][q_len][num_heads] fp32 or NULL.
+ *   workspace: mla_decode_workspace_size_shared bytes (of the same batch, q_len,
+ *        num_heads, num_prefixes), 256-byte aligned, its first 256 zeroed once
+ *        before the first use: the one last given to mla_decode_plan_shared. Not
+ *        shared by calls that overlap on the GPU.
+ * Arithmetic: fp32 accumulation and softmax sums; softmax weights are rounded to
+ * the cache's type for the tensor core (bf16; f16 for fp8 pools, whose queries
+ * are f16 as mla_decode's are and whose kv_scale multiplies the scores and the
+ * output). Calls with the same plan give the same bits. */
+int mla_decode_shared(const mla_kv_pool* pool, int layer, const void* q, const int32_t* page_indptr, const int32_t* page_ids,
+                      int max_blocks, int batch, int q_len, int num_heads, int num_prefixes, float softmax_scale,
+                      void* workspace, void* out, float* lse, void* stream);
+
+/* ---------------------------------------------------------------- compact store
+ * A paged store of latent rows in fewer bits, with scales of the values' own:
+ * for prefixes that wait to be used again. data is [num_layers][num_pages]
+ * [page_size][row bytes], 16-byte aligned. A row holds, one after the other,
+ *   MLA_QUANT_E4M3: 512 e4m3 codes, 4 fp32 scales (128 dims each),
+ *   MLA_QUANT_E2M1: 256 bytes of two e2m1 codes (dims 2i low, 2i + 1 high), 16
+ *                   bf16 scales (32 dims each),
+ * and the 64 rope dims in bf16. With a the largest |c_kv| of a group, in IEEE
+ * fp32: scale = a / 448, or a / 6 rounded to bf16; code = the nearest to x /
+ * scale (ties to even, saturating), zero where the scale is zero. A group with an
+ * infinity or NaN has a NaN scale and reads as NaN. */
+#define MLA_QUANT_E4M3 0
+#define MLA_QUANT_E2M1 1
+#define MLA_QUANT_E4M3_ROW 656 /* bytes */
+#define MLA_QUANT_E2M1_ROW 416
+
+typedef struct {
+  void* data;
+  int num_layers;
+  int num_pages;
+  int page_size; /* 16, 32, 64 or 128 */
+  int format;    /* MLA_QUANT_E4M3 or MLA_QUANT_E2M1 */
+} mla_quant_pool;
+
+/* Writes rows[i] at slot slot_mapping[i] (page * page_size + offset) of `layer`,
+ * quantised; i < n. Negative slots are pad rows; a slot beyond the layer sets
+ * MLA_STATUS_BAD_SLOT and is skipped. No slot twice.
+ *   rows: device [n][576] bf16, 16-byte aligned. slot_mapping: device [n] int64.
+ *   workspace: for the status word (256-byte aligned), or NULL. */
+int mla_quant_write(const mla_quant_pool* pool, int layer, const void* rows, const int64_t* slot_mapping, int n,
+                    void* workspace, void* stream);
+
+/* Reads slot slots[i] of `layer` back, i < n, into row i of `rows` or (into !=
+ * NULL) into slot into_slots[i] of layer into_layer of a decode pool. Values are
+ * code * scale in fp32, rounded once to bf16; an e4m3 pool stores them as
+ * mla_kv_write does (divided by its kv_scale in fp32). If either slot of i is
+ * negative nothing is written for it; one beyond its layer sets
+ * MLA_STATUS_BAD_SLOT likewise. A slot may be read twice but not written twice.
+ *   rows: device [n][576] bf16, 16-byte aligned, or NULL with `into`.
+ *   slots, into_slots: device [n] int64; into_slots NULL without `into`.
+ * Outputs share no memory with the store. */
+int mla_quant_read(const mla_quant_pool* pool, int layer, const int64_t* slots, int n, const mla_kv_pool* into, int into_layer,
+                   const int64_t* into_slots, void* rows, void* workspace, void* stream);
+
 /* Reads the status word of `workspace` into *code (MLA_STATUS_* bits) and, if
  * `clear` is nonzero, resets it. Synchronises `stream`: diagnostics only. */
 int mla_get_error(void* workspace, int* code, int clear, void* stream);

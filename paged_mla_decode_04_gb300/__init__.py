@@ -1,7 +1,8 @@
 """Paged MLA decode for GB300: thin Python binding of libmla_decode.so.
 
 Argument marshalling only: every step runs in the library's CUDA kernels. (The
-prefill step's calls go through a compiled binding, the others through ctypes.)
+prefill step's calls, the shared prefixes' and the store's go through a compiled binding,
+the others through ctypes.)
 PyTorch supplies device memory and streams. If the library is missing or
 cannot be loaded this module raises; there is no fallback path.
 
@@ -16,6 +17,10 @@ Calls (same names as the C ABI in include/mla_decode.h):
   uv_project(attn_out, w_uv, y, workspace=None)
   extend_tables / rope_write / prefill: a step of ragged chunks of new tokens
   (page tables from lengths, rotary latent write, 192/128 attention)
+  plan_shared / decode_shared: decode of requests that share prefixes, each
+  prefix attended once for its group
+  quant_write / quant_read: a compact store of latent rows (QuantPool: e4m3 or
+  4-bit codes with scales of their groups) and its way back
   get_error(workspace, clear=False)
 """
 from __future__ import annotations
@@ -56,7 +61,8 @@ EXPORTED = ["mla_kv_write", "mla_decode_workspace_size", "mla_decode_num_cluster
             "mla_decode_plan", "mla_decode", "mla_uv_project", "mla_get_error",
             "mla_decode_noalloc", "mla_decode_workspace_size_q", "mla_decode_plan_q",
             "mla_decode_q", "mla_selftest_bounded_wait", "mla_extend_tables", "mla_rope_write",
-            "mla_prefill", "mla_prefill_workspace_size"]
+            "mla_prefill", "mla_prefill_workspace_size", "mla_decode_workspace_size_shared",
+            "mla_decode_plan_shared", "mla_decode_shared", "mla_quant_write", "mla_quant_read"]
 NOALLOC_SCRATCH_BYTES = 48 << 20
 
 
@@ -120,6 +126,16 @@ def load_library(path: str = LIB_PATH):
     lib.mla_prefill.restype = I
     lib.mla_prefill_workspace_size.argtypes = [I, I, L, I, I]
     lib.mla_prefill_workspace_size.restype = Z
+    lib.mla_decode_workspace_size_shared.argtypes = [I, I, I, I]
+    lib.mla_decode_workspace_size_shared.restype = Z
+    lib.mla_decode_plan_shared.argtypes = [P, P, P, I, I, I, I, I, I, P, Z, P]
+    lib.mla_decode_plan_shared.restype = I
+    lib.mla_decode_shared.argtypes = [ctypes.c_char_p, I, P, P, P, I, I, I, I, I, ctypes.c_float, P, P, P, P]
+    lib.mla_decode_shared.restype = I
+    lib.mla_quant_write.argtypes = [ctypes.c_char_p, I, P, P, I, P, P]
+    lib.mla_quant_write.restype = I
+    lib.mla_quant_read.argtypes = [ctypes.c_char_p, I, P, I, ctypes.c_char_p, I, P, P, P, P]
+    lib.mla_quant_read.restype = I
     _lib = lib
     return lib
 
@@ -378,6 +394,9 @@ def _step():
         b = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(b)
         b.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (lib.mla_extend_tables, lib.mla_rope_write, lib.mla_prefill)])
+        b.bind_shared(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.mla_decode_plan_shared, lib.mla_decode_shared, lib.mla_decode_workspace_size_shared, lib.mla_quant_write,
+            lib.mla_quant_read)])
         _binding = b
     return _binding
 
@@ -451,3 +470,88 @@ def prefill(pool: KVPool, layer: int, q: torch.Tensor, q_indptr: torch.Tensor, c
     if rc:
         _check(rc, "mla_prefill")
     return out
+
+
+# ----------------------------------------------------------------- shared prefixes
+
+def workspace_size_shared(batch: int, q_len: int, num_heads: int, num_prefixes: int) -> int:
+    n = load_library().mla_decode_workspace_size_shared(batch, q_len, num_heads, num_prefixes)
+    if n == 0:
+        raise MlaError("mla_decode_workspace_size_shared: unsupported arguments")
+    return n
+
+
+def alloc_workspace_shared(batch: int, q_len: int, num_heads: int, num_prefixes: int, device=None) -> torch.Tensor:
+    """A workspace for plan_shared() and decode_shared() with its status word cleared."""
+    ws = torch.empty(workspace_size_shared(batch, q_len, num_heads, num_prefixes), dtype=torch.uint8,
+                     device=device or torch.device("cuda"))
+    ws[:256].zero_()
+    return ws
+
+
+def plan_shared(context_lens: torch.Tensor, prefix_indptr: torch.Tensor, prefix_lens: torch.Tensor, q_len: int,
+                num_heads: int, page_size: int, workspace: torch.Tensor, num_clusters: int = 0, stream=None) -> None:
+    """The schedule of decode_shared() calls: requests prefix_indptr[g] to
+    prefix_indptr[g + 1] share their first prefix_lens[g] cached positions."""
+    rc = (_binding or _step()).plan_shared(context_lens, prefix_indptr, prefix_lens, q_len, num_heads, page_size, workspace,
+                                           num_clusters, stream)
+    if rc:
+        _check(rc, "mla_decode_plan_shared")
+
+
+def decode_shared(pool: KVPool, layer: int, q: torch.Tensor, num_prefixes: int, softmax_scale: float,
+                  workspace: torch.Tensor, out: torch.Tensor, block_table: Optional[torch.Tensor] = None,
+                  page_indptr: Optional[torch.Tensor] = None, page_ids: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """q [batch, q_len, heads, 576] -> out [batch, q_len, heads, 512] (lse [batch,
+    q_len, heads]) as decode_q() without a window, each group's prefix read and
+    attended once, by the plan in workspace."""
+    rc = (_binding or _step()).decode_shared(
+        pool.data, pool.kv_scale, layer, q, num_prefixes, softmax_scale, workspace, out, block_table, page_indptr, page_ids,
+        lse, stream)
+    if rc:
+        _check(rc, "mla_decode_shared")
+    return out
+
+
+# ----------------------------------------------------------------- compact store
+
+QUANT_E4M3_ROW = 656
+QUANT_E2M1_ROW = 416
+
+
+@dataclass
+class QuantPool:
+    """A compact store of latent rows [num_layers, num_pages, page_size, row bytes]
+    of torch.uint8: 656 bytes a row (e4m3 codes, an fp32 scale for each 128 dims)
+    or 416 (e2m1 codes, a bf16 scale for each 32 dims); the rope dims stay bf16."""
+    data: torch.Tensor
+
+
+def alloc_quant_pool(num_layers: int, num_pages: int, page_size: int, codes: str = "e4m3", device=None) -> QuantPool:
+    """A store of zeros; codes "e4m3" or "e2m1"."""
+    rows = {"e4m3": QUANT_E4M3_ROW, "e2m1": QUANT_E2M1_ROW}
+    if codes not in rows:
+        raise ValueError('codes must be "e4m3" or "e2m1"')
+    return QuantPool(torch.zeros(num_layers, num_pages, page_size, rows[codes], dtype=torch.uint8,
+                                 device=device or torch.device("cuda")))
+
+
+def quant_write(store: QuantPool, layer: int, rows: torch.Tensor, slot_mapping: torch.Tensor,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise latent rows [n, 576] into their slots [n] of the store."""
+    rc = (_binding or _step()).quant_write(store.data, layer, rows, slot_mapping, workspace, stream)
+    if rc:
+        _check(rc, "mla_quant_write")
+
+
+def quant_read(store: QuantPool, layer: int, slots: torch.Tensor, rows: Optional[torch.Tensor] = None,
+               pool: Optional[KVPool] = None, pool_layer: int = 0, pool_slots: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Read slots [n] of the store back: into rows [n, 576], or into pool_slots [n] of
+    a layer of a decode pool."""
+    data, scale = (None, 1.0) if pool is None else (pool.data, pool.kv_scale)
+    rc = (_binding or _step()).quant_read(store.data, layer, slots, rows, data, scale, pool_layer, pool_slots, workspace,
+                                          stream)
+    if rc:
+        _check(rc, "mla_quant_read")

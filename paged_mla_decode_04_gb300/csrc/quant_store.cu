@@ -1,0 +1,190 @@
+// Compact latent store: rows of codes with scales of their own groups, written from
+// bf16 rows and read back.
+//
+// Per group of dims (128 for e4m3, 32 for e2m1) a = max |x|:
+//   e4m3: scale = a / 448 in fp32,              code = e4m3(x / scale)
+//   e2m1: scale = a / 6 rounded to bf16 (once), code = e2m1(x / scale)
+// with IEEE fp32 divisions, rounded to the nearest code (ties to even) and saturating.
+// Groups of zeros, or so small that the scale is zero, have codes of zero; a group with an
+// infinity or NaN has scale NaN and reads as NaN throughout.
+//
+// A warp a row: reading and writing is all there is to it, 1,816 bytes a token (e4m3).
+#include <cuda_bf16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+#include <math_constants.h>
+
+#include "../../include/mla_decode.h"
+#include "ptx.cuh"
+#include "shared_internal.h"
+
+namespace mla {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kRowVecs = kDimRow * 2 / 16;  // 16-byte pieces of a bf16 row: 64 of c_kv, 8 of rope
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Largest magnitude among a piece's eight values, as bf16 bits (NaN above infinity).
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  return max(a & 0xffffu, a >> 16);
+}
+
+__device__ __forceinline__ float scale_of(uint32_t top, float most) {
+  return top >= 0x7f80u ? CUDART_NAN_F : __fdiv_rn(__uint_as_float(top << 16), most);
+}
+
+__device__ __forceinline__ float over(float x, float scale) { return scale > 0.f ? __fdiv_rn(x, scale) : 0.f; }
+
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, float s) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(over(lo_f(a), s), over(hi_f(a), s)), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(over(lo_f(b), s), over(hi_f(b), s)), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
+__device__ __forceinline__ uint32_t e2m1x2(uint32_t a, float s) {
+  return __nv_cvt_float2_to_fp4x2(make_float2(over(lo_f(a), s), over(hi_f(a), s)), __NV_E2M1, cudaRoundNearest);
+}
+
+template <int kFormat>
+__global__ void __launch_bounds__(32 * kWarps) store_write_kernel(const StoreWriteArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= a.n) return;
+  const uint4* src = a.rows + static_cast<int64_t>(t) * kRowVecs;
+  const int64_t slot = a.slots[t];
+  const uint4 v[2] = {src[lane], src[lane + 32]};
+  uint4 rope;
+  if (lane < 8) rope = src[64 + lane];
+  if (slot < 0) return;  // pad row
+  if (slot >= a.layer_rows) {
+    if (lane == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_SLOT);
+    return;
+  }
+  if (kFormat == MLA_QUANT_E4M3) {
+    uint8_t* dst = a.layer_base + slot * kStoreE4m3Row;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // piece 32 h + lane: group 2 h + lane / 16
+      uint32_t top = largest(v[h]);
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float s = scale_of(top, 448.f);
+      reinterpret_cast<uint2*>(dst)[lane + 32 * h] = make_uint2(e4m3x4(v[h].x, v[h].y, s), e4m3x4(v[h].z, v[h].w, s));
+      if ((lane & 15) == 0) reinterpret_cast<float*>(dst + kDimCkv)[2 * h + (lane >> 4)] = s;
+    }
+    if (lane < 8) reinterpret_cast<uint4*>(dst + kDimCkv + 16)[lane] = rope;
+  } else {
+    uint8_t* dst = a.layer_base + slot * kStoreE2m1Row;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // piece 32 h + lane: group 8 h + lane / 4
+      uint32_t top = largest(v[h]);
+#pragma unroll
+      for (int d = 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const __nv_bfloat16 sb = __float2bfloat16_rn(scale_of(top, 6.f));
+      const float s = __bfloat162float(sb);
+      reinterpret_cast<uint32_t*>(dst)[lane + 32 * h] =
+          e2m1x2(v[h].x, s) | e2m1x2(v[h].y, s) << 8 | e2m1x2(v[h].z, s) << 16 | e2m1x2(v[h].w, s) << 24;
+      if ((lane & 3) == 0) reinterpret_cast<__nv_bfloat16*>(dst + 256)[8 * h + (lane >> 2)] = sb;
+    }
+    if (lane < 8) reinterpret_cast<uint4*>(dst + 288)[lane] = rope;
+  }
+}
+
+// Two e4m3 codes, as floats.
+__device__ __forceinline__ float2 of_e4m3x2(uint32_t v) {
+  const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(v));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float2 of_e2m1x2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(v), __NV_E2M1);
+  return __half22float2(__half2(h));
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x4(float p, float q, float r, float t, float s) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(p, s), __fdiv_rn(q, s)), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(r, s), __fdiv_rn(t, s)), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
+// A lane has dims 16 lane .. 16 lane + 15, and (the first eight) rope dims 8 lane ...
+template <int kFormat, int kOut>
+__global__ void __launch_bounds__(32 * kWarps) store_read_kernel(const StoreReadArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= a.n) return;
+  const int64_t slot = a.slots[t], to = a.out_slots ? a.out_slots[t] : t;
+  if (slot < 0 || to < 0) return;
+  if (slot >= a.layer_rows || to >= a.out_rows) {
+    if (lane == 0 && a.status) atomicOr(a.status, MLA_STATUS_BAD_SLOT);
+    return;
+  }
+  float x[16], s;
+  const uint8_t* src = a.layer_base + slot * (kFormat == MLA_QUANT_E4M3 ? kStoreE4m3Row : kStoreE2m1Row);
+  uint4 rope;
+  if (lane < 8) rope = reinterpret_cast<const uint4*>(src + (kFormat == MLA_QUANT_E4M3 ? 528 : 288))[lane];
+  if (kFormat == MLA_QUANT_E4M3) {
+    const uint4 c = reinterpret_cast<const uint4*>(src)[lane];
+    s = reinterpret_cast<const float*>(src + kDimCkv)[lane >> 3];
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = of_e4m3x2(w[i >> 1] >> (16 * (i & 1)) & 0xffffu);
+      x[2 * i] = f.x * s;
+      x[2 * i + 1] = f.y * s;
+    }
+  } else {
+    const uint2 c = reinterpret_cast<const uint2*>(src)[lane];
+    s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src + 256)[lane >> 1]);
+    const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = of_e2m1x2(w[i >> 2] >> (8 * (i & 3)) & 0xffu);
+      x[2 * i] = f.x * s;
+      x[2 * i + 1] = f.y * s;
+    }
+  }
+  if (kOut == MLA_DTYPE_BF16) {
+    uint4* dst = reinterpret_cast<uint4*>(a.out) + to * kRowVecs;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      dst[2 * lane + h] = make_uint4(pack_bf16x2(x[8 * h], x[8 * h + 1]), pack_bf16x2(x[8 * h + 2], x[8 * h + 3]),
+                                     pack_bf16x2(x[8 * h + 4], x[8 * h + 5]), pack_bf16x2(x[8 * h + 6], x[8 * h + 7]));
+    if (lane < 8) dst[64 + lane] = rope;
+  } else {
+    uint8_t* dst = a.out + to * kDimRow;
+    const float k = a.kv_scale;
+    reinterpret_cast<uint4*>(dst)[lane] =
+        make_uint4(to_e4m3x4(x[0], x[1], x[2], x[3], k), to_e4m3x4(x[4], x[5], x[6], x[7], k),
+                   to_e4m3x4(x[8], x[9], x[10], x[11], k), to_e4m3x4(x[12], x[13], x[14], x[15], k));
+    if (lane < 8)
+      reinterpret_cast<uint2*>(dst + kDimCkv)[lane] =
+          make_uint2(to_e4m3x4(lo_f(rope.x), hi_f(rope.x), lo_f(rope.y), hi_f(rope.y), k),
+                     to_e4m3x4(lo_f(rope.z), hi_f(rope.z), lo_f(rope.w), hi_f(rope.w), k));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_store_write(const StoreWriteArgs& a, int format, cudaStream_t stream) {
+  const dim3 grid((a.n + kWarps - 1) / kWarps), block(32 * kWarps);
+  if (format == MLA_QUANT_E4M3) return launch_pdl(store_write_kernel<MLA_QUANT_E4M3>, grid, block, 0, stream, a);
+  return launch_pdl(store_write_kernel<MLA_QUANT_E2M1>, grid, block, 0, stream, a);
+}
+
+cudaError_t launch_store_read(const StoreReadArgs& a, int format, int out_dtype, cudaStream_t stream) {
+  const dim3 grid((a.n + kWarps - 1) / kWarps), block(32 * kWarps);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, stream, a); };
+  if (format == MLA_QUANT_E4M3)
+    return out_dtype == MLA_DTYPE_BF16 ? go(store_read_kernel<MLA_QUANT_E4M3, MLA_DTYPE_BF16>)
+                                       : go(store_read_kernel<MLA_QUANT_E4M3, MLA_DTYPE_FP8_E4M3>);
+  return out_dtype == MLA_DTYPE_BF16 ? go(store_read_kernel<MLA_QUANT_E2M1, MLA_DTYPE_BF16>)
+                                     : go(store_read_kernel<MLA_QUANT_E2M1, MLA_DTYPE_FP8_E4M3>);
+}
+
+}  // namespace mla

@@ -1,0 +1,275 @@
+// Schedule of a decode over shared prefixes, and the join of its partial sums.
+//
+// The plan reads only lengths: group g's requests [prefix_indptr[g], [g + 1]) share
+// their first P positions, P the least of prefix_lens[g] and its requests' cached
+// lengths. A tile of the group's rows attends the P positions once and then each of its
+// requests' own ones (see shared_internal.h). One block of threads, a launch a step; its
+// time is that of a few passes over the requests, one after the other.
+#include <cuda_bf16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include "../../include/mla_decode.h"
+#include "ptx.cuh"
+#include "scan.cuh"
+#include "shared_internal.h"
+
+namespace mla {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// The first of n ascending values' index whose successor exceeds x: the last i with
+// start(i) <= x.
+template <typename F>
+__device__ __forceinline__ int last_at_most(int n, int64_t x, F start) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start(mid) <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A request's cached positions; none for a length out of range.
+__device__ __forceinline__ int length_of(int l) { return l < 0 || l >= kShMostLength ? 0 : l; }
+
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanArgs a) {
+  __shared__ int64_t sh[64];
+  __shared__ int bad;
+  pdl_launch_dependents();
+  pdl_wait();
+  ShHeader* hd = reinterpret_cast<ShHeader*>(a.ws);
+  ShGroup* groups = reinterpret_cast<ShGroup*>(a.ws + a.lay.groups);
+  ShTile* tiles = reinterpret_cast<ShTile*>(a.ws + a.lay.tiles);
+  ShSegment* segs = reinterpret_cast<ShSegment*>(a.ws + a.lay.segs);
+  ShItem* items = reinterpret_cast<ShItem*>(a.ws + a.lay.items);
+  int* cluster_start = reinterpret_cast<int*>(a.ws + a.lay.cluster_start);
+  ShSplit* splits = reinterpret_cast<ShSplit*>(a.ws + a.lay.splits);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  if (tid == 0) bad = 0;
+  __syncthreads();
+
+  // Groups in ascending order within the batch; else nothing is planned.
+  int wrong = 0;
+  for (int g = tid; g <= a.num_prefixes; g += blockDim.x) {
+    const int p = a.prefix_indptr[g];
+    if (p < 0 || p > a.batch || (g > 0 && p < a.prefix_indptr[g - 1])) wrong = 1;
+  }
+  const bool refused = __syncthreads_or(wrong) != 0;
+  if (refused && tid == 0) bad = 1;
+
+  // Shared positions and tiles of each group.
+  const int r = a.q_len * a.num_heads;
+  for (int g = warp; g < a.num_prefixes && !refused; g += warps) {
+    const int first = a.prefix_indptr[g], count = a.prefix_indptr[g + 1] - first;
+    int p = a.prefix_lens[g];
+    int least = INT_MAX, any_bad = p < 0;
+    for (int b = lane; b < count; b += 32) {
+      const int l = a.context_lens[first + b];
+      any_bad |= l != length_of(l);
+      least = min(least, length_of(l));
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    any_bad = __any_sync(0xffffffffu, any_bad);
+    if (lane == 0) {
+      if (any_bad && count > 0) bad = 1;
+      // (a request by itself has its positions in one segment)
+      p = count > 1 ? min(max(p, 0), least) : 0;
+      groups[g] = ShGroup{first, count, p, 0};
+    }
+  }
+  __syncthreads();
+  int64_t before = 0;
+  for (int g0 = 0; g0 < a.num_prefixes && !refused; g0 += blockDim.x) {
+    const int g = g0 + tid;
+    int64_t v[1] = {0}, total[1];
+    if (g < a.num_prefixes) v[0] = (static_cast<int64_t>(groups[g].count) * r + a.lay.tile_rows - 1) / a.lay.tile_rows;
+    block_scan<1>(v, total, sh);
+    if (g < a.num_prefixes) groups[g].tile0 = static_cast<int>(before + v[0]);
+    before += total[0];
+  }
+  const int num_tiles = refused ? 0 : static_cast<int>(before);
+  __syncthreads();
+
+  // A warp a tile: its segments, a lane a request.
+  const int unit = sh_copy_tokens(a.page_size);
+  for (int t = warp; t < num_tiles; t += warps) {
+    const int g = last_at_most(a.num_prefixes, t, [&](int i) { return groups[i].tile0; });
+    const ShGroup gr = groups[g];
+    const int64_t from = static_cast<int64_t>(t - gr.tile0) * a.lay.tile_rows;  // within the group's rows
+    const int rows = static_cast<int>(min(static_cast<int64_t>(gr.count) * r - from, static_cast<int64_t>(a.lay.tile_rows)));
+    const int64_t row0 = static_cast<int64_t>(gr.first) * r + from;
+    ShSegment* out = segs + static_cast<int64_t>(t) * a.lay.segs_per_tile;
+    const int shared_blocks = (gr.prefix + kShTokens - 1) / kShTokens;
+    if (lane == 0) out[0] = ShSegment{gr.first, 0, rows, 0, 0, 0, gr.prefix, gr.prefix};
+    const int b0 = static_cast<int>(from / r), b1 = static_cast<int>((from + rows - 1) / r);  // requests of the group
+    int done = shared_blocks;
+    for (int j0 = b0; j0 <= b1; j0 += 32) {
+      const int j = j0 + lane;
+      int n = 0;
+      ShSegment s = {};
+      if (j <= b1) {
+        const int64_t first_row = static_cast<int64_t>(j) * r;  // of the request, within the group
+        s.owner = gr.first + j;
+        s.row_lo = static_cast<int>(max(first_row - from, static_cast<int64_t>(0)));
+        s.row_hi = static_cast<int>(min(first_row + r - from, static_cast<int64_t>(rows)));
+        const int last_i = static_cast<int>((from + s.row_hi - 1 - first_row) / a.num_heads);
+        s.base = length_of(a.context_lens[s.owner]);
+        s.tok_lo = gr.prefix;
+        s.tok0 = gr.prefix / unit * unit;
+        s.tok_hi = s.base + last_i + 1;
+        n = (s.tok_hi - s.tok0 + kShTokens - 1) / kShTokens;
+      }
+      int upto = n;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += u;
+      }
+      s.block0 = done + upto - n;
+      if (j <= b1) out[1 + j - b0] = s;
+      done += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) {
+      ShTile w = {};
+      w.row0 = static_cast<int>(row0);
+      w.rows = rows;
+      w.seg0 = t * a.lay.segs_per_tile + (shared_blocks == 0 ? 1 : 0);
+      w.segs = b1 - b0 + 1 + (shared_blocks == 0 ? 0 : 1);
+      w.blocks = done;
+      tiles[t] = w;
+    }
+  }
+  __syncthreads();
+
+  // All tiles' weights (their blocks and an item's cost, which comes first), cut into
+  // equal ranges.
+  int64_t weight = 0;
+  for (int t0 = 0; t0 < num_tiles; t0 += blockDim.x) {
+    int64_t v[1] = {t0 + tid < num_tiles ? tiles[t0 + tid].blocks + kShItemCost : 0}, total[1];
+    block_scan<1>(v, total, sh);
+    weight += total[0];
+  }
+  const int64_t c = max(static_cast<int64_t>(1), min(weight, static_cast<int64_t>(a.clusters)));
+  auto range_begin = [&](int64_t k) { return k * weight / c; };
+  auto cluster_of = [&](int64_t x) { return static_cast<int>(((x + 1) * c + weight - 1) / weight - 1); };
+  int64_t at = 0, num_items = 0, num_parts = 0, num_split = 0;
+  for (int t0 = 0; t0 < num_tiles; t0 += blockDim.x) {
+    const int t = t0 + tid;
+    const int blocks = t < num_tiles ? tiles[t].blocks : 0;
+    int64_t v[1] = {t < num_tiles ? blocks + kShItemCost : 0}, total[1];
+    block_scan<1>(v, total, sh);
+    const int64_t off = at + v[0] + kShItemCost;  // the tile's first block
+    at += total[0];
+    int c0 = 0, pieces = 0;
+    if (t < num_tiles) {
+      c0 = cluster_of(off);
+      pieces = cluster_of(off + blocks - 1) - c0 + 1;
+    }
+    // items, partial sums and split tiles before this one's
+    int64_t w[2] = {pieces, pieces > 1 ? pieces | (1ll << 40) : 0}, sums[2];
+    block_scan<2>(w, sums, sh);
+    const int item0 = static_cast<int>(num_items + w[0]);
+    const int part0 = static_cast<int>(num_parts + (w[1] & ((1ll << 40) - 1)));
+    for (int k = 0; k < pieces; ++k) {
+      ShItem i = {};
+      i.tile = t;
+      i.begin = static_cast<int>(max(range_begin(c0 + k), off) - off);
+      i.end = static_cast<int>(min(range_begin(c0 + k + 1), off + blocks) - off);
+      i.part = pieces > 1 ? part0 + k : -1;
+      i.cluster = c0 + k;
+      items[item0 + k] = i;
+    }
+    if (pieces > 1) splits[num_split + (w[1] >> 40)] = ShSplit{t, pieces, part0, 0};
+    num_items += sums[0];
+    num_parts += sums[1] & ((1ll << 40) - 1);
+    num_split += sums[1] >> 40;
+  }
+  __syncthreads();
+  for (int k = tid; k <= a.clusters; k += blockDim.x) {  // (items are in the clusters' order)
+    int lo = 0, hi = static_cast<int>(num_items);
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (items[mid].cluster < k) lo = mid + 1;
+      else hi = mid;
+    }
+    cluster_start[k] = lo;
+  }
+  if (tid == 0) {
+    if (bad) atomicOr(&hd->status, MLA_STATUS_BAD_LENGTH);
+    hd->batch = a.batch;
+    hd->q_len = a.q_len;
+    hd->num_heads = a.num_heads;
+    hd->num_prefixes = a.num_prefixes;
+    hd->page_size = a.page_size;
+    hd->num_clusters = static_cast<int>(c);
+    hd->num_tiles = num_tiles;
+    hd->num_items = static_cast<int>(num_items);
+    hd->num_split = static_cast<int>(num_split);
+    hd->planned = 1;
+  }
+}
+
+constexpr int kMergeRows = 4;  // rows a block, a warp each
+
+// out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over a split tile's pieces k, M the
+// largest m_k. Pieces without a position of the row have l_k = 0; their O_k is not read.
+__global__ void __launch_bounds__(32 * kMergeRows) shared_merge_kernel(const ShDecodeArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const ShHeader* hd = reinterpret_cast<const ShHeader*>(a.ws);
+  if (!sh_planned(hd, a) || static_cast<int>(blockIdx.x) >= hd->num_split) return;
+  const ShSplit sp = reinterpret_cast<const ShSplit*>(a.ws + a.lay.splits)[blockIdx.x];
+  const ShTile tile = reinterpret_cast<const ShTile*>(a.ws + a.lay.tiles)[sp.tile];
+  const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= tile.rows) return;
+  const float2* stats = reinterpret_cast<const float2*>(a.ws + a.lay.stats) + static_cast<int64_t>(sp.part0) * kShRows + row;
+  const float4* part = reinterpret_cast<const float4*>(a.ws + a.lay.partial) +
+                       (static_cast<int64_t>(sp.part0) * kShRows + row) * (kDimCkv / 4);
+  float top = -CUDART_INF_F;
+  for (int k = lane; k < sp.pieces; k += 32) {
+    const float2 s = stats[static_cast<int64_t>(k) * kShRows];
+    if (s.y != 0.f) top = fmaxf(top, s.x);
+  }
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float4 acc[4] = {};
+  float sum = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < sp.pieces; ++k) {
+    const float2 s = stats[static_cast<int64_t>(k) * kShRows];
+    if (s.y == 0.f) continue;
+    const float w = exp2f(s.x - top);
+    sum = fmaf(w, s.y, sum);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = part[static_cast<int64_t>(k) * kShRows * (kDimCkv / 4) + lane + 32 * j];
+      acc[j].x = fmaf(w, x.x, acc[j].x);
+      acc[j].y = fmaf(w, x.y, acc[j].y);
+      acc[j].z = fmaf(w, x.z, acc[j].z);
+      acc[j].w = fmaf(w, x.w, acc[j].w);
+    }
+  }
+  const float inv = a.out_scale / sum;
+  const int64_t out_row = static_cast<int64_t>(tile.row0) + row;
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kDimCkv);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    dst[lane + 32 * j] = make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
+  if (a.lse && lane == 0) a.lse[out_row] = (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+}  // namespace
+
+cudaError_t launch_shared_plan(const ShPlanArgs& a, cudaStream_t stream) {
+  return launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
+}
+
+cudaError_t launch_shared_merge(const ShDecodeArgs& a, cudaStream_t stream) {
+  // (a split tile lies across a boundary between two clusters' ranges)
+  const int most = a.lay.max_tiles < a.clusters ? a.lay.max_tiles : a.clusters;
+  return launch_pdl(shared_merge_kernel, dim3(most, (a.lay.tile_rows + kMergeRows - 1) / kMergeRows), dim3(32 * kMergeRows),
+                    0, stream, a);
+}
+
+}  // namespace mla

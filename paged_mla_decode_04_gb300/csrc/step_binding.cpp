@@ -1,5 +1,5 @@
-// Python binding of the prefill-step calls: checks the tensors and calls the C
-// entry points of include/mla_decode.h.
+// Python binding of the prefill-step, shared-prefix and compact-store calls: checks the
+// tensors and calls the C entry points of include/mla_decode.h.
 //
 // A step's calls come once per layer with a dozen tensors each, and a small
 // step's kernels take less time than marshalling those through ctypes did (10 to
@@ -22,6 +22,11 @@ namespace {
 decltype(&mla_extend_tables) extend_tables_fn = nullptr;
 decltype(&mla_rope_write) rope_write_fn = nullptr;
 decltype(&mla_prefill) prefill_fn = nullptr;
+decltype(&mla_decode_shared) decode_shared_fn = nullptr;
+decltype(&mla_decode_plan_shared) plan_shared_fn = nullptr;
+decltype(&mla_decode_workspace_size_shared) shared_size_fn = nullptr;
+decltype(&mla_quant_write) quant_write_fn = nullptr;
+decltype(&mla_quant_read) quant_read_fn = nullptr;
 
 constexpr int64_t kLatentDim = 576, kCkvDim = 512, kNopeDim = 128, kRopeDim = 64, kQkDim = 192, kVDim = 128;
 constexpr auto kI32 = at::kInt, kI64 = at::kLong, kBf16 = at::kBFloat16, kF32 = at::kFloat;
@@ -117,6 +122,26 @@ mla_kv_pool pool_of(PyObject* data, PyObject* scale, int device) {
   p.dtype = type == kBf16 ? MLA_DTYPE_BF16 : MLA_DTYPE_FP8_E4M3;
   p.kv_scale = real(scale);
   return p;
+}
+
+mla_quant_pool store_of(PyObject* data, int device) {
+  const at::Tensor& d = tensor(data, "store");
+  const int64_t row = d.dim() == 4 ? d.size(3) : 0;
+  if (d.scalar_type() != at::kByte || (row != MLA_QUANT_E4M3_ROW && row != MLA_QUANT_E2M1_ROW))
+    refuse("store must be uint8 [num_layers, num_pages, page_size, 656 (e4m3) or 416 (e2m1)]");
+  mla_quant_pool p = {};
+  p.data = here(d, "store", device);
+  p.num_layers = int_of(d.size(0), "num_layers");
+  p.num_pages = int_of(d.size(1), "num_pages");
+  p.page_size = int_of(d.size(2), "page_size");
+  p.format = row == MLA_QUANT_E4M3_ROW ? MLA_QUANT_E4M3 : MLA_QUANT_E2M1;
+  return p;
+}
+
+const int64_t* slots_of(PyObject* o, const char* name, int64_t rows, int device) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.dim() != 1 || t.numel() != rows) refuse(std::string(name) + " must be [rows]");
+  return here<int64_t>(t, name, kI64, device);
 }
 
 // Runs a call's body: its status code as an int, or an exception.
@@ -332,20 +357,150 @@ PyObject* prefill(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+PyObject* plan_shared(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call(n, 9, [&] {
+    const int dev = c10::cuda::current_device();
+    const at::Tensor &lens = tensor(v[0], "context_lens"), &indptr = tensor(v[1], "prefix_indptr"),
+                     &prefix = tensor(v[2], "prefix_lens"), &work = tensor(v[6], "workspace");
+    if (lens.dim() != 1 || prefix.dim() != 1 || indptr.dim() != 1 || indptr.numel() != prefix.numel() + 1)
+      refuse("context_lens [batch], prefix_lens [prefixes] and prefix_indptr [prefixes + 1] expected");
+    const int q_len = integer32(v[3], "q_len"), heads = integer32(v[4], "num_heads"), page = integer32(v[5], "page_size"),
+              clusters = integer32(v[7], "num_clusters");
+    const auto* lens_p = here<int32_t>(lens, "context_lens", kI32, dev);
+    const auto* indptr_p = here<int32_t>(indptr, "prefix_indptr", kI32, dev);
+    const auto* prefix_p = here<int32_t>(prefix, "prefix_lens", kI32, dev);
+    void* work_p = here(work, "workspace", dev);
+    void* stream = stream_of(v[8], dev);
+    const int batch = int_of(lens.numel(), "batch"), prefixes = int_of(prefix.numel(), "prefixes");
+    const size_t bytes = work.nbytes();
+    return without_gil([&] {
+      return plan_shared_fn(lens_p, indptr_p, prefix_p, batch, prefixes, q_len, heads, page, clusters, work_p, bytes, stream);
+    });
+  });
+}
+
+PyObject* decode_shared(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call(n, 13, [&]() -> int {
+    const int dev = c10::cuda::current_device();
+    const at::Tensor &q = tensor(v[3], "q"), &work = tensor(v[6], "workspace"), &out = tensor(v[7], "out");
+    if (q.dim() != 4 || q.size(3) != kLatentDim) refuse("q must be [batch, q_len, heads, 576]");
+    const int64_t batch = q.size(0), q_len = q.size(1), heads = q.size(2);
+    const bool has_lse = v[11] != Py_None;
+    if (!out.sizes().equals({batch, q_len, heads, kCkvDim}) || (has_lse && !tensor(v[11], "lse").sizes().equals({batch, q_len, heads})))
+      refuse("out must be [batch, q_len, heads, 512], lse [batch, q_len, heads]");
+    const int32_t *page_indptr = nullptr, *ids = nullptr;
+    int64_t max_blocks = 0;
+    if (v[8] != Py_None) {
+      const at::Tensor& t = tensor(v[8], "block_table");
+      if (t.dim() != 2 || t.size(0) != batch) refuse("block_table must be [batch, max_blocks]");
+      ids = here<int32_t>(t, "block_table", kI32, dev);
+      max_blocks = t.size(1);
+    } else {
+      if (v[9] == Py_None || v[10] == Py_None) refuse("give block_table, or page_indptr [batch+1] and page_ids");
+      const at::Tensor& t = tensor(v[9], "page_indptr");
+      if (t.dim() != 1 || t.numel() != batch + 1) refuse("give block_table, or page_indptr [batch+1] and page_ids");
+      page_indptr = here<int32_t>(t, "page_indptr", kI32, dev);
+      ids = here<int32_t>(v[10], "page_ids", kI32, dev);
+    }
+    const mla_kv_pool pool = pool_of(v[0], v[1], dev);
+    const int layer = integer32(v[2], "layer"), prefixes = integer32(v[4], "num_prefixes");
+    const float scale = real(v[5]);
+    const auto* q_p = here<void>(q, "q", kBf16, dev);
+    void *work_p = here(work, "workspace", dev), *out_p = here<void>(out, "out", kBf16, dev);
+    float* lse_p = here_or_none<float>(v[11], "lse", kF32, dev);
+    void* stream = stream_of(v[12], dev);
+    const int blocks = int_of(max_blocks, "max_blocks"), b = int_of(batch, "batch"), l = int_of(q_len, "q_len"),
+              h = int_of(heads, "heads");
+    const size_t bytes = work.nbytes();
+    return without_gil([&] {
+      // (the plan looked at the workspace's size; another one's is refused here)
+      if (b > 0 && prefixes > 0 && bytes < shared_size_fn(b, l, h, prefixes)) return MLA_ERR_WORKSPACE;
+      return decode_shared_fn(&pool, layer, q_p, page_indptr, ids, blocks, b, l, h, prefixes, scale, work_p, out_p, lse_p, stream);
+    });
+  });
+}
+
+PyObject* quant_write(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call(n, 6, [&]() -> int {
+    const int dev = c10::cuda::current_device();
+    const mla_quant_pool store = store_of(v[0], dev);
+    const int layer = integer32(v[1], "layer");
+    const at::Tensor& rows = tensor(v[2], "rows");
+    if (rows.dim() != 2 || rows.size(1) != kLatentDim) refuse("rows must be [rows, 576]");
+    const void* rows_p = here<void>(rows, "rows", kBf16, dev);
+    const int64_t* slots_p = slots_of(v[3], "slot_mapping", rows.size(0), dev);
+    void* ws = status_workspace(v[4], dev);
+    void* stream = stream_of(v[5], dev);
+    const int t = int_of(rows.size(0), "rows");
+    return without_gil([&] { return quant_write_fn(&store, layer, rows_p, slots_p, t, ws, stream); });
+  });
+}
+
+PyObject* quant_read(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call(n, 10, [&]() -> int {
+    const int dev = c10::cuda::current_device();
+    const mla_quant_pool store = store_of(v[0], dev);
+    const int layer = integer32(v[1], "layer");
+    const int64_t count = tensor(v[2], "slots").numel();
+    const int64_t* slots_p = slots_of(v[2], "slots", count, dev);
+    void* rows_p = nullptr;
+    const int64_t* into_p = nullptr;
+    mla_kv_pool pool = {};
+    int into_layer = 0;
+    const bool into = v[4] != Py_None;
+    if (into == (v[3] != Py_None)) refuse("give rows, or pool with pool_slots");
+    if (into) {
+      pool = pool_of(v[4], v[5], dev);
+      into_layer = integer32(v[6], "pool_layer");
+      into_p = slots_of(v[7], "pool_slots", count, dev);
+    } else {
+      const at::Tensor& rows = tensor(v[3], "rows");
+      if (v[7] != Py_None) refuse("pool_slots go with pool");
+      if (rows.dim() != 2 || rows.size(0) != count || rows.size(1) != kLatentDim) refuse("rows must be [slots, 576]");
+      rows_p = here<void>(rows, "rows", kBf16, dev);
+    }
+    void* ws = status_workspace(v[8], dev);
+    void* stream = stream_of(v[9], dev);
+    const int t = int_of(count, "slots");
+    return without_gil([&] {
+      return quant_read_fn(&store, layer, slots_p, t, into ? &pool : nullptr, into_layer, into_p, rows_p, ws, stream);
+    });
+  });
+}
+
+void entry_points(PyObject* const* v, void** p, int count) {
+  for (int i = 0; i < count; ++i) {
+    p[i] = PyLong_AsVoidPtr(v[i]);
+    if (!p[i]) {
+      if (PyErr_Occurred()) throw PythonError{};
+      refuse("an entry point is missing");
+    }
+  }
+}
+
 // The library's entry points: mla_extend_tables, mla_rope_write, mla_prefill.
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return call(n, 3, [&] {
     void* p[3];
-    for (int i = 0; i < 3; ++i) {
-      p[i] = PyLong_AsVoidPtr(v[i]);
-      if (!p[i]) {
-        if (PyErr_Occurred()) throw PythonError{};
-        refuse("an entry point is missing");
-      }
-    }
+    entry_points(v, p, 3);
     extend_tables_fn = reinterpret_cast<decltype(extend_tables_fn)>(p[0]);
     rope_write_fn = reinterpret_cast<decltype(rope_write_fn)>(p[1]);
     prefill_fn = reinterpret_cast<decltype(prefill_fn)>(p[2]);
+    return 0;
+  });
+}
+
+// Those of the shared prefixes and the store: mla_decode_plan_shared, mla_decode_shared,
+// mla_decode_workspace_size_shared, mla_quant_write, mla_quant_read.
+PyObject* bind_shared(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return call(n, 5, [&] {
+    void* p[5];
+    entry_points(v, p, 5);
+    plan_shared_fn = reinterpret_cast<decltype(plan_shared_fn)>(p[0]);
+    decode_shared_fn = reinterpret_cast<decltype(decode_shared_fn)>(p[1]);
+    shared_size_fn = reinterpret_cast<decltype(shared_size_fn)>(p[2]);
+    quant_write_fn = reinterpret_cast<decltype(quant_write_fn)>(p[3]);
+    quant_read_fn = reinterpret_cast<decltype(quant_read_fn)>(p[4]);
     return 0;
   });
 }
@@ -358,6 +513,11 @@ PyMODINIT_FUNC PyInit__step_binding() {
       {"extend_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(extend_tables)), METH_FASTCALL, nullptr},
       {"rope_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_write)), METH_FASTCALL, nullptr},
       {"prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefill)), METH_FASTCALL, nullptr},
+      {"bind_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind_shared)), METH_FASTCALL, nullptr},
+      {"plan_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan_shared)), METH_FASTCALL, nullptr},
+      {"decode_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_shared)), METH_FASTCALL, nullptr},
+      {"quant_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quant_write)), METH_FASTCALL, nullptr},
+      {"quant_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quant_read)), METH_FASTCALL, nullptr},
       {nullptr, nullptr, 0, nullptr}};
   static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
   return PyModule_Create(&module);
