@@ -98,7 +98,11 @@ int mla_decode_shared(const mla_kv_pool* pool, int layer, const void* q, const i
   a.scale_log2 = softmax_scale * 1.4426950408889634f * (fp8 ? pool->kv_scale : 1.f);
   a.out_scale = fp8 ? pool->kv_scale : 1.f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = mla::launch_shared_decode(a, st);
+  CUtensorMap map = {};
+  if (!fp8 && !mla::make_map_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool->data, rows, mla::kDimRow, mla::kDimRow * 2, 64,
+                                mla::sh_copy_tokens(pool->page_size)))
+    return MLA_ERR_CUDA;
+  cudaError_t e = mla::launch_shared_decode(map, a, st);
   if (e == cudaSuccess) e = mla::launch_shared_merge(a, st);
   return done(e);
 }

@@ -1,98 +1,656 @@
-// Attention of a decode over shared prefixes: a warp a row, one position after the other.
+// Attention of a decode over shared prefixes, on the tensor core: rows of queries (of all
+// requests and heads of a tile) against positions that they share, 576 dims a key, the
+// first 512 of which are the value.
+//   S_t = scale q . K_t,  out = sum_t softmax(S)_t K_t[0:512]
+//
+// 2 * (576 + 512) flops a row and position: with 256 rows to a position it is the tensor
+// core that bounds it, and the accumulator that shapes it. 256 rows of 512 values in fp32
+// fill two SMs' tensor memory, with nothing left for scores. So a cluster of four blocks
+// works as two pairs (products of M = 256 over two SMs, each with half of the columns'
+// operand in its shared memory):
+//   blocks 0, 1  S = Q K^T and its softmax. Tensor memory: Q's 512 dims (256 columns of
+//                bf16 pairs), two buffers of S (128 columns each); the rope dims of Q and a
+//                ring of K's pieces in shared memory.
+//   blocks 2, 3  O += P V. Tensor memory: O (512 columns). Shared memory: two buffers of
+//                P, a ring of V's pieces.
+// The two products are 576 and 512 dims long, so both pairs are busy, and neither waits
+// for the other within a block of positions: weights P go one way, from the softmax
+// warps' registers into the other pair's shared memory (32 KB a block's 128 positions and
+// 2,304 cycles of products), with a factor for each row by which O is rescaled where the
+// running maximum moved. The first pair runs ahead by two blocks of positions.
+//
+// A cluster works through its items (see shared_internal.h): blocks of a tile's
+// positions, those that all its rows share and then each request's own. In the latter only
+// the request's rows take part: other rows' scores are not looked at, and the product's
+// row mask leaves their accumulators alone, so that one request's cache never touches
+// another's result. Positions outside a segment are masked by selection in S; their rows of
+// V are made zero, or left out 16 at a time.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <math_constants.h>
 
 #include "../../include/mla_decode.h"
-#include "ptx.cuh"
+#include "ptx_shared.cuh"
 #include "shared_internal.h"
 
 namespace mla {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWorkers = 8;                 // warps: softmax (the first four); accumulators (all)
+constexpr int kProducerWarp = kWorkers, kIssueWarp = kWorkers + 1;
+constexpr int kThreads = 32 * (kWorkers + 2);
+constexpr int kChunk = 64 * 128;            // [64 positions][64 dims]
+// Scores' pair: K in stages of three chunks (192 dims), three stages a block.
+constexpr int kKStages = 8, kKStageBytes = 3 * kChunk, kKParts = 3;
+constexpr int kOffQRope = kKStages * kKStageBytes;  // [128 rows][64 dims]
+// Accumulators' pair: P of 128 rows, two chunks of 64 positions; V in stages of 64
+// positions, four chunks (256 dims).
+constexpr int kPChunk = 128 * 128, kPBytes = 2 * kPChunk, kPBuffers = 2;
+constexpr int kOffV = kPBuffers * kPBytes;
+constexpr int kVStages = 4, kVStageBytes = 4 * kChunk;
+constexpr int kOffSmall = kOffQRope + 128 * 128;
+static_assert(kOffV + kVStages * kVStageBytes <= kOffSmall, "both pairs' buffers end before the small ones");
+constexpr int kOffAlpha = kOffSmall;                        // float [buffers][128]
+constexpr int kOffStats = kOffAlpha + kPBuffers * 128 * 4;  // float2 [128]
+constexpr int kOffBar = kOffStats + 128 * 8;
 
-template <bool kFp8>
-__global__ void __launch_bounds__(32 * kWarps) shared_decode_kernel(const ShDecodeArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  ShHeader* hd = reinterpret_cast<ShHeader*>(a.ws);
-  const int lane = threadIdx.x & 31, row = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  if (!sh_planned(hd, a)) {
-    if (threadIdx.x == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
-    return;
+enum {
+  // In the scores' pair. (Of its first block: K landed, Q in place, S read.)
+  kBarKFull = 0,                       // [kKStages]
+  kBarKFree = kBarKFull + kKStages,    // [kKStages]
+  kBarQ = kBarKFree + kKStages,
+  kBarS = kBarQ + 1,                   // [2] scores complete
+  kBarSFree = kBarS + 2,               // [2]
+  kBarPFree = kBarSFree + 2,           // [2] P multiplied
+  kBarStatsFree = kBarPFree + 2,
+  // In the accumulators' pair. (Of its first block: P ready, O read.)
+  kBarVFull = kBarStatsFree + 1,       // [kVStages]
+  kBarVFree = kBarVFull + kVStages,    // [kVStages]
+  kBarP = kBarVFree + kVStages,        // [2] weights have arrived
+  kBarPReady = kBarP + 2,              // [2] and O is rescaled, V landed
+  kBarPV = kBarPReady + 2,             // a block's product complete
+  kBarO = kBarPV + 1,                  // an item's last one
+  kBarStats = kBarO + 1,               // an item's maxima and sums have arrived
+  kBarOFree = kBarStats + 1,
+  kNumBars = kBarOFree + 1
+};
+
+constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 16 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
+constexpr uint32_t kColS = 256;             // + 128 a buffer; Q from 0
+constexpr float kRescaleThreshold = 8.0f;   // log2 units
+// The reference of a row that has seen no position: below every score, and finite, so that
+// a score of -inf against it is a weight of zero.
+constexpr float kNoMax = -1e30f;
+constexpr uint16_t kScorePair = 0x3, kAccPair = 0xc;  // blocks of the cluster
+
+// A block of positions, as every role sees it.
+struct Block {
+  int owner;
+  int t0;              // first position
+  int v0, v1;          // those of the segment: [t0 + v0, t0 + v1)
+  int row_lo, row_hi;  // rows that attend it
+  int end;             // row of query position i: below t0 + end + i
+  bool add;            // to what these rows have already
+};
+
+// Walks a tile's blocks [begin, end), a segment ahead in what it has loaded.
+struct Walk {
+  const ShSegment* segs;
+  ShSegment s, next;
+  int k, count, x, end, begin, prefix_end;
+  __device__ __forceinline__ void start(const ShDecodeArgs& a, const ShTile& tile, const ShItem& it) {
+    segs = reinterpret_cast<const ShSegment*>(a.ws + a.lay.segs) + tile.seg0;
+    count = tile.segs;
+    x = begin = it.begin;
+    end = it.end;
+    // (a tile of several segments: the first is the prefix if all rows have it)
+    int lo = 0, hi = count;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (segs[mid].block0 <= x) lo = mid;
+      else hi = mid;
+    }
+    k = lo;
+    s = segs[k];
+    const ShSegment first = segs[0];
+    prefix_end = first.base == first.tok_hi ? blocks(first) : 0;
+    next = segs[min(k + 1, count - 1)];
   }
-  if (static_cast<int>(blockIdx.x) >= hd->num_clusters) return;
-  const int* start = reinterpret_cast<const int*>(a.ws + a.lay.cluster_start);
+  __device__ static __forceinline__ int blocks(const ShSegment& g) { return (g.tok_hi - g.tok0 + kShTokens - 1) / kShTokens; }
+  __device__ __forceinline__ bool more() const { return x < end; }
+  __device__ __forceinline__ Block get() {
+    if (k + 1 < count && x >= next.block0) {
+      s = next;
+      ++k;
+      next = segs[min(k + 1, count - 1)];
+    }
+    Block b;
+    b.owner = s.owner;
+    b.t0 = s.tok0 + (x - s.block0) * kShTokens;
+    b.v0 = max(s.tok_lo - b.t0, 0);
+    b.v1 = min(s.tok_hi - b.t0, kShTokens);
+    b.row_lo = s.row_lo;
+    b.row_hi = s.row_hi;
+    b.end = s.base + 1 - b.t0;
+    b.add = x > max(s.block0, begin) || (k > 0 && begin < prefix_end);
+    ++x;
+    return b;
+  }
+};
+
+struct Params {
+  CUtensorMap rows;  // the pool as [rows][576], box {64, positions of a copy}
+  ShDecodeArgs a;
+};
+
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
+    shared_decode_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const ShDecodeArgs& a = p.a;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bar0 = sbase + kOffBar;
+  auto bar = [&](int i) -> uint32_t { return bar0 + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * kNumBars + 4);
+  ShHeader* hd = reinterpret_cast<ShHeader*>(a.ws);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank(), half = rank & 1;
+  const bool scores = rank < 2;  // which pair
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      int count = 1;
+      if (i == kBarQ || (i >= kBarSFree && i < kBarSFree + 2)) count = 8;       // softmax warps of both blocks
+      if (i >= kBarP && i < kBarP + 2) count = 4;                               // those of one
+      if (i == kBarStats) count = 4;
+      if (i >= kBarPReady && i < kBarPReady + 2) count = 2 * kWorkers;
+      if (i == kBarOFree) count = 2 * kWorkers;
+      if (i == kBarStatsFree) count = kWorkers;
+      mbar_init(bar(i), count);
+    }
+    *abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == kProducerWarp && lane == 0) tma_prefetch_map(&p.rows);
+  if (warp == kIssueWarp) {
+    tmem_alloc2(smem_addr(tmem_slot), 512);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  cluster_sync();  // all blocks' barriers are initialised before any arrival from another
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // This pair's first block's barriers; the block that this one's rows are shared with.
+  const uint32_t lead0 = mapa(bar0, rank & 2), peer0 = mapa(bar0, rank ^ 2);
+  auto lead = [&](int i) -> uint32_t { return lead0 + 8u * i; };
+  auto peer = [&](int i) -> uint32_t { return peer0 + 8u * i; };
+  pdl_wait();
+  auto fail = [&] {
+    *abort_flag = 1;
+    atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
+  };
+  // (a barrier seen complete, what the cluster's other blocks did before it is acquired)
+  auto spin = [&](uint32_t b, uint32_t parity) -> bool {
+    if (!mbar_spin(b, parity, abort_flag)) return false;
+    mbar_test_wait_cluster(b, parity);
+    return true;
+  };
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+    if (!mbar_spin_warp(b, parity, abort_flag)) return false;
+    mbar_test_wait_cluster(b, parity);
+    return true;
+  };
+  const int cluster = blockIdx.x >> 2;
+  const bool planned = sh_planned(hd, a);
+  if (!planned && threadIdx.x == 0 && rank == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
+  const int* cstart = reinterpret_cast<const int*>(a.ws + a.lay.cluster_start);
   const ShItem* items = reinterpret_cast<const ShItem*>(a.ws + a.lay.items);
-  for (int k = start[blockIdx.x]; k < start[blockIdx.x + 1]; ++k) {
-    const ShItem it = items[k];
-    const ShTile tile = reinterpret_cast<const ShTile*>(a.ws + a.lay.tiles)[it.tile];
-    if (row >= tile.rows) continue;
-    const int64_t out_row = static_cast<int64_t>(tile.row0) + row;
-    const int i = static_cast<int>(out_row / a.num_heads) % a.q_len;
-    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + out_row * kDimRow;
-    float q[18], o[16] = {};
-    for (int d = 0; d < 18; ++d) q[d] = __bfloat162float(qp[lane + 32 * d]);
-    float m = -1e30f, l = 0.f;
-    for (int s = 0; s < tile.segs; ++s) {
-      const ShSegment sg = reinterpret_cast<const ShSegment*>(a.ws + a.lay.segs)[tile.seg0 + s];
-      if (row < sg.row_lo || row >= sg.row_hi) continue;
-      const int lo = max(sg.tok_lo, sg.tok0 + max(it.begin - sg.block0, 0) * kShTokens);
-      const int64_t till = sg.tok0 + static_cast<int64_t>(it.end - sg.block0) * kShTokens;
-      const int hi = static_cast<int>(min(till, static_cast<int64_t>(min(sg.tok_hi, sg.base + i + 1))));
-      const int pages = a.page_indptr ? a.page_indptr[sg.owner + 1] - a.page_indptr[sg.owner] : a.max_blocks;
-      const int32_t* ids = a.page_indptr ? a.page_ids + a.page_indptr[sg.owner]
-                                         : a.page_ids + static_cast<int64_t>(sg.owner) * a.max_blocks;
-      for (int t = lo; t < hi; ++t) {
-        const int j = t / a.page_size;
-        const int id = j < pages ? ids[j] : -1;
-        float x[18] = {};
-        if (id < 0 || id >= a.num_pages) {
-          if (lane == 0) atomicOr(&hd->status, MLA_STATUS_BAD_PAGE);
-        } else {
-          const int64_t at = ((static_cast<int64_t>(a.layer) * a.num_pages + id) * a.page_size + t % a.page_size) * kDimRow;
-          for (int d = 0; d < 18; ++d) {
-            if (kFp8) x[d] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(a.pool)[at + lane + 32 * d]);
-            else x[d] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool)[at + lane + 32 * d]);
+  const ShTile* tiles = reinterpret_cast<const ShTile*>(a.ws + a.lay.tiles);
+  int item0 = 0, item1 = 0;
+  if (planned && cluster < hd->num_clusters) {
+    item0 = cstart[cluster];
+    item1 = cstart[cluster + 1];
+  }
+  const int unit = sh_copy_tokens(a.page_size);
+
+  if (warp == kProducerWarp) {
+    // Each block of the scores' pair brings its 64 of a block's positions, all dims; each of
+    // the accumulators' pair all positions, its 256 value dims.
+    const int subs = (scores ? 64 : 128) / unit;  // copies along the positions
+    const int64_t layer_row0 = static_cast<int64_t>(a.layer) * a.num_pages * a.page_size;
+    const int no_row = static_cast<int>(static_cast<int64_t>(a.num_layers) * a.num_pages * a.page_size);  // reads as zeros
+    bool ok = true;
+    uint32_t stage = 0, use = 0, issued = 0;  // of the ring
+    // A lane looks up the pool's row of one copy of a block.
+    auto row_of = [&](const Block& b) -> int {
+      if (lane >= subs) return no_row;
+      const int t = b.t0 + (scores ? 64 * static_cast<int>(half) : 0) + unit * lane;
+      if (t >= b.t0 + b.v1 || t + unit <= b.t0 + b.v0) return no_row;
+      const int j = t / a.page_size;
+      const int64_t first = a.page_indptr ? a.page_indptr[b.owner] : static_cast<int64_t>(b.owner) * a.max_blocks;
+      const int n = a.page_indptr ? a.page_indptr[b.owner + 1] - a.page_indptr[b.owner] : a.max_blocks;
+      const int id = j < n ? a.page_ids[first + j] : -1;
+      if (id < 0 || id >= a.num_pages) {
+        if (scores) atomicOr(&hd->status, MLA_STATUS_BAD_PAGE);
+        return no_row;
+      }
+      return static_cast<int>(layer_row0 + static_cast<int64_t>(id) * a.page_size + t % a.page_size);
+    };
+    for (int k = item0; k < item1 && ok; ++k) {
+      const ShItem it = items[k];
+      Walk w;
+      w.start(a, tiles[it.tile], it);
+      int row = row_of(w.get()), next_row = no_row;
+      for (int x = it.begin; x < it.end && ok; ++x, row = next_row) {
+        if (w.more()) next_row = row_of(w.get());
+        const int parts = scores ? kKParts : 2;
+        for (int part = 0; part < parts && ok; ++part) {
+          ok = warp_wait(bar((scores ? kBarKFree : kBarVFree) + stage), use ^ 1u);
+          if (!ok) break;
+          if (scores) {
+            const uint32_t dst = sbase + stage * kKStageBytes;
+            if (half == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarKFull + stage), 2 * kKStageBytes);
+            for (int i = 0; i < subs; ++i) {
+              const int r = __shfl_sync(0xffffffffu, row, i);
+              if (lane == 0)
+                for (int c = 0; c < 3; ++c)
+                  tma2_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, lead(kBarKFull + stage), 64 * (3 * part + c), r);
+            }
+          } else {
+            const uint32_t dst = sbase + kOffV + stage * kVStageBytes;
+            if (lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + stage), kVStageBytes);
+            for (int i = 0; i < subs / 2; ++i) {
+              const int r = __shfl_sync(0xffffffffu, row, part * (subs / 2) + i);
+              if (lane == 0)
+                for (int c = 0; c < 4; ++c)
+                  tma_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, bar(kBarVFull + stage),
+                              256 * static_cast<int>(half) + 64 * c, r);
+            }
+          }
+          ++issued;
+          if (++stage == static_cast<uint32_t>(scores ? kKStages : kVStages)) {
+            stage = 0;
+            use ^= 1u;
           }
         }
-        float dot = 0.f;
-        for (int d = 0; d < 18; ++d) dot = fmaf(q[d], x[d], dot);
-        for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        const float sc = dot * a.scale_log2;
-        const float mn = fmaxf(m, sc), f = exp2f(m - mn), p = exp2f(sc - mn);
-        m = mn;
-        l = fmaf(l, f, p);
-        for (int d = 0; d < 16; ++d) o[d] = fmaf(p, x[d], o[d] * f);
       }
     }
-    if (it.part >= 0) {
-      const int64_t at = static_cast<int64_t>(it.part) * kShRows + row;
-      if (lane == 0) reinterpret_cast<float2*>(a.ws + a.lay.stats)[at] = make_float2(m, l);
-      float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + at * kDimCkv;
-      for (int d = 0; d < 16; ++d) dst[lane + 32 * d] = o[d];
-    } else {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + out_row * kDimCkv;
-      for (int d = 0; d < 16; ++d) dst[lane + 32 * d] = __float2bfloat16_rn(o[d] * (a.out_scale / l));
-      if (a.lse && lane == 0) a.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
+    if (!ok && lane == 0) fail();
+    if (*abort_flag && lane == 0 && (!scores || half == 0)) {  // let the copies in flight land (each wait bounded)
+      const uint32_t n = scores ? kKStages : kVStages;
+      for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i)
+        mbar_wait(bar((scores ? kBarKFull : kBarVFull) + i % n), (i / n) & 1u, nullptr);
     }
+  } else if (warp == kIssueWarp) {
+    if (scores && half == 0 && elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16(256, kShTokens, false, false);
+      const uint32_t ring = desc_lo(sbase), rope = desc_lo(sbase + kOffQRope);
+      uint32_t n = 0, stage = 0, use = 0;
+      bool ok = true;
+      for (int k = item0; k < item1 && ok; ++k) {
+        const int blocks = items[k].end - items[k].begin;
+        ok = spin(bar(kBarQ), (k - item0) & 1u);
+        for (int x = 0; x < blocks && ok; ++x, ++n) {
+          const uint32_t buf = n & 1u;
+          if (!(ok = spin(bar(kBarSFree + buf), ((n >> 1) & 1u) ^ 1u))) break;
+          const uint32_t d = tmem + kColS + 128 * buf;
+#pragma unroll
+          for (int part = 0; part < kKParts; ++part) {
+            if (!ok || !(ok = spin(bar(kBarKFull + stage), use))) break;
+            tc_fence_after();
+            const uint32_t kb = ring + stage * (kKStageBytes >> 4);
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int step = 4 * (3 * part + c) + e;  // dims 16 step ...
+                if (step < 32) mma2_bf16_ts(d, tmem + 8 * step, kb + c * (kChunk >> 4) + 2 * e, idesc, step != 0);
+                else mma2_bf16_ss(d, rope + 2 * e, kb + c * (kChunk >> 4) + 2 * e, idesc, 1);
+              }
+            mma2_commit_to(bar(kBarKFree + stage), kScorePair);
+            if (++stage == kKStages) {
+              stage = 0;
+              use ^= 1u;
+            }
+          }
+          if (ok) mma2_commit_to(bar(kBarS + buf), kScorePair);
+        }
+      }
+      if (!ok) fail();
+    } else if (!scores && half == 0 && elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16(256, 256, false, true);
+      uint32_t n = 0, stage = 0;
+      bool ok = true;
+      for (int k = item0; k < item1 && ok; ++k) {
+        const ShItem it = items[k];
+        const ShTile tile = tiles[it.tile];
+        Walk w;
+        w.start(a, tile, it);
+        ok = spin(bar(kBarOFree), ((k - item0) & 1u) ^ 1u);
+        for (; w.more() && ok; ++n) {
+          const Block b = w.get();
+          const uint32_t buf = n & 1u;
+          const bool all = b.row_lo == 0 && b.row_hi == tile.rows;
+          uint32_t off[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int lo = min(max(b.row_lo - 32 * i, 0), 32), hi = min(max(b.row_hi - 32 * i, 0), 32);
+            const uint32_t below_hi = hi == 32 ? ~0u : (1u << hi) - 1u, below_lo = lo == 32 ? ~0u : (1u << lo) - 1u;
+            off[i] = ~(below_hi & ~below_lo);
+          }
+          if (!(ok = spin(bar(kBarPReady + buf), (n >> 1) & 1u))) break;
+          tc_fence_after();
+          const uint32_t pa = desc_lo(sbase + buf * kPBytes);
+          const int k0 = b.v0 >> 4, k1 = (b.v1 + 15) >> 4;  // steps of 16 positions
+          bool add = b.add;
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t vb = desc_lo_mn(sbase + kOffV + stage * kVStageBytes, kChunk);
+            for (int e = max(k0, 4 * h); e < min(k1, 4 * h + 4); ++e) {
+              const uint32_t pe = pa + h * (kPChunk >> 4) + 2 * (e & 3), ve = vb + 128 * (e & 3);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                if (all) mma2_bf16_ss(tmem + 256 * c, pe, ve + c * (2 * kChunk >> 4), idesc, add);
+                else mma2_bf16_ss_rows(tmem + 256 * c, pe, ve + c * (2 * kChunk >> 4), idesc, off, add);
+              }
+              add = true;
+            }
+            mma2_commit_to(bar(kBarVFree + stage), kAccPair);
+            if (++stage == kVStages) stage = 0;
+          }
+          mma2_commit_to(bar(kBarPFree + buf), kScorePair);
+          mma2_commit_to(bar(kBarPV), kAccPair);
+          if (!w.more()) mma2_commit_to(bar(kBarO), kAccPair);
+        }
+      }
+      if (!ok) fail();
+    }
+  } else if (scores && warp < 4) {
+    // Softmax: a row a thread.
+    const int lrow = 32 * warp + lane, r = 128 * static_cast<int>(half) + lrow;
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const float scale = a.scale_log2, threshold = kRescaleThreshold / scale;
+    const uint64_t scale2 = f2_make(scale, scale);
+    const uint32_t p_row = mapa(sbase, rank ^ 2) + lrow * 128, sw = lrow & 7;  // this row of the peer's P
+    const uint32_t alpha_at = mapa(sbase + kOffAlpha, rank ^ 2) + 4 * lrow;
+    const uint32_t stats_at = mapa(sbase + kOffStats, rank ^ 2) + 8 * lrow;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int k = item0; k < item1 && ok; ++k) {
+      const ShItem it = items[k];
+      const ShTile tile = tiles[it.tile];
+      Walk w;
+      w.start(a, tile, it);
+      // The queries, into place once the scores of the item before are complete (which the
+      // last of its blocks told).
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
+                                                          (static_cast<int64_t>(tile.row0) + r) * (kDimRow * 2));
+        const bool real = r < tile.rows;
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 x = real ? src[8 * c + i] : make_uint4(0, 0, 0, 0);
+            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+          }
+          tmem_st32(tbase + 32 * c, v);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = real ? src[64 + i] : make_uint4(0, 0, 0, 0);
+          st_shared_v4(sbase + kOffQRope + lrow * 128 + 16 * (i ^ sw), x.x, x.y, x.z, x.w);
+        }
+        fence_proxy_async_smem();
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(lead(kBarQ));
+      }
+      const int i = static_cast<int>((static_cast<int64_t>(tile.row0) + r) / a.num_heads) % a.q_len;
+      float ref = kNoMax, l = 0.f;
+      for (; w.more(); ++n) {
+        const Block b = w.get();
+        const uint32_t buf = n & 1u;
+        const int w0 = 128 * static_cast<int>(half) + 32 * warp;  // this warp's first row
+        const bool here = b.row_lo < w0 + 32 && b.row_hi > w0;
+        const bool mine = r >= b.row_lo && r < b.row_hi;
+        if (!(ok = warp_wait(bar(kBarS + buf), (n >> 1) & 1u))) break;
+        tc_fence_after();
+        float alpha = 1.f;
+        uint32_t s[128];
+        if (here) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tbase + kColS + 128 * buf + 32 * c, s + 32 * c);
+          tmem_wait_ld();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead(kBarSFree + buf));
+        if (here) {
+          const int b0 = mine ? b.v0 : kShTokens, e0 = mine ? min(b.v1, b.end + i) : 0;
+          if (!__all_sync(0xffffffffu, b0 == 0 && e0 == kShTokens)) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t above = e0 >= 32 * g + 32 ? ~0u : (1u << max(e0 - 32 * g, 0)) - 1u;
+              const uint32_t below = b0 >= 32 * g + 32 ? ~0u : (1u << max(b0 - 32 * g, 0)) - 1u;
+              const uint32_t keep = above & ~below;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(keep & (1u << c))) s[32 * g + c] = 0xff800000u;
+            }
+          }
+          float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          }
+          mx = fmaxf(mx, mx1);
+          if (mx > ref + threshold) {
+            alpha = exp2_approx((ref - mx) * scale);
+            l *= alpha;
+            ref = mx;
+            if (!b.add) alpha = 1.f;  // (nothing there to rescale)
+          }
+          const float neg = -ref * scale;
+          const uint64_t neg2 = f2_make(neg, neg);
+          uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            float t0, t1;
+            f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
+            const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
+            sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
+            s[c] = pack_bf16x2(p0, p1);
+          }
+          float s0, s1, s2, s3;
+          f2_split(sum2[0], s0, s1);
+          f2_split(sum2[1], s2, s3);
+          l += (s0 + s1) + (s2 + s3);
+        }
+        if (!(ok = warp_wait(bar(kBarPFree + buf), ((n >> 1) & 1u) ^ 1u))) break;
+        const uint32_t rb = peer(kBarP + buf);
+        if (here) {
+          const uint32_t dst = p_row + buf * kPBytes;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            st_async_v4(dst + (c >> 3) * kPChunk + 16 * ((c & 7) ^ sw), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3], rb);
+          st_async_b32(alpha_at + 512 * buf, __float_as_uint(alpha), rb);
+        }
+        if (lane == 0) mbar_arrive_expect_tx_cluster(rb, here ? 32 * (256 + 4) : 0);
+      }
+      if (!ok) break;
+      if (!(ok = warp_wait(bar(kBarStatsFree), ((k - item0) & 1u) ^ 1u))) break;
+      st_async_v2(stats_at, __float_as_uint(ref * scale), __float_as_uint(l), peer(kBarStats));
+      if (lane == 0) mbar_arrive_expect_tx_cluster(peer(kBarStats), 32 * 8);
+    }
+    if (!ok) fail();
+  } else if (!scores && warp < kWorkers) {
+    // Accumulators: the warps of a quarter of the lanes have half of the columns each.
+    const int lrow = 32 * (warp & 3) + lane, r = 128 * static_cast<int>(half) + lrow, side = warp >> 2;
+    const uint32_t tO = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256 * side;
+    const float* alphas = reinterpret_cast<const float*>(smem + kOffAlpha);
+    const float2* stats = reinterpret_cast<const float2*>(smem + kOffStats);
+    uint32_t n = 0, stage = 0, use = 0;
+    bool ok = true;
+    for (int k = item0; k < item1 && ok; ++k) {
+      const ShItem it = items[k];
+      const ShTile tile = tiles[it.tile];
+      Walk w;
+      w.start(a, tile, it);
+      for (; w.more(); ++n) {
+        const Block b = w.get();
+        const uint32_t buf = n & 1u;
+        const int w0 = r - lane;
+        const bool here = b.row_lo < w0 + 32 && b.row_hi > w0;
+        if (!(ok = warp_wait(bar(kBarP + buf), (n >> 1) & 1u))) break;
+        const float alpha = here ? alphas[128 * buf + lrow] : 1.f;
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          // (the weights of this block have come, so the product of block n - 2 is complete)
+          if (!(ok = warp_wait(bar(kBarPV), (n - 1) & 1u))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
+            tmem_st32(tO + 32 * c, o);
+          }
+          tmem_wait_st();
+        }
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (!(ok = warp_wait(bar(kBarVFull + stage), use))) break;
+          // Rows of V outside the segment, among the 16 at its ends that are multiplied.
+          const uint32_t v = sbase + kOffV + stage * kVStageBytes;
+          const int lo0 = (b.v0 & ~15) - 64 * h, lo1 = b.v0 - 64 * h, hi0 = b.v1 - 64 * h, hi1 = ((b.v1 + 15) & ~15) - 64 * h;
+          auto zero = [&](int from, int to) {  // 512 bytes a row: a warp each
+            for (int t = max(from, 0) + warp; t < min(to, 64); t += kWorkers)
+              st_shared_v4(v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7), 0, 0, 0, 0);
+          };
+          if (b.v0 & 15) zero(lo0, lo1);
+          if (b.v1 & 15) zero(hi0, hi1);
+          // Positions that only later queries of a request see: an infinity or NaN there
+          // would reach the others through a weight of zero. (Those that see it have it in
+          // their scores.)
+          for (int t = max(b.end - 64 * h, 0) + warp; t < min(hi0, 64); t += kWorkers) {
+            const uint32_t at = v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7);
+            uint32_t x[4];
+            ld_shared_v4(at, x[0], x[1], x[2], x[3]);
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+            if (__any_sync(0xffffffffu, odd)) st_shared_v4(at, 0, 0, 0, 0);
+          }
+          if (++stage == kVStages) {
+            stage = 0;
+            use ^= 1u;
+          }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(lead(kBarPReady + buf));
+      }
+      if (!ok) break;
+      if (!(ok = warp_wait(bar(kBarStats), (k - item0) & 1u))) break;
+      const float2 ml = stats[lrow];
+      if (!(ok = warp_wait(bar(kBarO), (k - item0) & 1u))) break;
+      tc_fence_after();
+      const bool real = r < tile.rows;
+      const int64_t out_row = static_cast<int64_t>(tile.row0) + r;
+      const int64_t part_row = static_cast<int64_t>(it.part) * kShRows + r;
+      const bool part = it.part >= 0;
+      const float inv = part ? 1.f : a.out_scale / ml.y;
+      // (a piece without a position of the row: its accumulator was never begun)
+      const bool store = real && !(part && ml.y == 0.f);
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * c, o);
+        tmem_wait_ld();
+        // columns [0, 128) of a side are the first block's dims, the others the second's
+        const int dim = 128 * side + 32 * (c & 3) + (c >= 4 ? 256 : 0);
+        if (store && part) {
+          float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + part_row * kDimCkv + dim;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) st_global_v8(dst + 8 * v, o + 8 * v);
+        } else if (store) {
+          uint8_t* dst = static_cast<uint8_t*>(a.out) + (out_row * kDimCkv + dim) * 2;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              pk[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]) * inv, __uint_as_float(o[16 * v + 2 * e + 1]) * inv);
+            st_global_v8(dst + 32 * v, pk);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(lead(kBarOFree));
+        mbar_arrive_cluster(peer(kBarStatsFree));
+      }
+      if (side == 0 && real) {
+        if (part) reinterpret_cast<float2*>(a.ws + a.lay.stats)[part_row] = ml;
+        else if (a.lse) a.lse[out_row] = (ml.x + log2f(ml.y)) * 0.69314718055994531f;
+      }
+    }
+    if (!ok) fail();
   }
+  __syncwarp();
+  __syncthreads();
+  if (*abort_flag) {  // stores from other blocks may be on their way here
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 100000ull) {}
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // no block ends while another's products, stores or arrivals reach into it
+  tc_fence_after();
+  if (warp == kIssueWarp) tmem_dealloc2(tmem, 512);
 }
 
 }  // namespace
 
+// Clusters of the kernel that run at once on the current device (cached), or -1.
 int shared_max_active_clusters() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return -1;
-  return sms / kShClusterBlocks;
+  static int cached[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return -1;
+  if (cached[dev] > 0) return cached[dev];
+  if (cudaFuncSetAttribute(shared_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return -1;
+  int sms = 0, n = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kShClusterBlocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(sms / kShClusterBlocks * kShClusterBlocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, shared_decode_kernel, &cfg) != cudaSuccess || n <= 0) return -1;
+  return cached[dev] = n;
 }
 
-cudaError_t launch_shared_decode(const ShDecodeArgs& a, cudaStream_t stream) {
-  const dim3 grid(a.clusters, kShRows / kWarps);
-  if (a.dtype == MLA_DTYPE_FP8_E4M3) return launch_pdl(shared_decode_kernel<true>, grid, dim3(32 * kWarps), 0, stream, a);
-  return launch_pdl(shared_decode_kernel<false>, grid, dim3(32 * kWarps), 0, stream, a);
+cudaError_t launch_shared_decode(const CUtensorMap& rows, const ShDecodeArgs& a, cudaStream_t stream) {
+  if (a.dtype == MLA_DTYPE_FP8_E4M3) return launch_shared_rows(a, stream);
+  static bool attr_set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_once(shared_decode_kernel, kSmemBytes, attr_set);
+  if (e != cudaSuccess) return e;
+  Params p;
+  p.rows = rows;
+  p.a = a;
+  return launch_pdl(shared_decode_kernel, dim3(kShClusterBlocks * a.clusters), dim3(kThreads), kSmemBytes, stream, p);
 }
 
 }  // namespace mla

@@ -158,7 +158,9 @@ __device__ __forceinline__ bool sh_planned(const ShHeader* hd, const ShDecodeArg
 cudaError_t launch_shared_plan(const ShPlanArgs& a, cudaStream_t stream);
 cudaError_t launch_shared_merge(const ShDecodeArgs& a, cudaStream_t stream);
 // shared_decode.cu
-cudaError_t launch_shared_decode(const ShDecodeArgs& a, cudaStream_t stream);
+// rows: the pool as [rows][576], box {64, sh_copy_tokens}
+cudaError_t launch_shared_decode(const CUtensorMap& rows, const ShDecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_shared_rows(const ShDecodeArgs& a, cudaStream_t stream);
 int shared_max_active_clusters();
 
 // ---------------------------------------------------------------- compact latent store
