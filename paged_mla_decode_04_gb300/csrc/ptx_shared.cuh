@@ -39,6 +39,22 @@ __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_bar
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// Arrival on any block's barrier that expects `bytes` more; publishes nothing (what is
+// expected completes on the barrier by itself).
+__device__ __forceinline__ void mbar_arrive_expect_tx_relaxed(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+               : "memory");
+}
+
+// Copies `bytes` (a multiple of 16, as the addresses are) of this block's shared memory into
+// another block's and completes them on a barrier of that block.
+__device__ __forceinline__ void bulk_copy_to(uint32_t cluster_dst, uint32_t src, uint32_t bytes, uint32_t cluster_bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   cluster_dst),
+               "r"(src), "r"(bytes), "r"(cluster_bar)
+               : "memory");
+}
+
 __device__ __forceinline__ void st_async_b32(uint32_t addr, uint32_t v, uint32_t remote_bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
                "r"(remote_bar)

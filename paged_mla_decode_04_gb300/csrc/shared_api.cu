@@ -98,11 +98,13 @@ int mla_decode_shared(const mla_kv_pool* pool, int layer, const void* q, const i
   a.scale_log2 = softmax_scale * 1.4426950408889634f * (fp8 ? pool->kv_scale : 1.f);
   a.out_scale = fp8 ? pool->kv_scale : 1.f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CUtensorMap map = {};
-  if (!fp8 && !mla::make_map_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool->data, rows, mla::kDimRow, mla::kDimRow * 2, 64,
-                                mla::sh_copy_tokens(pool->page_size)))
+  CUtensorMap maps[3] = {};
+  const uint32_t copy = mla::sh_copy_tokens(pool->page_size);
+  if (!fp8 && (!mla::make_map_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool->data, rows, mla::kDimRow, mla::kDimRow * 2, 64, copy) ||
+               !mla::make_map_chunks(&maps[1], pool->data, rows, mla::kDimRow, mla::kDimRow * 2, copy, 3) ||
+               !mla::make_map_chunks(&maps[2], pool->data, rows, mla::kDimRow, mla::kDimRow * 2, copy, 4)))
     return MLA_ERR_CUDA;
-  cudaError_t e = mla::launch_shared_decode(map, a, st);
+  cudaError_t e = mla::launch_shared_decode(maps, a, st);
   if (e == cudaSuccess) e = mla::launch_shared_merge(a, st);
   return done(e);
 }

@@ -26,6 +26,7 @@
 // another's result. Positions outside a segment are masked by selection in S; their rows of
 // V are made zero, or left out 16 at a time.
 #include <cuda_bf16.h>
+#include <limits.h>
 #include <math_constants.h>
 
 #include "../../include/mla_decode.h"
@@ -35,23 +36,31 @@
 namespace mla {
 namespace {
 
-constexpr int kWorkers = 8;                 // warps: softmax (the first four); accumulators (all)
+constexpr int kWorkers = 8;                 // warps of softmax or accumulators, two groups of four
 constexpr int kProducerWarp = kWorkers, kIssueWarp = kWorkers + 1;
-constexpr int kThreads = 32 * (kWorkers + 2);
+constexpr int kThreads = 384;               // (the last two warps idle)
+// Registers a thread after setmaxnreg; they add up to the launch's 3 x 168.
+constexpr int kRegsWorker = 208, kRegsOther = 88;
+static_assert(2 * kRegsWorker + kRegsOther == 3 * 168, "register split");
 constexpr int kChunk = 64 * 128;            // [64 positions][64 dims]
 // Scores' pair: K in stages of three chunks (192 dims), three stages a block.
-constexpr int kKStages = 8, kKStageBytes = 3 * kChunk, kKParts = 3;
+constexpr int kKStages = 5, kKStageBytes = 3 * kChunk, kKParts = 3;
 constexpr int kOffQRope = kKStages * kKStageBytes;  // [128 rows][64 dims]
 // Accumulators' pair: P of 128 rows, two chunks of 64 positions; V in stages of 64
 // positions, four chunks (256 dims).
-constexpr int kPChunk = 128 * 128, kPBytes = 2 * kPChunk, kPBuffers = 2;
+constexpr int kPChunk = 128 * 128, kPBytes = 2 * kPChunk, kPBuffers = 3;
 constexpr int kOffV = kPBuffers * kPBytes;
-constexpr int kVStages = 4, kVStageBytes = 4 * kChunk;
-constexpr int kOffSmall = kOffQRope + 128 * 128;
+constexpr int kVStages = 3, kVStageBytes = 4 * kChunk;
+constexpr int kOffPOut = kOffQRope + 128 * 128;  // P on its way to the other pair
+constexpr int kOffSmall = kOffPOut + 2 * kPBytes;
 static_assert(kOffV + kVStages * kVStageBytes <= kOffSmall, "both pairs' buffers end before the small ones");
 constexpr int kOffAlpha = kOffSmall;                        // float [buffers][128]
 constexpr int kOffStats = kOffAlpha + kPBuffers * 128 * 4;  // float2 [128]
-constexpr int kOffBar = kOffStats + 128 * 8;
+// Scores' pair: each row's reference maximum, as the block before left it; the sum and
+// reference of the group that an item's last block is not of.
+constexpr int kOffRef = kOffStats + 128 * 8;                // float [128]
+constexpr int kOffSum = kOffRef + 128 * 4;                  // float2 [2 items][128]
+constexpr int kOffBar = kOffSum + 2 * 128 * 8;
 
 enum {
   // In the scores' pair. (Of its first block: K landed, Q in place, S read.)
@@ -60,15 +69,17 @@ enum {
   kBarQ = kBarKFree + kKStages,
   kBarS = kBarQ + 1,                   // [2] scores complete
   kBarSFree = kBarS + 2,               // [2]
-  kBarPFree = kBarSFree + 2,           // [2] P multiplied
-  kBarStatsFree = kBarPFree + 2,
+  kBarOutFree = kBarSFree + 2,         // [2 groups] P has left
+  kBarPFree = kBarOutFree + 2,         // [kPBuffers] P multiplied (in both pairs)
+  kBarStatsFree = kBarPFree + kPBuffers,
+  kBarRef = kBarStatsFree + 1,         // [2 groups][4 warps] the reference is there
+  kBarSum = kBarRef + 8,               // [2 items][4 warps] the other group's sum is
   // In the accumulators' pair. (Of its first block: P ready, O read.)
-  kBarVFull = kBarStatsFree + 1,       // [kVStages]
+  kBarVFull = kBarSum + 8,       // [kVStages]
   kBarVFree = kBarVFull + kVStages,    // [kVStages]
-  kBarP = kBarVFree + kVStages,        // [2] weights have arrived
-  kBarPReady = kBarP + 2,              // [2] and O is rescaled, V landed
-  kBarPV = kBarPReady + 2,             // a block's product complete
-  kBarO = kBarPV + 1,                  // an item's last one
+  kBarP = kBarVFree + kVStages,        // [kPBuffers] weights have arrived
+  kBarPReady = kBarP + kPBuffers,      // [kPBuffers] and O is rescaled, V landed
+  kBarO = kBarPReady + kPBuffers,      // an item's last product complete
   kBarStats = kBarO + 1,               // an item's maxima and sums have arrived
   kBarOFree = kBarStats + 1,
   kNumBars = kBarOFree + 1
@@ -140,6 +151,8 @@ struct Walk {
 
 struct Params {
   CUtensorMap rows;  // the pool as [rows][576], box {64, positions of a copy}
+  // Where a copy brings 64 positions: as [chunk][rows][64], boxes of three and four chunks.
+  CUtensorMap chunks3, chunks4;
   ShDecodeArgs a;
 };
 
@@ -157,14 +170,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank(), half = rank & 1;
   const bool scores = rank < 2;  // which pair
+  const int unit = sh_copy_tokens(a.page_size), page_shift = 31 - __clz(a.page_size);
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int count = 1;
-      if (i == kBarQ || (i >= kBarSFree && i < kBarSFree + 2)) count = 8;       // softmax warps of both blocks
-      if (i >= kBarP && i < kBarP + 2) count = 4;                               // those of one
+      if (i == kBarQ) count = 2 * kWorkers;
+      if (i >= kBarSFree && i < kBarSFree + 2) count = 8;                       // a group of both blocks
+      if (i >= kBarP && i < kBarP + kPBuffers) count = 4;                               // a group of one
       if (i == kBarStats) count = 4;
-      if (i >= kBarPReady && i < kBarPReady + 2) count = 2 * kWorkers;
+      if (i >= kBarPReady && i < kBarPReady + kPBuffers) count = 2 * kWorkers;
       if (i == kBarOFree) count = 2 * kWorkers;
       if (i == kBarStatsFree) count = kWorkers;
       mbar_init(bar(i), count);
@@ -172,7 +187,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
-  if (warp == kProducerWarp && lane == 0) tma_prefetch_map(&p.rows);
+  if (warp == kProducerWarp && lane == 0) tma_prefetch_map(unit != 64 ? &p.rows : scores ? &p.chunks3 : &p.chunks4);
   if (warp == kIssueWarp) {
     tmem_alloc2(smem_addr(tmem_slot), 512);
     tmem_relinquish2();
@@ -190,15 +205,21 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
     atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
   };
-  // (a barrier seen complete, what the cluster's other blocks did before it is acquired)
-  auto spin = [&](uint32_t b, uint32_t parity) -> bool {
-    if (!mbar_spin(b, parity, abort_flag)) return false;
-    mbar_test_wait_cluster(b, parity);
+  // Waits of a thread and of a warp. (What a wait of the first kind is for is ordered by
+  // tcgen05 fences or the copy's own completion; the others acquire what this block's or the
+  // cluster's threads wrote to shared memory, for the whole warp.)
+  auto spin = [&](uint32_t b, uint32_t parity) -> bool { return mbar_spin(b, parity, abort_flag); };
+  auto spin_cluster = [&](uint32_t b, uint32_t parity) -> bool { return spin(b, parity) && mbar_test_wait_cluster(b, parity); };
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return mbar_spin_warp(b, parity, abort_flag); };
+  auto warp_wait_block = [&](uint32_t b, uint32_t parity) -> bool {
+    if (!mbar_spin_warp(b, parity, abort_flag)) return false;
+    __syncwarp();
     return true;
   };
-  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+  auto warp_wait_cluster = [&](uint32_t b, uint32_t parity) -> bool {
     if (!mbar_spin_warp(b, parity, abort_flag)) return false;
-    mbar_test_wait_cluster(b, parity);
+    if (lane == 0) mbar_test_wait_cluster(b, parity);
+    __syncwarp();
     return true;
   };
   const int cluster = blockIdx.x >> 2;
@@ -212,75 +233,121 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     item0 = cstart[cluster];
     item1 = cstart[cluster + 1];
   }
-  const int unit = sh_copy_tokens(a.page_size);
 
+  if (warp >= kWorkers) setmaxnreg_dec<kRegsOther>();
   if (warp == kProducerWarp) {
     // Each block of the scores' pair brings its 64 of a block's positions, all dims; each of
-    // the accumulators' pair all positions, its 256 value dims.
-    const int subs = (scores ? 64 : 128) / unit;  // copies along the positions
-    const int64_t layer_row0 = static_cast<int64_t>(a.layer) * a.num_pages * a.page_size;
-    const int no_row = static_cast<int>(static_cast<int64_t>(a.num_layers) * a.num_pages * a.page_size);  // reads as zeros
-    bool ok = true;
-    uint32_t stage = 0, use = 0, issued = 0;  // of the ring
-    // A lane looks up the pool's row of one copy of a block.
-    auto row_of = [&](const Block& b) -> int {
-      if (lane >= subs) return no_row;
-      const int t = b.t0 + (scores ? 64 * static_cast<int>(half) : 0) + unit * lane;
-      if (t >= b.t0 + b.v1 || t + unit <= b.t0 + b.v0) return no_row;
-      const int j = t / a.page_size;
-      const int64_t first = a.page_indptr ? a.page_indptr[b.owner] : static_cast<int64_t>(b.owner) * a.max_blocks;
-      const int n = a.page_indptr ? a.page_indptr[b.owner + 1] - a.page_indptr[b.owner] : a.max_blocks;
-      const int id = j < n ? a.page_ids[first + j] : -1;
-      if (id < 0 || id >= a.num_pages) {
-        if (scores) atomicOr(&hd->status, MLA_STATUS_BAD_PAGE);
-        return no_row;
-      }
-      return static_cast<int>(layer_row0 + static_cast<int64_t>(id) * a.page_size + t % a.page_size);
-    };
-    for (int k = item0; k < item1 && ok; ++k) {
-      const ShItem it = items[k];
-      Walk w;
-      w.start(a, tiles[it.tile], it);
-      int row = row_of(w.get()), next_row = no_row;
-      for (int x = it.begin; x < it.end && ok; ++x, row = next_row) {
-        if (w.more()) next_row = row_of(w.get());
-        const int parts = scores ? kKParts : 2;
-        for (int part = 0; part < parts && ok; ++part) {
-          ok = warp_wait(bar((scores ? kBarKFree : kBarVFree) + stage), use ^ 1u);
-          if (!ok) break;
-          if (scores) {
-            const uint32_t dst = sbase + stage * kKStageBytes;
-            if (half == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarKFull + stage), 2 * kKStageBytes);
-            for (int i = 0; i < subs; ++i) {
-              const int r = __shfl_sync(0xffffffffu, row, i);
-              if (lane == 0)
-                for (int c = 0; c < 3; ++c)
-                  tma2_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, lead(kBarKFull + stage), 64 * (3 * part + c), r);
-            }
+    // the accumulators' pair all positions, its 256 value dims. One lane does it all; page
+    // ids are asked for two blocks ahead. (Looked up as they were needed, and with a copy for
+    // each 64 dims, this warp took 6,100 cycles a block.)
+    if (lane == 0) {
+      const int subs = (scores ? 64 : 128) / unit;  // copies along the positions
+      const int offset = scores ? 64 * static_cast<int>(half) : 0;
+      const int layer_row0 = static_cast<int>(static_cast<int64_t>(a.layer) * a.num_pages * a.page_size);
+      const int no_row = static_cast<int>(static_cast<int64_t>(a.num_layers) * a.num_pages * a.page_size);  // reads as zeros
+      constexpr int kNone = INT_MIN;  // not a position of the segment
+      bool ok = true;
+      uint32_t stage = 0, use = 0, issued = 0;  // of the ring
+      struct Ids {
+        int v[8];
+        int t;
+      };
+      int owner = -1, list_pages = a.max_blocks;
+      const int32_t* list = nullptr;
+      auto ask = [&](const Block& b, Ids& ids) {
+        if (b.owner != owner) {
+          owner = b.owner;
+          if (a.page_indptr) {
+            list = a.page_ids + a.page_indptr[owner];
+            list_pages = a.page_indptr[owner + 1] - a.page_indptr[owner];
           } else {
-            const uint32_t dst = sbase + kOffV + stage * kVStageBytes;
-            if (lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + stage), kVStageBytes);
-            for (int i = 0; i < subs / 2; ++i) {
-              const int r = __shfl_sync(0xffffffffu, row, part * (subs / 2) + i);
-              if (lane == 0)
-                for (int c = 0; c < 4; ++c)
-                  tma_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, bar(kBarVFull + stage),
-                              256 * static_cast<int>(half) + 64 * c, r);
-            }
-          }
-          ++issued;
-          if (++stage == static_cast<uint32_t>(scores ? kKStages : kVStages)) {
-            stage = 0;
-            use ^= 1u;
+            list = a.page_ids + static_cast<int64_t>(owner) * a.max_blocks;
           }
         }
+        ids.t = b.t0 + offset;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = ids.t + unit * i, j = t >> page_shift;
+          const bool in = i < subs && t < b.t0 + b.v1 && t + unit > b.t0 + b.v0;
+          ids.v[i] = !in ? kNone : j < list_pages ? list[j] : -1;
+        }
+      };
+      auto row_of = [&](const Ids& ids, int i) -> int {
+        const int id = ids.v[i];
+        if (id >= 0 && id < a.num_pages)
+          return layer_row0 + (id << page_shift) + ((ids.t + unit * i) & (a.page_size - 1));
+        if (id != kNone && scores) atomicOr(&hd->status, MLA_STATUS_BAD_PAGE);
+        return no_row;
+      };
+      for (int k = item0; k < item1 && ok; ++k) {
+        const ShItem it = items[k];
+        Walk w;
+        w.start(a, tiles[it.tile], it);
+        Ids ids, next, later;
+        ask(w.get(), ids);
+        if (w.more()) ask(w.get(), next);
+        for (int x = it.begin; x < it.end && ok; ++x) {
+          if (w.more()) ask(w.get(), later);
+          if (scores) {
+            int rows[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rows[i] = i < subs ? row_of(ids, i) : 0;
+#pragma unroll 1
+            for (int part = 0; part < kKParts; ++part) {
+              if (!(ok = mbar_spin(bar(kBarKFree + stage), use ^ 1u, abort_flag))) break;
+              const uint32_t dst = sbase + stage * kKStageBytes, full = lead(kBarKFull + stage);
+              if (half == 0) mbar_arrive_expect_tx(bar(kBarKFull + stage), 2 * kKStageBytes);
+              if (unit == 64) {
+                tma2_load_3d(dst, &p.chunks3, full, 0, rows[0], 3 * part);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (i < subs)
+                    for (int c = 0; c < 3; ++c)
+                      tma2_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, full, 64 * (3 * part + c), rows[i]);
+              }
+              ++issued;
+              if (++stage == kKStages) {
+                stage = 0;
+                use ^= 1u;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              if (!ok || !(ok = mbar_spin(bar(kBarVFree + stage), use ^ 1u, abort_flag))) break;
+              const uint32_t dst = sbase + kOffV + stage * kVStageBytes, full = bar(kBarVFull + stage);
+              mbar_arrive_expect_tx(full, kVStageBytes);
+              if (unit == 64) {
+                tma_load_3d(dst, &p.chunks4, full, 0, row_of(ids, part), 4 * static_cast<int>(half));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int j = i - part * (subs / 2);
+                  if (i < subs && j >= 0 && j < subs / 2) {
+                    const int r = row_of(ids, i);
+                    for (int c = 0; c < 4; ++c)
+                      tma_load_2d(dst + c * kChunk + j * unit * 128, &p.rows, full, 256 * static_cast<int>(half) + 64 * c, r);
+                  }
+                }
+              }
+              ++issued;
+              if (++stage == kVStages) {
+                stage = 0;
+                use ^= 1u;
+              }
+            }
+          }
+          ids = next;
+          next = later;
+        }
       }
-    }
-    if (!ok && lane == 0) fail();
-    if (*abort_flag && lane == 0 && (!scores || half == 0)) {  // let the copies in flight land (each wait bounded)
-      const uint32_t n = scores ? kKStages : kVStages;
-      for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i)
-        mbar_wait(bar((scores ? kBarKFull : kBarVFull) + i % n), (i / n) & 1u, nullptr);
+      if (!ok) fail();
+      if (*abort_flag && (!scores || half == 0)) {  // let the copies in flight land (each wait bounded)
+        const uint32_t n = scores ? kKStages : kVStages;
+        for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i)
+          mbar_wait(bar((scores ? kBarKFull : kBarVFull) + i % n), (i / n) & 1u, nullptr);
+      }
     }
   } else if (warp == kIssueWarp) {
     if (scores && half == 0 && elect_one()) {
@@ -290,7 +357,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
         const int blocks = items[k].end - items[k].begin;
-        ok = spin(bar(kBarQ), (k - item0) & 1u);
+        ok = spin_cluster(bar(kBarQ), (k - item0) & 1u);
         for (int x = 0; x < blocks && ok; ++x, ++n) {
           const uint32_t buf = n & 1u;
           if (!(ok = spin(bar(kBarSFree + buf), ((n >> 1) & 1u) ^ 1u))) break;
@@ -330,7 +397,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         ok = spin(bar(kBarOFree), ((k - item0) & 1u) ^ 1u);
         for (; w.more() && ok; ++n) {
           const Block b = w.get();
-          const uint32_t buf = n & 1u;
+          const uint32_t buf = n % kPBuffers;
           const bool all = b.row_lo == 0 && b.row_hi == tile.rows;
           uint32_t off[8];
 #pragma unroll
@@ -339,7 +406,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t below_hi = hi == 32 ? ~0u : (1u << hi) - 1u, below_lo = lo == 32 ? ~0u : (1u << lo) - 1u;
             off[i] = ~(below_hi & ~below_lo);
           }
-          if (!(ok = spin(bar(kBarPReady + buf), (n >> 1) & 1u))) break;
+          if (!(ok = spin_cluster(bar(kBarPReady + buf), (n / kPBuffers) & 1u))) break;
           tc_fence_after();
           const uint32_t pa = desc_lo(sbase + buf * kPBytes);
           const int k0 = b.v0 >> 4, k1 = (b.v1 + 15) >> 4;  // steps of 16 positions
@@ -358,76 +425,89 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             mma2_commit_to(bar(kBarVFree + stage), kAccPair);
             if (++stage == kVStages) stage = 0;
           }
-          mma2_commit_to(bar(kBarPFree + buf), kScorePair);
-          mma2_commit_to(bar(kBarPV), kAccPair);
+          mma2_commit_to(bar(kBarPFree + buf), kScorePair | kAccPair);
           if (!w.more()) mma2_commit_to(bar(kBarO), kAccPair);
         }
       }
       if (!ok) fail();
     }
-  } else if (scores && warp < 4) {
-    // Softmax: a row a thread.
-    const int lrow = 32 * warp + lane, r = 128 * static_cast<int>(half) + lrow;
-    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+  } else if (scores && warp < kWorkers) {
+    setmaxnreg_inc<kRegsWorker>();
+    // Softmax: a row a thread. The two groups of four warps take the even and the odd
+    // blocks, of their own buffers of S and P, so that one group's loads
+    // and waits hide behind the other's exponentials. A row's reference maximum goes from block to block through
+    // shared memory; each group has a sum of its own.
+    const int group = warp >> 2, quarter = warp & 3;
+    const int lrow = 32 * quarter + lane, r = 128 * static_cast<int>(half) + lrow;
+    const int w0 = r - lane;  // this warp's first row
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float scale = a.scale_log2, threshold = kRescaleThreshold / scale;
     const uint64_t scale2 = f2_make(scale, scale);
-    const uint32_t p_row = mapa(sbase, rank ^ 2) + lrow * 128, sw = lrow & 7;  // this row of the peer's P
+    const uint32_t sw = lrow & 7, tS = tbase + kColS + 128 * group;
+    const uint32_t p_here = sbase + kOffPOut + group * kPBytes;                    // P, and
+    const uint32_t p_there = mapa(sbase, rank ^ 2);                                // the peer's
     const uint32_t alpha_at = mapa(sbase + kOffAlpha, rank ^ 2) + 4 * lrow;
     const uint32_t stats_at = mapa(sbase + kOffStats, rank ^ 2) + 8 * lrow;
+    float* refs = reinterpret_cast<float*>(smem + kOffRef);
+    float2* sums = reinterpret_cast<float2*>(smem + kOffSum);
+    const uint32_t ref_mine = bar(kBarRef + 4 * group + quarter), ref_other = bar(kBarRef + 4 * (group ^ 1) + quarter);
+    // An item's queries, into place once the scores of the item before are complete: half a
+    // row a thread.
+    auto load_queries = [&](const ShTile& tile) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
+                                                        (static_cast<int64_t>(tile.row0) + r) * (kDimRow * 2));
+      const bool real = r < tile.rows;
+      uint4 rope[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rope[i] = real ? src[64 + 4 * group + i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = real ? src[32 * group + 8 * c + i] : make_uint4(0, 0, 0, 0);
+          v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+        }
+        tmem_st32(tbase + 128 * group + 32 * c, v);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st_shared_v4(sbase + kOffQRope + lrow * 128 + 16 * ((4 * group + i) ^ sw), rope[i].x, rope[i].y, rope[i].z, rope[i].w);
+      fence_proxy_async_smem();
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_release_cluster(lead(kBarQ));
+    };
     uint32_t n = 0;
     bool ok = true;
+    if (item0 < item1) load_queries(tiles[items[item0].tile]);
     for (int k = item0; k < item1 && ok; ++k) {
       const ShItem it = items[k];
       const ShTile tile = tiles[it.tile];
+      const int i = static_cast<int>((static_cast<int64_t>(tile.row0) + r) / a.num_heads) % a.q_len;
+      float ref = kNoMax, sum_ref = kNoMax, l = 0.f;
+      const uint32_t first = n, last = n + (it.end - it.begin) - 1;
       Walk w;
       w.start(a, tile, it);
-      // The queries, into place once the scores of the item before are complete (which the
-      // last of its blocks told).
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
-                                                          (static_cast<int64_t>(tile.row0) + r) * (kDimRow * 2));
-        const bool real = r < tile.rows;
-#pragma unroll 2
-        for (int c = 0; c < 8; ++c) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 x = real ? src[8 * c + i] : make_uint4(0, 0, 0, 0);
-            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
-          }
-          tmem_st32(tbase + 32 * c, v);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 x = real ? src[64 + i] : make_uint4(0, 0, 0, 0);
-          st_shared_v4(sbase + kOffQRope + lrow * 128 + 16 * (i ^ sw), x.x, x.y, x.z, x.w);
-        }
-        fence_proxy_async_smem();
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(lead(kBarQ));
-      }
-      const int i = static_cast<int>((static_cast<int64_t>(tile.row0) + r) / a.num_heads) % a.q_len;
-      float ref = kNoMax, l = 0.f;
-      for (; w.more(); ++n) {
+      for (; n <= last; ++n) {
         const Block b = w.get();
-        const uint32_t buf = n & 1u;
-        const int w0 = 128 * static_cast<int>(half) + 32 * warp;  // this warp's first row
+        if ((n & 1u) != static_cast<uint32_t>(group)) continue;
         const bool here = b.row_lo < w0 + 32 && b.row_hi > w0;
         const bool mine = r >= b.row_lo && r < b.row_hi;
-        if (!(ok = warp_wait(bar(kBarS + buf), (n >> 1) & 1u))) break;
+        if (!(ok = warp_wait(bar(kBarS + group), (n >> 1) & 1u))) break;
         tc_fence_after();
         float alpha = 1.f;
         uint32_t s[128];
+        float mx = -CUDART_INF_F;
         if (here) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tbase + kColS + 128 * buf + 32 * c, s + 32 * c);
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
           tmem_wait_ld();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead(kBarSFree + buf));
+        if (lane == 0) mbar_arrive_cluster(lead(kBarSFree + group));
         if (here) {
           const int b0 = mine ? b.v0 : kShTokens, e0 = mine ? min(b.v1, b.end + i) : 0;
           if (!__all_sync(0xffffffffu, b0 == 0 && e0 == kShTokens)) {
@@ -441,19 +521,27 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!(keep & (1u << c))) s[32 * g + c] = 0xff800000u;
             }
           }
-          float mx = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+          float mx1 = -CUDART_INF_F;
 #pragma unroll
           for (int c = 0; c < 128; c += 4) {
             mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
             mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
           }
           mx = fmaxf(mx, mx1);
-          if (mx > ref + threshold) {
-            alpha = exp2_approx((ref - mx) * scale);
-            l *= alpha;
-            ref = mx;
-            if (!b.add) alpha = 1.f;  // (nothing there to rescale)
-          }
+        }
+        // The reference from the block before, and on to the next.
+        if (n > 0 && !(ok = warp_wait_block(ref_other, ((n - 1) >> 1) & 1u))) break;
+        ref = n == first ? kNoMax : refs[lrow];
+        if (mx > ref + threshold) {
+          if (b.add) alpha = exp2_approx((ref - mx) * scale);  // (else nothing is there to rescale)
+          ref = mx;
+        }
+        refs[lrow] = ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ref_mine);
+        if (here) {
+          if (sum_ref != ref) l *= exp2_approx((sum_ref - ref) * scale);
+          sum_ref = ref;
           const float neg = -ref * scale;
           const uint64_t neg2 = f2_make(neg, neg);
           uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
@@ -470,24 +558,63 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           f2_split(sum2[1], s2, s3);
           l += (s0 + s1) + (s2 + s3);
         }
-        if (!(ok = warp_wait(bar(kBarPFree + buf), ((n >> 1) & 1u) ^ 1u))) break;
-        const uint32_t rb = peer(kBarP + buf);
+        // P leaves by way of this block's memory. (Stored row by row into the peer's it took
+        // 4,600 cycles; a copy runs beside everything else.)
+        if (!(ok = warp_wait(bar(kBarOutFree + group), ((n >> 1) & 1u) ^ 1u))) break;
         if (here) {
-          const uint32_t dst = p_row + buf * kPBytes;
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            st_async_v4(dst + (c >> 3) * kPChunk + 16 * ((c & 7) ^ sw), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3], rb);
-          st_async_b32(alpha_at + 512 * buf, __float_as_uint(alpha), rb);
+            st_shared_v4(p_here + (c >> 3) * kPChunk + lrow * 128 + 16 * ((c & 7) ^ sw), s[4 * c], s[4 * c + 1], s[4 * c + 2],
+                         s[4 * c + 3]);
+          fence_proxy_async_smem();
         }
-        if (lane == 0) mbar_arrive_expect_tx_cluster(rb, here ? 32 * (256 + 4) : 0);
+        __syncwarp();
+        if (n == last && k + 1 < item1) load_queries(tiles[items[k + 1].tile]);
+        const uint32_t buf = n % kPBuffers, rb = peer(kBarP + buf);
+        if (!(ok = warp_wait(bar(kBarPFree + buf), ((n / kPBuffers) & 1u) ^ 1u))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx_relaxed(rb, here ? 32 * (256 + 4) : 0);
+          if (here) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              bulk_copy_to(p_there + buf * kPBytes + c * kPChunk + 32 * quarter * 128, p_here + c * kPChunk + 32 * quarter * 128,
+                           32 * 128, rb);
+          }
+        }
+        if (here) st_async_b32(alpha_at + 512 * buf, __float_as_uint(alpha), rb);
       }
       if (!ok) break;
+      // The queries of the next item (the last scores are the other group's); then the row's
+      // maximum and sum, from the group of the last block. (Every warp waits for each item's
+      // phase, so that none takes one for the next but one.)
+      const bool mine_last = (last & 1u) == static_cast<uint32_t>(group);
+      // (one group may be done with the next item's blocks before the other reads this one's
+      // sum, but no further: their blocks alternate)
+      const int odd = (k - item0) & 1;
+      float2* sum = sums + 128 * odd + lrow;
+      const uint32_t sum_bar = bar(kBarSum + 4 * odd + quarter);
+      if (!mine_last) {
+        if (!(ok = warp_wait(bar(kBarS + (last & 1u)), (last >> 1) & 1u))) break;
+        *sum = make_float2(sum_ref, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sum_bar);
+        tc_fence_after();
+        if (k + 1 < item1) load_queries(tiles[items[k + 1].tile]);
+      }
       if (!(ok = warp_wait(bar(kBarStatsFree), ((k - item0) & 1u) ^ 1u))) break;
-      st_async_v2(stats_at, __float_as_uint(ref * scale), __float_as_uint(l), peer(kBarStats));
-      if (lane == 0) mbar_arrive_expect_tx_cluster(peer(kBarStats), 32 * 8);
+      if (mine_last) {
+        if (!(ok = warp_wait_block(sum_bar, ((k - item0) >> 1) & 1u))) break;
+        const float2 other = *sum;
+        if (sum_ref != ref) l *= exp2_approx((sum_ref - ref) * scale);
+        if (other.x != ref) l = fmaf(other.y, exp2_approx((other.x - ref) * scale), l);
+        else l += other.y;
+        st_async_v2(stats_at, __float_as_uint(ref * scale), __float_as_uint(l), peer(kBarStats));
+        if (lane == 0) mbar_arrive_expect_tx_relaxed(peer(kBarStats), 32 * 8);
+      }
     }
     if (!ok) fail();
   } else if (!scores && warp < kWorkers) {
+    setmaxnreg_inc<kRegsWorker>();
     // Accumulators: the warps of a quarter of the lanes have half of the columns each.
     const int lrow = 32 * (warp & 3) + lane, r = 128 * static_cast<int>(half) + lrow, side = warp >> 2;
     const uint32_t tO = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256 * side;
@@ -502,14 +629,50 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       w.start(a, tile, it);
       for (; w.more(); ++n) {
         const Block b = w.get();
-        const uint32_t buf = n & 1u;
+        const uint32_t buf = n % kPBuffers;
         const int w0 = r - lane;
         const bool here = b.row_lo < w0 + 32 && b.row_hi > w0;
-        if (!(ok = warp_wait(bar(kBarP + buf), (n >> 1) & 1u))) break;
+        // Rows of V outside the segment, among the 16 at its ends that are multiplied, and
+        // positions that only later queries of a request see: an infinity or NaN there would
+        // reach the others through a weight of zero. (Those that see it have it in their
+        // scores.)
+        bool wrote = false;
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (!(ok = warp_wait_block(bar(kBarVFull + stage), use))) break;
+          const uint32_t v = sbase + kOffV + stage * kVStageBytes;
+          const int lo0 = (b.v0 & ~15) - 64 * h, lo1 = b.v0 - 64 * h, hi0 = b.v1 - 64 * h, hi1 = ((b.v1 + 15) & ~15) - 64 * h;
+          auto zero = [&](int from, int to) {  // 512 bytes a row: a warp each
+            for (int t = max(from, 0) + warp; t < min(to, 64); t += kWorkers) {
+              st_shared_v4(v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7), 0, 0, 0, 0);
+              wrote = true;
+            }
+          };
+          if (b.v0 & 15) zero(lo0, lo1);
+          if (b.v1 & 15) zero(hi0, hi1);
+          for (int t = max(b.end - 64 * h, 0) + warp; t < min(hi0, 64); t += kWorkers) {
+            const uint32_t at = v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7);
+            uint32_t x[4];
+            ld_shared_v4(at, x[0], x[1], x[2], x[3]);
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+            if (__any_sync(0xffffffffu, odd)) {
+              st_shared_v4(at, 0, 0, 0, 0);
+              wrote = true;
+            }
+          }
+          if (++stage == kVStages) {
+            stage = 0;
+            use ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (wrote) fence_proxy_async_smem();
+        if (!(ok = warp_wait_cluster(bar(kBarP + buf), (n / kPBuffers) & 1u))) break;
+        if (threadIdx.x == 0) mbar_arrive_remote_relaxed(peer(kBarOutFree + (n & 1u)));
         const float alpha = here ? alphas[128 * buf + lrow] : 1.f;
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
-          // (the weights of this block have come, so the product of block n - 2 is complete)
-          if (!(ok = warp_wait(bar(kBarPV), (n - 1) & 1u))) break;
+          if (!(ok = warp_wait(bar(kBarPFree + (n - 1) % kPBuffers), ((n - 1) / kPBuffers) & 1u))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
@@ -522,42 +685,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        for (int h = 0; h < 2 && ok; ++h) {
-          if (!(ok = warp_wait(bar(kBarVFull + stage), use))) break;
-          // Rows of V outside the segment, among the 16 at its ends that are multiplied.
-          const uint32_t v = sbase + kOffV + stage * kVStageBytes;
-          const int lo0 = (b.v0 & ~15) - 64 * h, lo1 = b.v0 - 64 * h, hi0 = b.v1 - 64 * h, hi1 = ((b.v1 + 15) & ~15) - 64 * h;
-          auto zero = [&](int from, int to) {  // 512 bytes a row: a warp each
-            for (int t = max(from, 0) + warp; t < min(to, 64); t += kWorkers)
-              st_shared_v4(v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7), 0, 0, 0, 0);
-          };
-          if (b.v0 & 15) zero(lo0, lo1);
-          if (b.v1 & 15) zero(hi0, hi1);
-          // Positions that only later queries of a request see: an infinity or NaN there
-          // would reach the others through a weight of zero. (Those that see it have it in
-          // their scores.)
-          for (int t = max(b.end - 64 * h, 0) + warp; t < min(hi0, 64); t += kWorkers) {
-            const uint32_t at = v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7);
-            uint32_t x[4];
-            ld_shared_v4(at, x[0], x[1], x[2], x[3]);
-            bool odd = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) odd |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
-            if (__any_sync(0xffffffffu, odd)) st_shared_v4(at, 0, 0, 0, 0);
-          }
-          if (++stage == kVStages) {
-            stage = 0;
-            use ^= 1u;
-          }
-        }
-        if (!ok) break;
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(lead(kBarPReady + buf));
+        // (a release at the cluster's scope takes 1,700 cycles: only for what was written to V)
+        if (lane == 0) {
+          if (wrote) mbar_arrive_release_cluster(lead(kBarPReady + buf));
+          else mbar_arrive_cluster(lead(kBarPReady + buf));
+        }
       }
       if (!ok) break;
-      if (!(ok = warp_wait(bar(kBarStats), (k - item0) & 1u))) break;
+      if (!(ok = warp_wait_cluster(bar(kBarStats), (k - item0) & 1u))) break;
       const float2 ml = stats[lrow];
       if (!(ok = warp_wait(bar(kBarO), (k - item0) & 1u))) break;
       tc_fence_after();
@@ -642,13 +779,15 @@ int shared_max_active_clusters() {
   return cached[dev] = n;
 }
 
-cudaError_t launch_shared_decode(const CUtensorMap& rows, const ShDecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_shared_decode(const CUtensorMap (&maps)[3], const ShDecodeArgs& a, cudaStream_t stream) {
   if (a.dtype == MLA_DTYPE_FP8_E4M3) return launch_shared_rows(a, stream);
   static bool attr_set[kMaxDevices] = {};
   const cudaError_t e = set_smem_once(shared_decode_kernel, kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
   Params p;
-  p.rows = rows;
+  p.rows = maps[0];
+  p.chunks3 = maps[1];
+  p.chunks4 = maps[2];
   p.a = a;
   return launch_pdl(shared_decode_kernel, dim3(kShClusterBlocks * a.clusters), dim3(kThreads), kSmemBytes, stream, p);
 }
