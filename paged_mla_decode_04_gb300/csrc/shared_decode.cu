@@ -44,23 +44,22 @@ constexpr int kRegsWorker = 208, kRegsOther = 88;
 static_assert(2 * kRegsWorker + kRegsOther == 3 * 168, "register split");
 constexpr int kChunk = 64 * 128;            // [64 positions][64 dims]
 // Scores' pair: K in stages of three chunks (192 dims), three stages a block.
-constexpr int kKStages = 5, kKStageBytes = 3 * kChunk, kKParts = 3;
+constexpr int kKStages = 6, kKStageBytes = 3 * kChunk, kKParts = 3;
 constexpr int kOffQRope = kKStages * kKStageBytes;  // [128 rows][64 dims]
 // Accumulators' pair: P of 128 rows, two chunks of 64 positions; V in stages of 64
 // positions, four chunks (256 dims).
 constexpr int kPChunk = 128 * 128, kPBytes = 2 * kPChunk, kPBuffers = 3;
 constexpr int kOffV = kPBuffers * kPBytes;
-constexpr int kVStages = 3, kVStageBytes = 4 * kChunk;
-constexpr int kOffPOut = kOffQRope + 128 * 128;  // P on its way to the other pair
-constexpr int kOffSmall = kOffPOut + 2 * kPBytes;
-static_assert(kOffV + kVStages * kVStageBytes <= kOffSmall, "both pairs' buffers end before the small ones");
-constexpr int kOffAlpha = kOffSmall;                        // float [buffers][128]
+constexpr int kVStages = 4, kVStageBytes = 4 * kChunk;
+constexpr int kOffAlpha = kOffV + kVStages * kVStageBytes;  // float [kPBuffers][128]
 constexpr int kOffStats = kOffAlpha + kPBuffers * 128 * 4;  // float2 [128]
-// Scores' pair: each row's reference maximum, as the block before left it; the sum and
-// reference of the group that an item's last block is not of.
-constexpr int kOffRef = kOffStats + 128 * 8;                // float [128]
+// Scores' pair: P on its way to the other; each row's reference maximum, as the block
+// before left it; the sum and reference of the group that an item's last block is not of.
+constexpr int kOffPOut = kOffQRope + 128 * 128;
+constexpr int kOffRef = kOffPOut + 2 * kPBytes;             // float [128]
 constexpr int kOffSum = kOffRef + 128 * 4;                  // float2 [2 items][128]
-constexpr int kOffBar = kOffSum + 2 * 128 * 8;
+constexpr int kOffBar = kOffStats + 128 * 8;
+static_assert(kOffSum + 2 * 128 * 8 <= kOffBar, "both pairs' buffers end before the barriers");
 
 enum {
   // In the scores' pair. (Of its first block: K landed, Q in place, S read.)
@@ -85,7 +84,8 @@ enum {
   kNumBars = kBarOFree + 1
 };
 
-constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 16 + 1024;
+// (all that a block may have: its start has to be at a multiple of 1,024, see the kernel)
+constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 8;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr uint32_t kColS = 256;             // + 128 a buffer; Q from 0
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
@@ -158,9 +158,8 @@ struct Params {
 
 __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     shared_decode_kernel(const __grid_constant__ Params p) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const ShDecodeArgs& a = p.a;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
   const uint32_t bar0 = sbase + kOffBar;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8u * i; };
@@ -223,7 +222,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     return true;
   };
   const int cluster = blockIdx.x >> 2;
-  const bool planned = sh_planned(hd, a);
+  // (Buffers at another start than the tensor core's patterns ask for: never seen; nothing is
+  // computed then, and the status tells.)
+  const bool planned = sh_planned(hd, a) && (sbase & 1023u) == 0;
   if (!planned && threadIdx.x == 0 && rank == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
   const int* cstart = reinterpret_cast<const int*>(a.ws + a.lay.cluster_start);
   const ShItem* items = reinterpret_cast<const ShItem*>(a.ws + a.lay.items);
@@ -406,7 +407,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t below_hi = hi == 32 ? ~0u : (1u << hi) - 1u, below_lo = lo == 32 ? ~0u : (1u << lo) - 1u;
             off[i] = ~(below_hi & ~below_lo);
           }
-          if (!(ok = spin_cluster(bar(kBarPReady + buf), (n / kPBuffers) & 1u))) break;
+          // (Acquiring at the cluster's scope takes 2,000 cycles here: only where the peer's
+          // threads wrote to V. What else they announce are copies that have landed and
+          // accumulators, which tcgen05 fences order.)
+          const bool edge = (b.v0 & 15) || (b.v1 & 15) || b.end < b.v1;
+          if (!(ok = edge ? spin_cluster(bar(kBarPReady + buf), (n / kPBuffers) & 1u)
+                          : spin(bar(kBarPReady + buf), (n / kPBuffers) & 1u)))
+            break;
           tc_fence_after();
           const uint32_t pa = desc_lo(sbase + buf * kPBytes);
           const int k0 = b.v0 >> 4, k1 = (b.v1 + 15) >> 4;  // steps of 16 positions
