@@ -67,4 +67,11 @@ __device__ __forceinline__ void st_async_v2(uint32_t addr, uint32_t a, uint32_t 
                : "memory");
 }
 
+// 32-byte vector load from global memory.
+__device__ __forceinline__ void ld_global_v8(const void* ptr, uint32_t* v) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(ptr));
+}
+
 }  // namespace mla

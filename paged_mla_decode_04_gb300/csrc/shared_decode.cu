@@ -37,14 +37,14 @@ namespace mla {
 namespace {
 
 constexpr int kWorkers = 8;                 // warps of softmax or accumulators, two groups of four
-constexpr int kProducerWarp = kWorkers, kIssueWarp = kWorkers + 1;
-constexpr int kThreads = 384;               // (the last two warps idle)
+constexpr int kProducerWarp = kWorkers, kIssueWarp = kWorkers + 1, kSendWarp = kWorkers + 2;
+constexpr int kThreads = 384;
 // Registers a thread after setmaxnreg; they add up to the launch's 3 x 168.
 constexpr int kRegsWorker = 208, kRegsOther = 88;
 static_assert(2 * kRegsWorker + kRegsOther == 3 * 168, "register split");
 constexpr int kChunk = 64 * 128;            // [64 positions][64 dims]
 // Scores' pair: K in stages of three chunks (192 dims), three stages a block.
-constexpr int kKStages = 6, kKStageBytes = 3 * kChunk, kKParts = 3;
+constexpr int kKStages = 5, kKStageBytes = 3 * kChunk, kKParts = 3;
 constexpr int kOffQRope = kKStages * kKStageBytes;  // [128 rows][64 dims]
 // Accumulators' pair: P of 128 rows, two chunks of 64 positions; V in stages of 64
 // positions, four chunks (256 dims).
@@ -58,8 +58,9 @@ constexpr int kOffStats = kOffAlpha + kPBuffers * 128 * 4;  // float2 [128]
 constexpr int kOffPOut = kOffQRope + 128 * 128;
 constexpr int kOffRef = kOffPOut + 2 * kPBytes;             // float [128]
 constexpr int kOffSum = kOffRef + 128 * 4;                  // float2 [2 items][128]
+constexpr int kOffAlphaOut = kOffSum + 2 * 128 * 8;         // float [2 groups][128]
 constexpr int kOffBar = kOffStats + 128 * 8;
-static_assert(kOffSum + 2 * 128 * 8 <= kOffBar, "both pairs' buffers end before the barriers");
+static_assert(kOffAlphaOut + 2 * 512 <= kOffBar, "both pairs' buffers end before the barriers");
 
 enum {
   // In the scores' pair. (Of its first block: K landed, Q in place, S read.)
@@ -68,7 +69,8 @@ enum {
   kBarQ = kBarKFree + kKStages,
   kBarS = kBarQ + 1,                   // [2] scores complete
   kBarSFree = kBarS + 2,               // [2]
-  kBarOutFree = kBarSFree + 2,         // [2 groups] P has left
+  kBarStaged = kBarSFree + 2,          // [2 groups] P is ready to leave
+  kBarOutFree = kBarStaged + 2,        // [2 groups] P has left
   kBarPFree = kBarOutFree + 2,         // [kPBuffers] P multiplied (in both pairs)
   kBarStatsFree = kBarPFree + kPBuffers,
   kBarRef = kBarStatsFree + 1,         // [2 groups][4 warps] the reference is there
@@ -104,36 +106,28 @@ struct Block {
   bool add;            // to what these rows have already
 };
 
-// Walks a tile's blocks [begin, end), a segment ahead in what it has loaded.
+// Walks an item's blocks, a segment ahead in what it has loaded.
 struct Walk {
   const ShSegment* segs;
   ShSegment s, next;
-  int k, count, x, end, begin, prefix_end;
-  __device__ __forceinline__ void start(const ShDecodeArgs& a, const ShTile& tile, const ShItem& it) {
-    segs = reinterpret_cast<const ShSegment*>(a.ws + a.lay.segs) + tile.seg0;
-    count = tile.segs;
+  int k, last, x, end, begin;
+  bool with_prefix;  // the item has blocks of the prefix
+  __device__ __forceinline__ void start(const ShDecodeArgs& a, const ShItem& it) {
+    segs = reinterpret_cast<const ShSegment*>(a.ws + a.lay.segs);
+    k = it.seg;
+    last = it.seg_last;
     x = begin = it.begin;
     end = it.end;
-    // (a tile of several segments: the first is the prefix if all rows have it)
-    int lo = 0, hi = count;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (segs[mid].block0 <= x) lo = mid;
-      else hi = mid;
-    }
-    k = lo;
-    s = segs[k];
-    const ShSegment first = segs[0];
-    prefix_end = first.base == first.tok_hi ? blocks(first) : 0;
-    next = segs[min(k + 1, count - 1)];
+    with_prefix = it.begin < it.prefix_end;
+    s = it.first;
+    next = segs[min(k + 1, last)];
   }
-  __device__ static __forceinline__ int blocks(const ShSegment& g) { return (g.tok_hi - g.tok0 + kShTokens - 1) / kShTokens; }
   __device__ __forceinline__ bool more() const { return x < end; }
   __device__ __forceinline__ Block get() {
-    if (k + 1 < count && x >= next.block0) {
+    if (k < last && x >= next.block0) {
       s = next;
       ++k;
-      next = segs[min(k + 1, count - 1)];
+      next = segs[min(k + 1, last)];
     }
     Block b;
     b.owner = s.owner;
@@ -143,11 +137,33 @@ struct Walk {
     b.row_lo = s.row_lo;
     b.row_hi = s.row_hi;
     b.end = s.base + 1 - b.t0;
-    b.add = x > max(s.block0, begin) || (k > 0 && begin < prefix_end);
+    // (rows of a request's own blocks have the prefix's before them, where the item has)
+    b.add = x > max(s.block0, begin) || (with_prefix && s.base != s.tok_hi);
     ++x;
     return b;
   }
 };
+
+// Four lanes' 128 bytes each, as four pieces of 32, transposed: piece j of lane i becomes
+// piece i of lane j. A lane that has 128 bytes of its own row reads and writes global memory
+// by way of this, so that an access covers eight whole lines (as the rows lie it is pieces of
+// 32: an item's queries took 4.6 us to come in and its results 6 to 8 to go out).
+__device__ __forceinline__ void turn(uint32_t* o, int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int pair = 0; pair < 2; ++pair) {
+      const int lo = d == 1 ? 16 * pair : 8 * pair, hi = lo + 8 * d;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? o[lo + e] : o[hi + e], d);
+        if (up) o[lo + e] = got;
+        else o[hi + e] = got;
+      }
+    }
+  }
+}
 
 struct Params {
   CUtensorMap rows;  // the pool as [rows][576], box {64, positions of a copy}
@@ -176,7 +192,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       int count = 1;
       if (i == kBarQ) count = 2 * kWorkers;
       if (i >= kBarSFree && i < kBarSFree + 2) count = 8;                       // a group of both blocks
-      if (i >= kBarP && i < kBarP + kPBuffers) count = 4;                               // a group of one
+      if (i >= kBarStaged && i < kBarStaged + 2) count = 4;                     // a group of one
       if (i == kBarStats) count = 4;
       if (i >= kBarPReady && i < kBarPReady + kPBuffers) count = 2 * kWorkers;
       if (i == kBarOFree) count = 2 * kWorkers;
@@ -228,7 +244,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   if (!planned && threadIdx.x == 0 && rank == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
   const int* cstart = reinterpret_cast<const int*>(a.ws + a.lay.cluster_start);
   const ShItem* items = reinterpret_cast<const ShItem*>(a.ws + a.lay.items);
-  const ShTile* tiles = reinterpret_cast<const ShTile*>(a.ws + a.lay.tiles);
   int item0 = 0, item1 = 0;
   if (planned && cluster < hd->num_clusters) {
     item0 = cstart[cluster];
@@ -283,7 +298,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       for (int k = item0; k < item1 && ok; ++k) {
         const ShItem it = items[k];
         Walk w;
-        w.start(a, tiles[it.tile], it);
+        w.start(a, it);
         Ids ids, next, later;
         ask(w.get(), ids);
         if (w.more()) ask(w.get(), next);
@@ -350,6 +365,37 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_wait(bar((scores ? kBarKFull : kBarVFull) + i % n), (i / n) & 1u, nullptr);
       }
     }
+  } else if (warp >= kSendWarp) {
+    // One lane for each group of softmax warps sends P to the other pair, rows that attend the
+    // block alone, so that no softmax warp waits for a buffer there. (Stored row by row into
+    // the peer's memory by the softmax warps it took them 4,600 cycles a block.)
+    if (scores && lane == 0) {
+      const uint32_t group = warp - kSendWarp, there = mapa(sbase, rank ^ 2);
+      uint32_t n = 0;
+      bool ok = true;
+      for (int k = item0; k < item1 && ok; ++k) {
+        const ShItem it = items[k];
+        Walk w;
+        w.start(a, it);
+        for (; w.more(); ++n) {
+          const Block b = w.get();
+          if ((n & 1u) != group) continue;
+          const int lo = max(b.row_lo - 128 * static_cast<int>(half), 0), hi = min(b.row_hi - 128 * static_cast<int>(half), 128);
+          const uint32_t buf = n % kPBuffers, rb = peer(kBarP + buf);
+          if (!(ok = spin(bar(kBarStaged + group), (n >> 1) & 1u))) break;
+          if (!(ok = spin(bar(kBarPFree + buf), ((n / kPBuffers) & 1u) ^ 1u))) break;
+          mbar_arrive_expect_tx_relaxed(rb, hi > lo ? (hi - lo) * 256 + 512 : 0);
+          if (hi > lo) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              bulk_copy_to(there + buf * kPBytes + c * kPChunk + lo * 128, sbase + kOffPOut + group * kPBytes + c * kPChunk + lo * 128,
+                           (hi - lo) * 128, rb);
+            bulk_copy_to(there + kOffAlpha + 512 * buf, sbase + kOffAlphaOut + 512 * group, 512, rb);
+          }
+        }
+      }
+      if (!ok) fail();
+    }
   } else if (warp == kIssueWarp) {
     if (scores && half == 0 && elect_one()) {
       constexpr uint32_t idesc = idesc_bf16(256, kShTokens, false, false);
@@ -392,14 +438,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
         const ShItem it = items[k];
-        const ShTile tile = tiles[it.tile];
         Walk w;
-        w.start(a, tile, it);
+        w.start(a, it);
         ok = spin(bar(kBarOFree), ((k - item0) & 1u) ^ 1u);
         for (; w.more() && ok; ++n) {
           const Block b = w.get();
           const uint32_t buf = n % kPBuffers;
-          const bool all = b.row_lo == 0 && b.row_hi == tile.rows;
+          const bool all = b.row_lo == 0 && b.row_hi == it.rows;
           uint32_t off[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -451,52 +496,101 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     const float scale = a.scale_log2, threshold = kRescaleThreshold / scale;
     const uint64_t scale2 = f2_make(scale, scale);
     const uint32_t sw = lrow & 7, tS = tbase + kColS + 128 * group;
-    const uint32_t p_here = sbase + kOffPOut + group * kPBytes;                    // P, and
-    const uint32_t p_there = mapa(sbase, rank ^ 2);                                // the peer's
-    const uint32_t alpha_at = mapa(sbase + kOffAlpha, rank ^ 2) + 4 * lrow;
+    const uint32_t p_here = sbase + kOffPOut + group * kPBytes + lrow * 128;  // this row of P
+    float* alpha_here = reinterpret_cast<float*>(smem + kOffAlphaOut) + 128 * group + lrow;
     const uint32_t stats_at = mapa(sbase + kOffStats, rank ^ 2) + 8 * lrow;
     float* refs = reinterpret_cast<float*>(smem + kOffRef);
     float2* sums = reinterpret_cast<float2*>(smem + kOffSum);
     const uint32_t ref_mine = bar(kBarRef + 4 * group + quarter), ref_other = bar(kBarRef + 4 * (group ^ 1) + quarter);
-    // An item's queries, into place once the scores of the item before are complete: half a
-    // row a thread.
-    auto load_queries = [&](const ShTile& tile) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
-                                                        (static_cast<int64_t>(tile.row0) + r) * (kDimRow * 2));
-      const bool real = r < tile.rows;
-      uint4 rope[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) rope[i] = real ? src[64 + 4 * group + i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 x = real ? src[32 * group + 8 * c + i] : make_uint4(0, 0, 0, 0);
-          v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
-        }
-        tmem_st32(tbase + 128 * group + 32 * c, v);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        st_shared_v4(sbase + kOffQRope + lrow * 128 + 16 * ((4 * group + i) ^ sw), rope[i].x, rope[i].y, rope[i].z, rope[i].w);
-      fence_proxy_async_smem();
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_release_cluster(lead(kBarQ));
-    };
-    uint32_t n = 0;
+    uint32_t n = 0, last = 0;
+    float ref = kNoMax, sum_ref = kNoMax, l = 0.f;
     bool ok = true;
-    if (item0 < item1) load_queries(tiles[items[item0].tile]);
-    for (int k = item0; k < item1 && ok; ++k) {
-      const ShItem it = items[k];
-      const ShTile tile = tiles[it.tile];
-      const int i = static_cast<int>((static_cast<int64_t>(tile.row0) + r) / a.num_heads) % a.q_len;
-      float ref = kNoMax, sum_ref = kNoMax, l = 0.f;
-      const uint32_t first = n, last = n + (it.end - it.begin) - 1;
+    for (int k = item0 - 1; ok; ++k) {
+      // The next item's queries, into place once the scores of this one are complete (which a
+      // group's last block tells, or a wait for the other's): half a row's c_kv dims a thread.
+      const bool mine_last = (last & 1u) == static_cast<uint32_t>(group);
+      if (k >= item0 && !mine_last) {
+        if (!(ok = warp_wait(bar(kBarS + (last & 1u)), (last >> 1) & 1u))) break;
+        tc_fence_after();
+      }
+      if (k + 1 < item1) {
+        const int row0 = items[k + 1].row0, rows = items[k + 1].rows;
+        const uint8_t* src = static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(row0) + w0) * (kDimRow * 2);
+        uint4 rope[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the rope dims: 16 bytes of row 8 i + lane / 4
+          const int row = 8 * i + (lane >> 2);
+          rope[i] = make_uint4(0, 0, 0, 0);
+          if (w0 + row < rows)
+            rope[i] = *reinterpret_cast<const uint4*>(src + row * (kDimRow * 2) + 2 * kDimCkv + 64 * group + 16 * (lane & 3));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[64];  // 256 bytes of a row, in two turns
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = (lane & 28) + i;
+              uint32_t* v = x + 32 * c + 8 * i;
+              if (w0 + row < rows) {
+                ld_global_v8(src + row * (kDimRow * 2) + 512 * group + 256 * h + 128 * c + 32 * (lane & 3), v);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0;
+              }
+            }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            turn(x + 32 * c, lane);
+            tmem_st32(tbase + 128 * group + 64 * h + 32 * c, x + 32 * c);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * i + (lane >> 2);
+          st_shared_v4(sbase + kOffQRope + (32 * quarter + row) * 128 + 16 * ((4 * group + (lane & 3)) ^ (row & 7)), rope[i].x,
+                       rope[i].y, rope[i].z, rope[i].w);
+        }
+        fence_proxy_async_smem();
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(lead(kBarQ));
+      }
+      if (k >= item0) {
+        // The row's maximum and sum, from the group of the last block. (Every warp waits for
+        // each item's phase, so that none takes one for the next but one. One group may be done
+        // with the next item's blocks before the other reads this one's sum, but no further:
+        // their blocks alternate.)
+        const int odd = (k - item0) & 1;
+        float2* sum = sums + 128 * odd + lrow;
+        const uint32_t sum_bar = bar(kBarSum + 4 * odd + quarter);
+        if (!mine_last) {
+          *sum = make_float2(sum_ref, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sum_bar);
+        }
+        if (!(ok = warp_wait(bar(kBarStatsFree), ((k - item0) & 1u) ^ 1u))) break;
+        if (mine_last) {
+          if (!(ok = warp_wait_block(sum_bar, ((k - item0) >> 1) & 1u))) break;
+          const float2 other = *sum;
+          if (sum_ref != ref) l *= exp2_approx((sum_ref - ref) * scale);
+          if (other.x != ref) l = fmaf(other.y, exp2_approx((other.x - ref) * scale), l);
+          else l += other.y;
+          st_async_v2(stats_at, __float_as_uint(ref * scale), __float_as_uint(l), peer(kBarStats));
+          if (lane == 0) mbar_arrive_expect_tx_relaxed(peer(kBarStats), 32 * 8);
+        }
+      }
+      if (k + 1 >= item1) break;
+      const ShItem it = items[k + 1];
+      const int i = static_cast<int>((static_cast<int64_t>(it.row0) + r) / a.num_heads) % a.q_len;
+      ref = sum_ref = kNoMax;
+      l = 0.f;
+      const uint32_t first = n;
+      last = n + (it.end - it.begin) - 1;
       Walk w;
-      w.start(a, tile, it);
+      w.start(a, it);
       for (; n <= last; ++n) {
         const Block b = w.get();
         if ((n & 1u) != static_cast<uint32_t>(group)) continue;
@@ -565,58 +659,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           f2_split(sum2[1], s2, s3);
           l += (s0 + s1) + (s2 + s3);
         }
-        // P leaves by way of this block's memory. (Stored row by row into the peer's it took
-        // 4,600 cycles; a copy runs beside everything else.)
+        // P leaves by way of this block's memory, with the factor of each row.
         if (!(ok = warp_wait(bar(kBarOutFree + group), ((n >> 1) & 1u) ^ 1u))) break;
         if (here) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            st_shared_v4(p_here + (c >> 3) * kPChunk + lrow * 128 + 16 * ((c & 7) ^ sw), s[4 * c], s[4 * c + 1], s[4 * c + 2],
-                         s[4 * c + 3]);
-          fence_proxy_async_smem();
+            st_shared_v4(p_here + (c >> 3) * kPChunk + 16 * ((c & 7) ^ sw), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
         }
+        *alpha_here = alpha;
+        fence_proxy_async_smem();
         __syncwarp();
-        if (n == last && k + 1 < item1) load_queries(tiles[items[k + 1].tile]);
-        const uint32_t buf = n % kPBuffers, rb = peer(kBarP + buf);
-        if (!(ok = warp_wait(bar(kBarPFree + buf), ((n / kPBuffers) & 1u) ^ 1u))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx_relaxed(rb, here ? 32 * (256 + 4) : 0);
-          if (here) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              bulk_copy_to(p_there + buf * kPBytes + c * kPChunk + 32 * quarter * 128, p_here + c * kPChunk + 32 * quarter * 128,
-                           32 * 128, rb);
-          }
-        }
-        if (here) st_async_b32(alpha_at + 512 * buf, __float_as_uint(alpha), rb);
-      }
-      if (!ok) break;
-      // The queries of the next item (the last scores are the other group's); then the row's
-      // maximum and sum, from the group of the last block. (Every warp waits for each item's
-      // phase, so that none takes one for the next but one.)
-      const bool mine_last = (last & 1u) == static_cast<uint32_t>(group);
-      // (one group may be done with the next item's blocks before the other reads this one's
-      // sum, but no further: their blocks alternate)
-      const int odd = (k - item0) & 1;
-      float2* sum = sums + 128 * odd + lrow;
-      const uint32_t sum_bar = bar(kBarSum + 4 * odd + quarter);
-      if (!mine_last) {
-        if (!(ok = warp_wait(bar(kBarS + (last & 1u)), (last >> 1) & 1u))) break;
-        *sum = make_float2(sum_ref, l);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sum_bar);
-        tc_fence_after();
-        if (k + 1 < item1) load_queries(tiles[items[k + 1].tile]);
-      }
-      if (!(ok = warp_wait(bar(kBarStatsFree), ((k - item0) & 1u) ^ 1u))) break;
-      if (mine_last) {
-        if (!(ok = warp_wait_block(sum_bar, ((k - item0) >> 1) & 1u))) break;
-        const float2 other = *sum;
-        if (sum_ref != ref) l *= exp2_approx((sum_ref - ref) * scale);
-        if (other.x != ref) l = fmaf(other.y, exp2_approx((other.x - ref) * scale), l);
-        else l += other.y;
-        st_async_v2(stats_at, __float_as_uint(ref * scale), __float_as_uint(l), peer(kBarStats));
-        if (lane == 0) mbar_arrive_expect_tx_relaxed(peer(kBarStats), 32 * 8);
+        if (lane == 0) mbar_arrive(bar(kBarStaged + group));
       }
     }
     if (!ok) fail();
@@ -631,9 +684,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int k = item0; k < item1 && ok; ++k) {
       const ShItem it = items[k];
-      const ShTile tile = tiles[it.tile];
       Walk w;
-      w.start(a, tile, it);
+      w.start(a, it);
       for (; w.more(); ++n) {
         const Block b = w.get();
         const uint32_t buf = n % kPBuffers;
@@ -705,34 +757,42 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       const float2 ml = stats[lrow];
       if (!(ok = warp_wait(bar(kBarO), (k - item0) & 1u))) break;
       tc_fence_after();
-      const bool real = r < tile.rows;
-      const int64_t out_row = static_cast<int64_t>(tile.row0) + r;
+      const bool real = r < it.rows;
+      const int64_t out_row = static_cast<int64_t>(it.row0) + r;
       const int64_t part_row = static_cast<int64_t>(it.part) * kShRows + r;
       const bool part = it.part >= 0;
-      const float inv = part ? 1.f : a.out_scale / ml.y;
       // (a piece without a position of the row: its accumulator was never begun)
       const bool store = real && !(part && ml.y == 0.f);
+      const uint32_t stores = __ballot_sync(0xffffffffu, store);
+      // columns [0, 128) of a side are the first block's dims, the others the second's
+      auto dim_of = [&](int col) { return 128 * side + (col & 127) + (col >= 128 ? 256 : 0); };
+      if (part) {
+        float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + (part_row - (lane & 3)) * kDimCkv + 8 * (lane & 3);
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+          turn(o, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (stores >> ((lane & 28) + i) & 1u) st_global_v8(dst + i * kDimCkv + dim_of(32 * c), o + 8 * i);
+        }
+      } else {
+        uint8_t* dst = static_cast<uint8_t*>(a.out) + (out_row - (lane & 3)) * (kDimCkv * 2) + 32 * (lane & 3);
+        const float inv = a.out_scale / ml.y;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * c, o);
-        tmem_wait_ld();
-        // columns [0, 128) of a side are the first block's dims, the others the second's
-        const int dim = 128 * side + 32 * (c & 3) + (c >= 4 ? 256 : 0);
-        if (store && part) {
-          float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + part_row * kDimCkv + dim;
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[64], pk[32];
+          tmem_ld32(tO + 64 * c, o);
+          tmem_ld32(tO + 64 * c + 32, o + 32);
+          tmem_wait_ld();
 #pragma unroll
-          for (int v = 0; v < 4; ++v) st_global_v8(dst + 8 * v, o + 8 * v);
-        } else if (store) {
-          uint8_t* dst = static_cast<uint8_t*>(a.out) + (out_row * kDimCkv + dim) * 2;
+          for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          turn(pk, lane);
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              pk[e] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * e]) * inv, __uint_as_float(o[16 * v + 2 * e + 1]) * inv);
-            st_global_v8(dst + 32 * v, pk);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (stores >> ((lane & 28) + i) & 1u) st_global_v8(dst + i * kDimCkv * 2 + dim_of(64 * c) * 2, pk + 8 * i);
         }
       }
       tc_fence_before();

@@ -48,13 +48,17 @@ struct ShSegment {
   int base;
 };
 
-// Blocks [begin, end) of a tile.
+// Blocks [begin, end) of a tile, with what the kernel's roles start from (each load that
+// waits for another costs them half a microsecond).
 struct ShItem {
-  int tile;
   int begin, end;
-  int part;  // -1: the whole tile; else the partial sums' number
+  int part;            // -1: the whole tile; else the partial sums' number
   int cluster;
-  int pad[3];
+  int row0, rows;      // the tile's
+  int seg, seg_last;   // segment of the first block; the tile's last one
+  int prefix_end;      // blocks of the prefix
+  int pad[7];
+  ShSegment first;     // segment `seg`
 };
 
 struct ShSplit {
@@ -68,7 +72,7 @@ struct ShGroup {
   int tile0;         // tiles of the groups before it
 };
 
-static_assert(sizeof(ShTile) == 32 && sizeof(ShSegment) == 32 && sizeof(ShItem) == 32, "two 16-byte words");
+static_assert(sizeof(ShTile) == 32 && sizeof(ShSegment) == 32 && sizeof(ShItem) == 96, "16-byte words");
 
 struct ShHeader {
   int status;  // sticky MLA_STATUS_* bits

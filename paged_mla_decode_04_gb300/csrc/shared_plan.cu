@@ -172,13 +172,25 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
     block_scan<2>(w, sums, sh);
     const int item0 = static_cast<int>(num_items + w[0]);
     const int part0 = static_cast<int>(num_parts + (w[1] & ((1ll << 40) - 1)));
+    ShTile tile = {};
+    int prefix_end = 0;
+    if (pieces > 0) {
+      tile = tiles[t];
+      const ShSegment g = segs[tile.seg0];
+      if (g.base == g.tok_hi) prefix_end = (g.tok_hi + kShTokens - 1) / kShTokens;
+    }
     for (int k = 0; k < pieces; ++k) {
       ShItem i = {};
-      i.tile = t;
       i.begin = static_cast<int>(max(range_begin(c0 + k), off) - off);
       i.end = static_cast<int>(min(range_begin(c0 + k + 1), off + blocks) - off);
       i.part = pieces > 1 ? part0 + k : -1;
       i.cluster = c0 + k;
+      i.row0 = tile.row0;
+      i.rows = tile.rows;
+      i.seg = tile.seg0 + last_at_most(tile.segs, i.begin, [&](int j) { return segs[tile.seg0 + j].block0; });
+      i.seg_last = tile.seg0 + tile.segs - 1;
+      i.prefix_end = prefix_end;
+      i.first = segs[i.seg];
       items[item0 + k] = i;
     }
     if (pieces > 1) splits[num_split + (w[1] >> 40)] = ShSplit{t, pieces, part0, 0};

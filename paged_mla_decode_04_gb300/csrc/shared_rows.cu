@@ -27,16 +27,15 @@ __global__ void __launch_bounds__(32 * kWarps) shared_rows_kernel(const ShDecode
   const ShItem* items = reinterpret_cast<const ShItem*>(a.ws + a.lay.items);
   for (int k = start[blockIdx.x]; k < start[blockIdx.x + 1]; ++k) {
     const ShItem it = items[k];
-    const ShTile tile = reinterpret_cast<const ShTile*>(a.ws + a.lay.tiles)[it.tile];
-    if (row >= tile.rows) continue;
-    const int64_t out_row = static_cast<int64_t>(tile.row0) + row;
+    if (row >= it.rows) continue;
+    const int64_t out_row = static_cast<int64_t>(it.row0) + row;
     const int i = static_cast<int>(out_row / a.num_heads) % a.q_len;
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + out_row * kDimRow;
     float q[18], o[16] = {};
     for (int d = 0; d < 18; ++d) q[d] = __bfloat162float(qp[lane + 32 * d]);
     float m = -1e30f, l = 0.f;
-    for (int s = 0; s < tile.segs; ++s) {
-      const ShSegment sg = reinterpret_cast<const ShSegment*>(a.ws + a.lay.segs)[tile.seg0 + s];
+    for (int s = it.seg; s <= it.seg_last; ++s) {
+      const ShSegment sg = reinterpret_cast<const ShSegment*>(a.ws + a.lay.segs)[s];
       if (row < sg.row_lo || row >= sg.row_hi) continue;
       const int lo = max(sg.tok_lo, sg.tok0 + max(it.begin - sg.block0, 0) * kShTokens);
       const int64_t till = sg.tok0 + static_cast<int64_t>(it.end - sg.block0) * kShTokens;
