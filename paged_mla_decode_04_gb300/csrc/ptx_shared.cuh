@@ -67,6 +67,11 @@ __device__ __forceinline__ void st_async_v2(uint32_t addr, uint32_t a, uint32_t 
                : "memory");
 }
 
+// Asks for `bytes` (a multiple of 16, as the address is) to be brought into L2.
+__device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
+}
+
 // 32-byte vector load from global memory.
 __device__ __forceinline__ void ld_global_v8(const void* ptr, uint32_t* v) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

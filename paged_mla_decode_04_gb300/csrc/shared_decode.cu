@@ -145,9 +145,9 @@ struct Walk {
 };
 
 // Four lanes' 128 bytes each, as four pieces of 32, transposed: piece j of lane i becomes
-// piece i of lane j. A lane that has 128 bytes of its own row reads and writes global memory
-// by way of this, so that an access covers eight whole lines (as the rows lie it is pieces of
-// 32: an item's queries took 4.6 us to come in and its results 6 to 8 to go out).
+// piece i of lane j. A lane that has 128 bytes of its own row writes them by way of this, so
+// that a store covers eight whole lines (as the rows lie it is 32 pieces of 32 bytes: an
+// item's results took 6 to 8 us to go out instead of 4 to 6).
 __device__ __forceinline__ void turn(uint32_t* o, int lane) {
 #pragma unroll
   for (int d = 1; d < 4; d <<= 1) {
@@ -240,15 +240,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   const int cluster = blockIdx.x >> 2;
   // (Buffers at another start than the tensor core's patterns ask for: never seen; nothing is
   // computed then, and the status tells.)
-  const bool planned = sh_planned(hd, a) && (sbase & 1023u) == 0;
-  if (!planned && threadIdx.x == 0 && rank == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
   const int* cstart = reinterpret_cast<const int*>(a.ws + a.lay.cluster_start);
   const ShItem* items = reinterpret_cast<const ShItem*>(a.ws + a.lay.items);
-  int item0 = 0, item1 = 0;
-  if (planned && cluster < hd->num_clusters) {
-    item0 = cstart[cluster];
-    item1 = cstart[cluster + 1];
-  }
+  int item0 = cstart[cluster], item1 = cstart[cluster + 1];  // (asked for with the header)
+  const bool planned = sh_planned(hd, a) && (sbase & 1023u) == 0;
+  if (!planned && threadIdx.x == 0 && rank == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
+  if (!planned || cluster >= hd->num_clusters) item0 = item1 = 0;
 
   if (warp >= kWorkers) setmaxnreg_dec<kRegsOther>();
   if (warp == kProducerWarp) {
@@ -299,6 +296,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         const ShItem it = items[k];
         Walk w;
         w.start(a, it);
+        if (scores && k + 1 < item1) {  // the next item's queries (each block its rows) on their way to L2
+          const int row0 = items[k + 1].row0 + 128 * static_cast<int>(half);
+          const int rows = min(items[k + 1].rows - 128 * static_cast<int>(half), 128);
+          if (rows > 0)
+            prefetch_l2(static_cast<const uint8_t*>(a.q) + static_cast<int64_t>(row0) * (kDimRow * 2), rows * (kDimRow * 2));
+        }
         Ids ids, next, later;
         ask(w.get(), ids);
         if (w.more()) ask(w.get(), next);
@@ -393,6 +396,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             bulk_copy_to(there + kOffAlpha + 512 * buf, sbase + kOffAlphaOut + 512 * group, 512, rb);
           }
         }
+      }
+      if (!ok) fail();
+    } else if (!scores && warp == kSendWarp && lane == 0) {
+      // P has landed: its room in the other pair is free. (Told by the accumulators' warps,
+      // which wait for V as well, it took long enough to bound the whole.)
+      int blocks = 0;
+      for (int k = item0; k < item1; ++k) blocks += items[k].end - items[k].begin;
+      bool ok = true;
+      for (int n = 0; n < blocks && ok; ++n) {
+        ok = spin(bar(kBarP + n % kPBuffers), (n / kPBuffers) & 1u);
+        if (ok) mbar_arrive_remote_relaxed(peer(kBarOutFree + (n & 1)));
       }
       if (!ok) fail();
     }
@@ -524,27 +538,24 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           if (w0 + row < rows)
             rope[i] = *reinterpret_cast<const uint4*>(src + row * (kDimRow * 2) + 2 * kDimCkv + 64 * group + 16 * (lane & 3));
         }
-#pragma unroll
+        // (Pieces of 32 bytes of 32 rows a load; by whole lines and turned, as the results go
+        // out, it took longer: the turns' instructions have to be fetched for the first item.)
+        const uint8_t* mine = src + lane * (kDimRow * 2) + 512 * group;
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          uint32_t x[64];  // 256 bytes of a row, in two turns
+          uint32_t x[64];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 8; ++c) {
+            if (w0 + lane < rows) {
+              ld_global_v8(mine + 256 * h + 32 * c, x + 8 * c);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = (lane & 28) + i;
-              uint32_t* v = x + 32 * c + 8 * i;
-              if (w0 + row < rows) {
-                ld_global_v8(src + row * (kDimRow * 2) + 512 * group + 256 * h + 128 * c + 32 * (lane & 3), v);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0;
-              }
+              for (int e = 0; e < 8; ++e) x[8 * c + e] = 0;
             }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            turn(x + 32 * c, lane);
-            tmem_st32(tbase + 128 * group + 64 * h + 32 * c, x + 32 * c);
           }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) tmem_st32(tbase + 128 * group + 64 * h + 32 * c, x + 32 * c);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -728,7 +739,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (wrote) fence_proxy_async_smem();
         if (!(ok = warp_wait_cluster(bar(kBarP + buf), (n / kPBuffers) & 1u))) break;
-        if (threadIdx.x == 0) mbar_arrive_remote_relaxed(peer(kBarOutFree + (n & 1u)));
         const float alpha = here ? alphas[128 * buf + lrow] : 1.f;
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
           if (!(ok = warp_wait(bar(kBarPFree + (n - 1) % kPBuffers), ((n - 1) / kPBuffers) & 1u))) break;
@@ -768,7 +778,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       auto dim_of = [&](int col) { return 128 * side + (col & 127) + (col >= 128 ? 256 : 0); };
       if (part) {
         float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + (part_row - (lane & 3)) * kDimCkv + 8 * (lane & 3);
-#pragma unroll 2
+#pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);

@@ -24,7 +24,9 @@ constexpr int kShTokens = 128;
 constexpr int kShClusterBlocks = 4;  // thread blocks of a cluster
 // A tile's first block costs a cluster this many more (queries into place, the
 // pipeline's start, the result's way out).
-constexpr int kShItemCost = 3;
+constexpr int kShItemCost = 6;
+// Clusters are used as far as each has this many blocks.
+constexpr int kShLeastBlocks = 3;
 
 // Cached positions of a request are fewer (a tile's blocks then count in 32 bits).
 constexpr int kShMostLength = 1 << 29;
@@ -61,8 +63,9 @@ struct ShItem {
   ShSegment first;     // segment `seg`
 };
 
+// A split tile.
 struct ShSplit {
-  int tile, pieces, part0, pad;
+  int row0, rows, pieces, part0;
 };
 
 // A group as the plan sees it.

@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
     block_scan<1>(v, total, sh);
     weight += total[0];
   }
-  const int64_t c = max(static_cast<int64_t>(1), min(weight, static_cast<int64_t>(a.clusters)));
+  // No more clusters than have some blocks each: pieces have to be joined.
+  const int64_t all = weight - static_cast<int64_t>(kShItemCost) * num_tiles;
+  const int64_t c = max(static_cast<int64_t>(1), min(all / kShLeastBlocks, static_cast<int64_t>(a.clusters)));
   auto range_begin = [&](int64_t k) { return k * weight / c; };
   auto cluster_of = [&](int64_t x) { return static_cast<int>(((x + 1) * c + weight - 1) / weight - 1); };
   int64_t at = 0, num_items = 0, num_parts = 0, num_split = 0;
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
       i.first = segs[i.seg];
       items[item0 + k] = i;
     }
-    if (pieces > 1) splits[num_split + (w[1] >> 40)] = ShSplit{t, pieces, part0, 0};
+    if (pieces > 1) splits[num_split + (w[1] >> 40)] = ShSplit{tile.row0, tile.rows, pieces, part0};
     num_items += sums[0];
     num_parts += sums[1] & ((1ll << 40) - 1);
     num_split += sums[1] >> 40;
@@ -223,52 +225,76 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   }
 }
 
-constexpr int kMergeRows = 4;  // rows a block, a warp each
+constexpr int kMergeRows = 4;   // rows a block, two warps each
+constexpr int kMergeBatch = 8;  // pieces whose loads are issued together
 
 // out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over a split tile's pieces k, M the
 // largest m_k. Pieces without a position of the row have l_k = 0; their O_k is not read.
-__global__ void __launch_bounds__(32 * kMergeRows) shared_merge_kernel(const ShDecodeArgs a) {
+// Weights come first, 32 pieces at a time, a lane each; then the sums, in the pieces' order.
+// Bound by the latency of its loads and by L2.
+__global__ void __launch_bounds__(64 * kMergeRows) shared_merge_kernel(const ShDecodeArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const ShHeader* hd = reinterpret_cast<const ShHeader*>(a.ws);
+  const ShSplit sp = reinterpret_cast<const ShSplit*>(a.ws + a.lay.splits)[blockIdx.x];  // (asked for with the header)
   if (!sh_planned(hd, a) || static_cast<int>(blockIdx.x) >= hd->num_split) return;
-  const ShSplit sp = reinterpret_cast<const ShSplit*>(a.ws + a.lay.splits)[blockIdx.x];
-  const ShTile tile = reinterpret_cast<const ShTile*>(a.ws + a.lay.tiles)[sp.tile];
-  const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= tile.rows) return;
+  const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 6), side = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
+  if (row >= sp.rows) return;
   const float2* stats = reinterpret_cast<const float2*>(a.ws + a.lay.stats) + static_cast<int64_t>(sp.part0) * kShRows + row;
+  constexpr int kRowVecs = kDimCkv / 4;
   const float4* part = reinterpret_cast<const float4*>(a.ws + a.lay.partial) +
-                       (static_cast<int64_t>(sp.part0) * kShRows + row) * (kDimCkv / 4);
+                       (static_cast<int64_t>(sp.part0) * kShRows + row) * kRowVecs + side * (kRowVecs / 2) + lane;
   float top = -CUDART_INF_F;
   for (int k = lane; k < sp.pieces; k += 32) {
     const float2 s = stats[static_cast<int64_t>(k) * kShRows];
     if (s.y != 0.f) top = fmaxf(top, s.x);
   }
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float4 acc[4] = {};
+  float4 acc[2] = {};
   float sum = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < sp.pieces; ++k) {
-    const float2 s = stats[static_cast<int64_t>(k) * kShRows];
-    if (s.y == 0.f) continue;
-    const float w = exp2f(s.x - top);
-    sum = fmaf(w, s.y, sum);
+  for (int k0 = 0; k0 < sp.pieces; k0 += 32) {
+    float mine = 0.f;
+    bool there = false;
+    if (k0 + lane < sp.pieces) {
+      const float2 s = stats[static_cast<int64_t>(k0 + lane) * kShRows];
+      there = s.y != 0.f;
+      mine = there ? exp2f(s.x - top) : 0.f;
+      sum = fmaf(mine, s.y, sum);
+    }
+    const uint32_t with = __ballot_sync(0xffffffffu, there);
+    const int n = min(sp.pieces - k0, 32);
+    for (int b0 = 0; b0 < n; b0 += kMergeBatch) {
+      float4 x[kMergeBatch][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 x = part[static_cast<int64_t>(k) * kShRows * (kDimCkv / 4) + lane + 32 * j];
-      acc[j].x = fmaf(w, x.x, acc[j].x);
-      acc[j].y = fmaf(w, x.y, acc[j].y);
-      acc[j].z = fmaf(w, x.z, acc[j].z);
-      acc[j].w = fmaf(w, x.w, acc[j].w);
+      for (int k = 0; k < kMergeBatch; ++k) {
+        x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (with >> (b0 + k) & 1u) {
+          const float4* src = part + static_cast<int64_t>(k0 + b0 + k) * kShRows * kRowVecs;
+          x[k][0] = src[0];
+          x[k][1] = src[32];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeBatch; ++k) {
+        const float w = __shfl_sync(0xffffffffu, mine, b0 + k);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[j].x = fmaf(w, x[k][j].x, acc[j].x);
+          acc[j].y = fmaf(w, x[k][j].y, acc[j].y);
+          acc[j].z = fmaf(w, x[k][j].z, acc[j].z);
+          acc[j].w = fmaf(w, x[k][j].w, acc[j].w);
+        }
+      }
     }
   }
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   const float inv = a.out_scale / sum;
-  const int64_t out_row = static_cast<int64_t>(tile.row0) + row;
-  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kDimCkv);
+  const int64_t out_row = static_cast<int64_t>(sp.row0) + row;
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kDimCkv) + side * (kRowVecs / 2) + lane;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    dst[lane + 32 * j] = make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
-  if (a.lse && lane == 0) a.lse[out_row] = (top + log2f(sum)) * 0.69314718055994531f;
+  for (int j = 0; j < 2; ++j)
+    dst[32 * j] = make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
+  if (a.lse && side == 0 && lane == 0) a.lse[out_row] = (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -280,7 +306,7 @@ cudaError_t launch_shared_plan(const ShPlanArgs& a, cudaStream_t stream) {
 cudaError_t launch_shared_merge(const ShDecodeArgs& a, cudaStream_t stream) {
   // (a split tile lies across a boundary between two clusters' ranges)
   const int most = a.lay.max_tiles < a.clusters ? a.lay.max_tiles : a.clusters;
-  return launch_pdl(shared_merge_kernel, dim3(most, (a.lay.tile_rows + kMergeRows - 1) / kMergeRows), dim3(32 * kMergeRows),
+  return launch_pdl(shared_merge_kernel, dim3(most, (a.lay.tile_rows + kMergeRows - 1) / kMergeRows), dim3(64 * kMergeRows),
                     0, stream, a);
 }
 
