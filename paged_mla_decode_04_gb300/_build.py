@@ -22,7 +22,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla_decode.so")
 SOURCES = ["mla_api.cu", "kv_write.cu", "plan_merge.cu", "decode_sm103.cu", "uv_project.cu", "selftest.cu",
            "step_api.cu", "step_tables.cu", "rope_write.cu", "prefill_gather.cu", "prefill_expand.cu", "prefill_attn.cu",
-           "prefill_absorb.cu", "shared_api.cu", "shared_plan.cu", "shared_decode.cu", "shared_rows.cu", "quant_store.cu"]
+           "prefill_absorb.cu", "shared_api.cu", "shared_plan.cu", "shared_decode.cu", "quant_store.cu"]
 HEADERS = ["ptx.cuh", "mla_internal.h", "trace.cuh", "host_util.h", "step_internal.h", "ptx_prefill.cuh", "scan.cuh",
            "shared_internal.h", "ptx_shared.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

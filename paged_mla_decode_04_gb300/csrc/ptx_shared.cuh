@@ -33,12 +33,6 @@ __device__ __forceinline__ void mma2_commit_to(uint32_t bar, uint16_t mask) {
       : "memory");
 }
 
-// Arrival on any block's barrier that publishes this thread's shared-memory writes, and
-// those it has seen, to the cluster.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
 // Arrival on any block's barrier that expects `bytes` more; publishes nothing (what is
 // expected completes on the barrier by itself).
 __device__ __forceinline__ void mbar_arrive_expect_tx_relaxed(uint32_t cluster_bar, uint32_t bytes) {
@@ -70,6 +64,11 @@ __device__ __forceinline__ void st_async_v2(uint32_t addr, uint32_t a, uint32_t 
 // Asks for `bytes` (a multiple of 16, as the address is) to be brought into L2.
 __device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
+}
+
+// A pair of bf16 as f16, saturating.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
+  return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
 // 32-byte vector load from global memory.

@@ -100,10 +100,17 @@ int mla_decode_shared(const mla_kv_pool* pool, int layer, const void* q, const i
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap maps[3] = {};
   const uint32_t copy = mla::sh_copy_tokens(pool->page_size);
-  if (!fp8 && (!mla::make_map_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool->data, rows, mla::kDimRow, mla::kDimRow * 2, 64, copy) ||
-               !mla::make_map_chunks(&maps[1], pool->data, rows, mla::kDimRow, mla::kDimRow * 2, copy, 3) ||
-               !mla::make_map_chunks(&maps[2], pool->data, rows, mla::kDimRow, mla::kDimRow * 2, copy, 4)))
+  if (fp8) {
+    constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    constexpr auto plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (!mla::make_map_2d(&maps[1], u8, pool->data, rows, mla::kDimRow, mla::kDimRow, 192, copy, plain) ||
+        !mla::make_map_2d(&maps[2], u8, pool->data, rows, mla::kDimRow, mla::kDimRow, 256, copy, plain))
+      return MLA_ERR_CUDA;
+  } else if (!mla::make_map_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pool->data, rows, mla::kDimRow, mla::kDimRow * 2, 64, copy) ||
+             !mla::make_map_chunks(&maps[1], pool->data, rows, mla::kDimRow, mla::kDimRow * 2, copy, 3) ||
+             !mla::make_map_chunks(&maps[2], pool->data, rows, mla::kDimRow, mla::kDimRow * 2, copy, 4)) {
     return MLA_ERR_CUDA;
+  }
   cudaError_t e = mla::launch_shared_decode(maps, a, st);
   if (e == cudaSuccess) e = mla::launch_shared_merge(a, st);
   return done(e);

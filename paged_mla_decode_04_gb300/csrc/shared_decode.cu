@@ -38,10 +38,16 @@ namespace {
 
 constexpr int kWorkers = 8;                 // warps of softmax or accumulators, two groups of four
 constexpr int kProducerWarp = kWorkers, kIssueWarp = kWorkers + 1, kSendWarp = kWorkers + 2;
-constexpr int kThreads = 384;
-// Registers a thread after setmaxnreg; they add up to the launch's 3 x 168.
-constexpr int kRegsWorker = 208, kRegsOther = 88;
-static_assert(2 * kRegsWorker + kRegsOther == 3 * 168, "register split");
+constexpr int kConvertWarp = kWorkers + 4;  // (fp8 pools) four that widen the codes
+// Registers a thread after setmaxnreg; they add up to the launch's 3 x 168 (bf16 pools) or
+// 4 x 128.
+template <bool kFp8>
+struct Regs {
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kWorker = kFp8 ? 176 : 208, kOther = kFp8 ? 64 : 88, kConvert = 96;
+};
+static_assert(2 * Regs<false>::kWorker + Regs<false>::kOther == 3 * 168, "register split");
+static_assert(2 * Regs<true>::kWorker + Regs<true>::kOther + Regs<true>::kConvert == 4 * 128, "register split");
 constexpr int kChunk = 64 * 128;            // [64 positions][64 dims]
 // Scores' pair: K in stages of three chunks (192 dims), three stages a block.
 constexpr int kKStages = 5, kKStageBytes = 3 * kChunk, kKParts = 3;
@@ -83,7 +89,10 @@ enum {
   kBarO = kBarPReady + kPBuffers,      // an item's last product complete
   kBarStats = kBarO + 1,               // an item's maxima and sums have arrived
   kBarOFree = kBarStats + 1,
-  kNumBars = kBarOFree + 1
+  // (fp8 pools) In either pair: codes have landed; every warp that widens has read its share.
+  kBarRaw = kBarOFree + 1,             // [most stages]
+  kBarMeet = kBarRaw + (kKStages > kVStages ? kKStages : kVStages),
+  kNumBars = kBarMeet + 1
 };
 
 // (all that a block may have: its start has to be at a multiple of 1,024, see the kernel)
@@ -166,13 +175,15 @@ __device__ __forceinline__ void turn(uint32_t* o, int lane) {
 }
 
 struct Params {
-  CUtensorMap rows;  // the pool as [rows][576], box {64, positions of a copy}
-  // Where a copy brings 64 positions: as [chunk][rows][64], boxes of three and four chunks.
-  CUtensorMap chunks3, chunks4;
+  // bf16 pools: as [rows][576], box {64, positions of a copy}; where a copy brings 64 positions
+  // as [chunk][rows][64], boxes of three and four chunks. fp8 pools: (none), boxes of 192 and
+  // of 256 codes.
+  CUtensorMap rows, chunks3, chunks4;
   ShDecodeArgs a;
 };
 
-__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool kFp8>
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads, 1)
     shared_decode_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const ShDecodeArgs& a = p.a;
@@ -194,6 +205,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       if (i >= kBarSFree && i < kBarSFree + 2) count = 8;                       // a group of both blocks
       if (i >= kBarStaged && i < kBarStaged + 2) count = 4;                     // a group of one
       if (i == kBarStats) count = 4;
+      if (kFp8 && i >= kBarKFull && i < kBarKFull + kKStages) count = 8;        // warps that widen, of both blocks
+      if (kFp8 && i >= kBarVFull && i < kBarVFull + kVStages) count = 4;        // those of one
+      if (i == kBarMeet) count = 4;
       if (i >= kBarPReady && i < kBarPReady + kPBuffers) count = 2 * kWorkers;
       if (i == kBarOFree) count = 2 * kWorkers;
       if (i == kBarStatsFree) count = kWorkers;
@@ -202,7 +216,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
-  if (warp == kProducerWarp && lane == 0) tma_prefetch_map(unit != 64 ? &p.rows : scores ? &p.chunks3 : &p.chunks4);
+  if (warp == kProducerWarp && lane == 0) tma_prefetch_map(unit != 64 && !kFp8 ? &p.rows : scores ? &p.chunks3 : &p.chunks4);
   if (warp == kIssueWarp) {
     tmem_alloc2(smem_addr(tmem_slot), 512);
     tmem_relinquish2();
@@ -220,11 +234,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
     atomicOr(&hd->status, MLA_STATUS_TIMEOUT);
   };
-  // Waits of a thread and of a warp. (What a wait of the first kind is for is ordered by
-  // tcgen05 fences or the copy's own completion; the others acquire what this block's or the
-  // cluster's threads wrote to shared memory, for the whole warp.)
+  // Waits of a thread and of a warp. What the first two are for is ordered by tcgen05 and
+  // proxy fences before the arrival, or by the copy's own completion (an acquire at the
+  // cluster's scope takes 2,000 cycles beside products in flight); the others acquire what
+  // this block's or the cluster's threads wrote to shared memory, for the whole warp.
   auto spin = [&](uint32_t b, uint32_t parity) -> bool { return mbar_spin(b, parity, abort_flag); };
-  auto spin_cluster = [&](uint32_t b, uint32_t parity) -> bool { return spin(b, parity) && mbar_test_wait_cluster(b, parity); };
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return mbar_spin_warp(b, parity, abort_flag); };
   auto warp_wait_block = [&](uint32_t b, uint32_t parity) -> bool {
     if (!mbar_spin_warp(b, parity, abort_flag)) return false;
@@ -247,7 +261,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   if (!planned && threadIdx.x == 0 && rank == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
   if (!planned || cluster >= hd->num_clusters) item0 = item1 = 0;
 
-  if (warp >= kWorkers) setmaxnreg_dec<kRegsOther>();
+  if (warp >= kConvertWarp) {
+    if (kFp8) setmaxnreg_dec<Regs<kFp8>::kConvert>();
+  } else if (warp >= kWorkers) {
+    setmaxnreg_dec<Regs<kFp8>::kOther>();
+  }
   if (warp == kProducerWarp) {
     // Each block of the scores' pair brings its 64 of a block's positions, all dims; each of
     // the accumulators' pair all positions, its 256 value dims. One lane does it all; page
@@ -315,8 +333,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             for (int part = 0; part < kKParts; ++part) {
               if (!(ok = mbar_spin(bar(kBarKFree + stage), use ^ 1u, abort_flag))) break;
               const uint32_t dst = sbase + stage * kKStageBytes, full = lead(kBarKFull + stage);
-              if (half == 0) mbar_arrive_expect_tx(bar(kBarKFull + stage), 2 * kKStageBytes);
-              if (unit == 64) {
+              if (kFp8) {  // codes, behind the room that they will take when widened
+                mbar_arrive_expect_tx(bar(kBarRaw + stage), kKStageBytes / 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (i < subs)
+                    tma_load_2d(dst + kKStageBytes / 2 + i * unit * 192, &p.chunks3, bar(kBarRaw + stage), 192 * part, rows[i]);
+              } else if (half == 0) {
+                mbar_arrive_expect_tx(bar(kBarKFull + stage), 2 * kKStageBytes);
+              }
+              if (kFp8) {
+              } else if (unit == 64) {
                 tma2_load_3d(dst, &p.chunks3, full, 0, rows[0], 3 * part);
               } else {
 #pragma unroll
@@ -336,8 +363,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             for (int part = 0; part < 2; ++part) {
               if (!ok || !(ok = mbar_spin(bar(kBarVFree + stage), use ^ 1u, abort_flag))) break;
               const uint32_t dst = sbase + kOffV + stage * kVStageBytes, full = bar(kBarVFull + stage);
-              mbar_arrive_expect_tx(full, kVStageBytes);
-              if (unit == 64) {
+              mbar_arrive_expect_tx(kFp8 ? bar(kBarRaw + stage) : full, kFp8 ? kVStageBytes / 2 : kVStageBytes);
+              if (unit == 64 && !kFp8) {
                 tma_load_3d(dst, &p.chunks4, full, 0, row_of(ids, part), 4 * static_cast<int>(half));
               } else {
 #pragma unroll
@@ -345,7 +372,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                   const int j = i - part * (subs / 2);
                   if (i < subs && j >= 0 && j < subs / 2) {
                     const int r = row_of(ids, i);
-                    for (int c = 0; c < 4; ++c)
+                    if (kFp8)
+                      tma_load_2d(dst + kVStageBytes / 2 + j * unit * 256, &p.chunks4, bar(kBarRaw + stage),
+                                  256 * static_cast<int>(half), r);
+                    for (int c = 0; c < (kFp8 ? 0 : 4); ++c)
                       tma_load_2d(dst + c * kChunk + j * unit * 128, &p.rows, full, 256 * static_cast<int>(half) + 64 * c, r);
                   }
                 }
@@ -362,12 +392,64 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) fail();
-      if (*abort_flag && (!scores || half == 0)) {  // let the copies in flight land (each wait bounded)
+      if (*abort_flag && (kFp8 || !scores || half == 0)) {  // let the copies in flight land (each wait bounded)
         const uint32_t n = scores ? kKStages : kVStages;
         for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i)
-          mbar_wait(bar((scores ? kBarKFull : kBarVFull) + i % n), (i / n) & 1u, nullptr);
+          mbar_wait(bar((kFp8 ? kBarRaw : scores ? kBarKFull : kBarVFull) + i % n), (i / n) & 1u, nullptr);
       }
     }
+  } else if (kFp8 && warp >= kConvertWarp) {
+    // Codes, 64 positions of `width` each, widened to f16 where they lie: read by all four
+    // warps before any of them writes. (e4m3 values are exact in f16.)
+    const int width = scores ? 192 : 256, stages = scores ? kKStages : kVStages;
+    const int parts = scores ? kKParts : 2, bytes = scores ? kKStageBytes : kVStageBytes;
+    const int t = threadIdx.x - 32 * kConvertWarp, per_row = width / 16;
+    const uint32_t ring = sbase + (scores ? 0 : kOffV);
+    int blocks = 0;
+    for (int k = item0; k < item1; ++k) blocks += items[k].end - items[k].begin;
+    uint32_t use = 0, meet = 0;
+    int stage = 0;
+    bool ok = true;
+    for (int n = 0; n < parts * blocks && ok; ++n) {
+      if (!(ok = warp_wait_block(bar(kBarRaw + stage), use))) break;
+      const uint32_t slot = ring + stage * bytes;
+      uint32_t v[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < (scores ? 6 : 8)) ld_shared_v4(slot + bytes / 2 + 16 * (t + 128 * i), v[i][0], v[i][1], v[i][2], v[i][3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarMeet));
+      if (!(ok = warp_wait(bar(kBarMeet), meet))) break;
+      meet ^= 1u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < (scores ? 6 : 8)) {
+          const int piece = t + 128 * i, row = piece / per_row, q = piece % per_row, chunk = q >> 2;
+          const uint32_t at = slot + chunk * kChunk + row * 128;
+          uint32_t f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = e4m3x2_to_f16x2(static_cast<uint16_t>(v[i][e >> 1] >> (16 * (e & 1))));
+          // (odd chunks the other half first: a phase of eight threads has two chunks' pieces)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const bool hi = (j ^ chunk) & 1;
+            st_shared_v4(at + 16 * ((2 * (q & 3) + (hi ? 1 : 0)) ^ (row & 7)), hi ? f[4] : f[0], hi ? f[5] : f[1],
+                         hi ? f[6] : f[2], hi ? f[7] : f[3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (scores) mbar_arrive_cluster(lead(kBarKFull + stage));
+        else mbar_arrive(bar(kBarVFull + stage));
+      }
+      if (++stage == stages) {
+        stage = 0;
+        use ^= 1u;
+      }
+    }
+    if (!ok) fail();
   } else if (warp >= kSendWarp) {
     // One lane for each group of softmax warps sends P to the other pair, rows that attend the
     // block alone, so that no softmax warp waits for a buffer there. (Stored row by row into
@@ -412,13 +494,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kIssueWarp) {
     if (scores && half == 0 && elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16(256, kShTokens, false, false);
+      constexpr uint32_t idesc = kFp8 ? idesc_f16(256, kShTokens, false, false) : idesc_bf16(256, kShTokens, false, false);
       const uint32_t ring = desc_lo(sbase), rope = desc_lo(sbase + kOffQRope);
       uint32_t n = 0, stage = 0, use = 0;
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
         const int blocks = items[k].end - items[k].begin;
-        ok = spin_cluster(bar(kBarQ), (k - item0) & 1u);
+        ok = spin(bar(kBarQ), (k - item0) & 1u);
         for (int x = 0; x < blocks && ok; ++x, ++n) {
           const uint32_t buf = n & 1u;
           if (!(ok = spin(bar(kBarSFree + buf), ((n >> 1) & 1u) ^ 1u))) break;
@@ -447,7 +529,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) fail();
     } else if (!scores && half == 0 && elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16(256, 256, false, true);
+      constexpr uint32_t idesc = kFp8 ? idesc_f16(256, 256, false, true) : idesc_bf16(256, 256, false, true);
       uint32_t n = 0, stage = 0;
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
@@ -466,13 +548,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t below_hi = hi == 32 ? ~0u : (1u << hi) - 1u, below_lo = lo == 32 ? ~0u : (1u << lo) - 1u;
             off[i] = ~(below_hi & ~below_lo);
           }
-          // (Acquiring at the cluster's scope takes 2,000 cycles here: only where the peer's
-          // threads wrote to V. What else they announce are copies that have landed and
-          // accumulators, which tcgen05 fences order.)
-          const bool edge = (b.v0 & 15) || (b.v1 & 15) || b.end < b.v1;
-          if (!(ok = edge ? spin_cluster(bar(kBarPReady + buf), (n / kPBuffers) & 1u)
-                          : spin(bar(kBarPReady + buf), (n / kPBuffers) & 1u)))
-            break;
+          if (!(ok = spin(bar(kBarPReady + buf), (n / kPBuffers) & 1u))) break;
           tc_fence_after();
           const uint32_t pa = desc_lo(sbase + buf * kPBytes);
           const int k0 = b.v0 >> 4, k1 = (b.v1 + 15) >> 4;  // steps of 16 positions
@@ -498,7 +574,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) fail();
     }
   } else if (scores && warp < kWorkers) {
-    setmaxnreg_inc<kRegsWorker>();
+    setmaxnreg_inc<Regs<kFp8>::kWorker>();
     // Softmax: a row a thread. The two groups of four warps take the even and the odd
     // blocks, of their own buffers of S and P, so that one group's loads
     // and waits hide behind the other's exponentials. A row's reference maximum goes from block to block through
@@ -553,6 +629,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 8; ++e) x[8 * c + e] = 0;
             }
           }
+          if (kFp8) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] = bf16x2_to_f16x2(x[c]);
+          }
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < 2; ++c) tmem_st32(tbase + 128 * group + 64 * h + 32 * c, x + 32 * c);
@@ -560,6 +640,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = 8 * i + (lane >> 2);
+          if (kFp8)
+            rope[i] = make_uint4(bf16x2_to_f16x2(rope[i].x), bf16x2_to_f16x2(rope[i].y), bf16x2_to_f16x2(rope[i].z),
+                                 bf16x2_to_f16x2(rope[i].w));
           st_shared_v4(sbase + kOffQRope + (32 * quarter + row) * 128 + 16 * ((4 * group + (lane & 3)) ^ (row & 7)), rope[i].x,
                        rope[i].y, rope[i].z, rope[i].w);
         }
@@ -567,7 +650,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(lead(kBarQ));
+        if (lane == 0) mbar_arrive_cluster(lead(kBarQ));
       }
       if (k >= item0) {
         // The row's maximum and sum, from the group of the last block. (Every warp waits for
@@ -663,7 +746,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
             const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
             sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
-            s[c] = pack_bf16x2(p0, p1);
+            s[c] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
           }
           float s0, s1, s2, s3;
           f2_split(sum2[0], s0, s1);
@@ -685,7 +768,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (!ok) fail();
   } else if (!scores && warp < kWorkers) {
-    setmaxnreg_inc<kRegsWorker>();
+    setmaxnreg_inc<Regs<kFp8>::kWorker>();
     // Accumulators: the warps of a quarter of the lanes have half of the columns each.
     const int lrow = 32 * (warp & 3) + lane, r = 128 * static_cast<int>(half) + lrow, side = warp >> 2;
     const uint32_t tO = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256 * side;
@@ -706,6 +789,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         // positions that only later queries of a request see: an infinity or NaN there would
         // reach the others through a weight of zero. (Those that see it have it in their
         // scores.)
+        constexpr uint32_t kExponent = kFp8 ? 0x7c00u : 0x7f80u;
         bool wrote = false;
         for (int h = 0; h < 2 && ok; ++h) {
           if (!(ok = warp_wait_block(bar(kBarVFull + stage), use))) break;
@@ -725,7 +809,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             ld_shared_v4(at, x[0], x[1], x[2], x[3]);
             bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) odd |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
+            for (int i = 0; i < 4; ++i) odd |= (x[i] & kExponent) == kExponent || (x[i] & (kExponent << 16)) == kExponent << 16;
             if (__any_sync(0xffffffffu, odd)) {
               st_shared_v4(at, 0, 0, 0, 0);
               wrote = true;
@@ -756,11 +840,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        // (a release at the cluster's scope takes 1,700 cycles: only for what was written to V)
-        if (lane == 0) {
-          if (wrote) mbar_arrive_release_cluster(lead(kBarPReady + buf));
-          else mbar_arrive_cluster(lead(kBarPReady + buf));
-        }
+        // (What was written to V is in this block's memory since the proxy fence, and read there
+        // by its own tensor core: no release at the cluster's scope, which takes 1,700 cycles.)
+        if (lane == 0) mbar_arrive_cluster(lead(kBarPReady + buf));
       }
       if (!ok) break;
       if (!(ok = warp_wait_cluster(bar(kBarStats), (k - item0) & 1u))) break;
@@ -831,42 +913,57 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kIssueWarp) tmem_dealloc2(tmem, 512);
 }
 
-}  // namespace
-
-// Clusters of the kernel that run at once on the current device (cached), or -1.
-int shared_max_active_clusters() {
-  static int cached[kMaxDevices] = {};
-  const int dev = current_device();
-  if (dev < 0) return -1;
-  if (cached[dev] > 0) return cached[dev];
-  if (cudaFuncSetAttribute(shared_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return -1;
-  int sms = 0, n = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+template <bool kFp8>
+int max_active_clusters() {
+  if (cudaFuncSetAttribute(shared_decode_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+    return -1;
+  int sms = 0, n = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return -1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kShClusterBlocks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(sms / kShClusterBlocks * kShClusterBlocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Regs<kFp8>::kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, shared_decode_kernel, &cfg) != cudaSuccess || n <= 0) return -1;
-  return cached[dev] = n;
+  if (cudaOccupancyMaxActiveClusters(&n, shared_decode_kernel<kFp8>, &cfg) != cudaSuccess || n <= 0) return -1;
+  return n;
+}
+
+template <bool kFp8>
+cudaError_t launch_variant(const Params& p, cudaStream_t stream) {
+  static bool attr_set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_once(shared_decode_kernel<kFp8>, kSmemBytes, attr_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(shared_decode_kernel<kFp8>, dim3(kShClusterBlocks * p.a.clusters), dim3(Regs<kFp8>::kThreads), kSmemBytes,
+                    stream, p);
+}
+
+}  // namespace
+
+// Clusters of the kernel that run at once on the current device (cached), or -1: the smaller
+// of the variants' counts, so that a plan serves either.
+int shared_max_active_clusters() {
+  static int cached[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return -1;
+  if (cached[dev] > 0) return cached[dev];
+  const int a = max_active_clusters<false>(), b = max_active_clusters<true>();
+  if (a <= 0 || b <= 0) return -1;
+  return cached[dev] = a < b ? a : b;
 }
 
 cudaError_t launch_shared_decode(const CUtensorMap (&maps)[3], const ShDecodeArgs& a, cudaStream_t stream) {
-  if (a.dtype == MLA_DTYPE_FP8_E4M3) return launch_shared_rows(a, stream);
-  static bool attr_set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_once(shared_decode_kernel, kSmemBytes, attr_set);
-  if (e != cudaSuccess) return e;
   Params p;
   p.rows = maps[0];
   p.chunks3 = maps[1];
   p.chunks4 = maps[2];
   p.a = a;
-  return launch_pdl(shared_decode_kernel, dim3(kShClusterBlocks * a.clusters), dim3(kThreads), kSmemBytes, stream, p);
+  return a.dtype == MLA_DTYPE_FP8_E4M3 ? launch_variant<true>(p, stream) : launch_variant<false>(p, stream);
 }
 
 }  // namespace mla
