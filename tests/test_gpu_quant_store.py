@@ -77,6 +77,30 @@ def test_write_of_other_sizes(lib, codes, kind):
 
 
 @pytest.mark.parametrize("codes", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("power", [0, -60, -70, -120, 100])
+def test_every_quotient(lib, codes, power):
+    """Every significand that a value can have over every one that its group's largest can have, down to quotients
+    that round to zero: the code of the IEEE quotient."""
+    size = 128 if codes == "e4m3" else 32
+    low = 20 if codes == "e4m3" else 6
+    x = (1 + torch.arange(128, dtype=torch.float64) / 128)[None, :] * 2.0 ** -torch.arange(low, dtype=torch.float64)[:, None]
+    x = x.flatten()
+    per = size - 1
+    x = torch.cat([x, x[:-x.numel() % per]]).view(-1, per)
+    top = 2 * (1 + torch.arange(128, dtype=torch.float64) / 128)
+    groups = torch.cat([top[:, None, None].expand(-1, x.shape[0], 1), x[None].expand(128, -1, -1)], 2).reshape(-1, size)
+    groups[::2, 1:] *= -1
+    n = -(-groups.shape[0] * size // 512)
+    flat = torch.zeros(n * 512, dtype=torch.float64)
+    flat[:groups.numel()] = groups.flatten()
+    rows = torch.zeros(n, 576, dtype=torch.bfloat16, device="cuda")
+    rows[:, :512] = (flat.view(n, 512) * 2.0 ** power).to(torch.bfloat16).cuda()
+    store = lib.alloc_quant_pool(1, n // 16 + 1, 16, codes)
+    lib.quant_write(store, 0, rows, torch.arange(n, device="cuda"))
+    same_bytes(store.data[0].view(-1, ROWS[codes])[:n], store_row(rows, codes), codes)
+
+
+@pytest.mark.parametrize("codes", ["e4m3", "e2m1"])
 def test_infinities_and_nan(lib, codes):
     n, size = 40, 128 if codes == "e4m3" else 32
     rows = rows_of(n, 5)
