@@ -66,7 +66,9 @@ constexpr int kOffRef = kOffPOut + 2 * kPBytes;             // float [128]
 constexpr int kOffSum = kOffRef + 128 * 4;                  // float2 [2 items][128]
 constexpr int kOffAlphaOut = kOffSum + 2 * 128 * 8;         // float [2 groups][128]
 constexpr int kOffBar = kOffStats + 128 * 8;
-static_assert(kOffAlphaOut + 2 * 512 <= kOffBar, "both pairs' buffers end before the barriers");
+constexpr int kOffNotes = kOffAlphaOut + 2 * 512;            // Block [kNotes]
+constexpr int kNotes = 4;  // (the copies run less than four blocks ahead of the softmax)
+static_assert(kOffNotes + kNotes * 32 <= kOffBar, "both pairs' buffers end before the barriers");
 
 enum {
   // In the scores' pair. (Of its first block: K landed, Q in place, S read.)
@@ -84,6 +86,7 @@ enum {
   // In the accumulators' pair. (Of its first block: P ready, O read.)
   kBarVFull = kBarSum + 8,       // [kVStages]
   kBarVFree = kBarVFull + kVStages,    // [kVStages]
+  kBarNote = kBarVFree,                // [kNotes] (scores' pair) the block is described
   kBarP = kBarVFree + kVStages,        // [kPBuffers] weights have arrived
   kBarPReady = kBarP + kPBuffers,      // [kPBuffers] and O is rescaled, V landed
   kBarO = kBarPReady + kPBuffers,      // an item's last product complete
@@ -106,14 +109,15 @@ constexpr float kNoMax = -1e30f;
 constexpr uint16_t kScorePair = 0x3, kAccPair = 0xc;  // blocks of the cluster
 
 // A block of positions, as every role sees it.
-struct Block {
+struct alignas(16) Block {
   int owner;
   int t0;              // first position
   int v0, v1;          // those of the segment: [t0 + v0, t0 + v1)
   int row_lo, row_hi;  // rows that attend it
   int end;             // row of query position i: below t0 + end + i
-  bool add;            // to what these rows have already
+  int add;             // to what these rows have already
 };
+static_assert(sizeof(Block) == 32 && kNotes <= kVStages, "two 16-byte words");
 
 // Walks an item's blocks, a segment ahead in what it has loaded.
 struct Walk {
@@ -252,6 +256,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
     return true;
   };
   const int cluster = blockIdx.x >> 2;
+  Block* notes = reinterpret_cast<Block*>(smem + kOffNotes);
   // (Buffers at another start than the tensor core's patterns ask for: never seen; nothing is
   // computed then, and the status tells.)
   const int* cstart = reinterpret_cast<const int*>(a.ws + a.lay.cluster_start);
@@ -268,134 +273,125 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
   }
   if (warp == kProducerWarp) {
     // Each block of the scores' pair brings its 64 of a block's positions, all dims; each of
-    // the accumulators' pair all positions, its 256 value dims. One lane does it all; page
-    // ids are asked for two blocks ahead. (Looked up as they were needed, and with a copy for
-    // each 64 dims, this warp took 6,100 cycles a block.)
-    if (lane == 0) {
-      const int subs = (scores ? 64 : 128) / unit;  // copies along the positions
-      const int offset = scores ? 64 * static_cast<int>(half) : 0;
-      const int layer_row0 = static_cast<int>(static_cast<int64_t>(a.layer) * a.num_pages * a.page_size);
-      const int no_row = static_cast<int>(static_cast<int64_t>(a.num_layers) * a.num_pages * a.page_size);  // reads as zeros
-      constexpr int kNone = INT_MIN;  // not a position of the segment
-      bool ok = true;
-      uint32_t stage = 0, use = 0, issued = 0;  // of the ring
-      struct Ids {
-        int v[8];
-        int t;
-      };
-      int owner = -1, list_pages = a.max_blocks;
-      const int32_t* list = nullptr;
-      auto ask = [&](const Block& b, Ids& ids) {
-        if (b.owner != owner) {
-          owner = b.owner;
-          if (a.page_indptr) {
-            list = a.page_ids + a.page_indptr[owner];
-            list_pages = a.page_indptr[owner + 1] - a.page_indptr[owner];
-          } else {
-            list = a.page_ids + static_cast<int64_t>(owner) * a.max_blocks;
-          }
-        }
-        ids.t = b.t0 + offset;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int t = ids.t + unit * i, j = t >> page_shift;
-          const bool in = i < subs && t < b.t0 + b.v1 && t + unit > b.t0 + b.v0;
-          ids.v[i] = !in ? kNone : j < list_pages ? list[j] : -1;
-        }
-      };
-      auto row_of = [&](const Ids& ids, int i) -> int {
-        const int id = ids.v[i];
-        if (id >= 0 && id < a.num_pages)
-          return layer_row0 + (id << page_shift) + ((ids.t + unit * i) & (a.page_size - 1));
-        if (id != kNone && scores) atomicOr(&hd->status, MLA_STATUS_BAD_PAGE);
-        return no_row;
-      };
-      for (int k = item0; k < item1 && ok; ++k) {
-        const ShItem it = items[k];
-        Walk w;
-        w.start(a, it);
-        if (scores && k + 1 < item1) {  // the next item's queries (each block its rows) on their way to L2
-          const int row0 = items[k + 1].row0 + 128 * static_cast<int>(half);
-          const int rows = min(items[k + 1].rows - 128 * static_cast<int>(half), 128);
-          if (rows > 0)
-            prefetch_l2(static_cast<const uint8_t*>(a.q) + static_cast<int64_t>(row0) * (kDimRow * 2), rows * (kDimRow * 2));
-        }
-        Ids ids, next, later;
-        ask(w.get(), ids);
-        if (w.more()) ask(w.get(), next);
-        for (int x = it.begin; x < it.end && ok; ++x) {
-          if (w.more()) ask(w.get(), later);
-          if (scores) {
-            int rows[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rows[i] = i < subs ? row_of(ids, i) : 0;
-#pragma unroll 1
-            for (int part = 0; part < kKParts; ++part) {
-              if (!(ok = mbar_spin(bar(kBarKFree + stage), use ^ 1u, abort_flag))) break;
-              const uint32_t dst = sbase + stage * kKStageBytes, full = lead(kBarKFull + stage);
-              if (kFp8) {  // codes, behind the room that they will take when widened
-                mbar_arrive_expect_tx(bar(kBarRaw + stage), kKStageBytes / 2);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (i < subs)
-                    tma_load_2d(dst + kKStageBytes / 2 + i * unit * 192, &p.chunks3, bar(kBarRaw + stage), 192 * part, rows[i]);
-              } else if (half == 0) {
-                mbar_arrive_expect_tx(bar(kBarKFull + stage), 2 * kKStageBytes);
-              }
-              if (kFp8) {
-              } else if (unit == 64) {
-                tma2_load_3d(dst, &p.chunks3, full, 0, rows[0], 3 * part);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (i < subs)
-                    for (int c = 0; c < 3; ++c)
-                      tma2_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, full, 64 * (3 * part + c), rows[i]);
-              }
-              ++issued;
-              if (++stage == kKStages) {
-                stage = 0;
-                use ^= 1u;
-              }
-            }
-          } else {
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              if (!ok || !(ok = mbar_spin(bar(kBarVFree + stage), use ^ 1u, abort_flag))) break;
-              const uint32_t dst = sbase + kOffV + stage * kVStageBytes, full = bar(kBarVFull + stage);
-              mbar_arrive_expect_tx(kFp8 ? bar(kBarRaw + stage) : full, kFp8 ? kVStageBytes / 2 : kVStageBytes);
-              if (unit == 64 && !kFp8) {
-                tma_load_3d(dst, &p.chunks4, full, 0, row_of(ids, part), 4 * static_cast<int>(half));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const int j = i - part * (subs / 2);
-                  if (i < subs && j >= 0 && j < subs / 2) {
-                    const int r = row_of(ids, i);
-                    if (kFp8)
-                      tma_load_2d(dst + kVStageBytes / 2 + j * unit * 256, &p.chunks4, bar(kBarRaw + stage),
-                                  256 * static_cast<int>(half), r);
-                    for (int c = 0; c < (kFp8 ? 0 : 4); ++c)
-                      tma_load_2d(dst + c * kChunk + j * unit * 128, &p.rows, full, 256 * static_cast<int>(half) + 64 * c, r);
-                  }
-                }
-              }
-              ++issued;
-              if (++stage == kVStages) {
-                stage = 0;
-                use ^= 1u;
-              }
-            }
-          }
-          ids = next;
-          next = later;
+    // the accumulators' pair all positions, its 256 value dims. A lane has a copy's page id,
+    // asked for two blocks ahead; a stage's copies are one instruction of several lanes, or one
+    // copy. (Ids looked up as they were needed, and a copy for each 64 dims one after the
+    // other, it took this warp 6,100 cycles a block.)
+    const int subs = (scores ? 64 : 128) / unit;  // copies along the positions
+    const int offset = (scores ? 64 * static_cast<int>(half) : 0) + unit * lane;
+    const int layer_row0 = static_cast<int>(static_cast<int64_t>(a.layer) * a.num_pages * a.page_size);
+    const int no_row = static_cast<int>(static_cast<int64_t>(a.num_layers) * a.num_pages * a.page_size);  // reads as zeros
+    bool ok = true;
+    uint32_t stage = 0, use = 0, issued = 0;  // of the ring
+    struct Page {
+      int id;  // kNone: no position of the segment
+      int t;
+    };
+    constexpr int kNone = INT_MIN;
+    int owner = -1, list_pages = a.max_blocks;
+    const int32_t* list = nullptr;
+    auto ask = [&](const Block& b) {
+      if (b.owner != owner) {
+        owner = b.owner;
+        if (a.page_indptr) {
+          list = a.page_ids + a.page_indptr[owner];
+          list_pages = a.page_indptr[owner + 1] - a.page_indptr[owner];
+        } else {
+          list = a.page_ids + static_cast<int64_t>(owner) * a.max_blocks;
         }
       }
+      const int t = b.t0 + offset, j = t >> page_shift;
+      const bool in = lane < subs && t < b.t0 + b.v1 && t + unit > b.t0 + b.v0;
+      return Page{!in ? kNone : j < list_pages ? list[j] : -1, t};
+    };
+    auto row_of = [&](const Page& g) -> int {
+      if (g.id >= 0 && g.id < a.num_pages) return layer_row0 + (g.id << page_shift) + (g.t & (a.page_size - 1));
+      if (g.id != kNone && scores) atomicOr(&hd->status, MLA_STATUS_BAD_PAGE);
+      return no_row;
+    };
+    uint32_t n = 0;
+    for (int k = item0; k < item1 && ok; ++k) {
+      const ShItem it = items[k];
+      Walk w;
+      w.start(a, it);
+      Block b[3];  // this one, the next two
+      Page g[3];
+      b[0] = w.get();
+      g[0] = ask(b[0]);
+      if (w.more()) {
+        b[1] = w.get();
+        g[1] = ask(b[1]);
+      }
+      if (scores && lane == 0 && k + 1 < item1) {  // the next item's queries (each block its rows) on their way to L2
+        const int row0 = items[k + 1].row0 + 128 * static_cast<int>(half);
+        const int rows = min(items[k + 1].rows - 128 * static_cast<int>(half), 128);
+        if (rows > 0)
+          prefetch_l2(static_cast<const uint8_t*>(a.q) + static_cast<int64_t>(row0) * (kDimRow * 2), rows * (kDimRow * 2));
+      }
+      for (int x = it.begin; x < it.end && ok; ++x, ++n) {
+        if (w.more()) {
+          b[2] = w.get();
+          g[2] = ask(b[2]);
+        }
+        const int row = row_of(g[0]);
+        if (scores) {
+          if (lane == 0) {  // what the softmax warps need of the block
+            notes[n % kNotes] = b[0];
+            mbar_arrive(bar(kBarNote + n % kNotes));
+          }
+          const int i = unit == 64 ? 0 : lane / 3, c = lane % 3;
+          const int copied = __shfl_sync(0xffffffffu, row, i & 31);
+#pragma unroll 1
+          for (int part = 0; part < kKParts; ++part) {
+            if (!(ok = warp_wait(bar(kBarKFree + stage), use ^ 1u))) break;
+            const uint32_t dst = sbase + stage * kKStageBytes, full = lead(kBarKFull + stage);
+            if (kFp8) {  // codes, behind the room that they will take when widened
+              if (lane == 0) mbar_arrive_expect_tx(bar(kBarRaw + stage), kKStageBytes / 2);
+              if (lane < subs)
+                tma_load_2d(dst + kKStageBytes / 2 + lane * unit * 192, &p.chunks3, bar(kBarRaw + stage), 192 * part, row);
+            } else {
+              if (half == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarKFull + stage), 2 * kKStageBytes);
+              if (unit == 64) {
+                if (lane == 0) tma2_load_3d(dst, &p.chunks3, full, 0, copied, 3 * part);
+              } else if (lane < 3 * subs) {
+                tma2_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, full, 64 * (3 * part + c), copied);
+              }
+            }
+            ++issued;
+            if (++stage == kKStages) {
+              stage = 0;
+              use ^= 1u;
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            if (!(ok = warp_wait(bar(kBarVFree + stage), use ^ 1u))) break;
+            const uint32_t dst = sbase + kOffV + stage * kVStageBytes;
+            const uint32_t full = bar((kFp8 ? kBarRaw : kBarVFull) + stage);
+            const int j = lane - part * (subs / 2);
+            if (lane == 0) mbar_arrive_expect_tx(full, kFp8 ? kVStageBytes / 2 : kVStageBytes);
+            if (j >= 0 && j < subs / 2) {
+              if (kFp8) tma_load_2d(dst + kVStageBytes / 2 + j * unit * 256, &p.chunks4, full, 256 * static_cast<int>(half), row);
+              else tma_load_3d(dst + j * unit * 512, &p.chunks4, full, 0, row, 4 * static_cast<int>(half));
+            }
+            ++issued;
+            if (++stage == kVStages) {
+              stage = 0;
+              use ^= 1u;
+            }
+          }
+        }
+        b[0] = b[1], b[1] = b[2];
+        g[0] = g[1], g[1] = g[2];
+      }
+    }
+    if (lane == 0) {
       if (!ok) fail();
       if (*abort_flag && (kFp8 || !scores || half == 0)) {  // let the copies in flight land (each wait bounded)
-        const uint32_t n = scores ? kKStages : kVStages;
-        for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i)
-          mbar_wait(bar((kFp8 ? kBarRaw : scores ? kBarKFull : kBarVFull) + i % n), (i / n) & 1u, nullptr);
+        const uint32_t stages = scores ? kKStages : kVStages;
+        for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
+          mbar_wait(bar((kFp8 ? kBarRaw : scores ? kBarKFull : kBarVFull) + i % stages), (i / stages) & 1u, nullptr);
       }
     }
   } else if (kFp8 && warp >= kConvertWarp) {
@@ -551,16 +547,19 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
           if (!(ok = spin(bar(kBarPReady + buf), (n / kPBuffers) & 1u))) break;
           tc_fence_after();
           const uint32_t pa = desc_lo(sbase + buf * kPBytes);
+          // V lies as it was copied: `span` positions of four chunks, then the next
+          const uint32_t span = kFp8 ? 64 : unit;
           const int k0 = b.v0 >> 4, k1 = (b.v1 + 15) >> 4;  // steps of 16 positions
           bool add = b.add;
           for (int h = 0; h < 2; ++h) {
-            const uint32_t vb = desc_lo_mn(sbase + kOffV + stage * kVStageBytes, kChunk);
+            const uint32_t vb = desc_lo_mn(sbase + kOffV + stage * kVStageBytes, span * 128);
             for (int e = max(k0, 4 * h); e < min(k1, 4 * h + 4); ++e) {
-              const uint32_t pe = pa + h * (kPChunk >> 4) + 2 * (e & 3), ve = vb + 128 * (e & 3);
+              const uint32_t pe = pa + h * (kPChunk >> 4) + 2 * (e & 3), t16 = 16 * (e & 3);
+              const uint32_t ve = vb + (t16 / span * 512 * span + t16 % span * 128 >> 4);
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                if (all) mma2_bf16_ss(tmem + 256 * c, pe, ve + c * (2 * kChunk >> 4), idesc, add);
-                else mma2_bf16_ss_rows(tmem + 256 * c, pe, ve + c * (2 * kChunk >> 4), idesc, off, add);
+                if (all) mma2_bf16_ss(tmem + 256 * c, pe, ve + c * 16 * span, idesc, add);
+                else mma2_bf16_ss_rows(tmem + 256 * c, pe, ve + c * 16 * span, idesc, off, add);
               }
               add = true;
             }
@@ -681,13 +680,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       const int i = static_cast<int>((static_cast<int64_t>(it.row0) + r) / a.num_heads) % a.q_len;
       ref = sum_ref = kNoMax;
       l = 0.f;
-      const uint32_t first = n;
-      last = n + (it.end - it.begin) - 1;
-      Walk w;
-      w.start(a, it);
-      for (; n <= last; ++n) {
-        const Block b = w.get();
-        if ((n & 1u) != static_cast<uint32_t>(group)) continue;
+      const uint32_t first = k + 1 == item0 ? 0 : last + 1;
+      n = first;
+      last = first + (it.end - it.begin) - 1;
+      n += (n ^ group) & 1u;  // (the other group's block first)
+      for (; n <= last; n += 2) {
+        if (!(ok = warp_wait_block(bar(kBarNote + n % kNotes), (n / kNotes) & 1u))) break;
+        const Block b = notes[n % kNotes];
         const bool here = b.row_lo < w0 + 32 && b.row_hi > w0;
         const bool mine = r >= b.row_lo && r < b.row_hi;
         if (!(ok = warp_wait(bar(kBarS + group), (n >> 1) & 1u))) break;
@@ -795,16 +794,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
           if (!(ok = warp_wait_block(bar(kBarVFull + stage), use))) break;
           const uint32_t v = sbase + kOffV + stage * kVStageBytes;
           const int lo0 = (b.v0 & ~15) - 64 * h, lo1 = b.v0 - 64 * h, hi0 = b.v1 - 64 * h, hi1 = ((b.v1 + 15) & ~15) - 64 * h;
+          const int span = kFp8 ? 64 : unit;
+          auto at_row = [&](int t) { return v + t / span * 512 * span + ((lane >> 3) * span + t % span) * 128 + 16 * (lane & 7); };
           auto zero = [&](int from, int to) {  // 512 bytes a row: a warp each
             for (int t = max(from, 0) + warp; t < min(to, 64); t += kWorkers) {
-              st_shared_v4(v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7), 0, 0, 0, 0);
+              st_shared_v4(at_row(t), 0, 0, 0, 0);
               wrote = true;
             }
           };
           if (b.v0 & 15) zero(lo0, lo1);
           if (b.v1 & 15) zero(hi0, hi1);
           for (int t = max(b.end - 64 * h, 0) + warp; t < min(hi0, 64); t += kWorkers) {
-            const uint32_t at = v + (lane >> 3) * kChunk + t * 128 + 16 * (lane & 7);
+            const uint32_t at = at_row(t);
             uint32_t x[4];
             ld_shared_v4(at, x[0], x[1], x[2], x[3]);
             bool odd = false;
