@@ -29,6 +29,8 @@
 #include <limits.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "../../include/mla_decode.h"
 #include "ptx_shared.cuh"
 #include "shared_internal.h"
@@ -37,7 +39,7 @@ namespace mla {
 namespace {
 
 constexpr int kWorkers = 8;                 // warps of softmax or accumulators, two groups of four
-constexpr int kProducerWarp = kWorkers, kIssueWarp = kWorkers + 1, kSendWarp = kWorkers + 2;
+constexpr int kProducerWarp = kWorkers, kIssueWarp = kWorkers + 1, kSendWarp = kWorkers + 2, kProducerWarp2 = kWorkers + 3;
 constexpr int kConvertWarp = kWorkers + 4;  // (fp8 pools) four that widen the codes
 // Registers a thread after setmaxnreg; they add up to the launch's 3 x 168 (bf16 pools) or
 // 4 x 128.
@@ -271,18 +273,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
   } else if (warp >= kWorkers) {
     setmaxnreg_dec<Regs<kFp8>::kOther>();
   }
-  if (warp == kProducerWarp) {
+  if (warp == kProducerWarp || warp == kProducerWarp2) {
     // Each block of the scores' pair brings its 64 of a block's positions, all dims; each of
     // the accumulators' pair all positions, its 256 value dims. A lane has a copy's page id,
-    // asked for two blocks ahead; a stage's copies are one instruction of several lanes, or one
-    // copy. (Ids looked up as they were needed, and a copy for each 64 dims one after the
-    // other, it took this warp 6,100 cycles a block.)
+    // asked for a block ahead; a stage's copies are one instruction of several lanes, or one copy.
+    // Two warps take the even and the odd blocks: one needs 2,300 cycles for a block, as long
+    // as the products. (With ids looked up as they were needed, and a copy for each 64 dims
+    // one after the other, it was 6,100.)
+    const uint32_t mine = warp == kProducerWarp ? 0 : 1;
     const int subs = (scores ? 64 : 128) / unit;  // copies along the positions
     const int offset = (scores ? 64 * static_cast<int>(half) : 0) + unit * lane;
     const int layer_row0 = static_cast<int>(static_cast<int64_t>(a.layer) * a.num_pages * a.page_size);
     const int no_row = static_cast<int>(static_cast<int64_t>(a.num_layers) * a.num_pages * a.page_size);  // reads as zeros
     bool ok = true;
-    uint32_t stage = 0, use = 0, issued = 0;  // of the ring
+    uint32_t issued = 0;  // stages, of blocks up to this warp's last
     struct Page {
       int id;  // kNone: no position of the segment
       int t;
@@ -309,41 +313,53 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       if (g.id != kNone && scores) atomicOr(&hd->status, MLA_STATUS_BAD_PAGE);
       return no_row;
     };
-    uint32_t n = 0;
+    constexpr uint32_t kStages = kKStages;
+    uint32_t n0 = 0;  // blocks of the items before
     for (int k = item0; k < item1 && ok; ++k) {
       const ShItem it = items[k];
       Walk w;
       w.start(a, it);
-      Block b[3];  // this one, the next two
-      Page g[3];
-      b[0] = w.get();
-      g[0] = ask(b[0]);
-      if (w.more()) {
-        b[1] = w.get();
-        g[1] = ask(b[1]);
+      const uint32_t blocks = it.end - it.begin;
+      uint32_t at = (n0 ^ mine) & 1u;  // this warp's first block of the item
+      Block now = {}, next = {};
+      Page page = {kNone, 0}, next_page = {kNone, 0};
+      auto take = [&] {  // a block of this warp's; the next is the other's
+        const Block b = w.get();
+        if (w.more()) w.get();
+        return b;
+      };
+      if (at == 1 && w.more()) w.get();
+      if (at < blocks) {
+        now = take();
+        page = ask(now);
       }
-      if (scores && lane == 0 && k + 1 < item1) {  // the next item's queries (each block its rows) on their way to L2
+      if (scores && mine == 0 && lane == 0 && k + 1 < item1) {  // the next item's queries (each block its rows) on their way to L2
         const int row0 = items[k + 1].row0 + 128 * static_cast<int>(half);
         const int rows = min(items[k + 1].rows - 128 * static_cast<int>(half), 128);
         if (rows > 0)
           prefetch_l2(static_cast<const uint8_t*>(a.q) + static_cast<int64_t>(row0) * (kDimRow * 2), rows * (kDimRow * 2));
       }
-      for (int x = it.begin; x < it.end && ok; ++x, ++n) {
+      for (; at < blocks && ok; at += 2) {
         if (w.more()) {
-          b[2] = w.get();
-          g[2] = ask(b[2]);
+          next = take();
+          next_page = ask(next);
         }
-        const int row = row_of(g[0]);
+        const int row = row_of(page);
+        const uint32_t n = n0 + at;
         if (scores) {
-          if (lane == 0) {  // what the softmax warps need of the block
-            notes[n % kNotes] = b[0];
-            mbar_arrive(bar(kBarNote + n % kNotes));
-          }
           const int i = unit == 64 ? 0 : lane / 3, c = lane % 3;
           const int copied = __shfl_sync(0xffffffffu, row, i & 31);
 #pragma unroll 1
-          for (int part = 0; part < kKParts; ++part) {
-            if (!(ok = warp_wait(bar(kBarKFree + stage), use ^ 1u))) break;
+          for (uint32_t part = 0; part < kKParts; ++part) {
+            const uint32_t use = kKParts * n + part, stage = use % kStages;
+            if (!(ok = warp_wait(bar(kBarKFree + stage), (use / kStages & 1u) ^ 1u))) break;
+            issued = use + 1;
+            if (part == 0 && lane == 0) {
+              // What the softmax warps need of the block. (Now that block n - 2 is multiplied in
+              // part, its buffer of scores was free: block n - 4's note has been read.)
+              notes[n % kNotes] = now;
+              mbar_arrive(bar(kBarNote + n % kNotes));
+            }
             const uint32_t dst = sbase + stage * kKStageBytes, full = lead(kBarKFull + stage);
             if (kFp8) {  // codes, behind the room that they will take when widened
               if (lane == 0) mbar_arrive_expect_tx(bar(kBarRaw + stage), kKStageBytes / 2);
@@ -357,101 +373,93 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
                 tma2_load_2d(dst + c * kChunk + i * unit * 128, &p.rows, full, 64 * (3 * part + c), copied);
               }
             }
-            ++issued;
-            if (++stage == kKStages) {
-              stage = 0;
-              use ^= 1u;
-            }
           }
         } else {
 #pragma unroll 1
-          for (int part = 0; part < 2; ++part) {
-            if (!(ok = warp_wait(bar(kBarVFree + stage), use ^ 1u))) break;
+          for (uint32_t part = 0; part < 2; ++part) {
+            const uint32_t use = 2 * n + part, stage = use % kVStages;
+            if (!(ok = warp_wait(bar(kBarVFree + stage), (use / kVStages & 1u) ^ 1u))) break;
+            issued = use + 1;
             const uint32_t dst = sbase + kOffV + stage * kVStageBytes;
             const uint32_t full = bar((kFp8 ? kBarRaw : kBarVFull) + stage);
-            const int j = lane - part * (subs / 2);
+            const int j = lane - static_cast<int>(part) * (subs / 2);
             if (lane == 0) mbar_arrive_expect_tx(full, kFp8 ? kVStageBytes / 2 : kVStageBytes);
             if (j >= 0 && j < subs / 2) {
               if (kFp8) tma_load_2d(dst + kVStageBytes / 2 + j * unit * 256, &p.chunks4, full, 256 * static_cast<int>(half), row);
               else tma_load_3d(dst + j * unit * 512, &p.chunks4, full, 0, row, 4 * static_cast<int>(half));
             }
-            ++issued;
-            if (++stage == kVStages) {
-              stage = 0;
-              use ^= 1u;
-            }
           }
         }
-        b[0] = b[1], b[1] = b[2];
-        g[0] = g[1], g[1] = g[2];
+        now = next;
+        page = next_page;
       }
+      n0 += blocks;
     }
     if (lane == 0) {
       if (!ok) fail();
       if (*abort_flag && (kFp8 || !scores || half == 0)) {  // let the copies in flight land (each wait bounded)
         const uint32_t stages = scores ? kKStages : kVStages;
         for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
-          mbar_wait(bar((kFp8 ? kBarRaw : scores ? kBarKFull : kBarVFull) + i % stages), (i / stages) & 1u, nullptr);
+          mbar_wait(bar((kFp8 ? kBarRaw : scores ? kBarKFull : kBarVFull) + i % stages), (i / stages) & 1u, nullptr, 100000000ull);
       }
     }
   } else if (kFp8 && warp >= kConvertWarp) {
     // Codes, 64 positions of `width` each, widened to f16 where they lie: read by all four
     // warps before any of them writes. (e4m3 values are exact in f16.)
-    const int width = scores ? 192 : 256, stages = scores ? kKStages : kVStages;
-    const int parts = scores ? kKParts : 2, bytes = scores ? kKStageBytes : kVStageBytes;
-    const int t = threadIdx.x - 32 * kConvertWarp, per_row = width / 16;
-    const uint32_t ring = sbase + (scores ? 0 : kOffV);
     int blocks = 0;
     for (int k = item0; k < item1; ++k) blocks += items[k].end - items[k].begin;
-    uint32_t use = 0, meet = 0;
-    int stage = 0;
     bool ok = true;
-    for (int n = 0; n < parts * blocks && ok; ++n) {
-      if (!(ok = warp_wait_block(bar(kBarRaw + stage), use))) break;
-      const uint32_t slot = ring + stage * bytes;
-      uint32_t v[8][4];
+    auto widen = [&](auto width, auto stages, auto parts, uint32_t ring, auto tell) {
+      constexpr int kWidth = decltype(width)::value, kStages = decltype(stages)::value, kParts = decltype(parts)::value;
+      constexpr int kPieces = 64 * kWidth / 16 / 128, kPerRow = kWidth / 16, kBytes = 64 * kWidth * 2;
+      const int t = threadIdx.x - 32 * kConvertWarp;
+      uint32_t use = 0, meet = 0;
+      int stage = 0;
+      for (int n = 0; n < kParts * blocks; ++n) {
+        if (!(ok = warp_wait_block(bar(kBarRaw + stage), use))) break;
+        const uint32_t slot = ring + stage * kBytes;
+        uint32_t v[kPieces][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < (scores ? 6 : 8)) ld_shared_v4(slot + bytes / 2 + 16 * (t + 128 * i), v[i][0], v[i][1], v[i][2], v[i][3]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarMeet));
-      if (!(ok = warp_wait(bar(kBarMeet), meet))) break;
-      meet ^= 1u;
+        for (int i = 0; i < kPieces; ++i) ld_shared_v4(slot + kBytes / 2 + 16 * (t + 128 * i), v[i][0], v[i][1], v[i][2], v[i][3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarMeet));
+        if (!(ok = warp_wait(bar(kBarMeet), meet))) break;
+        meet ^= 1u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i < (scores ? 6 : 8)) {
-          const int piece = t + 128 * i, row = piece / per_row, q = piece % per_row, chunk = q >> 2;
-          const uint32_t at = slot + chunk * kChunk + row * 128;
+        for (int i = 0; i < kPieces; ++i) {
+          const int piece = t + 128 * i, row = piece / kPerRow, q = piece % kPerRow, chunk = q >> 2;
+          const uint32_t at = slot + chunk * kChunk + row * 128, first = 2 * (q & 3) ^ (row & 7);
           uint32_t f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = e4m3x2_to_f16x2(static_cast<uint16_t>(v[i][e >> 1] >> (16 * (e & 1))));
           // (odd chunks the other half first: a phase of eight threads has two chunks' pieces)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const bool hi = (j ^ chunk) & 1;
-            st_shared_v4(at + 16 * ((2 * (q & 3) + (hi ? 1 : 0)) ^ (row & 7)), hi ? f[4] : f[0], hi ? f[5] : f[1],
-                         hi ? f[6] : f[2], hi ? f[7] : f[3]);
-          }
+          const bool hi = chunk & 1;
+          st_shared_v4(at + 16 * (first ^ (hi ? 1 : 0)), hi ? f[4] : f[0], hi ? f[5] : f[1], hi ? f[6] : f[2], hi ? f[7] : f[3]);
+          st_shared_v4(at + 16 * (first ^ (hi ? 0 : 1)), hi ? f[0] : f[4], hi ? f[1] : f[5], hi ? f[2] : f[6], hi ? f[3] : f[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tell(stage);
+        if (++stage == kStages) {
+          stage = 0;
+          use ^= 1u;
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (scores) mbar_arrive_cluster(lead(kBarKFull + stage));
-        else mbar_arrive(bar(kBarVFull + stage));
-      }
-      if (++stage == stages) {
-        stage = 0;
-        use ^= 1u;
-      }
-    }
+    };
+    using std::integral_constant;
+    if (scores)
+      widen(integral_constant<int, 192>{}, integral_constant<int, kKStages>{}, integral_constant<int, kKParts>{}, sbase,
+            [&](int stage) { mbar_arrive_cluster(lead(kBarKFull + stage)); });
+    else
+      widen(integral_constant<int, 256>{}, integral_constant<int, kVStages>{}, integral_constant<int, 2>{}, sbase + kOffV,
+            [&](int stage) { mbar_arrive(bar(kBarVFull + stage)); });
     if (!ok) fail();
-  } else if (warp >= kSendWarp) {
-    // One lane for each group of softmax warps sends P to the other pair, rows that attend the
-    // block alone, so that no softmax warp waits for a buffer there. (Stored row by row into
-    // the peer's memory by the softmax warps it took them 4,600 cycles a block.)
+  } else if (warp == kSendWarp) {
+    // One lane sends P to the other pair, rows that attend the block alone, so that no softmax
+    // warp waits for a buffer there. (Stored row by row into the peer's memory by the softmax
+    // warps it took them 4,600 cycles a block.)
     if (scores && lane == 0) {
-      const uint32_t group = warp - kSendWarp, there = mapa(sbase, rank ^ 2);
+      const uint32_t there = mapa(sbase, rank ^ 2);
       uint32_t n = 0;
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
@@ -460,9 +468,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         w.start(a, it);
         for (; w.more(); ++n) {
           const Block b = w.get();
-          if ((n & 1u) != group) continue;
           const int lo = max(b.row_lo - 128 * static_cast<int>(half), 0), hi = min(b.row_hi - 128 * static_cast<int>(half), 128);
-          const uint32_t buf = n % kPBuffers, rb = peer(kBarP + buf);
+          const uint32_t group = n & 1u, buf = n % kPBuffers, rb = peer(kBarP + buf);
           if (!(ok = spin(bar(kBarStaged + group), (n >> 1) & 1u))) break;
           if (!(ok = spin(bar(kBarPFree + buf), ((n / kPBuffers) & 1u) ^ 1u))) break;
           mbar_arrive_expect_tx_relaxed(rb, hi > lo ? (hi - lo) * 256 + 512 : 0);
@@ -476,7 +483,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         }
       }
       if (!ok) fail();
-    } else if (!scores && warp == kSendWarp && lane == 0) {
+    } else if (!scores && lane == 0) {
       // P has landed: its room in the other pair is free. (Told by the accumulators' warps,
       // which wait for V as well, it took long enough to bound the whole.)
       int blocks = 0;
