@@ -261,9 +261,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
   Block* notes = reinterpret_cast<Block*>(smem + kOffNotes);
   // (Buffers at another start than the tensor core's patterns ask for: never seen; nothing is
   // computed then, and the status tells.)
-  const int* cstart = reinterpret_cast<const int*>(a.ws + a.lay.cluster_start);
+  const ShCluster* record = reinterpret_cast<const ShCluster*>(a.ws + a.lay.clusters) + cluster;
   const ShItem* items = reinterpret_cast<const ShItem*>(a.ws + a.lay.items);
-  int item0 = cstart[cluster], item1 = cstart[cluster + 1];  // (asked for with the header)
+  int item0 = record->item0, item1 = record->item1;  // (asked for with the header)
+  auto item = [&](int k) -> const ShItem& { return k == item0 ? record->first : items[k]; };
   const bool planned = sh_planned(hd, a) && (sbase & 1023u) == 0;
   if (!planned && threadIdx.x == 0 && rank == 0) atomicOr(&hd->status, MLA_STATUS_PLAN_MISMATCH);
   if (!planned || cluster >= hd->num_clusters) item0 = item1 = 0;
@@ -316,7 +317,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
     constexpr uint32_t kStages = kKStages;
     uint32_t n0 = 0;  // blocks of the items before
     for (int k = item0; k < item1 && ok; ++k) {
-      const ShItem it = items[k];
+      const ShItem it = item(k);
       Walk w;
       w.start(a, it);
       const uint32_t blocks = it.end - it.begin;
@@ -334,8 +335,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         page = ask(now);
       }
       if (scores && mine == 0 && lane == 0 && k + 1 < item1) {  // the next item's queries (each block its rows) on their way to L2
-        const int row0 = items[k + 1].row0 + 128 * static_cast<int>(half);
-        const int rows = min(items[k + 1].rows - 128 * static_cast<int>(half), 128);
+        const int row0 = item(k + 1).row0 + 128 * static_cast<int>(half);
+        const int rows = min(item(k + 1).rows - 128 * static_cast<int>(half), 128);
         if (rows > 0)
           prefetch_l2(static_cast<const uint8_t*>(a.q) + static_cast<int64_t>(row0) * (kDimRow * 2), rows * (kDimRow * 2));
       }
@@ -407,7 +408,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
     // Codes, 64 positions of `width` each, widened to f16 where they lie: read by all four
     // warps before any of them writes. (e4m3 values are exact in f16.)
     int blocks = 0;
-    for (int k = item0; k < item1; ++k) blocks += items[k].end - items[k].begin;
+    for (int k = item0; k < item1; ++k) blocks += item(k).end - item(k).begin;
     bool ok = true;
     auto widen = [&](auto width, auto stages, auto parts, uint32_t ring, auto tell) {
       constexpr int kWidth = decltype(width)::value, kStages = decltype(stages)::value, kParts = decltype(parts)::value;
@@ -463,7 +464,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       uint32_t n = 0;
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
-        const ShItem it = items[k];
+        const ShItem it = item(k);
         Walk w;
         w.start(a, it);
         for (; w.more(); ++n) {
@@ -487,7 +488,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       // P has landed: its room in the other pair is free. (Told by the accumulators' warps,
       // which wait for V as well, it took long enough to bound the whole.)
       int blocks = 0;
-      for (int k = item0; k < item1; ++k) blocks += items[k].end - items[k].begin;
+      for (int k = item0; k < item1; ++k) blocks += item(k).end - item(k).begin;
       bool ok = true;
       for (int n = 0; n < blocks && ok; ++n) {
         ok = spin(bar(kBarP + n % kPBuffers), (n / kPBuffers) & 1u);
@@ -502,7 +503,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       uint32_t n = 0, stage = 0, use = 0;
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
-        const int blocks = items[k].end - items[k].begin;
+        const int blocks = item(k).end - item(k).begin;
         ok = spin(bar(kBarQ), (k - item0) & 1u);
         for (int x = 0; x < blocks && ok; ++x, ++n) {
           const uint32_t buf = n & 1u;
@@ -536,7 +537,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       uint32_t n = 0, stage = 0;
       bool ok = true;
       for (int k = item0; k < item1 && ok; ++k) {
-        const ShItem it = items[k];
+        const ShItem it = item(k);
         Walk w;
         w.start(a, it);
         ok = spin(bar(kBarOFree), ((k - item0) & 1u) ^ 1u);
@@ -610,26 +611,28 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         tc_fence_after();
       }
       if (k + 1 < item1) {
-        const int row0 = items[k + 1].row0, rows = items[k + 1].rows;
+        // (rows that attend nothing of the item may hold anything)
+        const int row0 = item(k + 1).row0, rows = item(k + 1).row_hi, skip = item(k + 1).row_lo;
         const uint8_t* src = static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(row0) + w0) * (kDimRow * 2);
         uint4 rope[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // the rope dims: 16 bytes of row 8 i + lane / 4
           const int row = 8 * i + (lane >> 2);
           rope[i] = make_uint4(0, 0, 0, 0);
-          if (w0 + row < rows)
+          if (w0 + row >= skip && w0 + row < rows)
             rope[i] = *reinterpret_cast<const uint4*>(src + row * (kDimRow * 2) + 2 * kDimCkv + 64 * group + 16 * (lane & 3));
         }
         // (Pieces of 32 bytes of 32 rows a load; by whole lines and turned, as the results go
         // out, it took longer: the turns' instructions have to be fetched for the first item.)
         const uint8_t* mine = src + lane * (kDimRow * 2) + 512 * group;
+        constexpr int kRounds = kFp8 ? 4 : 2, kWords = 128 / kRounds;  // (as registers allow)
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[64];
+        for (int h = 0; h < kRounds; ++h) {
+          uint32_t x[kWords];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (w0 + lane < rows) {
-              ld_global_v8(mine + 256 * h + 32 * c, x + 8 * c);
+          for (int c = 0; c < kWords / 8; ++c) {
+            if (w0 + lane >= skip && w0 + lane < rows) {
+              ld_global_v8(mine + 4 * kWords * h + 32 * c, x + 8 * c);
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e) x[8 * c + e] = 0;
@@ -637,11 +640,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
           }
           if (kFp8) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = bf16x2_to_f16x2(x[c]);
+            for (int c = 0; c < kWords; ++c) x[c] = bf16x2_to_f16x2(x[c]);
           }
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) tmem_st32(tbase + 128 * group + 64 * h + 32 * c, x + 32 * c);
+          for (int c = 0; c < kWords / 32; ++c) tmem_st32(tbase + 128 * group + kWords * h + 32 * c, x + 32 * c);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -683,7 +686,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         }
       }
       if (k + 1 >= item1) break;
-      const ShItem it = items[k + 1];
+      const ShItem it = item(k + 1);
       const int i = static_cast<int>((static_cast<int64_t>(it.row0) + r) / a.num_heads) % a.q_len;
       ref = sum_ref = kNoMax;
       l = 0.f;
@@ -783,7 +786,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
     uint32_t n = 0, stage = 0, use = 0;
     bool ok = true;
     for (int k = item0; k < item1 && ok; ++k) {
-      const ShItem it = items[k];
+      const ShItem it = item(k);
       Walk w;
       w.start(a, it);
       for (; w.more(); ++n) {
@@ -866,33 +869,47 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       const uint32_t stores = __ballot_sync(0xffffffffu, store);
       // columns [0, 128) of a side are the first block's dims, the others the second's
       auto dim_of = [&](int col) { return 128 * side + (col & 127) + (col >= 128 ? 256 : 0); };
-      if (part) {
+      if (stores == 0) {
+      } else if (part) {
         float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + (part_row - (lane & 3)) * kDimCkv + 8 * (lane & 3);
+        uint32_t o[2][32];  // (the next columns are asked for while these go out)
+        tmem_ld32(tO, o[0]);
+        tmem_wait_ld();
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-          turn(o, lane);
+        for (int c = 0; c < 8; c += 2) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (stores >> ((lane & 28) + i) & 1u) st_global_v8(dst + i * kDimCkv + dim_of(32 * c), o + 8 * i);
+          for (int h = 0; h < 2; ++h) {
+            if (c + h < 7) tmem_ld32(tO + 32 * (c + h + 1), o[h ^ 1]);
+            turn(o[h], lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (stores >> ((lane & 28) + i) & 1u) st_global_v8(dst + i * kDimCkv + dim_of(32 * (c + h)), o[h] + 8 * i);
+            __syncwarp();
+            tmem_wait_ld();
+          }
         }
       } else {
         uint8_t* dst = static_cast<uint8_t*>(a.out) + (out_row - (lane & 3)) * (kDimCkv * 2) + 32 * (lane & 3);
         const float inv = a.out_scale / ml.y;
+        uint32_t o[64];
+        tmem_ld32(tO, o);
+        tmem_ld32(tO + 32, o + 32);
+        tmem_wait_ld();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t o[64], pk[32];
-          tmem_ld32(tO + 64 * c, o);
-          tmem_ld32(tO + 64 * c + 32, o + 32);
-          tmem_wait_ld();
+          uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (c < 3) {
+            tmem_ld32(tO + 64 * c + 64, o);
+            tmem_ld32(tO + 64 * c + 96, o + 32);
+          }
           turn(pk, lane);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (stores >> ((lane & 28) + i) & 1u) st_global_v8(dst + i * kDimCkv * 2 + dim_of(64 * c) * 2, pk + 8 * i);
+          __syncwarp();
+          tmem_wait_ld();
         }
       }
       tc_fence_before();

@@ -24,7 +24,7 @@ constexpr int kShTokens = 128;
 constexpr int kShClusterBlocks = 4;  // thread blocks of a cluster
 // A tile's first block costs a cluster this many more (queries into place, the
 // pipeline's start, the result's way out).
-constexpr int kShItemCost = 6;
+constexpr int kShItemCost = 8;
 // Clusters are used as far as each has this many blocks.
 constexpr int kShLeastBlocks = 3;
 
@@ -59,8 +59,16 @@ struct ShItem {
   int row0, rows;      // the tile's
   int seg, seg_last;   // segment of the first block; the tile's last one
   int prefix_end;      // blocks of the prefix
-  int pad[7];
+  int row_lo, row_hi;  // rows of the tile that attend any of the blocks
+  int pad[5];
   ShSegment first;     // segment `seg`
+};
+
+// A cluster's items [item0, item1), and the first of them.
+struct ShCluster {
+  int item0, item1;
+  int pad[6];
+  ShItem first;
 };
 
 // A split tile.
@@ -75,7 +83,7 @@ struct ShGroup {
   int tile0;         // tiles of the groups before it
 };
 
-static_assert(sizeof(ShTile) == 32 && sizeof(ShSegment) == 32 && sizeof(ShItem) == 96, "16-byte words");
+static_assert(sizeof(ShTile) == 32 && sizeof(ShSegment) == 32 && sizeof(ShItem) == 96 && sizeof(ShCluster) == 128, "16-byte words");
 
 struct ShHeader {
   int status;  // sticky MLA_STATUS_* bits
@@ -87,7 +95,7 @@ struct ShHeader {
 static_assert(sizeof(ShHeader) == 256, "one header of 256 bytes");
 
 struct ShLayout {
-  size_t groups, tiles, segs, items, cluster_start, splits, stats, partial, total;
+  size_t groups, tiles, segs, items, clusters, splits, stats, partial, total;
   int max_tiles;
   int tile_rows;      // rows of a full tile: whole requests where they fit
   int segs_per_tile;  // at most
@@ -111,8 +119,8 @@ __host__ __device__ inline ShLayout sh_layout(int batch, int q_len, int heads, i
   off = align_up(off + sizeof(ShSegment) * static_cast<size_t>(tiles) * L.segs_per_tile, 256);
   L.items = off;
   off = align_up(off + sizeof(ShItem) * static_cast<size_t>(tiles + clusters), 256);
-  L.cluster_start = off;
-  off = align_up(off + sizeof(int) * static_cast<size_t>(clusters + 1), 256);
+  L.clusters = off;
+  off = align_up(off + sizeof(ShCluster) * static_cast<size_t>(clusters), 256);
   L.splits = off;
   off = align_up(off + sizeof(ShSplit) * static_cast<size_t>(clusters), 256);
   const size_t parts = 2 * static_cast<size_t>(clusters);
