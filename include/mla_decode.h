@@ -391,8 +391,9 @@ size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, 
  *             [0, batch]; otherwise MLA_STATUS_BAD_LENGTH is set and the plan is
  *             empty (decode calls with it write nothing).
  *   num_clusters: as for mla_decode_plan, of the clusters of this kernel.
- *   page_size is 16, 32, 64 or 128, num_heads 1 to 1024; batch * q_len *
- *   num_heads stays below 2^31 (q_len * num_heads below 2^30). */
+ *   page_size is 16, 32, 64 or 128, num_heads 1 to 1024, batch and num_prefixes
+ *   at most 2^22; batch * q_len * num_heads stays below 2^31 (q_len * num_heads
+ *   below 2^30). */
 size_t mla_decode_workspace_size_shared(int batch, int q_len, int num_heads, int num_prefixes);
 int mla_decode_plan_shared(const int32_t* context_lens, const int32_t* prefix_indptr, const int32_t* prefix_lens, int batch,
                            int num_prefixes, int q_len, int num_heads, int page_size, int num_clusters, void* workspace,
@@ -411,7 +412,11 @@ int mla_decode_plan_shared(const int32_t* context_lens, const int32_t* prefix_in
  * Arithmetic: fp32 accumulation and softmax sums; softmax weights are rounded to
  * the cache's type for the tensor core (bf16; f16 for fp8 pools, whose queries
  * are f16 as mla_decode's are and whose kv_scale multiplies the scores and the
- * output). Calls with the same plan give the same bits. */
+ * output). Calls with the same plan give the same bits. Of a request's new
+ * tokens those that a query does not see do not touch its result, whatever they
+ * hold; one that it sees and that holds an infinity counts as its score says
+ * (NaN, or nothing where the score is -inf). After MLA_STATUS_TIMEOUT out and lse
+ * are unspecified. */
 int mla_decode_shared(const mla_kv_pool* pool, int layer, const void* q, const int32_t* page_indptr, const int32_t* page_ids,
                       int max_blocks, int batch, int q_len, int num_heads, int num_prefixes, float softmax_scale,
                       void* workspace, void* out, float* lse, void* stream);

@@ -12,7 +12,8 @@ using mla::valid_pool;
 int done(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
 bool sizes_ok(int batch, int q_len, int heads, int prefixes) {
-  if (batch < 0 || q_len < 1 || heads < 1 || heads > 1024 || prefixes < 0) return false;
+  constexpr int kMost = 1 << 22;  // (a plan's records count in 32 bits)
+  if (batch < 0 || batch > kMost || q_len < 1 || heads < 1 || heads > 1024 || prefixes < 0 || prefixes > kMost) return false;
   return static_cast<int64_t>(batch) * q_len * heads < (1ll << 31) && static_cast<int64_t>(q_len) * heads < (1ll << 30);
 }
 

@@ -24,7 +24,9 @@ constexpr int kShTokens = 128;
 constexpr int kShClusterBlocks = 4;  // thread blocks of a cluster
 // A tile's first block costs a cluster this many more (queries into place, the
 // pipeline's start, the result's way out).
-constexpr int kShItemCost = 8;
+constexpr int kShItemCost = 4;
+// A piece of a prefix's blocks costs this many more than one of requests' own.
+constexpr int kShRowsCost = 5;
 // Clusters are used as far as each has this many blocks.
 constexpr int kShLeastBlocks = 3;
 
@@ -36,7 +38,8 @@ struct ShTile {
   int rows;
   int seg0, segs;  // its segments
   int blocks;      // of all of them
-  int pad[3];
+  int shared;      // those of the prefix
+  int pad[2];
 };
 
 // Positions [tok_lo, tok_hi) of request `owner`'s pages, which rows [row_lo, row_hi) of

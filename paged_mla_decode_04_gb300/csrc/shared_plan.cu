@@ -32,6 +32,14 @@ __device__ __forceinline__ int last_at_most(int n, int64_t x, F start) {
   return lo;
 }
 
+// Pieces of a tile of so many blocks (the prefix's among them), of a weight of `most` each:
+// no more than blocks.
+__device__ __forceinline__ int pieces_of(int blocks, int shared, int most) {
+  const int64_t weight = static_cast<int64_t>(blocks) * most + static_cast<int64_t>(shared) * kShRowsCost;  // (times most)
+  const int64_t unit = static_cast<int64_t>(most) * most;
+  return static_cast<int>(min((weight + unit - 1) / unit, static_cast<int64_t>(blocks)));
+}
+
 // A request's cached positions; none for a length out of range.
 __device__ __forceinline__ int length_of(int l) { return l < 0 || l >= kShMostLength ? 0 : l; }
 
@@ -138,6 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
       w.seg0 = t * a.lay.segs_per_tile + (shared_blocks == 0 ? 1 : 0);
       w.segs = b1 - b0 + 1 + (shared_blocks == 0 ? 0 : 1);
       w.blocks = done;
+      w.shared = shared_blocks;
       tiles[t] = w;
     }
   }
@@ -148,6 +157,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   //    sequence, cut into equal ranges. Most clusters then have an item more than they need;
   //  - apart, where there are no more tiles than clusters: each tile in pieces of at most
   //    `most` blocks, a cluster each, with the least `most` for which the clusters suffice.
+  //    A piece of the prefix counts kShRowsCost blocks more: all rows' queries come in and
+  //    all rows' sums go out, where a piece of requests' own positions has theirs only. So a
+  //    prefix's blocks weigh 1 + kShRowsCost / most.
   // (4 tiles of about 100 blocks, 36 clusters: 44 us a decode cut, 42 apart; 20 tiles of about
   // 32 blocks: 69 cut, 79 apart, where a piece has as much as a whole tile.)
   int64_t weight = 0;
@@ -162,15 +174,19 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   if (tid == 0) apart = 0;
   __syncthreads();
   if (warp == 0 && num_tiles > 0 && num_tiles <= a.clusters && num_tiles <= 128) {
-    int mine[4];  // blocks of tiles lane, lane + 32, ...
+    int mine[4], shared[4];  // blocks of tiles lane, lane + 32, ...; of their prefixes
 #pragma unroll
-    for (int j = 0; j < 4; ++j) mine[j] = lane + 32 * j < num_tiles ? tiles[lane + 32 * j].blocks : 0;
+    for (int j = 0; j < 4; ++j) {
+      const ShTile t = lane + 32 * j < num_tiles ? tiles[lane + 32 * j] : ShTile{};
+      mine[j] = t.blocks;
+      shared[j] = t.shared;
+    }
     int lo = kShLeastBlocks, hi = max(kShLeastBlocks, static_cast<int>(all));  // (all blocks in one piece a tile: always)
     while (lo < hi) {
       const int mid = lo + (hi - lo) / 2;
       int pieces = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) pieces += (mine[j] + mid - 1) / mid;
+      for (int j = 0; j < 4; ++j) pieces += pieces_of(mine[j], shared[j], mid);
       pieces = __reduce_add_sync(0xffffffffu, pieces);
       if (pieces <= a.clusters) hi = mid;
       else lo = mid + 1;
@@ -184,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   int64_t at = 0, num_items = 0, num_parts = 0, num_split = 0;
   for (int t0 = 0; t0 < num_tiles; t0 += blockDim.x) {
     const int t = t0 + tid;
-    const int blocks = t < num_tiles ? tiles[t].blocks : 0;
+    const int blocks = t < num_tiles ? tiles[t].blocks : 0, shared = t < num_tiles ? tiles[t].shared : 0;
     int64_t v[1] = {t < num_tiles ? blocks + kShItemCost : 0}, total[1];
     block_scan<1>(v, total, sh);
     const int64_t off = at + v[0] + kShItemCost;  // the tile's first block
@@ -192,7 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
     int c0 = 0, pieces = 0;
     if (t < num_tiles) {
       c0 = cluster_of(off);
-      pieces = most > 0 ? (blocks + most - 1) / most : cluster_of(off + blocks - 1) - c0 + 1;
+      pieces = most > 0 ? pieces_of(blocks, shared, most) : cluster_of(off + blocks - 1) - c0 + 1;
     }
     // items, partial sums and split tiles before this one's
     int64_t w[2] = {pieces, pieces > 1 ? pieces | (1ll << 40) : 0}, sums[2];
@@ -200,17 +216,17 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
     const int item0 = static_cast<int>(num_items + w[0]);
     const int part0 = static_cast<int>(num_parts + (w[1] & ((1ll << 40) - 1)));
     ShTile tile = {};
-    int prefix_end = 0;
-    if (pieces > 0) {
-      tile = tiles[t];
-      const ShSegment g = segs[tile.seg0];
-      if (g.base == g.tok_hi) prefix_end = (g.tok_hi + kShTokens - 1) / kShTokens;
-    }
+    if (pieces > 0) tile = tiles[t];
+    int end = 0;
     for (int k = 0; k < pieces; ++k) {
       ShItem i = {};
       if (most > 0) {
-        i.begin = static_cast<int>(static_cast<int64_t>(blocks) * k / pieces);
-        i.end = static_cast<int>(static_cast<int64_t>(blocks) * (k + 1) / pieces);
+        // equal weights (times most), a block at least
+        const int64_t heavy = static_cast<int64_t>(shared) * (most + kShRowsCost);
+        const int64_t to = (heavy + static_cast<int64_t>(blocks - shared) * most) * (k + 1) / pieces;
+        const int64_t upto = to <= heavy ? to / (most + kShRowsCost) : shared + (to - heavy) / most;
+        i.begin = end;
+        i.end = end = static_cast<int>(min(max(upto, static_cast<int64_t>(end + 1)), static_cast<int64_t>(blocks - (pieces - 1 - k))));
         i.cluster = item0 + k;
       } else {
         i.begin = static_cast<int>(max(range_begin(c0 + k), off) - off);
@@ -222,10 +238,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
       i.rows = tile.rows;
       i.seg = tile.seg0 + last_at_most(tile.segs, i.begin, [&](int j) { return segs[tile.seg0 + j].block0; });
       i.seg_last = tile.seg0 + tile.segs - 1;
-      i.prefix_end = prefix_end;
+      i.prefix_end = shared;
       i.first = segs[i.seg];
       i.row_lo = i.first.row_lo;
-      i.row_hi = i.begin < prefix_end
+      i.row_hi = i.begin < shared
                      ? tile.rows
                      : segs[tile.seg0 + last_at_most(tile.segs, i.end - 1, [&](int j) { return segs[tile.seg0 + j].block0; })].row_hi;
       items[item0 + k] = i;

@@ -40,7 +40,7 @@ def pool(mem, **kw):
 
 
 def test_workspace_size_refuses(lib):
-    for bad in [(-1, 1, 16, 1), (4, 0, 16, 1), (4, 1, 0, 1), (4, 1, 1025, 1), (4, 1, 16, -1), (1 << 20, 2, 1024, 1),
+    for bad in [(-1, 1, 16, 1), (4, 0, 16, 1), (4, 1, 0, 1), (4, 1, 1025, 1), (4, 1, 16, -1), (1 << 20, 2, 1024, 1), ((1 << 22) + 1, 1, 1, 1), (4, 1, 16, (1 << 22) + 1),
                 (1, 1 << 20, 1024, 1)]:
         assert lib.mla_decode_workspace_size_shared(*bad) == 0
 
