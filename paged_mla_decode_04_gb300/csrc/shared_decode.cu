@@ -412,31 +412,31 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
     bool ok = true;
     auto widen = [&](auto width, auto stages, auto parts, uint32_t ring, auto tell) {
       constexpr int kWidth = decltype(width)::value, kStages = decltype(stages)::value, kParts = decltype(parts)::value;
-      constexpr int kPieces = 64 * kWidth / 16 / 128, kPerRow = kWidth / 16, kBytes = 64 * kWidth * 2;
-      const int t = threadIdx.x - 32 * kConvertWarp;
+      constexpr int kChunks = kWidth / 64, kBytes = 64 * kWidth * 2;
+      // A thread has 16 codes of each chunk of rows t / 4 and t / 4 + 32: whatever eight threads
+      // write at a time lies in eight different banks, and all offsets are constants.
+      const int t = threadIdx.x - 32 * kConvertWarp, row = t >> 2, piece = t & 3;
+      const uint32_t from = ring + kBytes / 2 + row * kWidth + 16 * piece, to = ring + row * 128 + 16 * (2 * piece ^ (row & 7));
       uint32_t use = 0, meet = 0;
       int stage = 0;
       for (int n = 0; n < kParts * blocks; ++n) {
         if (!(ok = warp_wait_block(bar(kBarRaw + stage), use))) break;
-        const uint32_t slot = ring + stage * kBytes;
-        uint32_t v[kPieces][4];
+        uint32_t v[2 * kChunks][4];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) ld_shared_v4(slot + kBytes / 2 + 16 * (t + 128 * i), v[i][0], v[i][1], v[i][2], v[i][3]);
+        for (int i = 0; i < 2 * kChunks; ++i)
+          ld_shared_v4(from + stage * kBytes + (i & 1) * 32 * kWidth + (i >> 1) * 64, v[i][0], v[i][1], v[i][2], v[i][3]);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarMeet));
         if (!(ok = warp_wait(bar(kBarMeet), meet))) break;
         meet ^= 1u;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int piece = t + 128 * i, row = piece / kPerRow, q = piece % kPerRow, chunk = q >> 2;
-          const uint32_t at = slot + chunk * kChunk + row * 128, first = 2 * (q & 3) ^ (row & 7);
+        for (int i = 0; i < 2 * kChunks; ++i) {
           uint32_t f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = e4m3x2_to_f16x2(static_cast<uint16_t>(v[i][e >> 1] >> (16 * (e & 1))));
-          // (odd chunks the other half first: a phase of eight threads has two chunks' pieces)
-          const bool hi = chunk & 1;
-          st_shared_v4(at + 16 * (first ^ (hi ? 1 : 0)), hi ? f[4] : f[0], hi ? f[5] : f[1], hi ? f[6] : f[2], hi ? f[7] : f[3]);
-          st_shared_v4(at + 16 * (first ^ (hi ? 0 : 1)), hi ? f[0] : f[4], hi ? f[1] : f[5], hi ? f[2] : f[6], hi ? f[3] : f[7]);
+          const uint32_t at = to + stage * kBytes + (i >> 1) * kChunk + (i & 1) * 32 * 128;
+          st_shared_v4(at, f[0], f[1], f[2], f[3]);
+          st_shared_v4(at ^ 16, f[4], f[5], f[6], f[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
