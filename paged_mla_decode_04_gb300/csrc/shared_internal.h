@@ -84,6 +84,8 @@ struct ShGroup {
   int first, count;  // requests
   int prefix;        // positions shared
   int tile0;         // tiles of the groups before it
+  int tile_rows;     // of a full tile
+  int pad[3];
 };
 
 static_assert(sizeof(ShTile) == 32 && sizeof(ShSegment) == 32 && sizeof(ShItem) == 96 && sizeof(ShCluster) == 128, "16-byte words");
@@ -100,18 +102,19 @@ static_assert(sizeof(ShHeader) == 256, "one header of 256 bytes");
 struct ShLayout {
   size_t groups, tiles, segs, items, clusters, splits, stats, partial, total;
   int max_tiles;
-  int tile_rows;      // rows of a full tile: whole requests where they fit
   int segs_per_tile;  // at most
 };
 
-// Rows of a request: where they fit, a tile has whole requests, so that no request's own
-// positions are attended by two tiles.
+// Rows of a tile that has whole requests, where one fits: no request's own positions are
+// attended by two tiles then. (The plan fills tiles up where that is less work.)
+__host__ __device__ inline int sh_whole_rows(int64_t r) { return r <= kShRows ? static_cast<int>(kShRows / r * r) : kShRows; }
+
 __host__ __device__ inline ShLayout sh_layout(int batch, int q_len, int heads, int prefixes, int clusters) {
   ShLayout L = {};
   const int64_t r = static_cast<int64_t>(q_len) * heads;
-  L.tile_rows = r <= kShRows ? static_cast<int>(kShRows / r * r) : kShRows;
-  L.segs_per_tile = 1 + (r <= kShRows ? static_cast<int>(kShRows / r) : 2);
-  const int64_t tiles = batch * r / L.tile_rows + (prefixes < batch ? prefixes : batch);
+  // the prefix; of a full tile's rows the first one's request and those that the others begin
+  L.segs_per_tile = 2 + static_cast<int>((kShRows - 2 + r) / r);
+  const int64_t tiles = batch * r / sh_whole_rows(r) + (prefixes < batch ? prefixes : batch);
   L.max_tiles = static_cast<int>(tiles);
   size_t off = sizeof(ShHeader);
   L.groups = off;

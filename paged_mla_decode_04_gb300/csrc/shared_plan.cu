@@ -40,6 +40,24 @@ __device__ __forceinline__ int pieces_of(int blocks, int shared, int most) {
   return static_cast<int>(min((weight + unit - 1) / unit, static_cast<int64_t>(blocks)));
 }
 
+__device__ __forceinline__ int64_t tiles_of(int64_t rows, int tile_rows) { return (rows + tile_rows - 1) / tile_rows; }
+
+// Rows of a group's tiles: whole requests, or as many as there is room for, whichever is
+// fewer blocks. The latter has fewer tiles, so fewer of the prefix's blocks; requests across
+// two tiles have their own positions in both. (40 requests of 96 rows and 550 positions each
+// behind 3,001 shared ones, e4m3: 55 us a decode in 15 full tiles, 59 in 20 of two requests.)
+__device__ __forceinline__ int tile_rows_of(int64_t r, int count, int prefix, int64_t cached) {
+  const int whole = sh_whole_rows(r);
+  if (whole == kShRows || count == 0) return whole;
+  const int64_t fewer = tiles_of(count * r, kShRows), saved = tiles_of(count * r, whole) - fewer;
+  int64_t period = r;  // tiles after which one ends with a request: r / gcd(r, kShRows)
+  while (period % 2 == 0) period /= 2;
+  const int64_t across = fewer - 1 - (fewer - 1) / period;
+  const int64_t shared_blocks = (prefix + kShTokens - 1) / kShTokens;
+  const int64_t own_blocks = (cached / count - prefix) / kShTokens + 1;  // (of a request, about)
+  return saved * (shared_blocks + kShItemCost) > across * own_blocks ? kShRows : whole;
+}
+
 // A request's cached positions; none for a length out of range.
 __device__ __forceinline__ int length_of(int l) { return l < 0 || l >= kShMostLength ? 0 : l; }
 
@@ -69,23 +87,26 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   if (refused && tid == 0) bad = 1;
 
   // Shared positions and tiles of each group.
-  const int r = a.q_len * a.num_heads;
+  const int64_t r = static_cast<int64_t>(a.q_len) * a.num_heads;
   for (int g = warp; g < a.num_prefixes && !refused; g += warps) {
     const int first = a.prefix_indptr[g], count = a.prefix_indptr[g + 1] - first;
     int p = a.prefix_lens[g];
     int least = INT_MAX, any_bad = p < 0;
+    int64_t cached = 0;
     for (int b = lane; b < count; b += 32) {
       const int l = a.context_lens[first + b];
       any_bad |= l != length_of(l);
       least = min(least, length_of(l));
+      cached += length_of(l);
     }
+    for (int d = 16; d > 0; d >>= 1) cached += __shfl_xor_sync(0xffffffffu, cached, d);
     least = __reduce_min_sync(0xffffffffu, least);
     any_bad = __any_sync(0xffffffffu, any_bad);
     if (lane == 0) {
       if (any_bad && count > 0) bad = 1;
       // (a request by itself has its positions in one segment)
       p = count > 1 ? min(max(p, 0), least) : 0;
-      groups[g] = ShGroup{first, count, p, 0};
+      groups[g] = ShGroup{first, count, p, 0, tile_rows_of(r, count, p, cached)};
     }
   }
   __syncthreads();
@@ -93,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   for (int g0 = 0; g0 < a.num_prefixes && !refused; g0 += blockDim.x) {
     const int g = g0 + tid;
     int64_t v[1] = {0}, total[1];
-    if (g < a.num_prefixes) v[0] = (static_cast<int64_t>(groups[g].count) * r + a.lay.tile_rows - 1) / a.lay.tile_rows;
+    if (g < a.num_prefixes) v[0] = tiles_of(static_cast<int64_t>(groups[g].count) * r, groups[g].tile_rows);
     block_scan<1>(v, total, sh);
     if (g < a.num_prefixes) groups[g].tile0 = static_cast<int>(before + v[0]);
     before += total[0];
@@ -106,8 +127,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   for (int t = warp; t < num_tiles; t += warps) {
     const int g = last_at_most(a.num_prefixes, t, [&](int i) { return groups[i].tile0; });
     const ShGroup gr = groups[g];
-    const int64_t from = static_cast<int64_t>(t - gr.tile0) * a.lay.tile_rows;  // within the group's rows
-    const int rows = static_cast<int>(min(static_cast<int64_t>(gr.count) * r - from, static_cast<int64_t>(a.lay.tile_rows)));
+    const int64_t from = static_cast<int64_t>(t - gr.tile0) * gr.tile_rows;  // within the group's rows
+    const int rows = static_cast<int>(min(static_cast<int64_t>(gr.count) * r - from, static_cast<int64_t>(gr.tile_rows)));
     const int64_t row0 = static_cast<int64_t>(gr.first) * r + from;
     ShSegment* out = segs + static_cast<int64_t>(t) * a.lay.segs_per_tile;
     const int shared_blocks = (gr.prefix + kShTokens - 1) / kShTokens;
@@ -181,7 +202,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
       mine[j] = t.blocks;
       shared[j] = t.shared;
     }
-    int lo = kShLeastBlocks, hi = max(kShLeastBlocks, static_cast<int>(all));  // (all blocks in one piece a tile: always)
+    int lo = kShLeastBlocks, hi = max(kShLeastBlocks, static_cast<int>(all) + kShRowsCost);  // (one piece a tile: always)
     while (lo < hi) {
       const int mid = lo + (hi - lo) / 2;
       int pieces = 0;
@@ -364,7 +385,7 @@ cudaError_t launch_shared_plan(const ShPlanArgs& a, cudaStream_t stream) {
 cudaError_t launch_shared_merge(const ShDecodeArgs& a, cudaStream_t stream) {
   // (a split tile lies across a boundary between two clusters' ranges)
   const int most = a.lay.max_tiles < a.clusters ? a.lay.max_tiles : a.clusters;
-  return launch_pdl(shared_merge_kernel, dim3(most, (a.lay.tile_rows + kMergeRows - 1) / kMergeRows), dim3(64 * kMergeRows),
+  return launch_pdl(shared_merge_kernel, dim3(most, kShRows / kMergeRows), dim3(64 * kMergeRows),
                     0, stream, a);
 }
 

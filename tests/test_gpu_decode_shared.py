@@ -327,3 +327,87 @@ def test_refusals(lib):
             lib.plan_shared(**{**plan, **bad})
     with pytest.raises(lib.MlaError):
         lib.workspace_size_shared(-1, 1, 16, 1)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,q_len", [(96, 1), (160, 1), (32, 3), (100, 1), (72, 2), (255, 1), (85, 3)])
+@pytest.mark.parametrize("prefix,own", [(1500, 60), (130, 700)])
+def test_requests_across_tiles(lib, fp8, heads, q_len, prefix, own):
+    """Row counts of which a tile leaves some over: tiles filled up, or of whole requests."""
+    c = Case([(7, prefix), (3, prefix // 2)], [own - 9 * b for b in range(7)] + [5, 0, own], heads=heads, q_len=q_len, page=32,
+             fp8=fp8, seed=heads)
+    verify(lib, c)
+    _, _, ws = run(lib, c)
+    r = heads * q_len
+    if prefix == 1500:  # tiles: full ones
+        assert int(ws.view(torch.int32)[8]) == -(-7 * r // 256) + -(-3 * r // 256)
+
+
+@pytest.mark.parametrize("heads,q_len", [(1, 1), (16, 1), (32, 3), (128, 1), (160, 1), (128, 3)])
+@pytest.mark.parametrize("groups,own", [([(9, 5000)], 300), ([(3, 100), (1, 900), (0, 5), (5, 64)], 1000), ([(1, 40000)], 0),
+                                        ([(60, 2500)], 600), ([(2, 700)] * 30, 40), ([(8, 65536)], 100)])
+@pytest.mark.parametrize("clusters", [0, 1, 5])
+def test_schedule_has_each_position_once(lib, heads, q_len, groups, own, clusters):
+    """The plan read back: tiles of all rows, their segments' positions, and each block of a
+    tile in one item of one cluster, with partial sums of its own where there are several."""
+    page, r = 32, heads * q_len
+    copy = min(page, 64)
+    which = [g for g, (k, _) in enumerate(groups) for _ in range(k)]
+    ctx = [groups[g][1] + own * (7 * b % 11) // 11 for b, g in enumerate(which)]
+    starts = [sum(k for k, _ in groups[:g]) for g in range(len(groups) + 1)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ws = lib.alloc_workspace_shared(len(ctx), q_len, heads, len(groups))
+    lib.plan_shared(torch.tensor(ctx, **i32), torch.tensor(starts, **i32), torch.tensor([p for _, p in groups], **i32), q_len, heads,
+                    page, ws, num_clusters=clusters)
+    torch.cuda.synchronize()
+    assert lib.get_error(ws) == 0
+    head = ws[:256].view(torch.int32).tolist()
+    num_clusters, num_tiles, num_items, num_split = head[7:11]
+    most_tiles = len(ctx) * r // (256 // r * r if r <= 256 else 256) + min(len(groups), len(ctx))
+    at, records = 256, []
+    for size, count in ((32, len(groups)), (32, most_tiles), (32, most_tiles * (2 + (254 + r) // r)), (96, num_items)):
+        records.append(ws[at:at + size * count].view(torch.int32).reshape(count, size // 4).tolist())
+        at = -(-(at + size * count) // 256) * 256
+    _, tiles, segments, items = records
+    assert num_tiles <= most_tiles and 1 <= num_clusters and (clusters == 0 or num_clusters <= clusters)
+
+    row = 0
+    for row0, rows, seg0, segs, blocks, shared, *_ in tiles[:num_tiles]:
+        assert row0 == row and 1 <= rows <= 256
+        row += rows
+        g = which[row0 // r]
+        first, count = starts[g], groups[g][0]
+        assert row <= (first + count) * r  # (of one group)
+        prefix = groups[g][1] if count > 1 else 0
+        assert shared == -(-prefix // 128)
+        own_segments = segments[seg0:seg0 + segs]
+        if prefix:
+            assert own_segments.pop(0) == [first, 0, rows, 0, 0, 0, prefix, prefix]
+        b, upto, done = row0 // r, 0, shared
+        for owner, row_lo, row_hi, block0, tok0, tok_lo, tok_hi, base in own_segments:
+            assert (owner, row_lo, block0, tok_lo, base) == (b, upto, done, prefix, ctx[b])
+            assert row_hi == min((b + 1) * r - row0, rows)
+            assert tok0 == prefix // copy * copy and tok_hi == ctx[b] + (row0 + row_hi - 1 - b * r) // heads + 1
+            done += -(-(tok_hi - tok0) // 128)
+            b, upto = b + 1, row_hi
+        assert upto == rows and done == blocks
+    assert row == len(ctx) * r
+
+    parts, split, n = [], 0, 0
+    for row0, rows, seg0, segs, blocks, shared, *_ in tiles[:num_tiles]:
+        mine = []
+        while n < num_items and items[n][4] == row0:
+            mine.append(items[n])
+            n += 1
+        assert [i[0] for i in mine] + [blocks] == [0] + [i[1] for i in mine]
+        split += len(mine) > 1
+        for begin, end, part, _, _, item_rows, seg, seg_last, prefix_end, row_lo, row_hi, *rest in mine:
+            assert begin < end and item_rows == rows and seg_last == seg0 + segs - 1 and prefix_end == shared
+            assert (part >= 0) == (len(mine) > 1)
+            parts += [part] if part >= 0 else []
+            assert rest[5:] == segments[seg] and segments[seg][3] <= begin and (seg == seg_last or segments[seg + 1][3] > begin)
+            last = max(k for k in range(seg0, seg0 + segs) if segments[k][3] < end)
+            want = (0, rows) if begin < shared else (segments[seg][1], segments[last][2])
+            assert (row_lo, row_hi) == want
+    assert n == num_items and split == num_split and sorted(parts) == list(range(len(parts)))
+    assert [i[3] for i in items] == sorted(i[3] for i in items) and items[-1][3] < num_clusters
