@@ -701,37 +701,41 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         const bool mine = r >= b.row_lo && r < b.row_hi;
         if (!(ok = warp_wait(bar(kBarS + group), (n >> 1) & 1u))) break;
         tc_fence_after();
-        float alpha = 1.f;
-        uint32_t s[128];
-        float mx = -CUDART_INF_F;
-        if (here) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
+        // A row's maximum first, then its weights: 64 columns at a time, of which the second are
+        // still there when the first are fetched once more. (All 128 at once do not fit the
+        // registers.)
+        float alpha = 1.f, mx = -CUDART_INF_F;
+        uint32_t s[64];
+        const int b0 = mine ? b.v0 : kShTokens, e0 = mine ? min(b.v1, b.end + i) : 0;
+        const bool all = __all_sync(0xffffffffu, b0 == 0 && e0 == kShTokens);
+        auto fetch = [&](int h) {
+          tmem_ld32(tS + 64 * h, s);
+          tmem_ld32(tS + 64 * h + 32, s + 32);
           tmem_wait_ld();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead(kBarSFree + group));
+          if (all) return;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int c0 = 64 * h + 32 * g;
+            const uint32_t above = e0 >= c0 + 32 ? ~0u : (1u << max(e0 - c0, 0)) - 1u;
+            const uint32_t below = b0 >= c0 + 32 ? ~0u : (1u << max(b0 - c0, 0)) - 1u;
+            const uint32_t keep = above & ~below;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(keep & (1u << c))) s[32 * g + c] = 0xff800000u;
+          }
+        };
         if (here) {
-          const int b0 = mine ? b.v0 : kShTokens, e0 = mine ? min(b.v1, b.end + i) : 0;
-          if (!__all_sync(0xffffffffu, b0 == 0 && e0 == kShTokens)) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const uint32_t above = e0 >= 32 * g + 32 ? ~0u : (1u << max(e0 - 32 * g, 0)) - 1u;
-              const uint32_t below = b0 >= 32 * g + 32 ? ~0u : (1u << max(b0 - 32 * g, 0)) - 1u;
-              const uint32_t keep = above & ~below;
+          for (int h = 0; h < 2; ++h) {
+            fetch(h);
+            float mx1 = -CUDART_INF_F;
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(keep & (1u << c))) s[32 * g + c] = 0xff800000u;
+            for (int c = 0; c < 64; c += 4) {
+              mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
             }
+            mx = fmaxf(mx, mx1);
           }
-          float mx1 = -CUDART_INF_F;
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            mx = fmax3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-          }
-          mx = fmaxf(mx, mx1);
         }
         // The reference from the block before, and on to the next.
         if (n > 0 && !(ok = warp_wait_block(ref_other, ((n - 1) >> 1) & 1u))) break;
@@ -743,6 +747,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         refs[lrow] = ref;
         __syncwarp();
         if (lane == 0) mbar_arrive(ref_mine);
+        // P leaves by way of this block's memory, with the factor of each row.
+        if (!(ok = warp_wait(bar(kBarOutFree + group), ((n >> 1) & 1u) ^ 1u))) break;
         if (here) {
           if (sum_ref != ref) l *= exp2_approx((sum_ref - ref) * scale);
           sum_ref = ref;
@@ -750,25 +756,28 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
           const uint64_t neg2 = f2_make(neg, neg);
           uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            float t0, t1;
-            f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
-            const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
-            sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
-            s[c] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          for (int h = 1; h >= 0; --h) {
+            if (h == 0) fetch(0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              float t0, t1;
+              f2_split(f2_fma(f2_make(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2, neg2), t0, t1);
+              const float p0 = exp2_approx(t0), p1 = exp2_approx(t1);
+              sum2[c & 1] = f2_add(sum2[c & 1], f2_make(p0, p1));
+              s[c] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              st_shared_v4(p_here + h * kPChunk + 16 * (c ^ sw), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
           }
           float s0, s1, s2, s3;
           f2_split(sum2[0], s0, s1);
           f2_split(sum2[1], s2, s3);
           l += (s0 + s1) + (s2 + s3);
         }
-        // P leaves by way of this block's memory, with the factor of each row.
-        if (!(ok = warp_wait(bar(kBarOutFree + group), ((n >> 1) & 1u) ^ 1u))) break;
-        if (here) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            st_shared_v4(p_here + (c >> 3) * kPChunk + 16 * ((c & 7) ^ sw), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
-        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead(kBarSFree + group));
         *alpha_here = alpha;
         fence_proxy_async_smem();
         __syncwarp();
