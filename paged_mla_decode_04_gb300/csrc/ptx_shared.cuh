@@ -49,12 +49,6 @@ __device__ __forceinline__ void bulk_copy_to(uint32_t cluster_dst, uint32_t src,
                : "memory");
 }
 
-__device__ __forceinline__ void st_async_b32(uint32_t addr, uint32_t v, uint32_t remote_bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
-               "r"(remote_bar)
-               : "memory");
-}
-
 __device__ __forceinline__ void st_async_v2(uint32_t addr, uint32_t a, uint32_t b, uint32_t remote_bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr), "r"(a),
                "r"(b), "r"(remote_bar)

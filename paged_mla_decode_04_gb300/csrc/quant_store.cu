@@ -85,9 +85,10 @@ template <int kFormat>
 __global__ void __launch_bounds__(32 * kWarps) store_write_kernel(const StoreWriteArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   if (t >= a.n) return;
-  const uint4* src = a.rows + static_cast<int64_t>(t) * kRowVecs;
+  const uint4* src = a.rows + t * kRowVecs;
   const int64_t slot = a.slots[t];
   const uint4 v[2] = {src[lane], src[lane + 32]};
   uint4 rope;
@@ -148,7 +149,8 @@ template <int kFormat, int kOut>
 __global__ void __launch_bounds__(32 * kWarps) store_read_kernel(const StoreReadArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   if (t >= a.n) return;
   const int64_t slot = a.slots[t], to = a.out_slots ? a.out_slots[t] : t;
   if (slot < 0 || to < 0) return;
@@ -204,13 +206,13 @@ __global__ void __launch_bounds__(32 * kWarps) store_read_kernel(const StoreRead
 }  // namespace
 
 cudaError_t launch_store_write(const StoreWriteArgs& a, int format, cudaStream_t stream) {
-  const dim3 grid((a.n + kWarps - 1) / kWarps), block(32 * kWarps);
+  const dim3 grid((a.n - 1) / kWarps + 1), block(32 * kWarps);
   if (format == MLA_QUANT_E4M3) return launch_pdl(store_write_kernel<MLA_QUANT_E4M3>, grid, block, 0, stream, a);
   return launch_pdl(store_write_kernel<MLA_QUANT_E2M1>, grid, block, 0, stream, a);
 }
 
 cudaError_t launch_store_read(const StoreReadArgs& a, int format, int out_dtype, cudaStream_t stream) {
-  const dim3 grid((a.n + kWarps - 1) / kWarps), block(32 * kWarps);
+  const dim3 grid((a.n - 1) / kWarps + 1), block(32 * kWarps);
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, stream, a); };
   if (format == MLA_QUANT_E4M3)
     return out_dtype == MLA_DTYPE_BF16 ? go(store_read_kernel<MLA_QUANT_E4M3, MLA_DTYPE_BF16>)

@@ -622,29 +622,48 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
           if (w0 + row >= skip && w0 + row < rows)
             rope[i] = *reinterpret_cast<const uint4*>(src + row * (kDimRow * 2) + 2 * kDimCkv + 64 * group + 16 * (lane & 3));
         }
-        // (Pieces of 32 bytes of 32 rows a load; by whole lines and turned, as the results go
+        // (Pieces of 32 bytes of 32 rows a load; where q is aligned to 16 bytes only, 16, and a call
+        // takes up to 4 us more, so there are both. By whole lines and turned, as the results go
         // out, it took longer: the turns' instructions have to be fetched for the first item.)
+        const bool wide = (reinterpret_cast<uintptr_t>(a.q) & 31u) == 0;
         const uint8_t* mine = src + lane * (kDimRow * 2) + 512 * group;
+        const bool in = w0 + lane >= skip && w0 + lane < rows;
         constexpr int kRounds = kFp8 ? 4 : 2, kWords = 128 / kRounds;  // (as registers allow)
+        if (wide) {
 #pragma unroll 1
-        for (int h = 0; h < kRounds; ++h) {
-          uint32_t x[kWords];
+          for (int h = 0; h < kRounds; ++h) {
+            uint32_t x[kWords];
 #pragma unroll
-          for (int c = 0; c < kWords / 8; ++c) {
-            if (w0 + lane >= skip && w0 + lane < rows) {
-              ld_global_v8(mine + 4 * kWords * h + 32 * c, x + 8 * c);
-            } else {
+            for (int c = 0; c < kWords / 8; ++c) {
+              if (in) {
+                ld_global_v8(mine + 4 * kWords * h + 32 * c, x + 8 * c);
+              } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[8 * c + e] = 0;
+                for (int e = 0; e < 8; ++e) x[8 * c + e] = 0;
+              }
             }
-          }
-          if (kFp8) {
+            if (kFp8) {
 #pragma unroll
-            for (int c = 0; c < kWords; ++c) x[c] = bf16x2_to_f16x2(x[c]);
-          }
-          __syncwarp();
+              for (int c = 0; c < kWords; ++c) x[c] = bf16x2_to_f16x2(x[c]);
+            }
+            __syncwarp();
 #pragma unroll
-          for (int c = 0; c < kWords / 32; ++c) tmem_st32(tbase + 128 * group + kWords * h + 32 * c, x + 32 * c);
+            for (int c = 0; c < kWords / 32; ++c) tmem_st32(tbase + 128 * group + kWords * h + 32 * c, x + 32 * c);
+          }
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t x[32];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint4 v = in ? reinterpret_cast<const uint4*>(mine + 128 * h)[c] : make_uint4(0, 0, 0, 0);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[4 * c + e] = kFp8 ? bf16x2_to_f16x2(w[e]) : w[e];
+            }
+            __syncwarp();
+            tmem_st32(tbase + 128 * group + 32 * h, x);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   const int64_t c = max(static_cast<int64_t>(1), min(all / kShLeastBlocks, static_cast<int64_t>(a.clusters)));
   if (tid == 0) apart = 0;
   __syncthreads();
-  if (warp == 0 && num_tiles > 0 && num_tiles <= a.clusters && num_tiles <= 128) {
+  if (warp == 0 && num_tiles > 0 && num_tiles <= a.clusters && num_tiles <= 128 && all < 1 << 30) {
     int mine[4], shared[4];  // blocks of tiles lane, lane + 32, ...; of their prefixes
 #pragma unroll
     for (int j = 0; j < 4; ++j) {

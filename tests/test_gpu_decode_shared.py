@@ -411,3 +411,45 @@ def test_schedule_has_each_position_once(lib, heads, q_len, groups, own, cluster
             assert (row_lo, row_hi) == want
     assert n == num_items and split == num_split and sorted(parts) == list(range(len(parts)))
     assert [i[3] for i in items] == sorted(i[3] for i in items) and items[-1][3] < num_clusters
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_queries_aligned_to_16_bytes_only(lib, fp8):
+    c = Case([(5, 300)], [5, 130, 0, 64, 127], heads=48, page=32, fp8=fp8, seed=4)
+    want, _, _ = run(lib, c)
+    room = torch.zeros(c.q.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    c.q = room[8:].view(c.q.shape).copy_(c.q)
+    assert c.q.data_ptr() % 32 == 16
+    verify(lib, c)
+    assert torch.equal(run(lib, c)[0], want)
+    with pytest.raises(lib.MlaError):
+        c.q = room[4:-4].view(c.q.shape)
+        run(lib, c)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pool_beyond_32_bit_offsets(lib, fp8):
+    c = Case([(4, 700)], [5, 130, 0, 64], heads=32, page=128, fp8=fp8, seed=6, layers=1)
+    want, _, _ = run(lib, c)
+    n, pages = c.pool.shape[1], (1 << 32) // (128 * 576 * (1 if fp8 else 2)) + 200
+    pool = torch.empty(1, pages, 128, 576, dtype=c.pool.dtype, device="cuda")
+    pool[0, pages - n:] = c.pool[0]
+    valid = (c.table >= 0) & (c.table < n)
+    c.pool, c.table = pool, torch.where(valid, c.table + (pages - n), c.table)
+    assert torch.equal(run(lib, c)[0], want)
+
+
+def test_lengths_of_a_garbled_batch_stay_in_the_workspace(lib):
+    """Every length the largest that counts: more blocks than 32 bits hold (plan alone)."""
+    batch = 8192
+    i32 = dict(dtype=torch.int32, device="cuda")
+    size = lib.workspace_size_shared(batch, 1, 1, 1)
+    room = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws = room[:size]
+    ws[:256].zero_()
+    lib.plan_shared(torch.full((batch,), (1 << 29) - 1, **i32), torch.tensor([0, batch], **i32), torch.tensor([1000], **i32), 1, 1, 64,
+                    ws)
+    torch.cuda.synchronize()
+    head = ws[:256].view(torch.int32).tolist()
+    assert lib.get_error(ws) == 0 and head[8] == 32 and head[9] <= 32 + head[7]
+    assert bool((room[size:] == 0x5A).all())
