@@ -99,7 +99,10 @@ int mla_decode_shared(const mla_kv_pool* pool, int layer, const void* q, const i
   a.scale_log2 = softmax_scale * 1.4426950408889634f * (fp8 ? pool->kv_scale : 1.f);
   a.out_scale = fp8 ? pool->kv_scale : 1.f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CUtensorMap maps[3] = {};
+  CUtensorMap maps[4] = {};
+  const uint64_t q_rows = static_cast<uint64_t>(batch) * q_len * num_heads;
+  if (!mla::make_map_2d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, q_rows, mla::kDimRow, mla::kDimRow * 2, 64, 32))
+    return MLA_ERR_CUDA;
   const uint32_t copy = mla::sh_copy_tokens(pool->page_size);
   if (fp8) {
     constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;

@@ -90,10 +90,11 @@ enum {
   kBarVFree = kBarVFull + kVStages,    // [kVStages]
   kBarNote = kBarVFree,                // [kNotes] (scores' pair) the block is described
   kBarP = kBarVFree + kVStages,        // [kPBuffers] weights have arrived
+  kBarQIn = kBarP,                     // [8 warps] (scores' pair) queries have landed
   kBarPReady = kBarP + kPBuffers,      // [kPBuffers] and O is rescaled, V landed
   kBarO = kBarPReady + kPBuffers,      // an item's last product complete
   kBarStats = kBarO + 1,               // an item's maxima and sums have arrived
-  kBarOFree = kBarStats + 1,
+  kBarOFree = kBarStats + 1,           // (from kBarP on: enough for the queries' eight)
   // (fp8 pools) In either pair: codes have landed; every warp that widens has read its share.
   kBarRaw = kBarOFree + 1,             // [most stages]
   kBarMeet = kBarRaw + (kKStages > kVStages ? kKStages : kVStages),
@@ -103,6 +104,7 @@ enum {
 // (all that a block may have: its start has to be at a multiple of 1,024, see the kernel)
 constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 8;
 static_assert(kSmemBytes <= 232448, "shared memory");
+static_assert(kBarQIn + kWorkers <= kBarRaw, "barriers that the other pair alone uses");
 constexpr uint32_t kColS = 256;             // + 128 a buffer; Q from 0
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 // The reference of a row that has seen no position: below every score, and finite, so that
@@ -183,8 +185,8 @@ __device__ __forceinline__ void turn(uint32_t* o, int lane) {
 struct Params {
   // bf16 pools: as [rows][576], box {64, positions of a copy}; where a copy brings 64 positions
   // as [chunk][rows][64], boxes of three and four chunks. fp8 pools: (none), boxes of 192 and
-  // of 256 codes.
-  CUtensorMap rows, chunks3, chunks4;
+  // of 256 codes. Queries as [rows][576], boxes of 32 rows and 64 dims.
+  CUtensorMap rows, chunks3, chunks4, q;
   ShDecodeArgs a;
 };
 
@@ -217,11 +219,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       if (i >= kBarPReady && i < kBarPReady + kPBuffers) count = 2 * kWorkers;
       if (i == kBarOFree) count = 2 * kWorkers;
       if (i == kBarStatsFree) count = kWorkers;
+      if (scores && i >= kBarQIn && i < kBarQIn + kWorkers) count = 1;
       mbar_init(bar(i), count);
     }
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
+  if (warp == 0 && lane == 0 && scores) tma_prefetch_map(&p.q);
   if (warp == kProducerWarp && lane == 0) tma_prefetch_map(unit != 64 && !kFp8 ? &p.rows : scores ? &p.chunks3 : &p.chunks4);
   if (warp == kIssueWarp) {
     tmem_alloc2(smem_addr(tmem_slot), 512);
@@ -611,68 +615,51 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         tc_fence_after();
       }
       if (k + 1 < item1) {
-        // (rows that attend nothing of the item may hold anything)
-        const int row0 = item(k + 1).row0, rows = item(k + 1).row_hi, skip = item(k + 1).row_lo;
-        const uint8_t* src = static_cast<const uint8_t*>(a.q) + (static_cast<int64_t>(row0) + w0) * (kDimRow * 2);
-        uint4 rope[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // the rope dims: 16 bytes of row 8 i + lane / 4
-          const int row = 8 * i + (lane >> 2);
-          rope[i] = make_uint4(0, 0, 0, 0);
-          if (w0 + row >= skip && w0 + row < rows)
-            rope[i] = *reinterpret_cast<const uint4*>(src + row * (kDimRow * 2) + 2 * kDimCkv + 64 * group + 16 * (lane & 3));
-        }
-        // (Pieces of 32 bytes of 32 rows a load; where q is aligned to 16 bytes only, 16, and a call
-        // takes up to 4 us more, so there are both. By whole lines and turned, as the results go
-        // out, it took longer: the turns' instructions have to be fetched for the first item.)
-        const bool wide = (reinterpret_cast<uintptr_t>(a.q) & 31u) == 0;
-        const uint8_t* mine = src + lane * (kDimRow * 2) + 512 * group;
-        const bool in = w0 + lane >= skip && w0 + lane < rows;
-        constexpr int kRounds = kFp8 ? 4 : 2, kWords = 128 / kRounds;  // (as registers allow)
-        if (wide) {
+        // A warp's rows of 64 dims a copy, by way of where it puts P when that has left; the rope
+        // dims to where they stay. (Rows that attend nothing of the item may hold anything. Loaded
+        // by the rows' threads, 32 bytes a time, the queries of 20 tiles took 6 us to come in.)
+        const int row0 = item(k + 1).row0;
+        if (w0 < item(k + 1).row_hi && w0 + 32 > item(k + 1).row_lo) {
+          const uint32_t before = k < item0 ? 0 : (last + 2 - group) >> 1;  // this group's blocks so far
+          if (!(ok = warp_wait(bar(kBarOutFree + group), (before & 1u) ^ 1u))) break;
+          const uint32_t landed = bar(kBarQIn + warp), room = p_here - 128 * lane;
+          const uint32_t rope = sbase + kOffQRope + 32 * quarter * 128;
 #pragma unroll 1
-          for (int h = 0; h < kRounds; ++h) {
-            uint32_t x[kWords];
-#pragma unroll
-            for (int c = 0; c < kWords / 8; ++c) {
-              if (in) {
-                ld_global_v8(mine + 4 * kWords * h + 32 * c, x + 8 * c);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[8 * c + e] = 0;
-              }
+          for (int h = 0; h < 2; ++h) {
+            const bool with_rope = h == 0 && group == 0;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(landed, with_rope ? 3 * 4096 : 2 * 4096);
+              tma_load_2d(room, &p.q, landed, 256 * group + 128 * h, row0 + w0);
+              tma_load_2d(room + kPChunk, &p.q, landed, 256 * group + 128 * h + 64, row0 + w0);
+              if (with_rope) tma_load_2d(rope, &p.q, landed, kDimCkv, row0 + w0);
             }
+            __syncwarp();
+            if (!(ok = warp_wait_block(landed, h))) {
+              if (lane == 0) mbar_wait(landed, h, nullptr, 100000000ull);  // (nothing may land in a block that has ended)
+              break;
+            }
+            uint32_t x[64];
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              ld_shared_v4(p_here + (c >> 3) * kPChunk + 16 * ((c & 7) ^ sw), x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
             if (kFp8) {
 #pragma unroll
-              for (int c = 0; c < kWords; ++c) x[c] = bf16x2_to_f16x2(x[c]);
+              for (int c = 0; c < 64; ++c) x[c] = bf16x2_to_f16x2(x[c]);
             }
             __syncwarp();
+            tmem_st32(tbase + 128 * group + 64 * h, x);
+            tmem_st32(tbase + 128 * group + 64 * h + 32, x + 32);
+            if (kFp8 && with_rope) {
 #pragma unroll
-            for (int c = 0; c < kWords / 32; ++c) tmem_st32(tbase + 128 * group + kWords * h + 32 * c, x + 32 * c);
-          }
-        } else {
-#pragma unroll 1
-          for (int h = 0; h < 4; ++h) {
-            uint32_t x[32];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 v = in ? reinterpret_cast<const uint4*>(mine + 128 * h)[c] : make_uint4(0, 0, 0, 0);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[4 * c + e] = kFp8 ? bf16x2_to_f16x2(w[e]) : w[e];
+              for (int c = 0; c < 8; ++c) {
+                uint32_t v[4];
+                const uint32_t at = rope + 128 * lane + 16 * c;
+                ld_shared_v4(at, v[0], v[1], v[2], v[3]);
+                st_shared_v4(at, bf16x2_to_f16x2(v[0]), bf16x2_to_f16x2(v[1]), bf16x2_to_f16x2(v[2]), bf16x2_to_f16x2(v[3]));
+              }
             }
-            __syncwarp();
-            tmem_st32(tbase + 128 * group + 32 * h, x);
           }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 8 * i + (lane >> 2);
-          if (kFp8)
-            rope[i] = make_uint4(bf16x2_to_f16x2(rope[i].x), bf16x2_to_f16x2(rope[i].y), bf16x2_to_f16x2(rope[i].z),
-                                 bf16x2_to_f16x2(rope[i].w));
-          st_shared_v4(sbase + kOffQRope + (32 * quarter + row) * 128 + 16 * ((4 * group + (lane & 3)) ^ (row & 7)), rope[i].x,
-                       rope[i].y, rope[i].z, rope[i].w);
+          if (!ok) break;
         }
         fence_proxy_async_smem();
         tmem_wait_st();
@@ -1010,11 +997,12 @@ int shared_max_active_clusters() {
   return cached[dev] = a < b ? a : b;
 }
 
-cudaError_t launch_shared_decode(const CUtensorMap (&maps)[3], const ShDecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_shared_decode(const CUtensorMap (&maps)[4], const ShDecodeArgs& a, cudaStream_t stream) {
   Params p;
   p.rows = maps[0];
   p.chunks3 = maps[1];
   p.chunks4 = maps[2];
+  p.q = maps[3];
   p.a = a;
   return a.dtype == MLA_DTYPE_FP8_E4M3 ? launch_variant<true>(p, stream) : launch_variant<false>(p, stream);
 }

@@ -181,8 +181,9 @@ cudaError_t launch_shared_merge(const ShDecodeArgs& a, cudaStream_t stream);
 // shared_decode.cu
 // maps: bf16 pools as [rows][576], box {64, sh_copy_tokens}; where that is 64, as
 // [chunk][rows][64 dims] with boxes of three and of four chunks. fp8 pools: none, boxes
-// {192, sh_copy_tokens} and {256, sh_copy_tokens}, unswizzled.
-cudaError_t launch_shared_decode(const CUtensorMap (&maps)[3], const ShDecodeArgs& a, cudaStream_t stream);
+// {192, sh_copy_tokens} and {256, sh_copy_tokens}, unswizzled. Then q as [rows][576], box
+// {64, 32}.
+cudaError_t launch_shared_decode(const CUtensorMap (&maps)[4], const ShDecodeArgs& a, cudaStream_t stream);
 int shared_max_active_clusters();
 
 // ---------------------------------------------------------------- compact latent store
