@@ -886,7 +886,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
       auto dim_of = [&](int col) { return 128 * side + (col & 127) + (col >= 128 ? 256 : 0); };
       if (stores == 0) {
       } else if (part) {
-        float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + (part_row - (lane & 3)) * kDimCkv + 8 * (lane & 3);
+        // [dims / 8][rows][8 dims]: a warp's rows are next to each other
+        float* dst = reinterpret_cast<float*>(a.ws + a.lay.partial) + it.part * static_cast<int64_t>(kShRows * kDimCkv) + 8 * r;
         uint32_t o[2][32];  // (the next columns are asked for while these go out)
         tmem_ld32(tO, o[0]);
         tmem_wait_ld();
@@ -895,10 +896,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (c + h < 7) tmem_ld32(tO + 32 * (c + h + 1), o[h ^ 1]);
-            turn(o[h], lane);
+            if (store) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (stores >> ((lane & 28) + i) & 1u) st_global_v8(dst + i * kDimCkv + dim_of(32 * (c + h)), o[h] + 8 * i);
+              for (int i = 0; i < 4; ++i) st_global_v8(dst + (dim_of(32 * (c + h)) + 8 * i) * kShRows, o[h] + 8 * i);
+            }
             __syncwarp();
             tmem_wait_ld();
           }

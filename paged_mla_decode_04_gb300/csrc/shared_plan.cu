@@ -10,7 +10,7 @@
 #include <math_constants.h>
 
 #include "../../include/mla_decode.h"
-#include "ptx.cuh"
+#include "ptx_shared.cuh"
 #include "scan.cuh"
 #include "shared_internal.h"
 
@@ -304,76 +304,71 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   }
 }
 
-constexpr int kMergeRows = 4;   // rows a block, two warps each
-constexpr int kMergeBatch = 8;  // pieces whose loads are issued together
+constexpr int kMergeWarps = 8;  // of a block
+// Pieces whose loads are issued together, and blocks of the grid an SM that the decode uses.
+// (6 pieces and 3 blocks, of more registers: 40.0 us instead of 41.3 a decode whose tiles are in
+// 9 pieces, but 56.5 instead of 54.5 and 219 instead of 216.5 where they are in 2 or 3.)
+constexpr int kMergeBatch = 4, kMergeBlocks = 4;
 
 // out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over a split tile's pieces k, M the
-// largest m_k. Pieces without a position of the row have l_k = 0; their O_k is not read.
-// Weights come first, 32 pieces at a time, a lane each; then the sums, in the pieces' order.
-// Bound by the latency of its loads and by L2.
-__global__ void __launch_bounds__(64 * kMergeRows) shared_merge_kernel(const ShDecodeArgs a) {
+// largest m_k of those seen so far. Pieces without a position of the row have l_k = 0 and
+// whatever their O_k hold. A warp has eight rows of 32 dims at a time, a lane eight dims of a
+// row; a batch's maxima, sums and accumulators come in together. Bound by the latency of its
+// loads and by L2: about 3 us of a decode of 5 to 40 MB of partial sums, besides a launch.
+__global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const ShDecodeArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const ShHeader* hd = reinterpret_cast<const ShHeader*>(a.ws);
-  const ShSplit sp = reinterpret_cast<const ShSplit*>(a.ws + a.lay.splits)[blockIdx.x];  // (asked for with the header)
-  if (!sh_planned(hd, a) || static_cast<int>(blockIdx.x) >= hd->num_split) return;
-  const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 6), side = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
-  if (row >= sp.rows) return;
-  const float2* stats = reinterpret_cast<const float2*>(a.ws + a.lay.stats) + static_cast<int64_t>(sp.part0) * kShRows + row;
-  constexpr int kRowVecs = kDimCkv / 4;
-  const float4* part = reinterpret_cast<const float4*>(a.ws + a.lay.partial) +
-                       (static_cast<int64_t>(sp.part0) * kShRows + row) * kRowVecs + side * (kRowVecs / 2) + lane;
-  float top = -CUDART_INF_F;
-  for (int k = lane; k < sp.pieces; k += 32) {
-    const float2 s = stats[static_cast<int64_t>(k) * kShRows];
-    if (s.y != 0.f) top = fmaxf(top, s.x);
-  }
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float4 acc[2] = {};
-  float sum = 0.f;
-  for (int k0 = 0; k0 < sp.pieces; k0 += 32) {
-    float mine = 0.f;
-    bool there = false;
-    if (k0 + lane < sp.pieces) {
-      const float2 s = stats[static_cast<int64_t>(k0 + lane) * kShRows];
-      there = s.y != 0.f;
-      mine = there ? exp2f(s.x - top) : 0.f;
-      sum = fmaf(mine, s.y, sum);
-    }
-    const uint32_t with = __ballot_sync(0xffffffffu, there);
-    const int n = min(sp.pieces - k0, 32);
-    for (int b0 = 0; b0 < n; b0 += kMergeBatch) {
-      float4 x[kMergeBatch][2];
+  if (!sh_planned(hd, a)) return;
+  constexpr int kAcross = kDimCkv / 32, kUnits = kShRows / 8 * kAcross;  // of a tile
+  const int lane = threadIdx.x & 31, units = hd->num_split * kUnits;
+  for (int u = blockIdx.x * kMergeWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kMergeWarps) {
+    const ShSplit sp = reinterpret_cast<const ShSplit*>(a.ws + a.lay.splits)[u / kUnits];
+    const int row = u % kUnits / kAcross * 8 + (lane & 7), dim = u % kAcross * 32 + 8 * (lane >> 3);
+    if (row >= sp.rows) continue;
+    const float2* stats = reinterpret_cast<const float2*>(a.ws + a.lay.stats) + static_cast<int64_t>(sp.part0) * kShRows + row;
+    const float* part = reinterpret_cast<const float*>(a.ws + a.lay.partial) +
+                        static_cast<int64_t>(sp.part0) * (kShRows * kDimCkv) + dim * kShRows + 8 * row;
+    float acc[8] = {}, sum = 0.f, top = -CUDART_INF_F;
+    for (int k0 = 0; k0 < sp.pieces; k0 += kMergeBatch) {
+      float2 ml[kMergeBatch];
+      float x[kMergeBatch][8];
+      float most = top;
 #pragma unroll
       for (int k = 0; k < kMergeBatch; ++k) {
-        x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (with >> (b0 + k) & 1u) {
-          const float4* src = part + static_cast<int64_t>(k0 + b0 + k) * kShRows * kRowVecs;
-          x[k][0] = src[0];
-          x[k][1] = src[32];
+        ml[k] = make_float2(0.f, 0.f);
+        if (k0 + k < sp.pieces) {
+          ml[k] = stats[static_cast<int64_t>(k0 + k) * kShRows];
+          ld_global_v8(part + static_cast<int64_t>(k0 + k) * (kShRows * kDimCkv), x[k]);
         }
       }
 #pragma unroll
-      for (int k = 0; k < kMergeBatch; ++k) {
-        const float w = __shfl_sync(0xffffffffu, mine, b0 + k);
+      for (int k = 0; k < kMergeBatch; ++k)
+        if (ml[k].y != 0.f) most = fmaxf(most, ml[k].x);
+      if (most != top) {
+        const float w = exp2f(top - most);  // (0 at first)
+        sum *= w;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          acc[j].x = fmaf(w, x[k][j].x, acc[j].x);
-          acc[j].y = fmaf(w, x[k][j].y, acc[j].y);
-          acc[j].z = fmaf(w, x[k][j].z, acc[j].z);
-          acc[j].w = fmaf(w, x[k][j].w, acc[j].w);
+        for (int e = 0; e < 8; ++e) acc[e] *= w;
+        top = most;
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeBatch; ++k) {
+        if (ml[k].y != 0.f) {
+          const float w = exp2f(ml[k].x - top);
+          sum = fmaf(w, ml[k].y, sum);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, x[k][e], acc[e]);
         }
       }
     }
+    const float inv = a.out_scale / sum;
+    const int64_t out_row = static_cast<int64_t>(sp.row0) + row;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kDimCkv + dim) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (a.lse && dim == 0) a.lse[out_row] = (top + log2f(sum)) * 0.69314718055994531f;
   }
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  const float inv = a.out_scale / sum;
-  const int64_t out_row = static_cast<int64_t>(sp.row0) + row;
-  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kDimCkv) + side * (kRowVecs / 2) + lane;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    dst[32 * j] = make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
-  if (a.lse && side == 0 && lane == 0) a.lse[out_row] = (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -383,10 +378,7 @@ cudaError_t launch_shared_plan(const ShPlanArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_shared_merge(const ShDecodeArgs& a, cudaStream_t stream) {
-  // (a split tile lies across a boundary between two clusters' ranges)
-  const int most = a.lay.max_tiles < a.clusters ? a.lay.max_tiles : a.clusters;
-  return launch_pdl(shared_merge_kernel, dim3(most, kShRows / kMergeRows), dim3(64 * kMergeRows),
-                    0, stream, a);
+  return launch_pdl(shared_merge_kernel, dim3(kMergeBlocks * kShClusterBlocks * a.clusters), dim3(32 * kMergeWarps), 0, stream, a);
 }
 
 }  // namespace mla
