@@ -9,15 +9,16 @@
 // works as two pairs (products of M = 256 over two SMs, each with half of the columns'
 // operand in its shared memory):
 //   blocks 0, 1  S = Q K^T and its softmax. Tensor memory: Q's 512 dims (256 columns of
-//                bf16 pairs), two buffers of S (128 columns each); the rope dims of Q and a
+//                16-bit pairs), two buffers of S (128 columns each); the rope dims of Q and a
 //                ring of K's pieces in shared memory.
-//   blocks 2, 3  O += P V. Tensor memory: O (512 columns). Shared memory: two buffers of
+//   blocks 2, 3  O += P V. Tensor memory: O (512 columns). Shared memory: three buffers of
 //                P, a ring of V's pieces.
 // The two products are 576 and 512 dims long, so both pairs are busy, and neither waits
 // for the other within a block of positions: weights P go one way, from the softmax
-// warps' registers into the other pair's shared memory (32 KB a block's 128 positions and
-// 2,304 cycles of products), with a factor for each row by which O is rescaled where the
-// running maximum moved. The first pair runs ahead by two blocks of positions.
+// warps' registers by way of their own shared memory into the other pair's (32 KB a block's
+// 128 positions and 2,304 cycles of products), with a factor for each row by which O is
+// rescaled where the running maximum moved. The first pair is up to five blocks of
+// positions ahead.
 //
 // A cluster works through its items (see shared_internal.h): blocks of a tile's
 // positions, those that all its rows share and then each request's own. In the latter only
@@ -25,6 +26,15 @@
 // row mask leaves their accumulators alone, so that one request's cache never touches
 // another's result. Positions outside a segment are masked by selection in S; their rows of
 // V are made zero, or left out 16 at a time.
+//
+// What bounds it: the tensor core, at 2,690 cycles a block of 256 rows and 128 positions (76 %
+// of the products' cycles, as a large library product has them; long calls meet the power limit)
+// where blocks are many: 1.37 PFLOP/s of 16,384 rows at 8,450 positions, 1.35 of 1,024 rows
+// at 65,700, 108 us. Where they are few, what a call cannot overlap: 2 us until queries are in
+// place, 4 from the first scores to the first product of values, 4 to 6 for an item's results
+// (they go out at L2's rate, of all SMs at once) and 3 for the join of its pieces, so that 4
+// tiles of 100 blocks take 41 us. e4m3 pools: four warps widen a block's codes in 2,800
+// cycles, about as long as the products, and queries become f16.
 #include <cuda_bf16.h>
 #include <limits.h>
 #include <math_constants.h>
@@ -163,8 +173,8 @@ struct Walk {
 
 // Four lanes' 128 bytes each, as four pieces of 32, transposed: piece j of lane i becomes
 // piece i of lane j. A lane that has 128 bytes of its own row writes them by way of this, so
-// that a store covers eight whole lines (as the rows lie it is 32 pieces of 32 bytes: an
-// item's results took 6 to 8 us to go out instead of 4 to 6).
+// that a store covers eight whole lines (as the rows lie it is 32 pieces of 32 bytes, and
+// an item's results took 2 us longer to go out).
 __device__ __forceinline__ void turn(uint32_t* o, int lane) {
 #pragma unroll
   for (int d = 1; d < 4; d <<= 1) {
@@ -357,7 +367,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
 #pragma unroll 1
           for (uint32_t part = 0; part < kKParts; ++part) {
             const uint32_t use = kKParts * n + part, stage = use % kStages;
-            if (!(ok = warp_wait(bar(kBarKFree + stage), (use / kStages & 1u) ^ 1u))) break;
+            // (this wait is the longest: as one that lets other warps issue, 54.0 us instead of 54.9
+            // a decode of an fp8 pool)
+            if (!(ok = mbar_wait(bar(kBarKFree + stage), (use / kStages & 1u) ^ 1u, abort_flag))) break;
+            __syncwarp();
             issued = use + 1;
             if (part == 0 && lane == 0) {
               // What the softmax warps need of the block. (Now that block n - 2 is multiplied in
