@@ -8,7 +8,9 @@
 // Groups of zeros, or so small that the scale is zero, have codes of zero; a group with an
 // infinity or NaN has scale NaN and reads as NaN throughout.
 //
-// A warp a row: reading and writing is all there is to it, 1,816 bytes a token (e4m3).
+// A warp a row: reading and writing is all there is to it, 1,816 bytes a token (e4m3). 131,072
+// rows: written in 40.5 us (5.9 TB/s, 88 % of a copy's rate), read from e2m1 into a pool in 40.2
+// (5.2 TB/s; three quarters of the bytes are writes). A few rows: 2.6 us.
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
