@@ -22,9 +22,9 @@ constexpr int kShRows = 256;
 constexpr int kShTokens = 128;
 constexpr int kShClusterBlocks = 4;  // thread blocks of a cluster
 // A tile's first block costs a cluster this many more (queries into place, the
-// pipeline's start, the result's way out: 8 us of a block's 1.4, in part behind the blocks of
-// the item before). 3, 4, 5 and 8 took 67.3, 67.2, 66.5 and 68.6 us a decode of 50 tiles, and
-// 68.2, 66.9, 67.0 and 69.6 one of 20.
+// pipeline's start, the result's way out, in part behind the item before). 3, 4, 5 and 8 took
+// 67.3, 67.2, 66.5 and 68.6 us a decode of five groups, 90 requests x 32 heads, and 68.2, 66.9,
+// 67.0 and 69.6 one of 20 tiles of 32 blocks.
 constexpr int kShItemCost = 4;
 // A piece of a prefix's blocks costs this many more than one of requests' own (see the plan).
 constexpr int kShRowsCost = 5;
