@@ -22,14 +22,15 @@ constexpr int kShRows = 256;
 constexpr int kShTokens = 128;
 constexpr int kShClusterBlocks = 4;  // thread blocks of a cluster
 // A tile's first block costs a cluster this many more (queries into place, the
-// pipeline's start, the result's way out, in part behind the item before). 3, 4, 5 and 8 took
-// 67.3, 67.2, 66.5 and 68.6 us a decode of five groups, 90 requests x 32 heads, and 68.2, 66.9,
-// 67.0 and 69.6 one of 20 tiles of 32 blocks.
+// pipeline's start, the result's way out, in part behind the item before). 2, 3, 4 and 6 took
+// 56.5, 55.0, 54.7 and 55.6 us a decode of 15 tiles of 37 blocks.
 constexpr int kShItemCost = 4;
 // A piece of a prefix's blocks costs this many more than one of requests' own (see the plan).
-constexpr int kShRowsCost = 5;
-// Clusters are used as far as each has this many blocks (2, 3 and 5: within 1 %).
-constexpr int kShLeastBlocks = 3;
+// Within 2 % from 3 to 7 but for small batches: 18 to 29 us, by turns one or the other.
+constexpr int kShRowsCost = 4;
+// Clusters are used as far as each has this many blocks. 2 instead of 3: 15.2 us instead of
+// 16.6, 18.9 instead of 20.1, 24.5 instead of 26.2; at worst 19.6 instead of 18.6.
+constexpr int kShLeastBlocks = 2;
 
 // Cached positions of a request are fewer (a tile's blocks then count in 32 bits).
 constexpr int kShMostLength = 1 << 29;
