@@ -367,10 +367,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
 #pragma unroll 1
           for (uint32_t part = 0; part < kKParts; ++part) {
             const uint32_t use = kKParts * n + part, stage = use % kStages;
-            // (this wait is the longest: as one that lets other warps issue, 54.0 us instead of 54.9
-            // a decode of an fp8 pool)
-            if (!(ok = mbar_wait(bar(kBarKFree + stage), (use / kStages & 1u) ^ 1u, abort_flag))) break;
-            __syncwarp();
+            // (This wait is the longest: as one that lets other warps issue, 54.0 us instead of 54.9
+            // a decode of an fp8 pool. Its lanes wait one by one, so they vote: all go on or none.)
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarKFree + stage), (use / kStages & 1u) ^ 1u, abort_flag)))) break;
             issued = use + 1;
             if (part == 0 && lane == 0) {
               // What the softmax warps need of the block. (Now that block n - 2 is multiplied in
