@@ -680,10 +680,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         if (lane == 0) mbar_arrive_cluster(lead(kBarQ));
       }
       if (k >= item0) {
-        // The row's maximum and sum, from the group of the last block. (Every warp waits for
-        // each item's phase, so that none takes one for the next but one. One group may be done
-        // with the next item's blocks before the other reads this one's sum, but no further:
-        // their blocks alternate.)
+        // The row's maximum and sum, from the group of the last block. First every warp waits until
+        // the item before's have been read: the last block's group needs the other's sum before it can
+        // send, so no warp's wait for that phase can come after the next one. One group may be done
+        // with the next item's blocks before the other reads this one's sum, but no further: the
+        // next item's end waits for this one's maxima and sums.
+        if (!(ok = warp_wait(bar(kBarStatsFree), ((k - item0) & 1u) ^ 1u))) break;
         const int odd = (k - item0) & 1;
         float2* sum = sums + 128 * odd + lrow;
         const uint32_t sum_bar = bar(kBarSum + 4 * odd + quarter);
@@ -692,7 +694,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
           __syncwarp();
           if (lane == 0) mbar_arrive(sum_bar);
         }
-        if (!(ok = warp_wait(bar(kBarStatsFree), ((k - item0) & 1u) ^ 1u))) break;
         if (mine_last) {
           if (!(ok = warp_wait_block(sum_bar, ((k - item0) >> 1) & 1u))) break;
           const float2 other = *sum;
