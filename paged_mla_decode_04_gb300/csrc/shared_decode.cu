@@ -120,6 +120,13 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units
 // The reference of a row that has seen no position: below every score, and finite, so that
 // a score of -inf against it is a weight of zero.
 constexpr float kNoMax = -1e30f;
+// Weights are this many powers of two larger than 2^(score - reference), in P, O and l alike (the
+// maximum that stands for them is smaller by as much), so that those of f16 use its range: with
+// the reference's lag they reach 2^15, and only weights below 2^-21 of a row's largest lose bits,
+// to 2^-32 of it. (Without, 65,536 positions of 2^-25 each were lost beside one of 1. bf16 has
+// fp32's range.)
+template <bool kFp8>
+constexpr float kWeightShift = kFp8 ? 7.0f : 0.0f;
 constexpr uint16_t kScorePair = 0x3, kAccPair = 0xc;  // blocks of the cluster
 
 // A block of positions, as every role sees it.
@@ -700,7 +707,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
           if (sum_ref != ref) l *= exp2_approx((sum_ref - ref) * scale);
           if (other.x != ref) l = fmaf(other.y, exp2_approx((other.x - ref) * scale), l);
           else l += other.y;
-          st_async_v2(stats_at, __float_as_uint(ref * scale), __float_as_uint(l), peer(kBarStats));
+          st_async_v2(stats_at, __float_as_uint(-fmaf(-ref, scale, kWeightShift<kFp8>)), __float_as_uint(l), peer(kBarStats));
           if (lane == 0) mbar_arrive_expect_tx_relaxed(peer(kBarStats), 32 * 8);
         }
       }
@@ -771,7 +778,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(Regs<kFp8>::kThreads
         if (here) {
           if (sum_ref != ref) l *= exp2_approx((sum_ref - ref) * scale);
           sum_ref = ref;
-          const float neg = -ref * scale;
+          const float neg = fmaf(-ref, scale, kWeightShift<kFp8>);
           const uint64_t neg2 = f2_make(neg, neg);
           uint64_t sum2[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
 #pragma unroll

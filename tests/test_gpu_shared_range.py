@@ -1,0 +1,36 @@
+"""decode_shared at the ends of what it takes: weights far below a row's largest."""
+import pytest
+import torch
+
+from shared_ref import CKV, Case
+from test_gpu_decode_shared import lib, run  # noqa: F401 (lib is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nats", [8.0, 12.0, 17.4, 20.0])
+def test_many_small_weights_beside_a_large_one(lib, fp8, nats):  # noqa: F811
+    """One position far above 60,000 others, whose values it does not share: what they add up to is there.
+
+    In f16 (e4m3 pools) a weight is off by 2^-11 of itself or by 2^-25. The largest weight of a row is 2^7 or more
+    there and in the sum, so that the second is 2^-32 of the sum at most, for each position."""
+    c = Case([(3, 60000)], [0, 40, 700], heads=16, page=64, fp8=fp8, seed=1, layers=1)
+    key = 8.0  # (of the dims behind the value's; exact in either type)
+    c.clean[..., CKV:] = 0
+    c.clean[..., :CKV] = c.clean[..., :CKV] & 0x7F if fp8 else c.clean[..., :CKV].abs()  # (of one sign: what is lost shows)
+    first = c.clean[0, int(c.full[0, 0]), 0]
+    first[:CKV] = 0
+    top = torch.tensor([key / c.scale], device="cuda")
+    first[CKV] = top.to(torch.float8_e4m3fn).view(torch.uint8)[0] if fp8 else top[0]
+    c.pool[0][c.used] = c.clean[0][c.used]
+    c.q.zero_()
+    c.q[..., CKV] = nats / c.softmax_scale / key
+    out, lse, ws = run(lib, c, clusters=1)  # (with more each has a largest weight of its own)
+    assert lib.get_error(ws) == 0
+    for b in c.real():
+        ref, ref_lse, bound, lse_bound = c.reference(b)
+        bound = bound + (2.0 ** -32 * c.rows(b)[:, :CKV].abs().sum(0) if fp8 else 0)
+        d = (out[b].double() - ref).abs()
+        assert bool((d <= bound).all()), (b, (d / bound).max().item(), out[b, 0, 0, 0].item(), ref[0, 0, 0].item())
+        assert bool(((lse[b].double() - ref_lse).abs() <= lse_bound).all())
