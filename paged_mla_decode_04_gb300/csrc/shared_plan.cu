@@ -58,7 +58,7 @@ __device__ __forceinline__ int tile_rows_of(int64_t r, int count, int prefix, in
   return saved * (shared_blocks + kShItemCost) > across * own_blocks ? kShRows : whole;
 }
 
-// A request's cached positions; none for a length out of range.
+// A request's cached positions, or a prefix's: none for a length out of range.
 __device__ __forceinline__ int length_of(int l) { return l < 0 || l >= kShMostLength ? 0 : l; }
 
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanArgs a) {
@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   for (int g = warp; g < a.num_prefixes && !refused; g += warps) {
     const int first = a.prefix_indptr[g], count = a.prefix_indptr[g + 1] - first;
     int p = a.prefix_lens[g];
-    int least = INT_MAX, any_bad = p < 0;
+    int least = INT_MAX, any_bad = p != length_of(p);
+    p = length_of(p);
     int64_t cached = 0;
     for (int b = lane; b < count; b += 32) {
       const int l = a.context_lens[first + b];
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
     if (lane == 0) {
       if (any_bad && count > 0) bad = 1;
       // (a request by itself has its positions in one segment)
-      p = count > 1 ? min(max(p, 0), least) : 0;
+      p = count > 1 ? min(p, least) : 0;
       groups[g] = ShGroup{first, count, p, 0, tile_rows_of(r, count, p, cached)};
     }
   }

@@ -1,8 +1,9 @@
-"""decode_shared at the ends of what it takes: weights far below a row's largest."""
+"""decode_shared at the ends of what it takes: weights far below a row's largest, and
+lengths out of range in a group of several requests."""
 import pytest
 import torch
 
-from shared_ref import CKV, Case
+from shared_ref import CKV, Case, check
 from test_gpu_decode_shared import lib, run  # noqa: F401 (lib is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +35,12 @@ def test_many_small_weights_beside_a_large_one(lib, fp8, nats):  # noqa: F811
         d = (out[b].double() - ref).abs()
         assert bool((d <= bound).all()), (b, (d / bound).max().item(), out[b, 0, 0, 0].item(), ref[0, 0, 0].item())
         assert bool(((lse[b].double() - ref_lse).abs() <= lse_bound).all())
+
+
+@pytest.mark.parametrize("prefix", [-1, -(1 << 31), 1 << 29, (1 << 31) - 1])
+def test_prefix_lengths_out_of_range_count_as_none(lib, prefix):  # noqa: F811
+    c = Case([(3, 0), (2, 100)], [200, 300, 250, 5, 9], heads=16, page=16, seed=2)
+    c.prefix = torch.tensor([prefix, 100], dtype=torch.int32, device="cuda")
+    out, lse, ws = run(lib, c)
+    assert lib.get_error(ws) == lib.STATUS_BAD_LENGTH
+    check(c, out, lse)
