@@ -386,7 +386,10 @@ size_t mla_prefill_workspace_size(int batch, int q_rows, int64_t max_kv_tokens, 
  * num_prefixes and page_size; other values set MLA_STATUS_PLAN_MISMATCH and
  * nothing is written.
  *   context_lens, prefix_lens: device, [batch] and [num_prefixes] int32. Lengths
- *             below 0 or from 2^29 on set MLA_STATUS_BAD_LENGTH and count as 0.
+ *             below 0 or from 2^29 on set MLA_STATUS_BAD_LENGTH (of a group without
+ *             requests none is looked at). Such a prefix length counts as 0; such
+ *             an L_b is left out of P, and its request has the group's P positions
+ *             (none by itself) and its new ones: the others' results stay.
  *   prefix_indptr: device, [num_prefixes + 1] int32, non-decreasing, within
  *             [0, batch]; otherwise MLA_STATUS_BAD_LENGTH is set and the plan is
  *             empty (decode calls with it write nothing).

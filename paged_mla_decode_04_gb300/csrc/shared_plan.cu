@@ -2,7 +2,7 @@
 //
 // The plan reads only lengths: group g's requests [prefix_indptr[g], [g + 1]) share
 // their first P positions, P the least of prefix_lens[g] and its requests' cached
-// lengths. A tile of the group's rows attends the P positions once and then each of its
+// lengths, as far as these are in range. A tile of the group's rows attends the P positions once and then each of its
 // requests' own ones (see shared_internal.h). One block of threads, a launch a step; its
 // time is that of a few passes over the requests, one after the other.
 #include <cuda_bf16.h>
@@ -54,7 +54,7 @@ __device__ __forceinline__ int tile_rows_of(int64_t r, int count, int prefix, in
   while (period % 2 == 0) period /= 2;
   const int64_t across = fewer - 1 - (fewer - 1) / period;
   const int64_t shared_blocks = (prefix + kShTokens - 1) / kShTokens;
-  const int64_t own_blocks = (cached / count - prefix) / kShTokens + 1;  // (of a request, about)
+  const int64_t own_blocks = max(cached / count - prefix, static_cast<int64_t>(0)) / kShTokens + 1;  // (of a request, about)
   return saved * (shared_blocks + kShItemCost) > across * own_blocks ? kShRows : whole;
 }
 
@@ -96,17 +96,21 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
     int64_t cached = 0;
     for (int b = lane; b < count; b += 32) {
       const int l = a.context_lens[first + b];
-      any_bad |= l != length_of(l);
-      least = min(least, length_of(l));
-      cached += length_of(l);
+      if (l == length_of(l)) {
+        least = min(least, l);
+        cached += l;
+      } else {
+        any_bad = 1;
+      }
     }
     for (int d = 16; d > 0; d >>= 1) cached += __shfl_xor_sync(0xffffffffu, cached, d);
     least = __reduce_min_sync(0xffffffffu, least);
     any_bad = __any_sync(0xffffffffu, any_bad);
     if (lane == 0) {
       if (any_bad && count > 0) bad = 1;
-      // (a request by itself has its positions in one segment)
-      p = count > 1 ? min(p, least) : 0;
+      // (a request by itself has its positions in one segment; nor is anything shared where no
+      // length is in range)
+      p = count > 1 && least < kShMostLength ? min(p, least) : 0;
       groups[g] = ShGroup{first, count, p, 0, tile_rows_of(r, count, p, cached)};
     }
   }
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
         s.row_lo = static_cast<int>(max(first_row - from, static_cast<int64_t>(0)));
         s.row_hi = static_cast<int>(min(first_row + r - from, static_cast<int64_t>(rows)));
         const int last_i = static_cast<int>((from + s.row_hi - 1 - first_row) / a.num_heads);
-        s.base = length_of(a.context_lens[s.owner]);
+        s.base = max(length_of(a.context_lens[s.owner]), gr.prefix);  // (of a length out of range: the prefix)
         s.tok_lo = gr.prefix;
         s.tok0 = gr.prefix / unit * unit;
         s.tok_hi = s.base + last_i + 1;

@@ -44,3 +44,32 @@ def test_prefix_lengths_out_of_range_count_as_none(lib, prefix):  # noqa: F811
     out, lse, ws = run(lib, c)
     assert lib.get_error(ws) == lib.STATUS_BAD_LENGTH
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q_len,heads", [(1, 16), (3, 32)])
+@pytest.mark.parametrize("where", [[0], [1], [2], [1, 2]])
+@pytest.mark.parametrize("bad", [-1, 1 << 29, (1 << 31) - 1])
+def test_a_cached_length_out_of_range_is_its_own_requests(lib, fp8, q_len, heads, where, bad):  # noqa: F811
+    """The others keep the prefix (of which they have no table entries of their own); the request itself has the
+    prefix and its new tokens."""
+    c = Case([(3, 203), (2, 90)], [20, 40, 133, 7, 60], heads=heads, q_len=q_len, page=16, fp8=fp8, seed=3)
+    lengths = c.ctx.clone()
+    c.ctx[where] = bad
+    out, lse, ws = run(lib, c)
+    assert lib.get_error(ws) == lib.STATUS_BAD_LENGTH
+    c.ctx = lengths
+    c.ctx[where] = 203
+    check(c, out, lse)
+
+
+def test_a_group_without_a_length_in_range(lib):  # noqa: F811
+    c = Case([(2, 0), (2, 64)], [30, 50, 7, 60], heads=16, page=16, seed=4)
+    c.prefix = torch.tensor([64, 64], dtype=torch.int32, device="cuda")
+    lengths = c.ctx.clone()
+    c.ctx[:2] = torch.tensor([-3, 1 << 30], dtype=torch.int32, device="cuda")
+    out, lse, ws = run(lib, c)
+    assert lib.get_error(ws) == lib.STATUS_BAD_LENGTH
+    c.ctx = lengths
+    c.ctx[:2] = 0
+    check(c, out, lse)
