@@ -95,10 +95,14 @@ static_assert(sizeof(ShTile) == 32 && sizeof(ShSegment) == 32 && sizeof(ShItem) 
 struct ShHeader {
   int status;  // sticky MLA_STATUS_* bits
   int batch, q_len, num_heads, num_prefixes, page_size;
-  int planned;
+  int planned;  // kShPlanned
   int num_clusters, num_tiles, num_items, num_split;
-  int pad[53];
+  int none;  // 0: where mla_decode's plan has its q_len
+  int pad[52];
 };
+// (no count that another plan has there: a workspace may serve several kinds of calls by turns, and
+// a plan one of them only)
+constexpr int kShPlanned = 0x53684c6e;
 static_assert(sizeof(ShHeader) == 256, "one header of 256 bytes");
 
 struct ShLayout {
@@ -173,7 +177,7 @@ struct ShDecodeArgs {
 // Whether the workspace holds a plan for this call. (Clusters beyond the grid's would go
 // unserved.)
 __device__ __forceinline__ bool sh_planned(const ShHeader* hd, const ShDecodeArgs& a) {
-  return hd->planned && hd->batch == a.batch && hd->q_len == a.q_len && hd->num_heads == a.num_heads &&
+  return hd->planned == kShPlanned && hd->batch == a.batch && hd->q_len == a.q_len && hd->num_heads == a.num_heads &&
          hd->num_prefixes == a.num_prefixes && hd->page_size == a.page_size && hd->num_clusters <= a.clusters;
 }
 

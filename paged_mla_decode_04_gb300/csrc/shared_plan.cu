@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
     hd->num_tiles = num_tiles;
     hd->num_items = static_cast<int>(num_items);
     hd->num_split = static_cast<int>(num_split);
-    hd->planned = 1;
+    hd->none = 0;
+    hd->planned = kShPlanned;
   }
 }
 

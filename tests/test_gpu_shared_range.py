@@ -1,5 +1,5 @@
-"""decode_shared at the ends of what it takes: weights far below a row's largest, and
-lengths out of range in a group of several requests."""
+"""decode_shared at the ends of what it takes: weights far below a row's largest, lengths out of
+range in a group of several requests, and workspaces that hold another call's plan."""
 import pytest
 import torch
 
@@ -72,4 +72,29 @@ def test_a_group_without_a_length_in_range(lib):  # noqa: F811
     assert lib.get_error(ws) == lib.STATUS_BAD_LENGTH
     c.ctx = lengths
     c.ctx[:2] = 0
+    check(c, out, lse)
+
+
+def test_plans_of_other_calls_in_the_same_workspace(lib):  # noqa: F811
+    """A plan of mla_decode whose record reads, word by word, as one for this call; and one after the other."""
+    c = Case([(20, 64)], [20, 40, 33, 5, 0], heads=16, q_len=16, page=16, seed=5)
+    ws = torch.zeros(max(lib.workspace_size_shared(20, 16, 16, 1), lib.workspace_size_q(20, 16, 16)), dtype=torch.uint8, device="cuda")
+    lib.plan(c.ctx, 16, 16, 1, ws, num_clusters=16)  # heads, page size, window, clusters: q_len, heads, prefixes, page size
+    torch.cuda.synchronize()
+    words = ws[:256].view(torch.int32).tolist()
+    assert words[1:6] == [20, 16, 16, 1, 16] and words[6] != 0 and words[7] <= 36
+    out, lse, _ = run(lib, c, ws=ws, plan=False)
+    assert lib.get_error(ws, clear=True) == lib.STATUS_PLAN_MISMATCH
+    assert bool((out == 7).all()) and bool((lse == 7).all())
+    run(lib, c, ws=ws, out=out, lse=lse)
+    assert lib.get_error(ws) == 0
+    check(c, out, lse)
+    # the other way round: what mla_decode_q's plan left as its q_len does not stay beside this plan
+    lib.plan_q(c.ctx, 16, 16, 16, 1, ws)
+    lib.plan_shared(c.ctx, c.indptr, c.prefix, 16, 16, 16, ws)
+    torch.cuda.synchronize()
+    words = ws[:256].view(torch.int32).tolist()
+    assert words[11] == 0
+    run(lib, c, ws=ws, plan=False, out=out, lse=lse)
+    assert lib.get_error(ws) == 0
     check(c, out, lse)
