@@ -415,11 +415,12 @@ int mla_decode_plan_shared(const int32_t* context_lens, const int32_t* prefix_in
  * Arithmetic: fp32 accumulation and softmax sums; softmax weights are rounded to
  * the cache's type for the tensor core (bf16; f16 for fp8 pools, whose queries
  * are f16 as mla_decode's are and whose kv_scale multiplies the scores and the
- * output). Calls with the same plan give the same bits. Of a request's new
- * tokens those that a query does not see do not touch its result, whatever they
- * hold; one that it sees and that holds an infinity counts as its score says
- * (NaN, or nothing where the score is -inf). After MLA_STATUS_TIMEOUT out and lse
- * are unspecified. */
+ * output). Scores are below 2^24 in size, in log2 units. Calls with the same plan
+ * give the same bits. Of a request's new tokens those that a query does not see
+ * do not touch its result, whatever they hold. A position that it sees and whose
+ * row holds an infinity makes its score infinite: NaN throughout for +inf; for
+ * -inf NaN in the infinite dims, or nothing where it is a new token behind the
+ * first. After MLA_STATUS_TIMEOUT out and lse are unspecified. */
 int mla_decode_shared(const mla_kv_pool* pool, int layer, const void* q, const int32_t* page_indptr, const int32_t* page_ids,
                       int max_blocks, int batch, int q_len, int num_heads, int num_prefixes, float softmax_scale,
                       void* workspace, void* out, float* lse, void* stream);

@@ -1,5 +1,7 @@
 """decode_shared at the ends of what it takes: weights far below a row's largest, lengths out of
-range in a group of several requests, and workspaces that hold another call's plan."""
+range in a group of several requests, infinite scores, and workspaces that hold another call's plan."""
+import math
+
 import pytest
 import torch
 
@@ -73,6 +75,33 @@ def test_a_group_without_a_length_in_range(lib):  # noqa: F811
     c.ctx = lengths
     c.ctx[:2] = 0
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("at", [-5, 0, 1])
+def test_an_infinity_that_is_seen(lib, sign, at):  # noqa: F811
+    """In a cached row, the first new token's and the second's, with scores of either infinity."""
+    c = Case([(3, 100)], [30, 125, 64], heads=32, q_len=3, page=16, seed=6)
+    c.q[1, ..., 7] = sign * c.q[1, ..., 7].abs().clamp(min=0.5)
+    want, want_lse, _ = run(lib, c)
+    t = int(c.ctx[1]) + at
+    c.pool[c.layer, int(c.full[1, t // c.page]), t % c.page, 7] = math.inf
+    out, lse, ws = run(lib, c)
+    assert lib.get_error(ws) == 0
+    others = [0, 2]
+    assert torch.equal(out[others], want[others]) and torch.equal(lse[others], want_lse[others])
+    first = max(at, 0)  # query position that sees it
+    assert torch.equal(out[1, :first], want[1, :first]) and torch.equal(lse[1, :first], want_lse[1, :first])
+    bad = out[1, first:].isnan()
+    if sign > 0:
+        assert bool(bad.all()) and bool(lse[1, first:].isnan().all())
+        return
+    assert bool(bad[..., 7].all()) == (at < 1) and not bool(bad[..., :7].any() or bad[..., 8:].any())
+    lat = torch.cat([c.rows(1)[:t], c.rows(1)[t + 1:]])  # as without the position
+    ref, ref_lse, bound, lse_bound = c.reference(1, lat)
+    keep = [x for x in range(CKV) if x != 7 or at == 1]
+    assert bool(((out[1].double() - ref).abs() <= bound)[first:][..., keep].all())
+    assert bool(((lse[1].double() - ref_lse).abs() <= lse_bound)[first:].all())
 
 
 def test_plans_of_other_calls_in_the_same_workspace(lib):  # noqa: F811
