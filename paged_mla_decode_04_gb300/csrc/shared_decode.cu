@@ -39,6 +39,7 @@
 #include <limits.h>
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "../../include/mla_decode.h"
@@ -1007,7 +1008,7 @@ cudaError_t launch_variant(const Params& p, cudaStream_t stream) {
 }  // namespace
 
 // Clusters of the kernel that run at once on the current device (cached), or -1: the smaller
-// of the variants' counts, so that a plan serves either.
+// of the variants' counts, so that a plan serves either. (36 on a GB300.)
 int shared_max_active_clusters() {
   static int cached[kMaxDevices] = {};
   const int dev = current_device();
@@ -1015,7 +1016,7 @@ int shared_max_active_clusters() {
   if (cached[dev] > 0) return cached[dev];
   const int a = max_active_clusters<false>(), b = max_active_clusters<true>();
   if (a <= 0 || b <= 0) return -1;
-  return cached[dev] = a < b ? a : b;
+  return cached[dev] = std::min({a, b, kShMostClusters});
 }
 
 cudaError_t launch_shared_decode(const CUtensorMap (&maps)[4], const ShDecodeArgs& a, cudaStream_t stream) {

@@ -21,6 +21,7 @@ namespace mla {
 constexpr int kShRows = 256;
 constexpr int kShTokens = 128;
 constexpr int kShClusterBlocks = 4;  // thread blocks of a cluster
+constexpr int kShMostClusters = 128; // that a plan deals to
 // A tile's first block costs a cluster this many more (queries into place, the
 // pipeline's start, the result's way out, in part behind the item before). 2, 3, 4 and 6 took
 // 56.5, 55.0, 54.7 and 55.6 us a decode of 15 tiles of 37 blocks.

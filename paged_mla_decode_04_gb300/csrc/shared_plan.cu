@@ -199,10 +199,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
   const int64_t c = max(static_cast<int64_t>(1), min(all / kShLeastBlocks, static_cast<int64_t>(a.clusters)));
   if (tid == 0) apart = 0;
   __syncthreads();
-  if (warp == 0 && num_tiles > 0 && num_tiles <= a.clusters && num_tiles <= 128 && all < 1 << 30) {
-    int mine[4], shared[4];  // blocks of tiles lane, lane + 32, ...; of their prefixes
+  if (warp == 0 && num_tiles > 0 && num_tiles <= a.clusters && all < 1 << 30) {
+    constexpr int kEach = kShMostClusters / 32;
+    int mine[kEach], shared[kEach];  // blocks of tiles lane, lane + 32, ...; of their prefixes
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kEach; ++j) {
       const ShTile t = lane + 32 * j < num_tiles ? tiles[lane + 32 * j] : ShTile{};
       mine[j] = t.blocks;
       shared[j] = t.shared;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const ShPlanA
       const int mid = lo + (hi - lo) / 2;
       int pieces = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) pieces += pieces_of(mine[j], shared[j], mid);
+      for (int j = 0; j < kEach; ++j) pieces += pieces_of(mine[j], shared[j], mid);
       pieces = __reduce_add_sync(0xffffffffu, pieces);
       if (pieces <= a.clusters) hi = mid;
       else lo = mid + 1;
