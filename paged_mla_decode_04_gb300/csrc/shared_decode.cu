@@ -27,14 +27,17 @@
 // another's result. Positions outside a segment are masked by selection in S; their rows of
 // V are made zero, or left out 16 at a time.
 //
-// What bounds it: the tensor core, at 2,690 cycles a block of 256 rows and 128 positions (76 %
-// of the products' cycles, as a large library product has them; long calls meet the power limit)
-// where blocks are many: 1.37 PFLOP/s of 16,384 rows at 8,450 positions, 1.35 of 1,024 rows
-// at 65,700, 108 us. Where they are few, what a call cannot overlap: 2 us until queries are in
+// What bounds it: the tensor core, at 2,690 cycles a block of 256 rows and 128 positions (the
+// scores' products take 2,304 of them at the full rate, the values' 2,048; 8 of 152 SMs have no
+// cluster; long calls meet the power limit) where blocks are many: 1.38 PFLOP/s of 16,384 rows at
+// 8,450 positions, 1.36 of 1,024 rows at 65,700, 108 us: 71 % of a library product's rate in
+// short, 79 % of its sustained one. A tile with few rows, and a request's own positions, take the
+// same products. Where blocks are few, what a call cannot overlap: 2 us until queries are in
 // place, 4 from the first scores to the first product of values, 4 to 6 for an item's results
 // (they go out at L2's rate, of all SMs at once) and 3 for the join of its pieces, so that 4
 // tiles of 100 blocks take 41 us. e4m3 pools: four warps widen a block's codes in 2,800
-// cycles, about as long as the products, and queries become f16.
+// cycles, about as long as the products, and queries become f16; 1,024 rows at 65,700 positions
+// take 127 us. (Of the roles' code 108 bytes of registers are spilled, 276 for e4m3 pools.)
 #include <cuda_bf16.h>
 #include <limits.h>
 #include <math_constants.h>

@@ -24,13 +24,18 @@ constexpr int kShClusterBlocks = 4;  // thread blocks of a cluster
 constexpr int kShMostClusters = 128; // that a plan deals to
 // A tile's first block costs a cluster this many more (queries into place, the
 // pipeline's start, the result's way out, in part behind the item before). 2, 3, 4 and 6 took
-// 56.5, 55.0, 54.7 and 55.6 us a decode of 15 tiles of 37 blocks.
+// 56.5, 55.0, 54.7 and 55.6 us a decode of 15 tiles of 37 blocks. Over 28 calls of 2 to 215
+// requests, 8 to 256 rows each, behind 17 to 50,000 positions, 2 and 3 are 0.3 % slower in the
+// mean (0.97 to 1.07 of the time) and 6 is 0.5 % slower (0.98 to 1.05) but for one call of theirs:
+// 69 requests of 128 rows behind 202 positions, 35 tiles for 36 clusters, 20.5 us instead of 33.1.
 constexpr int kShItemCost = 4;
 // A piece of a prefix's blocks costs this many more than one of requests' own (see the plan).
-// Within 2 % from 3 to 7 but for small batches: 18 to 29 us, by turns one or the other.
+// Within 2 % from 3 to 7 but for small batches: 18 to 29 us, by turns one or the other. (Those 28
+// calls: 2 is 0.2 % slower in the mean but for the same one, 7 is 0.3 % faster, 0.93 to 1.04.)
 constexpr int kShRowsCost = 4;
 // Clusters are used as far as each has this many blocks. 2 instead of 3: 15.2 us instead of
-// 16.6, 18.9 instead of 20.1, 24.5 instead of 26.2; at worst 19.6 instead of 18.6.
+// 16.6, 18.9 instead of 20.1, 24.5 instead of 26.2; at worst 19.6 instead of 18.6. (Those 28
+// calls: 3 is 1.5 % slower in the mean, 0.93 to 1.13; 1 is as fast, 0.93 to 1.13.)
 constexpr int kShLeastBlocks = 2;
 
 // Cached positions of a request are fewer (a tile's blocks then count in 32 bits).
